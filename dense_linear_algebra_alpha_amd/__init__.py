@@ -50,9 +50,21 @@ __all__ = [
     "xtvxy_csr_bf16_analysed_ex", "xtvxy_dense_f16", "xtvxy_dense_f16_ex", "xtvxy_csr_bf16_rowdot",
     "xtvxy_csr_bf16_rowdot_ex", "xtvxy_csr_bf16_tmv", "xtvxy_csr_bf16_tmv_ex", "xtvxy_logreg_newton_cg_bf16",
     "xtvxy_tile_stream_probe", "xtvxy_dense_f16_tune", "xtvxy_csr_bf16_tune",
+    "linear", "linear_backward", "ACTIVATIONS", "xtvxy_linear_f32_workspace_size", "xtvxy_linear_bf16_workspace_size",
+    "xtvxy_linear_f16_workspace_size", "xtvxy_linear_f32", "xtvxy_linear_bf16", "xtvxy_linear_f16",
+    "xtvxy_linear_backward_f32_workspace_size", "xtvxy_linear_backward_bf16_workspace_size",
+    "xtvxy_linear_backward_f16_workspace_size", "xtvxy_linear_backward_f32", "xtvxy_linear_backward_bf16",
+    "xtvxy_linear_backward_f16",
 ]
 
 load = _abi.load
+
+from .layers import (ACTIVATIONS, linear, linear_backward, xtvxy_linear_backward_bf16,  # noqa: E402,F401
+                     xtvxy_linear_backward_bf16_workspace_size, xtvxy_linear_backward_f16,
+                     xtvxy_linear_backward_f16_workspace_size, xtvxy_linear_backward_f32,
+                     xtvxy_linear_backward_f32_workspace_size, xtvxy_linear_bf16, xtvxy_linear_bf16_workspace_size,
+                     xtvxy_linear_f16, xtvxy_linear_f16_workspace_size, xtvxy_linear_f32,
+                     xtvxy_linear_f32_workspace_size)
 
 
 # ---------------------------------------------------------------------------

@@ -28,6 +28,12 @@ XTVXY_CSR_TILES = 11
 XTVXY_CSR_WAVES = 12
 XTVXY_CSR_ROWS = 13
 
+XTVXY_ACT_NONE = 0
+XTVXY_ACT_RELU = 1
+XTVXY_ACT_GELU = 2
+XTVXY_ACT_GELU_TANH = 3
+XTVXY_ACT_SILU = 4
+
 XTVXY_PROBE_ATOMIC_PER_XCD = 0
 XTVXY_PROBE_ATOMIC_DEVICE = 1
 XTVXY_PROBE_ITEM_STORES = 2
@@ -183,6 +189,13 @@ SIGNATURES = {
     "xtvxy_logreg_newton_cg_bf16": [_i64, _i64, _i64, _vp, _vp, _vp, _vp, _vp, _P(xtvxy_logreg_options), _vp, _sz,
                                     _vp, _P(xtvxy_logreg_report), _P(ctypes.c_double), _i64],
 }
+for _t in ("f32", "bf16", "f16"):
+    SIGNATURES["xtvxy_linear_%s_workspace_size" % _t] = [_i64, _i64, _i64, _i32, _P(_sz)]
+    SIGNATURES["xtvxy_linear_%s" % _t] = [_i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i64, _i32, _vp, _i64, _vp,
+                                          _i64, _vp, _sz, _vp]
+    SIGNATURES["xtvxy_linear_backward_%s_workspace_size" % _t] = [_i64, _i64, _i64, _i32, _i32, _P(_sz)]
+    SIGNATURES["xtvxy_linear_backward_%s" % _t] = [_i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _i32,
+                                                   _vp, _i64, _vp, _i64, _vp, _vp, _sz, _vp]
 
 _lib = None
 

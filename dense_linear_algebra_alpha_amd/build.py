@@ -23,8 +23,9 @@ ARCH = "gfx950"
 
 SOURCES = ["api.cpp", "model.cpp", "unfused.cpp", "logreg.cpp", "tune.cpp", "csr_analysis.cpp", "dense.hip", "csr.hip",
            "csr_waves.hip", "csr_rows.hip", "csr_bins.hip",
-           "aggregate.hip", "logreg.hip", "probe.hip", "noalloc.hip"]
-HEADERS = ["internal.h", "device_util.h", "csr_common.h"]
+           "aggregate.hip", "logreg.hip", "probe.hip", "noalloc.hip",
+           "linear.cpp", "linear_tile.hip"]
+HEADERS = ["internal.h", "device_util.h", "csr_common.h", "linear.h", "linear_util.h"]
 
 COMMON_FLAGS = [
     "-O3", "-std=c++17", "-fPIC", "-Wall", "-Wno-unused-function",

@@ -1,0 +1,65 @@
+// Internal declarations of the fully connected layer (linear.cpp, linear_*.hip): the products
+// X W^T, D W and D^T X with what follows them, and the gradient through the activation.
+#pragma once
+
+#include "internal.h"
+
+namespace xtvxy {
+
+enum ElemType { kF32 = 0, kBf16 = 1, kF16 = 2 };
+constexpr int elem_size(int t) { return t == kF32 ? 4 : 2; }
+
+// What is done with a product's sums z[i][j] (fp32) before they are stored:
+//   z += bias[j]; pre[i][j] = z; out[i][j] = act(z) + residual[i][j].
+// bias, pre and residual may be null; residual, pre and out have the product's element type.
+struct LinearEpilogue {
+  const float* bias;
+  const void* residual;
+  int64_t ldr;
+  void* pre;
+  int64_t ldp;
+  void* out;
+  int64_t ldo;
+  int32_t act;     // XTVXY_ACT_*
+  int32_t wide;    // rows of out, pre and residual allow 4-element (16 or 8 byte) accesses
+};
+
+// C[i][j] = sum over k of A(i, k) B(j, k), i < m, j < n, followed by the epilogue. Where
+// a_contraction_major, A(i, k) = A[k * lda + i], else A[i * lda + k]; B likewise.
+struct ProductArgs {
+  const void* A;
+  const void* B;
+  int64_t lda, ldb;
+  int64_t m, n, k;
+  int32_t type;
+  int32_t a_contraction_major, b_contraction_major;
+  int32_t a_wide, b_wide;   // 16-byte loads: aligned base, row pitch and contiguous extent
+  int32_t splits;           // parts of the contraction, each with sums of its own in `partial`
+  int64_t k_per_split;      // a multiple of the tile's depth; splits * k_per_split >= k
+  float* partial;           // [splits][m][n] when splits > 1
+  LinearEpilogue e;
+};
+
+constexpr int kTileDepth = 32;   // contraction steps of the 64 x 64 tile kernel
+hipError_t launch_product_tile(const ProductArgs& a, hipStream_t s);
+// Sums the parts of a split product in ascending order and applies the epilogue.
+hipError_t launch_product_finish(const ProductArgs& a, hipStream_t s);
+
+// d = g * act'(pre) (d may be null: column sums only; pre null: slope 1), and per-workgroup
+// column sums of the unrounded d: sums[groups][n].
+struct SlopeArgs {
+  const void* g;
+  const void* pre;
+  void* d;
+  int64_t ldg, ldp, ldd;
+  int64_t m, n;
+  int32_t type, act;
+  int32_t wide;          // 16-byte accesses of g, pre and d
+  float* sums;           // null: no column sums
+  int64_t rows_per_group, groups;
+};
+hipError_t launch_slope(const SlopeArgs& a, hipStream_t s);
+// db[j] = sum over groups of sums[group][j], in ascending order in fp64.
+hipError_t launch_column_finish(const float* sums, int64_t groups, int64_t n, float* db, hipStream_t s);
+
+}  // namespace xtvxy

@@ -1,0 +1,194 @@
+// Device helpers of the fully connected layer: element types, activations and their slopes, and
+// the epilogue that the product kernels share.
+#pragma once
+
+#include "device_util.h"
+#include "linear.h"
+
+namespace xtvxy {
+
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x8 __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+
+template <typename T>
+struct Vec;
+template <>
+struct Vec<float> {
+  typedef f32x4 x4;
+  typedef f32x8 x8;
+};
+template <>
+struct Vec<__bf16> {
+  typedef bf16x4 x4;
+  typedef bf16x8 x8;
+};
+template <>
+struct Vec<_Float16> {
+  typedef f16x4 x4;
+  typedef f16x8 x8;
+};
+
+// acc += sum over 32 contraction steps for a 16 x 16 tile. Lane l brings the 8 steps of row
+// l & 15 that belong to group l >> 4, the same steps for a and b; it gets column l & 15 of rows
+// 4 (l >> 4) + 0..3 of a's index by b's.
+__device__ __forceinline__ f32x4 mfma_16x16(bf16x8 a, bf16x8 b, f32x4 acc) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, acc, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4 mfma_16x16(f16x8 a, f16x8 b, f32x4 acc) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, acc, 0, 0, 0);
+}
+// fp32: eight products of 4 steps each; step s takes element s of each group's eight.
+__device__ __forceinline__ f32x4 mfma_16x16(f32x8 a, f32x8 b, f32x4 acc) {
+#pragma unroll
+  for (int s = 0; s < 8; ++s) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a[s], b[s], acc, 0, 0, 0);
+  return acc;
+}
+
+// exp(x) = 2^(x log2 e) by the hardware's exponential. The product's rounding costs |x| 2^-24
+// relative to the result: results of that size matter next to 1 only where |x| is small.
+__device__ __forceinline__ float fast_exp(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504f); }
+__device__ __forceinline__ float fast_rcp(float x) { return __builtin_amdgcn_rcpf(x); }
+
+// Phi(z) = erfc(-z / sqrt 2) / 2, the normal distribution function; *density gets exp(-z^2 / 2).
+// fp32 results take erfcf. For 16-bit results erfc(a) = exp(-a^2) P5(1 / (1 + 0.35 a)), a >= 0,
+// with P5 fitted to the least largest relative error (2.2e-5 on [0, 12]; half a step of fp16 is
+// 2.4e-4): 6 fused multiply-adds, one reciprocal and one exponential instead of erfcf's about 40
+// operations.
+template <bool kFast>
+__device__ __forceinline__ float normal_cdf(float z, float* density) {
+  if (!kFast) {
+    *density = expf(-0.5f * z * z);
+    return 0.5f * erfcf(z * -0.70710678f);
+  }
+  const float t = fast_rcp(fmaf(fabsf(z), 0.35f * 0.70710678f, 1.0f));
+  const float x = fast_exp(-0.5f * z * z);
+  float p = 0.5491096602476102f;
+  p = fmaf(p, t, -0.34366955118616876f);
+  p = fmaf(p, t, 0.474523528705992f);
+  p = fmaf(p, t, 0.1100193553124311f);
+  p = fmaf(p, t, 0.2108346123613167f);
+  p = fmaf(p, t, -0.0008098688139377294f);
+  const float tail = 0.5f * p * x;  // Phi(-|z|)
+  *density = x;
+  return z < 0.0f ? tail : 1.0f - tail;
+}
+
+// Twice the argument of the tanh in gelu's tanh form: (1 + tanh u) / 2 = 1 / (1 + exp(-2u)).
+__device__ __forceinline__ float gelu_tanh_arg(float z) {
+  return z * fmaf(z * z, 2.0f * 0.79788456f * 0.044715f, 2.0f * 0.79788456f);
+}
+
+template <bool kFast>
+__device__ __forceinline__ float sigmoid(float x) {
+  if (!kFast) return 1.0f / (1.0f + expf(-x));
+  return fast_rcp(1.0f + fast_exp(-x));
+}
+
+template <bool kFast, int kAct>
+__device__ __forceinline__ float activation(float z) {
+  if (kAct == XTVXY_ACT_RELU) return z < 0.0f ? 0.0f : z;  // NaN stays
+  if (kAct == XTVXY_ACT_GELU) {
+    float x;
+    return z * normal_cdf<kFast>(z, &x);
+  }
+  if (kAct == XTVXY_ACT_GELU_TANH) return z * sigmoid<kFast>(gelu_tanh_arg(z));
+  if (kAct == XTVXY_ACT_SILU) return z * sigmoid<kFast>(z);
+  return z;
+}
+
+// d activation / dz.
+template <bool kFast, int kAct>
+__device__ __forceinline__ float slope(float z) {
+  if (kAct == XTVXY_ACT_RELU) return z > 0.0f ? 1.0f : 0.0f;
+  if (kAct == XTVXY_ACT_GELU) {
+    float x;
+    const float c = normal_cdf<kFast>(z, &x);
+    return fmaf(z * x, 0.39894228f, c);
+  }
+  if (kAct == XTVXY_ACT_GELU_TANH) {
+    const float q = sigmoid<kFast>(gelu_tanh_arg(z));
+    const float w = q * (1.0f - q);
+    // where the sigmoid is flat its slope is zero whatever z^3 has grown to
+    return w == 0.0f ? q : fmaf(z * w, fmaf(z * z, 6.0f * 0.79788456f * 0.044715f, 2.0f * 0.79788456f), q);
+  }
+  if (kAct == XTVXY_ACT_SILU) {
+    const float q = sigmoid<kFast>(z);
+    return q * fmaf(z, 1.0f - q, 1.0f);
+  }
+  return 1.0f;
+}
+
+// Four elements of a row, from j0, of which `count` exist.
+template <typename T>
+__device__ __forceinline__ f32x4 load4(const T* p, int count, bool wide) {
+  f32x4 r = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (wide) {
+    const typename Vec<T>::x4 v = *reinterpret_cast<const typename Vec<T>::x4*>(p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r[i] = (float)v[i];
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < count) r[i] = (float)p[i];
+  }
+  return r;
+}
+
+template <typename T>
+__device__ __forceinline__ void store4(T* p, f32x4 v, int count, bool wide) {
+  if (wide) {
+    typename Vec<T>::x4 o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = (T)v[i];
+    *reinterpret_cast<typename Vec<T>::x4*>(p) = o;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < count) p[i] = (T)v[i];
+  }
+}
+
+template <bool kFast>
+__device__ __forceinline__ f32x4 activation4(f32x4 z, int act) {
+  f32x4 r = z;
+  switch (act) {
+#define XTVXY_ACT_CASE(A)                                                  \
+  case A:                                                                  \
+    _Pragma("unroll") for (int i = 0; i < 4; ++i) r[i] = activation<kFast, A>(z[i]); \
+    break;
+    XTVXY_ACT_CASE(XTVXY_ACT_RELU)
+    XTVXY_ACT_CASE(XTVXY_ACT_GELU)
+    XTVXY_ACT_CASE(XTVXY_ACT_GELU_TANH)
+    XTVXY_ACT_CASE(XTVXY_ACT_SILU)
+#undef XTVXY_ACT_CASE
+    default: break;
+  }
+  return r;
+}
+
+// The epilogue of four neighbouring columns j..j+3 of row i; columns >= n do not exist. z is kept
+// in fp32 through bias, activation and residual and rounded once per stored element.
+template <typename T>
+__device__ __forceinline__ void epilogue4(const LinearEpilogue& e, int64_t i, int64_t j, int64_t n, f32x4 z) {
+  const int count = n - j >= 4 ? 4 : (int)(n - j);
+  if (count <= 0) return;
+  const bool wide = e.wide && count == 4;
+  if (e.bias) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      if (c < count) z[c] += e.bias[j + c];
+  }
+  if (e.pre) store4<T>(static_cast<T*>(e.pre) + i * e.ldp + j, z, count, wide);
+  f32x4 y = activation4<sizeof(T) == 2>(z, e.act);
+  if (e.residual) y += load4<T>(static_cast<const T*>(e.residual) + i * e.ldr + j, count, wide);
+  store4<T>(static_cast<T*>(e.out) + i * e.ldo + j, y, count, wide);
+}
+
+}  // namespace xtvxy

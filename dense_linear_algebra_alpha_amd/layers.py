@@ -1,0 +1,262 @@
+"""A fully connected layer, its gradient and the AdamW step: the C names of include/xtvxy.h and the
+torch tensor helpers on them (argument marshalling only, as in the package's other helpers)."""
+from __future__ import annotations
+
+import ctypes
+import functools
+
+from . import _abi
+from ._abi import (XTVXY_ACT_GELU, XTVXY_ACT_GELU_TANH, XTVXY_ACT_NONE, XTVXY_ACT_RELU, XTVXY_ACT_SILU)
+
+ACTIVATIONS = {"none": XTVXY_ACT_NONE, "relu": XTVXY_ACT_RELU, "gelu": XTVXY_ACT_GELU,
+               "gelu_tanh": XTVXY_ACT_GELU_TANH, "silu": XTVXY_ACT_SILU}
+
+
+# ---------------------------------------------------------------------------
+# C names
+# ---------------------------------------------------------------------------
+
+def _size(name, *args) -> int:
+    b = ctypes.c_size_t()
+    _abi.call(name, *args, ctypes.byref(b))
+    return b.value
+
+
+def xtvxy_linear_f32_workspace_size(m, k, n, aligned16=1) -> int:
+    return _size("xtvxy_linear_f32_workspace_size", m, k, n, int(aligned16))
+
+
+def xtvxy_linear_bf16_workspace_size(m, k, n, aligned16=1) -> int:
+    return _size("xtvxy_linear_bf16_workspace_size", m, k, n, int(aligned16))
+
+
+def xtvxy_linear_f16_workspace_size(m, k, n, aligned16=1) -> int:
+    return _size("xtvxy_linear_f16_workspace_size", m, k, n, int(aligned16))
+
+
+def xtvxy_linear_f32(m, k, n, X, ldx, W, ldw, bias, residual, ldr, activation, out, ldo, pre, ldp, workspace,
+                     workspace_bytes, stream):
+    return _abi.call("xtvxy_linear_f32", m, k, n, X, ldx, W, ldw, bias, residual, ldr, activation, out, ldo, pre, ldp,
+                     workspace, workspace_bytes, stream)
+
+
+def xtvxy_linear_bf16(m, k, n, X, ldx, W, ldw, bias, residual, ldr, activation, out, ldo, pre, ldp, workspace,
+                      workspace_bytes, stream):
+    return _abi.call("xtvxy_linear_bf16", m, k, n, X, ldx, W, ldw, bias, residual, ldr, activation, out, ldo, pre, ldp,
+                     workspace, workspace_bytes, stream)
+
+
+def xtvxy_linear_f16(m, k, n, X, ldx, W, ldw, bias, residual, ldr, activation, out, ldo, pre, ldp, workspace,
+                     workspace_bytes, stream):
+    return _abi.call("xtvxy_linear_f16", m, k, n, X, ldx, W, ldw, bias, residual, ldr, activation, out, ldo, pre, ldp,
+                     workspace, workspace_bytes, stream)
+
+
+def xtvxy_linear_backward_f32_workspace_size(m, k, n, activation, aligned16=1) -> int:
+    return _size("xtvxy_linear_backward_f32_workspace_size", m, k, n, activation, int(aligned16))
+
+
+def xtvxy_linear_backward_bf16_workspace_size(m, k, n, activation, aligned16=1) -> int:
+    return _size("xtvxy_linear_backward_bf16_workspace_size", m, k, n, activation, int(aligned16))
+
+
+def xtvxy_linear_backward_f16_workspace_size(m, k, n, activation, aligned16=1) -> int:
+    return _size("xtvxy_linear_backward_f16_workspace_size", m, k, n, activation, int(aligned16))
+
+
+def xtvxy_linear_backward_f32(m, k, n, G, ldg, X, ldx, W, ldw, pre, ldp, activation, dX, lddx, dW, lddw, db, workspace,
+                              workspace_bytes, stream):
+    return _abi.call("xtvxy_linear_backward_f32", m, k, n, G, ldg, X, ldx, W, ldw, pre, ldp, activation, dX, lddx, dW,
+                     lddw, db, workspace, workspace_bytes, stream)
+
+
+def xtvxy_linear_backward_bf16(m, k, n, G, ldg, X, ldx, W, ldw, pre, ldp, activation, dX, lddx, dW, lddw, db, workspace,
+                               workspace_bytes, stream):
+    return _abi.call("xtvxy_linear_backward_bf16", m, k, n, G, ldg, X, ldx, W, ldw, pre, ldp, activation, dX, lddx, dW,
+                     lddw, db, workspace, workspace_bytes, stream)
+
+
+def xtvxy_linear_backward_f16(m, k, n, G, ldg, X, ldx, W, ldw, pre, ldp, activation, dX, lddx, dW, lddw, db, workspace,
+                              workspace_bytes, stream):
+    return _abi.call("xtvxy_linear_backward_f16", m, k, n, G, ldg, X, ldx, W, ldw, pre, ldp, activation, dX, lddx, dW,
+                     lddw, db, workspace, workspace_bytes, stream)
+
+
+# ---------------------------------------------------------------------------
+# torch tensor helpers
+# ---------------------------------------------------------------------------
+
+@functools.lru_cache(maxsize=None)
+def _suffix(dtype) -> str:
+    import torch
+    s = {torch.float32: "f32", torch.bfloat16: "bf16", torch.float16: "f16"}.get(dtype)
+    if s is None:
+        raise ValueError("element type must be float32, bfloat16 or float16, not %s" % dtype)
+    return s
+
+
+@functools.lru_cache(maxsize=4096)
+def _linear_bytes(suffix, m, k, n, aligned) -> int:
+    return _size("xtvxy_linear_%s_workspace_size" % suffix, m, k, n, aligned)
+
+
+@functools.lru_cache(maxsize=4096)
+def _backward_bytes(suffix, m, k, n, act, aligned) -> int:
+    return _size("xtvxy_linear_backward_%s_workspace_size" % suffix, m, k, n, act, aligned)
+
+
+def _activation_code(act) -> int:
+    code = ACTIVATIONS.get(act)
+    if code is None:
+        raise ValueError("activation must be one of %s, not %r" % (", ".join(ACTIVATIONS), act))
+    return code
+
+
+def _pitch(name, t, rows, cols, dtype, device) -> int:
+    """The row stride of a rows x cols matrix argument, checked."""
+    if t.dtype != dtype or t.device != device or t.dim() != 2:
+        raise ValueError("%s must be a 2-D %s tensor on %s" % (name, dtype, device))
+    r, c = t.shape
+    if r != rows or c != cols:
+        raise ValueError("%s must be %d x %d, not %d x %d" % (name, rows, cols, r, c))
+    s0, s1 = t.stride()
+    if s1 != 1 and cols > 1:
+        raise ValueError("%s needs unit column stride" % name)
+    if rows <= 1:
+        return max(cols, 1)
+    if s0 < cols or s0 < 1:
+        raise ValueError("%s needs a row stride of at least its width" % name)
+    return s0
+
+
+def _check_bias(name, t, n, device):
+    import torch
+    if t.dtype != torch.float32 or t.device != device or t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
+        raise ValueError("%s must be a contiguous float32 vector of %d elements on %s" % (name, n, device))
+
+
+def _scratch(need, workspace, device):
+    """(tensor made here or None, pointer, bytes) of the workspace of a call that needs `need` bytes."""
+    if workspace is not None:
+        if workspace.device != device or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on %s" % device)
+        return None, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    if need == 0:
+        return None, None, 0
+    import torch
+    ws = torch.empty(need, dtype=torch.uint8, device=device)
+    return ws, ws.data_ptr(), need
+
+
+def linear(X, W, bias=None, residual=None, act="none", *, save_pre=False, out=None, pre=None, workspace=None,
+           stream=None):
+    """out = act(X W^T + bias) + residual: a fully connected layer (xtvxy_linear_f32, _bf16, _f16).
+
+    X (m x k), W (n x k), residual and out (m x n) are 2-D tensors with unit column stride, of one
+    type: float32, bfloat16 or float16; bias is float32 (n). ``act`` is one of ACTIVATIONS. With
+    ``save_pre`` (or ``pre`` given) the call also stores X W^T + bias, which linear_backward takes,
+    and returns (out, pre). ``out`` may be the residual."""
+    from . import _keep_for_stream, _stream_handle
+    device, dtype = X.device, X.dtype
+    if device.type != "cuda":
+        raise ValueError("X must be on the GPU, not on %s" % device)
+    suffix = _suffix(dtype)
+    code = _activation_code(act)
+    if X.dim() != 2 or W.dim() != 2:
+        raise ValueError("X and W must be 2-D")
+    m, k = X.shape
+    n = W.shape[0]
+    ldx, ldw = _pitch("X", X, m, k, dtype, device), _pitch("W", W, n, k, dtype, device)
+    bias_ptr = residual_ptr = pre_ptr = None
+    ldr = ldp = n
+    if bias is not None:
+        _check_bias("bias", bias, n, device)
+        bias_ptr = bias.data_ptr()
+    if residual is not None:
+        ldr = _pitch("residual", residual, m, n, dtype, device)
+        residual_ptr = residual.data_ptr()
+    made_out = out is None
+    if made_out:
+        out = X.new_empty((m, n))
+        ldo = n or 1
+    else:
+        ldo = _pitch("out", out, m, n, dtype, device)
+    made_pre = save_pre and pre is None
+    if made_pre:
+        pre = X.new_empty((m, n))
+        ldp = n or 1
+    elif pre is not None:
+        ldp = _pitch("pre", pre, m, n, dtype, device)
+    if pre is not None:
+        pre_ptr = pre.data_ptr()
+    xp, wp = X.data_ptr(), W.data_ptr()
+    es = 4 if suffix == "f32" else 2
+    aligned = 0 if (xp | wp | ldx * es | ldw * es) & 15 else 1
+    made_ws, ws_ptr, ws_bytes = _scratch(_linear_bytes(suffix, m, k, n, aligned), workspace, device)
+    _abi.call("xtvxy_linear_" + suffix, m, k, n, xp, ldx, wp, ldw, bias_ptr, residual_ptr, ldr or 1, code,
+              out.data_ptr(), ldo, pre_ptr, ldp or 1, ws_ptr, ws_bytes, _stream_handle(stream))
+    if stream is not None:
+        _keep_for_stream(stream, out if made_out else None, pre if made_pre else None, made_ws)
+    return out if pre is None else (out, pre)
+
+
+def linear_backward(G, X, W, pre=None, act="none", *, need_dX=True, need_dW=True, need_db=True, dX=None, dW=None,
+                    db=None, workspace=None, stream=None):
+    """The gradient of linear: (dX, dW, db) for G = d loss / d out, with d = G * act'(pre),
+    dX = d W, dW = d^T X and db the column sums of d (float32). The residual's gradient is G.
+
+    ``pre`` is what linear stored (required unless act is "none"). Outputs that are not needed are
+    not computed and come back as None."""
+    import torch
+
+    from . import _keep_for_stream, _stream_handle
+    device, dtype = X.device, X.dtype
+    if device.type != "cuda":
+        raise ValueError("X must be on the GPU, not on %s" % device)
+    suffix = _suffix(dtype)
+    code = _activation_code(act)
+    if X.dim() != 2 or W.dim() != 2:
+        raise ValueError("X and W must be 2-D")
+    m, k = X.shape
+    n = W.shape[0]
+    ldx, ldw = _pitch("X", X, m, k, dtype, device), _pitch("W", W, n, k, dtype, device)
+    ldg = _pitch("G", G, m, n, dtype, device)
+    ldp, pre_ptr = n or 1, None
+    if code != XTVXY_ACT_NONE:
+        if pre is None:
+            raise ValueError("pre is required for activation %r" % act)
+        ldp = _pitch("pre", pre, m, n, dtype, device)
+        pre_ptr = pre.data_ptr()
+    made = []
+    lddx, lddw = k or 1, k or 1
+    if not need_dX:
+        dX = None
+    elif dX is None:
+        dX = X.new_empty((m, k))
+        made.append(dX)
+    else:
+        lddx = _pitch("dX", dX, m, k, dtype, device)
+    if not need_dW:
+        dW = None
+    elif dW is None:
+        dW = X.new_empty((n, k))
+        made.append(dW)
+    else:
+        lddw = _pitch("dW", dW, n, k, dtype, device)
+    if not need_db:
+        db = None
+    elif db is None:
+        db = torch.empty(n, dtype=torch.float32, device=device)
+        made.append(db)
+    else:
+        _check_bias("db", db, n, device)
+    gp, xp, wp = G.data_ptr(), X.data_ptr(), W.data_ptr()
+    es = 4 if suffix == "f32" else 2
+    aligned = 0 if (gp | xp | wp | ldg * es | ldx * es | ldw * es) & 15 else 1
+    made_ws, ws_ptr, ws_bytes = _scratch(_backward_bytes(suffix, m, k, n, code, aligned), workspace, device)
+    _abi.call("xtvxy_linear_backward_" + suffix, m, k, n, gp, ldg, xp, ldx, wp, ldw, pre_ptr, ldp, code,
+              None if dX is None else dX.data_ptr(), lddx, None if dW is None else dW.data_ptr(), lddw,
+              None if db is None else db.data_ptr(), ws_ptr, ws_bytes, _stream_handle(stream))
+    if stream is not None:
+        _keep_for_stream(stream, *made, made_ws)
+    return dX, dW, db

@@ -680,6 +680,83 @@ xtvxy_status xtvxy_logreg_newton_cg_bf16(int64_t m, int64_t n, int64_t nnz, cons
                                          size_t workspace_bytes, hipStream_t stream, xtvxy_logreg_report *report,
                                          double *history, int64_t history_rows);
 
+/* ------------------------------------------------------------------------ */
+/* A fully connected layer, its gradient, and the AdamW step                */
+/* ------------------------------------------------------------------------ */
+
+/* The layer on the same row-major features X that the pattern above reads:
+ *     z = X W^T + bias,   out = act(z) + residual,   pre = z (optional),
+ * X m x k (row stride ldx >= max(1, k)), W n x k (one row per output, row stride ldw), out, residual
+ * and pre m x n (row strides ldo, ldr, ldp >= max(1, n)), bias n floats. X, W, out, residual and
+ * pre share one element type (fp32, or bf16 / fp16 bit patterns); bias is fp32. z is summed in fp32
+ * and stays in fp32 through bias, activation and residual; out and pre are rounded once, as they
+ * are stored. bias, residual and pre may be NULL; m == 0 or n == 0 is a no-op, k == 0 gives z = bias.
+ * Activations, evaluated as the formulas say under IEEE (NaN propagates):
+ *     NONE       z
+ *     RELU       z < 0 ? 0 : z
+ *     GELU       z Phi(z), Phi the normal distribution function (the erf form)
+ *     GELU_TANH  z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3))) / 2
+ *     SILU       z / (1 + exp(-z))
+ * out may equal residual (same stride): each element is read before it is written. Any other
+ * overlap of an output with an input or another output gives XTVXY_ERROR_ALIASING (column blocks
+ * of one matrix, i.e. equal strides and disjoint columns, do not overlap). Results are bitwise
+ * reproducible for a given shape, type and alignment. Strides and pointers of any alignment are
+ * accepted; 16-byte aligned X and W rows are the fast case. */
+enum {
+  XTVXY_ACT_NONE = 0,
+  XTVXY_ACT_RELU = 1,
+  XTVXY_ACT_GELU = 2,
+  XTVXY_ACT_GELU_TANH = 3,
+  XTVXY_ACT_SILU = 4
+};
+
+/* Workspace bytes of the layer for this shape; aligned16 states whether X, W and their rows are
+ * 16-byte aligned (pointers and strides). */
+xtvxy_status xtvxy_linear_f32_workspace_size(int64_t m, int64_t k, int64_t n, int aligned16, size_t *bytes);
+xtvxy_status xtvxy_linear_bf16_workspace_size(int64_t m, int64_t k, int64_t n, int aligned16, size_t *bytes);
+xtvxy_status xtvxy_linear_f16_workspace_size(int64_t m, int64_t k, int64_t n, int aligned16, size_t *bytes);
+xtvxy_status xtvxy_linear_f32(int64_t m, int64_t k, int64_t n, const float *X, int64_t ldx, const float *W, int64_t ldw,
+                              const float *bias, const float *residual, int64_t ldr, int activation, float *out,
+                              int64_t ldo, float *pre, int64_t ldp, void *workspace, size_t workspace_bytes,
+                              hipStream_t stream);
+xtvxy_status xtvxy_linear_bf16(int64_t m, int64_t k, int64_t n, const uint16_t *X, int64_t ldx, const uint16_t *W,
+                               int64_t ldw, const float *bias, const uint16_t *residual, int64_t ldr, int activation,
+                               uint16_t *out, int64_t ldo, uint16_t *pre, int64_t ldp, void *workspace,
+                               size_t workspace_bytes, hipStream_t stream);
+xtvxy_status xtvxy_linear_f16(int64_t m, int64_t k, int64_t n, const uint16_t *X, int64_t ldx, const uint16_t *W,
+                              int64_t ldw, const float *bias, const uint16_t *residual, int64_t ldr, int activation,
+                              uint16_t *out, int64_t ldo, uint16_t *pre, int64_t ldp, void *workspace,
+                              size_t workspace_bytes, hipStream_t stream);
+
+/* The layer's gradient, from G = d loss / d out (m x n, row stride ldg) and the pre-activations that
+ * the forward call stored (the residual's gradient is G itself):
+ *     d = G .* act'(pre),   dX = d W (m x k, contiguous rows of lddx),   dW = d^T X (n x k, lddw),
+ *     db_j = sum_i d_ij (n floats).
+ * act'(z) of RELU is 1 where z > 0, else 0. pre may be NULL iff activation is XTVXY_ACT_NONE.
+ * dX, dW and db may each be NULL (not computed; W is read only for dX, X only for dW). d is formed
+ * in fp32; db sums it unrounded, and the products take it in the element type (fp32: unrounded).
+ * m == 0 gives dW = 0 and db = 0; n == 0 gives dX = 0. Otherwise as the layer. */
+xtvxy_status xtvxy_linear_backward_f32_workspace_size(int64_t m, int64_t k, int64_t n, int activation, int aligned16,
+                                                      size_t *bytes);
+xtvxy_status xtvxy_linear_backward_bf16_workspace_size(int64_t m, int64_t k, int64_t n, int activation, int aligned16,
+                                                       size_t *bytes);
+xtvxy_status xtvxy_linear_backward_f16_workspace_size(int64_t m, int64_t k, int64_t n, int activation, int aligned16,
+                                                      size_t *bytes);
+xtvxy_status xtvxy_linear_backward_f32(int64_t m, int64_t k, int64_t n, const float *G, int64_t ldg, const float *X,
+                                       int64_t ldx, const float *W, int64_t ldw, const float *pre, int64_t ldp,
+                                       int activation, float *dX, int64_t lddx, float *dW, int64_t lddw, float *db,
+                                       void *workspace, size_t workspace_bytes, hipStream_t stream);
+xtvxy_status xtvxy_linear_backward_bf16(int64_t m, int64_t k, int64_t n, const uint16_t *G, int64_t ldg,
+                                        const uint16_t *X, int64_t ldx, const uint16_t *W, int64_t ldw,
+                                        const uint16_t *pre, int64_t ldp, int activation, uint16_t *dX, int64_t lddx,
+                                        uint16_t *dW, int64_t lddw, float *db, void *workspace, size_t workspace_bytes,
+                                        hipStream_t stream);
+xtvxy_status xtvxy_linear_backward_f16(int64_t m, int64_t k, int64_t n, const uint16_t *G, int64_t ldg,
+                                       const uint16_t *X, int64_t ldx, const uint16_t *W, int64_t ldw,
+                                       const uint16_t *pre, int64_t ldp, int activation, uint16_t *dX, int64_t lddx,
+                                       uint16_t *dW, int64_t lddw, float *db, void *workspace, size_t workspace_bytes,
+                                       hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
