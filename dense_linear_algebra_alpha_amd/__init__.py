@@ -54,7 +54,8 @@ __all__ = [
     "xtvxy_linear_f16_workspace_size", "xtvxy_linear_f32", "xtvxy_linear_bf16", "xtvxy_linear_f16",
     "xtvxy_linear_backward_f32_workspace_size", "xtvxy_linear_backward_bf16_workspace_size",
     "xtvxy_linear_backward_f16_workspace_size", "xtvxy_linear_backward_f32", "xtvxy_linear_backward_bf16",
-    "xtvxy_linear_backward_f16",
+    "xtvxy_linear_backward_f16", "AdamW", "xtvxy_adamw_create", "xtvxy_adamw_destroy", "xtvxy_adamw_step",
+    "xtvxy_adamw_state_values",
 ]
 
 load = _abi.load
@@ -65,6 +66,8 @@ from .layers import (ACTIVATIONS, linear, linear_backward, xtvxy_linear_backward
                      xtvxy_linear_backward_f32_workspace_size, xtvxy_linear_bf16, xtvxy_linear_bf16_workspace_size,
                      xtvxy_linear_f16, xtvxy_linear_f16_workspace_size, xtvxy_linear_f32,
                      xtvxy_linear_f32_workspace_size)
+from .optimiser import (AdamW, xtvxy_adamw_create, xtvxy_adamw_destroy, xtvxy_adamw_state_values,  # noqa: E402,F401
+                        xtvxy_adamw_step)
 
 
 # ---------------------------------------------------------------------------

@@ -34,6 +34,11 @@ XTVXY_ACT_GELU = 2
 XTVXY_ACT_GELU_TANH = 3
 XTVXY_ACT_SILU = 4
 
+XTVXY_TYPE_NONE = 0
+XTVXY_TYPE_F32 = 1
+XTVXY_TYPE_BF16 = 2
+XTVXY_TYPE_F16 = 3
+
 XTVXY_PROBE_ATOMIC_PER_XCD = 0
 XTVXY_PROBE_ATOMIC_DEVICE = 1
 XTVXY_PROBE_ITEM_STORES = 2
@@ -196,6 +201,13 @@ for _t in ("f32", "bf16", "f16"):
     SIGNATURES["xtvxy_linear_backward_%s_workspace_size" % _t] = [_i64, _i64, _i64, _i32, _i32, _P(_sz)]
     SIGNATURES["xtvxy_linear_backward_%s" % _t] = [_i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _i32,
                                                    _vp, _i64, _vp, _i64, _vp, _vp, _sz, _vp]
+_vpp, _f64 = _P(_vp), ctypes.c_double
+SIGNATURES.update({
+    "xtvxy_adamw_create": [ctypes.c_int32, _P(_i64), _vpp, _i32, _vpp, _vpp, _vpp, _vpp, _i32, _vpp, _vpp],
+    "xtvxy_adamw_destroy": [_vp],
+    "xtvxy_adamw_step": [_vp, _vpp, _i32, _i64, _f64, _f64, _f64, _f64, _f64, ctypes.c_uint32, _vp],
+    "xtvxy_adamw_state_values": [_vp, _vpp, _vpp, _i32, _vp],
+})
 
 _lib = None
 

@@ -24,8 +24,8 @@ ARCH = "gfx950"
 SOURCES = ["api.cpp", "model.cpp", "unfused.cpp", "logreg.cpp", "tune.cpp", "csr_analysis.cpp", "dense.hip", "csr.hip",
            "csr_waves.hip", "csr_rows.hip", "csr_bins.hip",
            "aggregate.hip", "logreg.hip", "probe.hip", "noalloc.hip",
-           "linear.cpp", "linear_tile.hip"]
-HEADERS = ["internal.h", "device_util.h", "csr_common.h", "linear.h", "linear_util.h"]
+           "linear.cpp", "linear_tile.hip", "adamw.cpp", "adamw.hip"]
+HEADERS = ["internal.h", "device_util.h", "csr_common.h", "linear.h", "linear_util.h", "adamw.h"]
 
 COMMON_FLAGS = [
     "-O3", "-std=c++17", "-fPIC", "-Wall", "-Wno-unused-function",

@@ -757,6 +757,51 @@ xtvxy_status xtvxy_linear_backward_f16(int64_t m, int64_t k, int64_t n, const ui
                                        uint16_t *dW, int64_t lddw, float *db, void *workspace, size_t workspace_bytes,
                                        hipStream_t stream);
 
+/* Element types of the optimiser's gradients, copies and state values. */
+enum { XTVXY_TYPE_NONE = 0, XTVXY_TYPE_F32 = 1, XTVXY_TYPE_BF16 = 2, XTVXY_TYPE_F16 = 3 };
+
+/* The AdamW step over many tensors in one launch per 400 tensors. Step t = 1, 2, ... of an element:
+ *     m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2,
+ *     p = p (1 - lr weight_decay) - lr / (1 - beta1^t) m / (sqrt(v) / sqrt(1 - beta2^t) + eps),
+ * in fp32 with fp32 parameters; then the 16-bit copy of p, if the optimiser has copies. Each tensor
+ * is contiguous; its pointers may have any alignment that its types allow (16 bytes: fast).
+ *
+ * state_bits 32: m and v fp32. state_bits 8: m and v are codes, one byte per element, in blocks of 128
+ * elements of a tensor (the last may be shorter) that share a biased exponent e (one byte per block
+ * in m_exp and v_exp, 1..253): a value is its code's value times 2^(e - 127).
+ *     m: e4m3 (sign, 4 exponent bits of bias 7, 3 mantissa bits; 0x7f NaN, no infinities; up to 448)
+ *     v: 4 exponent bits of bias 15 and 4 mantissa bits (code c < 16: c 2^-18; up to 1.9375)
+ * A step decodes the states, updates them in fp32, uses those for p, and stores them with the smallest
+ * exponent that holds the block's largest finite value, rounded at random: up with the probability of
+ * the remainder (m's in steps of 2^-13, v's of 2^-19). A nonzero v is never stored as zero. The random
+ * bits are a hash of the element's number (through all tensors, each beginning at the next
+ * multiple of 128, mod 2^32), the seed and t, so a step is bitwise reproducible. A NaN or infinite m
+ * is stored as NaN, a NaN or infinite v as the largest code; the others of the block keep theirs.
+ * Fresh 8-bit states are zero codes with any exponents.
+ *
+ * xtvxy_adamw_create is a set-up call: it allocates and fills a table of the tensors in device memory
+ * (synchronising) and keeps the pointers to params, states and copies, which must stay valid until
+ * xtvxy_adamw_destroy. numel, params, m, v, m_exp, v_exp and copies are HOST arrays of `tensors`
+ * entries (m_exp and v_exp NULL for 32 bits, copies NULL for copy_type XTVXY_TYPE_NONE); entries of
+ * empty tensors may be NULL. Overlapping buffers give XTVXY_ERROR_ALIASING. Gradients (host
+ * array of device pointers, one type for all) are passed at each step and may be other tensors each
+ * time; they may not overlap what a step writes. The object is used on the device that was current when
+ * it was made (XTVXY_ERROR_INVALID_VALUE otherwise); steps of one object run in stream order.
+ * A captured step replays with the t and rates that it was captured with. */
+typedef struct xtvxy_adamw_s *xtvxy_adamw;
+xtvxy_status xtvxy_adamw_create(int32_t tensors, const int64_t *numel, float *const *params, int state_bits,
+                                void *const *m, void *const *v, uint8_t *const *m_exp, uint8_t *const *v_exp,
+                                int copy_type, void *const *copies, xtvxy_adamw *optimiser);
+xtvxy_status xtvxy_adamw_destroy(xtvxy_adamw optimiser);
+/* lr, eps, weight_decay finite and >= 0; betas in [0, 1); step >= 1. */
+xtvxy_status xtvxy_adamw_step(xtvxy_adamw optimiser, const void *const *grads, int grad_type, int64_t step, double lr,
+                              double beta1, double beta2, double eps, double weight_decay, uint32_t seed,
+                              hipStream_t stream);
+/* Writes the values that m and v stand for into fp32, bf16 or fp16 tensors (host arrays of device
+ * pointers; those of 8-bit states are exact in bf16 unless below its normal range). */
+xtvxy_status xtvxy_adamw_state_values(xtvxy_adamw optimiser, void *const *m_out, void *const *v_out, int type,
+                                      hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

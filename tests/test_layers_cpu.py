@@ -105,3 +105,44 @@ def test_helpers_refuse_what_the_kernels_cannot_take():
         xt.linear_backward(G, X, W, None, "gelu")
     with pytest.raises(ValueError):
         xt.linear_backward(G[:, :5], X, W)
+
+
+def test_adamw_argument_errors(lib):
+    import ctypes
+    ptrs = lambda *a: (ctypes.c_void_p * len(a))(*a)  # noqa: E731
+    h = ctypes.c_void_p()
+
+    def create(n=1, numel=(64,), p=(A,), bits=32, m=(A + MB,), v=(A + 2 * MB,), me=None, ve=None, ct=0, c=None):
+        return lib.xtvxy_adamw_create(n, numel and (ctypes.c_int64 * len(numel))(*numel), p and ptrs(*p), bits, m and ptrs(*m),
+                                      v and ptrs(*v), me and ptrs(*me), ve and ptrs(*ve), ct, c and ptrs(*c), ctypes.byref(h))
+
+    bad, null, alias = _abi.XTVXY_ERROR_INVALID_VALUE, _abi.XTVXY_ERROR_NULL_POINTER, _abi.XTVXY_ERROR_ALIASING
+    for kw in ({"n": -1}, {"bits": 16}, {"numel": (-1,)}, {"p": (A + 2,)}, {"m": (A + MB + 1,)}, {"ct": 1}, {"ct": 9}):
+        assert create(**kw) == bad, kw
+    for kw in ({"numel": None}, {"p": None}, {"m": None}, {"v": (None,)}, {"p": (None,)}, {"bits": 8}, {"ct": 2},
+               {"ct": 2, "c": (None,)}):
+        assert create(**kw) == null, kw
+    for kw in ({"m": (A + 128,)}, {"v": (A + MB + 4,)}, {"ct": 2, "c": (A + 252,)},
+               {"bits": 8, "me": (A + 3 * MB,), "ve": (A + 3 * MB,)}):
+        assert create(**kw) == alias, kw
+    assert h.value is None
+    assert lib.xtvxy_adamw_create(0, None, None, 32, None, None, None, None, 0, None, None) == null
+    assert create(n=0, numel=None, p=None, m=None, v=None) in (_abi.XTVXY_SUCCESS, _abi.XTVXY_ERROR_LAUNCH)
+    assert lib.xtvxy_adamw_step(None, None, 1, 1, 0.1, 0.9, 0.9, 1e-8, 0.0, 0, None) == null
+    assert lib.xtvxy_adamw_state_values(None, None, None, 1, None) == null
+
+
+def test_adamw_oracle_formats():
+    """The 8-bit formats' tables, ends included, and the oracle's rounding at its extremes."""
+    import numpy as np
+
+    import adamw_oracle as O
+    t = torch.arange(256, dtype=torch.uint8).view(torch.float8_e4m3fn).double().numpy()
+    assert np.array_equal(O.m_value(np.arange(256)), t, equal_nan=True)
+    v = O.v_value(np.arange(256))
+    assert v[0] == 0 and v[1] == 2.0 ** -18 and v[15] == 15 * 2.0 ** -18 and v[16] == 2.0 ** -14 and v[255] == 1.9375
+    assert (np.diff(v) > 0).all()
+    # every value is its own code
+    for value, n, bits, least in ((O.m_value, 127, 3, -6), (O.v_value, 256, 4, -14)):
+        code, frac = O.codes_and_fractions(value(np.arange(n)), bits, least)
+        assert np.array_equal(code, np.arange(n)) and not frac.any()
