@@ -22,6 +22,7 @@ struct LinearEpilogue {
   int64_t ldo;
   int32_t act;     // XTVXY_ACT_*
   int32_t wide;    // rows of out, pre and residual allow 4-element (16 or 8 byte) accesses
+  int32_t wide8;   // and 8-element ones
 };
 
 // C[i][j] = sum over k of A(i, k) B(j, k), i < m, j < n, followed by the epilogue. Where
@@ -42,11 +43,29 @@ struct ProductArgs {
 
 constexpr int kTileDepth = 32;   // contraction steps of the 64 x 64 tile kernel
 hipError_t launch_product_tile(const ProductArgs& a, hipStream_t s);
+// Both operands with 16-byte aligned rows of at most kRingMaxPitch bytes; what lies between a row's
+// end and the next multiple of 16 bytes is zero where the contraction is contiguous, and readable
+// where it is not. tile: 64, 128, or 256 (16-bit elements). k_per_split is a multiple of 32.
+constexpr int64_t kRingMaxPitch = (int64_t)1 << 23;  // 256 rows stay within 32-bit offsets
+hipError_t launch_product_ring(const ProductArgs& a, int tile, hipStream_t s);
+// Copies of up to kPackJobs matrices with rows of ldd elements (a multiple of 16 bytes, at least
+// cols), zero beyond cols.
+constexpr int kPackJobs = 4;
+struct PackJob {
+  const void* src;
+  void* dst;
+  int64_t ld, ldd, rows, cols;
+};
+struct PackArgs {
+  PackJob job[kPackJobs];
+  int32_t jobs;
+};
+hipError_t launch_pack(const PackArgs& a, int type, hipStream_t s);
 // Sums the parts of a split product in ascending order and applies the epilogue.
 hipError_t launch_product_finish(const ProductArgs& a, hipStream_t s);
 
 // d = g * act'(pre) (d may be null: column sums only; pre null: slope 1), and per-workgroup
-// column sums of the unrounded d: sums[groups][n].
+// column sums of the unrounded d: sums[groups][n]. Rows of d are zero from n up to ldd.
 struct SlopeArgs {
   const void* g;
   const void* pre;

@@ -138,20 +138,22 @@ __global__ __launch_bounds__(kThreads) void slope_rows(SlopeArgs a) {
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
           x[c] = (float)g[c];
-          if (kAct != XTVXY_ACT_NONE) x[c] *= slope<sizeof(T) == 2, kAct>((float)z[c]);
+          if (kAct != XTVXY_ACT_NONE) x[c] *= slope<kAct>((float)z[c]);
           o[c] = (T)x[c];
         }
         if (D) *reinterpret_cast<v8*>(D + i * a.ldd + j) = o;
       } else {
+        v8 o = {};
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
           x[c] = 0.0f;
           if (c < count) {
             x[c] = (float)G[i * a.ldg + j + c];
-            if (kAct != XTVXY_ACT_NONE) x[c] *= slope<sizeof(T) == 2, kAct>((float)P[i * a.ldp + j + c]);
-            if (D) D[i * a.ldd + j + c] = (T)x[c];
+            if (kAct != XTVXY_ACT_NONE) x[c] *= slope<kAct>((float)P[i * a.ldp + j + c]);
+            o[c] = (T)x[c];
           }
         }
+        if (D) *reinterpret_cast<v8*>(D + i * a.ldd + j) = o;  // ldd is a multiple of 8
       }
 #pragma unroll
       for (int c = 0; c < 8; ++c) sum[c] += x[c];
@@ -170,6 +172,28 @@ __global__ __launch_bounds__(kThreads) void slope_rows(SlopeArgs a) {
       for (int p = 0; p < kThreads / 64 - 1; ++p) sum[c] += part_sums[p][threadIdx.x][c];
       if (c < count) a.sums[(int64_t)blockIdx.y * a.n + j + c] = sum[c];
     }
+  }
+}
+
+// 16 bytes of a row at a time; the source may have any alignment (memory takes unaligned accesses).
+template <typename T>
+__global__ __launch_bounds__(kThreads) void pack_rows(PackArgs a) {
+  constexpr int kChunk = 16 / sizeof(T);
+  typedef T chunk __attribute__((ext_vector_type(kChunk)));
+  const PackJob& job = a.job[blockIdx.y];
+  const int64_t chunks = job.ldd / kChunk, total = job.rows * chunks;
+  for (int64_t at = (int64_t)blockIdx.x * kThreads + threadIdx.x; at < total; at += (int64_t)gridDim.x * kThreads) {
+    const int64_t i = at / chunks, c = (at % chunks) * kChunk;
+    const T* p = static_cast<const T*>(job.src) + i * job.ld + c;
+    chunk v = {};
+    if (job.cols - c >= kChunk) {
+      __builtin_memcpy(&v, p, 16);
+    } else {
+#pragma unroll
+      for (int x = 0; x < kChunk; ++x)
+        if (c + x < job.cols) v[x] = p[x];
+    }
+    *reinterpret_cast<chunk*>(static_cast<T*>(job.dst) + i * job.ldd + c) = v;
   }
 }
 
@@ -228,6 +252,18 @@ hipError_t launch_slope(const SlopeArgs& a, hipStream_t s) {
   if (a.type == kBf16) return slope_for<__bf16>(a, s);
   if (a.type == kF16) return slope_for<_Float16>(a, s);
   return slope_for<float>(a, s);
+}
+
+hipError_t launch_pack(const PackArgs& a, int type, hipStream_t s) {
+  int64_t most = 1;
+  for (int j = 0; j < a.jobs; ++j) {
+    const int64_t groups = (a.job[j].rows * (a.job[j].ldd * elem_size(type) / 16) + kThreads - 1) / kThreads;
+    most = groups > most ? groups : most;
+  }
+  const dim3 grid((unsigned)(most < 8192 ? most : 8192), (unsigned)a.jobs);
+  if (type == kF32) pack_rows<float><<<grid, kThreads, 0, s>>>(a);
+  else pack_rows<_Float16><<<grid, kThreads, 0, s>>>(a);
+  return hipGetLastError();
 }
 
 hipError_t launch_column_finish(const float* sums, int64_t groups, int64_t n, float* db, hipStream_t s) {

@@ -10,6 +10,7 @@ from ._abi import (XTVXY_ACT_GELU, XTVXY_ACT_GELU_TANH, XTVXY_ACT_NONE, XTVXY_AC
 
 ACTIVATIONS = {"none": XTVXY_ACT_NONE, "relu": XTVXY_ACT_RELU, "gelu": XTVXY_ACT_GELU,
                "gelu_tanh": XTVXY_ACT_GELU_TANH, "silu": XTVXY_ACT_SILU}
+_MAX_PITCH = 8 << 20  # bytes between rows up to which a matrix counts as aligned for the workspace queries
 
 
 # ---------------------------------------------------------------------------
@@ -191,7 +192,7 @@ def linear(X, W, bias=None, residual=None, act="none", *, save_pre=False, out=No
         pre_ptr = pre.data_ptr()
     xp, wp = X.data_ptr(), W.data_ptr()
     es = 4 if suffix == "f32" else 2
-    aligned = 0 if (xp | wp | ldx * es | ldw * es) & 15 else 1
+    aligned = 0 if (xp | wp | ldx * es | ldw * es) & 15 or max(ldx, ldw) * es > _MAX_PITCH else 1
     made_ws, ws_ptr, ws_bytes = _scratch(_linear_bytes(suffix, m, k, n, aligned), workspace, device)
     _abi.call("xtvxy_linear_" + suffix, m, k, n, xp, ldx, wp, ldw, bias_ptr, residual_ptr, ldr or 1, code,
               out.data_ptr(), ldo, pre_ptr, ldp or 1, ws_ptr, ws_bytes, _stream_handle(stream))
@@ -252,7 +253,7 @@ def linear_backward(G, X, W, pre=None, act="none", *, need_dX=True, need_dW=True
         _check_bias("db", db, n, device)
     gp, xp, wp = G.data_ptr(), X.data_ptr(), W.data_ptr()
     es = 4 if suffix == "f32" else 2
-    aligned = 0 if (gp | xp | wp | ldg * es | ldx * es | ldw * es) & 15 else 1
+    aligned = 0 if (gp | xp | wp | ldg * es | ldx * es | ldw * es) & 15 or max(ldg, ldx, ldw) * es > _MAX_PITCH else 1
     made_ws, ws_ptr, ws_bytes = _scratch(_backward_bytes(suffix, m, k, n, code, aligned), workspace, device)
     _abi.call("xtvxy_linear_backward_" + suffix, m, k, n, gp, ldg, xp, ldx, wp, ldw, pre_ptr, ldp, code,
               None if dX is None else dX.data_ptr(), lddx, None if dW is None else dW.data_ptr(), lddw,
