@@ -24,7 +24,7 @@ ARCH = "gfx950"
 SOURCES = ["api.cpp", "model.cpp", "unfused.cpp", "logreg.cpp", "tune.cpp", "csr_analysis.cpp", "dense.hip", "csr.hip",
            "csr_waves.hip", "csr_rows.hip", "csr_bins.hip",
            "aggregate.hip", "logreg.hip", "probe.hip", "noalloc.hip",
-           "linear.cpp", "linear_tile.hip", "linear_ring.hip", "adamw.cpp", "adamw.hip"]
+           "linear.cpp", "linear_tile.hip", "linear_ring.hip", "linear_few.hip", "adamw.cpp", "adamw.hip"]
 HEADERS = ["internal.h", "device_util.h", "csr_common.h", "linear.h", "linear_util.h", "adamw.h"]
 
 COMMON_FLAGS = [

@@ -63,47 +63,94 @@ double stage_us(int type, int tile, int64_t groups) {
   return groups <= 1 ? 0.18 : 0.13 * groups;
 }
 
-// The tile and the number of parts with the least estimated time: a launch and the first loads (3 us),
-// the busiest CU's stages, the epilogue (a CU stores a tile at about 8 bytes a cycle; 2 us more for
-// 256 x 256, which nothing overlaps), and for parts the sums written and read back at 8 TB/s (they
-// stay in the last-level cache) and a second launch.
+// Times and sizes of one product with a tile and a number of parts. Estimated: the stages (launch and
+// first loads are not counted), the epilogue's stores (a CU stores a tile at about 8 bytes a cycle),
+// and for parts the sums written and read back at 8 TB/s (they stay in the last-level cache).
+struct ProductCost {
+  int64_t groups = 0, stages = 0, per = 0;
+  double extra_us = 0;
+};
+bool product_cost(int type, int tile, int64_t splits, int64_t m, int64_t n, int64_t k, ProductCost* c) {
+  *c = {};
+  c->per = std::max<int64_t>(kTileDepth, cdiv(cdiv(k, splits), kTileDepth) * kTileDepth);
+  const int64_t tiles = cdiv(m, tile) * cdiv(n, tile);
+  if (splits > 1 && (c->per < 64 || tiles * splits > 16 * kComputeUnits || cdiv(k, c->per) != splits)) return false;
+  c->groups = tiles * splits;
+  c->stages = cdiv(c->per, type == kF32 ? 16 : 32);
+  c->extra_us = (double)cdiv(c->groups, kComputeUnits) * tile * tile * (splits > 1 ? 4 : elem_size(type)) / 8 / 2200 +
+                (tile == 256 ? 2.0 : 0.0) + (splits > 1 ? 2.0 * splits * m * n * 4 / 8e6 : 0.0);
+  return true;
+}
+
+constexpr int64_t kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64};
+
+void set_product(ProductPlan* p, int tile, int64_t splits, const ProductCost& c, int64_t m, int64_t n) {
+  p->tile = tile;
+  p->splits = splits;
+  p->k_per_split = c.per;
+  p->bytes = splits > 1 ? align_up((size_t)splits * m * n * 4) : 0;
+}
+
+// The layer's tile and number of parts with the least estimated time (2 us for the second launch of a
+// split product).
 ProductPlan plan_product(int type, int64_t m, int64_t n, int64_t k, bool ring) {
   ProductPlan best;
-  best.k_per_split = std::max<int64_t>(kTileDepth, cdiv(k, kTileDepth) * kTileDepth);
+  best.k_per_split = kTileDepth;
   if (m == 0 || n == 0) return best;
-  const int64_t steps = type == kF32 ? 16 : 32;
   double least = 0;
   for (int tile : {64, 128, 256}) {
     if (!ring ? tile != 64 : (tile == 256 && type == kF32)) continue;
-    const int64_t tiles = cdiv(m, tile) * cdiv(n, tile);
-    for (int64_t splits : {1, 2, 3, 4, 6, 8, 12, 16, 24, 32}) {
-      const int64_t per = cdiv(cdiv(k, splits), kTileDepth) * kTileDepth;
-      if (splits > 1 && (per < 96 || tiles * splits > 16 * kComputeUnits || cdiv(k, per) != splits)) break;
-      const int64_t groups = cdiv(tiles * splits, kComputeUnits);
-      const double sums = splits > 1 ? 2.0 * splits * m * n * 4 / 8e6 + 2.0 : 0.0;
-      const double store = (double)groups * tile * tile * (splits > 1 ? 4 : elem_size(type)) / 8 / 2200 + (tile == 256 ? 2.0 : 0.0);
-      const double us = 3.0 + cdiv(per, steps) * stage_us(type, tile, groups) + store + sums;
+    for (int64_t splits : kSplits) {
+      ProductCost c;
+      if (!product_cost(type, tile, splits, m, n, k, &c)) continue;
+      const double us = c.stages * stage_us(type, tile, cdiv(c.groups, kComputeUnits)) + c.extra_us + (splits > 1 ? 2.0 : 0.0);
       if (least == 0 || us < least) {
         least = us;
-        best.tile = ring ? tile : 0;
-        best.splits = splits;
-        best.k_per_split = std::max<int64_t>(per, kTileDepth);
-        best.bytes = splits > 1 ? align_up((size_t)splits * m * n * 4) : 0;
+        set_product(&best, ring ? tile : 0, splits, c, m, n);
       }
     }
   }
   return best;
 }
 
-bool product_fits(int64_t m, int64_t n) {
-  return cdiv(m, 64) * cdiv(n, 64) <= kMaxGroups && cdiv(m * cdiv(n, 4), 256) <= kMaxGroups;
+// The gradient's products dX (m x k, contraction n) and dW (n x k, contraction m) share a tile and a
+// launch: the CUs' stages are those of both, and at least the longer product's.
+void plan_gradient(int type, int64_t m, int64_t k, int64_t n, bool want_dx, bool want_dw, bool ring, ProductPlan* dx,
+                   ProductPlan* dw) {
+  dx->k_per_split = dw->k_per_split = kTileDepth;
+  if (m == 0 || k == 0 || n == 0) return;
+  double least = 0;
+  for (int tile : {64, 128, 256}) {
+    if (!ring ? tile != 64 : (tile == 256 && type == kF32)) continue;
+    for (int64_t sx : kSplits) {
+      ProductCost cx, cw;
+      if (want_dx ? !product_cost(type, tile, sx, m, k, n, &cx) : sx > 1) continue;
+      for (int64_t sw : kSplits) {
+        if (want_dw ? !product_cost(type, tile, sw, n, k, m, &cw) : sw > 1) continue;
+        const int64_t groups = cx.groups + cw.groups, rounds = cdiv(groups, kComputeUnits);
+        const double mean = (double)(cx.groups * cx.stages + cw.groups * cw.stages) / groups;
+        const double longest = (double)std::max(cx.stages, cw.stages) * stage_us(type, tile, 1);
+        const double us = std::max(longest, mean * stage_us(type, tile, rounds)) + cx.extra_us + cw.extra_us +
+                          (sx > 1 || sw > 1 ? 2.0 : 0.0);
+        if (least == 0 || us < least) {
+          least = us;
+          if (want_dx) set_product(dx, ring ? tile : 0, sx, cx, m, k);
+          if (want_dw) set_product(dw, ring ? tile : 0, sw, cw, n, k);
+        }
+      }
+    }
+  }
 }
 
-hipError_t run_product(ProductArgs a, const ProductPlan& p, void* ws, hipStream_t s) {
+bool product_fits(int64_t m, int64_t n) {
+  return cdiv(m, 64) * cdiv(n, 64) <= kMaxGroups;
+}
+
+hipError_t run_layer(ProductArgs a, const ProductPlan& p, void* ws, hipStream_t s) {
   a.splits = (int32_t)p.splits;
   a.k_per_split = p.k_per_split;
   a.partial = static_cast<float*>(ws);
-  hipError_t e = p.tile ? launch_product_ring(a, p.tile, s) : launch_product_tile(a, s);
+  hipError_t e = p.tile ? launch_layer_ring(a, p.tile, s) : launch_layer_tile(a, s);
   if (e == hipSuccess && a.splits > 1) e = launch_product_finish(a, s);
   return e;
 }
@@ -112,6 +159,7 @@ hipError_t run_product(ProductArgs a, const ProductPlan& p, void* ws, hipStream_
 // aligned and whole 16-byte chunks, else a copy in the workspace with rows padded by zeros. Small
 // products take any operand as it is.
 constexpr int64_t kSmallProduct = (int64_t)1 << 24;  // multiplications
+constexpr int64_t kSmallGradient = (int64_t)1 << 26;
 
 int64_t padded(int64_t cols, int es) { return cdiv(cols, 16 / es) * (16 / es); }
 
@@ -126,6 +174,7 @@ bool valid_act(int a) { return a >= XTVXY_ACT_NONE && a <= XTVXY_ACT_SILU; }
 // Plan of the layer: whether X and W are copied, the product, and the workspace.
 struct LinearPlan {
   bool pack_x = false, pack_w = false;
+  int few = 0, few_outputs = 0;  // the kernel for few rows: its wavefronts, its outputs of a workgroup
   ProductPlan product;
   size_t x_off = 0, w_off = 0, partial_off = 0, bytes = 0;
 };
@@ -133,6 +182,23 @@ struct LinearPlan {
 LinearPlan plan_linear(int type, int64_t m, int64_t k, int64_t n, bool x_whole, bool w_whole) {
   LinearPlan p;
   const int es = elem_size(type);
+  if (m <= kFewRows) {
+    // W cold, us: 16 outputs a workgroup against 32: 1 x 4096 x 4096 bf16 8.9, 11.9; 13 x 2048 x 8192 11.2, 10.5
+    // (X is loaded once per workgroup); 4 wavefronts against 8: bf16 8.9, 9.5, fp32 18.1, 16.9. Where the
+    // outputs are too few for the CUs the contraction is split: 1 x 8192 x 1024 12.1 to 9.7, 1 x 16384 x 256
+    // 20.1 to 9.0. The ring kernel with its best split: 13.9, 14.8, 13.9, 27.4, 13.2, 15.4; at 32 rows of
+    // 4096 x 4096 15.6 against 14.7, at 48 14.9 against 21.
+    p.few_outputs = m > 4 && n >= 8192 ? 32 : 16;
+    const int64_t groups = cdiv(n, p.few_outputs);
+    p.few = k >= 4096 && (type == kF32 || groups < kComputeUnits) ? 8 : 4;
+    int64_t splits = 1;
+    if (groups <= kComputeUnits / 2 && k * es >= 16384)
+      splits = std::max<int64_t>(1, std::min<int64_t>({8, kComputeUnits / groups, k / (p.few * 256)}));
+    p.product.k_per_split = std::max<int64_t>(32, cdiv(cdiv(k, p.few * splits), 32) * 32);
+    p.product.splits = std::max<int64_t>(1, cdiv(k, p.few * p.product.k_per_split));
+    if (p.product.splits > 1) p.bytes = p.product.bytes = align_up((size_t)p.product.splits * m * n * 4);
+    return p;
+  }
   const bool small = (double)m * n * k < (double)kSmallProduct;
   const bool ring = (x_whole && w_whole) || (!small && k > 0 && padded(k, es) * es <= kRingMaxPitch);
   p.pack_x = ring && !x_whole;
@@ -199,8 +265,6 @@ xtvxy_status linear_impl(int type, int64_t m, int64_t k, int64_t n, const void* 
   a.n = n;
   a.k = k;
   a.type = type;
-  a.a_wide = mx.aligned16();
-  a.b_wide = mw.aligned16();
   PackArgs pack{};
   if (plan.pack_x) {
     pack.job[pack.jobs++] = {X, base + plan.x_off, ldx, padded(k, es), m, k};
@@ -215,38 +279,52 @@ xtvxy_status linear_impl(int type, int64_t m, int64_t k, int64_t n, const void* 
   if (pack.jobs > 0 && launch_pack(pack, type, stream) != hipSuccess) return XTVXY_ERROR_LAUNCH;
   const auto wide = [&](int c) { return mo.aligned(c) && (!residual || mr.aligned(c)) && (!pre || mp.aligned(c)); };
   a.e = {bias, residual, ldr, pre, ldp, out, ldo, act, wide(4), wide(8)};
-  return status_of(run_product(a, plan.product, base + plan.partial_off, stream));
+  if (plan.few) {
+    a.splits = (int32_t)plan.product.splits;
+    a.k_per_split = plan.product.k_per_split;
+    a.partial = reinterpret_cast<float*>(base);
+    hipError_t e = launch_product_few(a, plan.few, plan.few_outputs, stream);
+    if (e == hipSuccess && a.splits > 1) e = launch_product_finish(a, stream);
+    return status_of(e);
+  }
+  return status_of(run_layer(a, plan.product, base + plan.partial_off, stream));
 }
 
-// Plan of the gradient: what is copied, whether d is formed (it is G itself where there is no
-// activation and G's rows suit the products), the products, which run one after the other, and the
-// workspace: copies of X and W, d, the column sums of the row groups, partial sums.
+// Plan of the gradient. Small ones form d as they load G and pre (`fused`: one launch, and one for
+// parts and column sums). Others first form d in the workspace (it is G itself where there is no
+// activation and G's rows suit the products) with the column sums of row groups, copy X and W where
+// their rows do not suit, and then run both products in one launch. Workspace: copies of X and W, d,
+// column sums, partial sums of dX and of dW.
 struct BackwardPlan {
-  bool pack_x = false, pack_w = false, form_d = false;
+  bool fused = false, pack_x = false, pack_w = false, form_d = false;
   int64_t ldd = 0, rows_per_group = 0, groups = 0;
   ProductPlan dx, dw;
-  size_t x_off = 0, w_off = 0, d_off = 0, sums_off = 0, partial_off = 0, bytes = 0;
+  size_t x_off = 0, w_off = 0, d_off = 0, sums_off = 0, dx_off = 0, dw_off = 0, bytes = 0;
 };
 
 BackwardPlan plan_backward(int type, int64_t m, int64_t k, int64_t n, int act, bool g_whole, bool x_whole, bool w_whole,
                            bool want_dx, bool want_dw) {
   BackwardPlan p;
   const int es = elem_size(type);
-  const bool small = (double)m * n * k < (double)kSmallProduct;
-  const bool can = k > 0 && padded(k, es) * es <= kRingMaxPitch && padded(n, 2) * es <= kRingMaxPitch;
-  const bool ring_dx = can && (w_whole || !small), ring_dw = can && (x_whole || !small);
-  p.pack_w = want_dx && ring_dx && !w_whole;
-  p.pack_x = want_dw && ring_dw && !x_whole;
-  const bool products = k > 0 && (want_dx || want_dw);
-  p.form_d = products && (act != XTVXY_ACT_NONE || (!g_whole && ((want_dx && ring_dx) || (want_dw && ring_dw))));
+  want_dx = want_dx && k > 0;
+  want_dw = want_dw && k > 0;
+  const bool fits_ring = padded(k, es) * es <= kRingMaxPitch && cdiv(n, 8) * 8 * es <= kRingMaxPitch;
+  // us on fp32, fused against not: 2048 x 128 x 64 17.3, 16.0 (and a launch less), 512 x 256 x 256 11.4, 14.5,
+  // 1024 x 256 x 256 13.4, 16.5, 1024 x 512 x 256 17.5, 18.5, 1501 x 1000 x 501 54, 49; 16-bit loses at
+  // every size (the tile kernel turns strided operands element by element): 512 x 256 x 256 20.5, 10.2
+  p.fused = (want_dx || want_dw) && (!fits_ring || (type == kF32 && (double)m * n * k <= (double)kSmallGradient));
+  const bool ring = (want_dx || want_dw) && !p.fused;
+  p.pack_w = want_dx && ring && !w_whole;
+  p.pack_x = want_dw && ring && !x_whole;
+  p.form_d = ring && (act != XTVXY_ACT_NONE || !g_whole);
   p.ldd = cdiv(n, 8) * 8;
-  // row groups: about four workgroups per CU, at least 32 rows each
-  const int64_t column_groups = std::max<int64_t>(1, cdiv(n, 512));
+  // row groups: about four workgroups per CU, at least 8 rows for each row that a workgroup takes at once
+  const bool narrow = n <= kSlopeNarrow;
+  const int64_t column_groups = std::max<int64_t>(1, cdiv(n, narrow ? 128 : 512));
   const int64_t groups = std::max<int64_t>(1, 4 * kComputeUnits / column_groups);
-  p.rows_per_group = std::max<int64_t>(32, cdiv(m, groups));
+  p.rows_per_group = std::max<int64_t>(narrow ? 64 : 32, cdiv(m, groups));
   p.groups = std::max<int64_t>(1, cdiv(m, p.rows_per_group));
-  p.dx = plan_product(type, m, k, n, ring_dx);
-  p.dw = plan_product(type, n, k, m, ring_dw);
+  plan_gradient(type, m, k, n, want_dx, want_dw, ring, &p.dx, &p.dw);
   const auto take = [&](bool want, size_t bytes) {
     const size_t at = p.bytes;
     if (want) p.bytes += bytes;
@@ -255,13 +333,15 @@ BackwardPlan plan_backward(int type, int64_t m, int64_t k, int64_t n, int act, b
   p.x_off = take(p.pack_x, packed_bytes(m, k, es));
   p.w_off = take(p.pack_w, packed_bytes(n, k, es));
   p.d_off = take(p.form_d, align_up((size_t)m * p.ldd * es));
-  p.sums_off = take(true, align_up((size_t)p.groups * n * 4));
-  p.partial_off = take(products, std::max(want_dx ? p.dx.bytes : 0, want_dw ? p.dw.bytes : 0));
+  p.sums_off = take(true, align_up((size_t)std::max(p.groups, p.fused ? p.dw.splits : 0) * n * 4));
+  p.dx_off = take(want_dx, p.dx.bytes);
+  p.dw_off = take(want_dw, p.dw.bytes);
   return p;
 }
 
 bool backward_fits(int64_t m, int64_t k, int64_t n) {
-  return product_fits(m, k) && product_fits(n, k) && cdiv(n, 512) <= kMaxGroups / 2048;
+  // both products are one launch
+  return cdiv(m, 64) * cdiv(k, 64) + cdiv(n, 64) * cdiv(k, 64) + cdiv(n, 16) <= kMaxGroups;
 }
 
 xtvxy_status backward_workspace(int type, int64_t m, int64_t k, int64_t n, int act, int aligned16, size_t* bytes) {
@@ -309,10 +389,49 @@ xtvxy_status backward_impl(int type, int64_t m, int64_t k, int64_t n, const void
   if (reads && p.bytes > 0 && (!ws || ws_bytes < p.bytes || reinterpret_cast<uintptr_t>(ws) % kAlign != 0))
     return XTVXY_ERROR_WORKSPACE;
   char* base = static_cast<char*>(ws);
-  hipError_t e = hipSuccess;
-  const void* D = G;
-  int64_t ldd = ldg;
-  if (reads && (p.form_d || db)) {
+  GradientArgs a{};
+  a.n = n;
+  a.db = db;
+  a.sums = reinterpret_cast<const float*>(base + p.sums_off);
+  if (dX && k > 0) {
+    a.dx.B = W;
+    a.dx.ldb = ldw;
+    a.dx.m = m;
+    a.dx.n = k;
+    a.dx.k = n;
+    a.dx.splits = (int32_t)p.dx.splits;
+    a.dx.k_per_split = p.dx.k_per_split;
+    a.dx.partial = reinterpret_cast<float*>(base + p.dx_off);
+    a.dx.e = {nullptr, nullptr, 0, nullptr, 0, dX, lddx, XTVXY_ACT_NONE, mdx.aligned(4), mdx.aligned(8)};
+  }
+  if (dW && k > 0) {
+    a.dw.B = X;
+    a.dw.ldb = ldx;
+    a.dw.m = n;
+    a.dw.n = k;
+    a.dw.k = m;
+    a.dw.splits = (int32_t)p.dw.splits;
+    a.dw.k_per_split = p.dw.k_per_split;
+    a.dw.partial = reinterpret_cast<float*>(base + p.dw_off);
+    a.dw.e = {nullptr, nullptr, 0, nullptr, 0, dW, lddw, XTVXY_ACT_NONE, mdw.aligned(4), mdw.aligned(8)};
+  }
+  a.dx.type = a.dw.type = type;
+  a.dx.A = a.dw.A = G;
+  a.dx.lda = a.dw.lda = ldg;
+  if (!reads) {  // no rows or no outputs: db is zero, and so are the products' empty sums
+    if (db && n > 0 && launch_zero(db, (size_t)n * 4, stream) != hipSuccess) return XTVXY_ERROR_LAUNCH;
+    return status_of(launch_gradient_tile(a, type, stream));
+  }
+  if (p.fused && (dW || !db)) {
+    a.pre = pre;
+    a.ldp = ldp;
+    a.act = act;
+    a.own_sums = db ? reinterpret_cast<float*>(base + p.sums_off) : nullptr;
+    a.sum_rows = p.dw.splits;
+    if (launch_gradient_tile(a, type, stream) != hipSuccess) return XTVXY_ERROR_LAUNCH;
+    return status_of(launch_gradient_finish(a, type, stream));
+  }
+  if (p.form_d || db) {
     SlopeArgs s{};
     s.g = G;
     s.ldg = ldg;
@@ -324,54 +443,39 @@ xtvxy_status backward_impl(int type, int64_t m, int64_t k, int64_t n, const void
     s.n = n;
     s.type = type;
     s.act = act;
-    s.wide = mg.aligned16() && (!pre || mp.aligned16());
     s.sums = db ? reinterpret_cast<float*>(base + p.sums_off) : nullptr;
     s.rows_per_group = p.rows_per_group;
     s.groups = p.groups;
-    e = launch_slope(s, stream);
-    if (e == hipSuccess && db) e = launch_column_finish(s.sums, s.groups, n, db, stream);
-  } else if (db && n > 0) {
-    e = launch_zero(db, (size_t)n * 4, stream);
+    if (launch_slope(s, stream) != hipSuccess) return XTVXY_ERROR_LAUNCH;
+    a.sum_rows = p.groups;
   }
-  if (e != hipSuccess) return XTVXY_ERROR_LAUNCH;
+  if (p.fused) {  // db without dW: the column sums are the row groups'
+    a.pre = pre;
+    a.ldp = ldp;
+    a.act = act;
+    if (launch_gradient_tile(a, type, stream) != hipSuccess) return XTVXY_ERROR_LAUNCH;
+    return status_of(launch_gradient_finish(a, type, stream));
+  }
   if (p.form_d) {
-    D = base + p.d_off;
-    ldd = p.ldd;
+    a.dx.A = a.dw.A = base + p.d_off;
+    a.dx.lda = a.dw.lda = p.ldd;
   }
   PackArgs pack{};
-  if (reads && p.pack_x) pack.job[pack.jobs++] = {X, base + p.x_off, ldx, padded(k, es), m, k};
-  if (reads && p.pack_w) pack.job[pack.jobs++] = {W, base + p.w_off, ldw, padded(k, es), n, k};
+  if (p.pack_x) {
+    pack.job[pack.jobs++] = {X, base + p.x_off, ldx, padded(k, es), m, k};
+    a.dw.B = base + p.x_off;
+    a.dw.ldb = padded(k, es);
+  }
+  if (p.pack_w) {
+    pack.job[pack.jobs++] = {W, base + p.w_off, ldw, padded(k, es), n, k};
+    a.dx.B = base + p.w_off;
+    a.dx.ldb = padded(k, es);
+  }
   if (pack.jobs > 0 && launch_pack(pack, type, stream) != hipSuccess) return XTVXY_ERROR_LAUNCH;
-  const Matrix md{D, m, n, ldd, es};
-  ProductArgs a{};
-  a.A = D;
-  a.lda = ldd;
-  a.a_wide = md.aligned16();
-  a.b_contraction_major = 1;
-  a.n = k;
-  a.type = type;
-  if (dX && m > 0 && k > 0) {
-    a.B = p.pack_w && reads ? base + p.w_off : W;
-    a.ldb = p.pack_w ? padded(k, es) : ldw;
-    a.b_wide = p.pack_w || mw.aligned16();
-    a.m = m;
-    a.k = n;
-    a.e = {nullptr, nullptr, 0, nullptr, 0, dX, lddx, XTVXY_ACT_NONE, mdx.aligned(4), mdx.aligned(8)};
-    e = run_product(a, p.dx, base + p.partial_off, stream);
-    if (e != hipSuccess) return XTVXY_ERROR_LAUNCH;
-  }
-  if (dW && n > 0 && k > 0) {
-    a.a_contraction_major = 1;
-    a.B = p.pack_x && reads ? base + p.x_off : X;
-    a.ldb = p.pack_x ? padded(k, es) : ldx;
-    a.b_wide = p.pack_x || mx.aligned16();
-    a.m = n;
-    a.k = m;
-    a.e = {nullptr, nullptr, 0, nullptr, 0, dW, lddw, XTVXY_ACT_NONE, mdw.aligned(4), mdw.aligned(8)};
-    e = run_product(a, p.dw, base + p.partial_off, stream);
-    if (e != hipSuccess) return XTVXY_ERROR_LAUNCH;
-  }
-  return XTVXY_SUCCESS;
+  // the products and db in one launch; with parts the sums are finished in a second one
+  if (launch_gradient_ring(a, type, dX && k > 0 ? p.dx.tile : p.dw.tile, stream) != hipSuccess) return XTVXY_ERROR_LAUNCH;
+  a.db = nullptr;
+  return status_of(launch_gradient_finish(a, type, stream));
 }
 
 }  // namespace

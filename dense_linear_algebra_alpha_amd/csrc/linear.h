@@ -34,7 +34,6 @@ struct ProductArgs {
   int64_t m, n, k;
   int32_t type;
   int32_t a_contraction_major, b_contraction_major;
-  int32_t a_wide, b_wide;   // 16-byte loads: aligned base, row pitch and contiguous extent
   int32_t splits;           // parts of the contraction, each with sums of its own in `partial`
   int64_t k_per_split;      // a multiple of the tile's depth; splits * k_per_split >= k
   float* partial;           // [splits][m][n] when splits > 1
@@ -42,12 +41,41 @@ struct ProductArgs {
 };
 
 constexpr int kTileDepth = 32;   // contraction steps of the 64 x 64 tile kernel
-hipError_t launch_product_tile(const ProductArgs& a, hipStream_t s);
-// Both operands with 16-byte aligned rows of at most kRingMaxPitch bytes; what lies between a row's
-// end and the next multiple of 16 bytes is zero where the contraction is contiguous, and readable
-// where it is not. tile: 64, 128, or 256 (16-bit elements). k_per_split is a multiple of 32.
+// The layer's product (both contractions contiguous) at any size and alignment.
+hipError_t launch_layer_tile(const ProductArgs& a, hipStream_t s);
+
+// Operands with 16-byte aligned rows of at most kRingMaxPitch bytes; what lies between a row's end and
+// the next multiple of 16 bytes is zero where the contraction is contiguous, and readable where it is
+// not. tile: 64, 128, or 256 (16-bit elements). k_per_split is a multiple of 32.
 constexpr int64_t kRingMaxPitch = (int64_t)1 << 23;  // 256 rows stay within 32-bit offsets
-hipError_t launch_product_ring(const ProductArgs& a, int tile, hipStream_t s);
+hipError_t launch_layer_ring(const ProductArgs& a, int tile, hipStream_t s);
+
+// The gradient's products dX = d W (d contraction-contiguous, W strided) and dW = d^T X (both
+// strided), either with m == 0 where it is not wanted, and db[j] = the sum over sum_rows of
+// sums[.][n] (db null: not wanted).
+struct GradientArgs {
+  ProductArgs dx, dw;
+  uint32_t dx_groups, dw_groups;  // workgroups (set by the launcher)
+  const float* sums;
+  int64_t sum_rows, n;
+  float* db;
+  // the tile kernel forms d itself: dx.A and dw.A are G, and
+  const void* pre;    // null: slope 1
+  int64_t ldp;
+  int32_t act;
+  float* own_sums;    // [dw.splits][n] column sums of d, or null
+};
+hipError_t launch_gradient_ring(const GradientArgs& a, int type, int tile, hipStream_t s);
+// At any size and alignment, d formed as it is loaded. (db is left to launch_gradient_finish.)
+hipError_t launch_gradient_tile(const GradientArgs& a, int type, hipStream_t s);
+// Sums the parts of split products, and the column sums' rows, each in ascending order.
+hipError_t launch_gradient_finish(const GradientArgs& a, int type, hipStream_t s);
+
+// At most kFewRows rows of A, both operands with the contraction contiguous, at any alignment. A
+// workgroup of `waves` (4 or 8) wavefronts takes `outputs` (16 or 32) rows of B; each wavefront of
+// each split takes k_per_split steps, a multiple of 32: splits * waves * k_per_split >= k.
+constexpr int64_t kFewRows = 32;
+hipError_t launch_product_few(const ProductArgs& a, int waves, int outputs, hipStream_t s);
 // Copies of up to kPackJobs matrices with rows of ldd elements (a multiple of 16 bytes, at least
 // cols), zero beyond cols.
 constexpr int kPackJobs = 4;
@@ -73,12 +101,10 @@ struct SlopeArgs {
   int64_t ldg, ldp, ldd;
   int64_t m, n;
   int32_t type, act;
-  int32_t wide;          // 16-byte accesses of g, pre and d
   float* sums;           // null: no column sums
   int64_t rows_per_group, groups;
 };
+constexpr int64_t kSlopeNarrow = 256;  // columns up to which a workgroup takes 128 instead of 512
 hipError_t launch_slope(const SlopeArgs& a, hipStream_t s);
-// db[j] = sum over groups of sums[group][j], in ascending order in fp64.
-hipError_t launch_column_finish(const float* sums, int64_t groups, int64_t n, float* db, hipStream_t s);
 
 }  // namespace xtvxy

@@ -171,9 +171,9 @@ constexpr int waitcnt(int vm, int lgkm) { return (vm & 15) | (7 << 4) | (lgkm <<
 
 // Tile of a workgroup: workgroups go to the 8 XCDs in turn, each of which has an L2 of its own, so
 // each XCD takes a contiguous range of the tiles, ordered in bands of kBand tile rows.
-__device__ __forceinline__ void tile_of(int64_t tiles_m, int64_t tiles_n, int64_t* tm, int64_t* tn) {
+__device__ __forceinline__ void tile_of(uint32_t id, int64_t tiles_m, int64_t tiles_n, int64_t* tm, int64_t* tn) {
   constexpr int kXcds = 8, kBand = 4;
-  const uint32_t tiles = (uint32_t)(tiles_m * tiles_n), id = blockIdx.x;
+  const uint32_t tiles = (uint32_t)(tiles_m * tiles_n);
   const uint32_t x = id % kXcds, q = tiles / kXcds, r = tiles % kXcds;
   const uint32_t t = x * q + (x < r ? x : r) + id / kXcds;
   const uint32_t band_tiles = kBand * (uint32_t)tiles_n, band = t / band_tiles, in = t % band_tiles;
@@ -265,20 +265,21 @@ __device__ __forceinline__ void epilogue_any(const float* area, const ProductArg
 
 // The staged rows as one part of a split product.
 template <int WN, int kRows>
-__device__ __forceinline__ void partial_rows(const float* area, const ProductArgs& a, int64_t i0, int64_t j0) {
+__device__ __forceinline__ void partial_rows(const float* area, const ProductArgs& a, uint32_t split, int64_t i0, int64_t j0) {
   constexpr int kLanes = WN / 4, kStep = 64 / kLanes;
   const int lane = threadIdx.x & 63, c4 = lane % kLanes;
   const int64_t j = j0 + c4 * 4;
   if (j >= a.n) return;
   const int count = a.n - j >= 4 ? 4 : (int)(a.n - j);
   const int rows = a.m - i0 >= kRows ? kRows : (int)(a.m - i0);
-  float* p = a.partial + ((int64_t)blockIdx.y * a.m + i0) * a.n + j;
+  float* p = a.partial + ((int64_t)split * a.m + i0) * a.n + j;
   for (int row = lane / kLanes; row < rows; row += kStep)
     store4<float>(p + row * a.n, *reinterpret_cast<const f32x4*>(area + staged_at<WN>(row, c4)), count, a.n % 4 == 0);
 }
 
+// Workgroup `id` of a product's tiles x splits, with `ring` of 4 (BM + BN) 64 bytes of LDS.
 template <typename T, int BM, int BN, bool kAMajor, bool kBMajor>
-__global__ __launch_bounds__(kThreads, BM * BN > 128 * 128 ? 1 : 2) void product_ring(ProductArgs a) {
+__device__ __forceinline__ void ring_tile(const ProductArgs& a, uint32_t id, uint8_t* ring) {
   typedef typename Stage<T>::frag frag;
   typedef Operand<T, BM, kAMajor> OpA;
   typedef Operand<T, BN, kBMajor> OpB;
@@ -286,14 +287,15 @@ __global__ __launch_bounds__(kThreads, BM * BN > 128 * 128 ? 1 : 2) void product
   constexpr int kSlot = OpA::kBytes + OpB::kBytes;
   constexpr int FA = BM / 32, FB = BN / 32;  // fragments of a wavefront's BM / 2 x BN / 2
   constexpr int kLoads = OpA::kLoads + OpB::kLoads;
-  __shared__ __align__(1024) uint8_t ring[kRing * kSlot];
   lds_byte* lds = (lds_byte*)ring;
   const uint32_t lds0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)lds);
 
+  const int64_t tiles_m = (a.m + BM - 1) / BM, tiles_n = (a.n + BN - 1) / BN;
+  const uint32_t tiles = (uint32_t)(tiles_m * tiles_n), split = id / tiles;
   int64_t tm, tn;
-  tile_of((a.m + BM - 1) / BM, (a.n + BN - 1) / BN, &tm, &tn);
+  tile_of(id % tiles, tiles_m, tiles_n, &tm, &tn);
   const int64_t i0 = tm * BM, j0 = tn * BN;
-  const int64_t k0 = (int64_t)blockIdx.y * a.k_per_split;
+  const int64_t k0 = (int64_t)split * a.k_per_split;
   const int64_t k_end = k0 + a.k_per_split < a.k ? k0 + a.k_per_split : a.k;
   int32_t left = (int32_t)(k_end - k0);
   const int32_t stages = (left + kStage - 1) / kStage;
@@ -387,40 +389,83 @@ __global__ __launch_bounds__(kThreads, BM * BN > 128 * 128 ? 1 : 2) void product
     __builtin_amdgcn_wave_barrier();
     const int64_t i = i0 + wi + part * kRows, j = j0 + wj;
     if (a.splits > 1)
-      partial_rows<WN, kRows>(area, a, i, j);
+      partial_rows<WN, kRows>(area, a, split, i, j);
     else
       epilogue_any<T, WN, kRows>(area, a, i, j);
     __builtin_amdgcn_wave_barrier();
   }
 }
 
-template <typename T, int BM, int BN>
-hipError_t ring_for(const ProductArgs& a, hipStream_t s) {
-  const dim3 grid((unsigned)(((a.m + BM - 1) / BM) * ((a.n + BN - 1) / BN)), (unsigned)a.splits);
-  if (a.a_contraction_major && a.b_contraction_major)
-    product_ring<T, BM, BN, true, true><<<grid, kThreads, 0, s>>>(a);
-  else if (a.b_contraction_major)
-    product_ring<T, BM, BN, false, true><<<grid, kThreads, 0, s>>>(a);
-  else
-    product_ring<T, BM, BN, false, false><<<grid, kThreads, 0, s>>>(a);
+constexpr int ring_bytes(int tile) { return kRing * 2 * tile * 64; }
+
+template <typename T, int TILE>
+__global__ __launch_bounds__(kThreads, TILE > 128 ? 1 : 2) void layer_ring(ProductArgs a) {
+  __shared__ __align__(1024) uint8_t ring[ring_bytes(TILE)];
+  ring_tile<T, TILE, TILE, false, false>(a, blockIdx.x, ring);
+}
+
+// The gradient's two products in one launch (the second's workgroups fill the CUs that the first's last
+// round leaves), and the sum of the row groups' column sums.
+template <typename T, int TILE>
+__global__ __launch_bounds__(kThreads, TILE > 128 ? 1 : 2) void gradient_ring(GradientArgs a) {
+  __shared__ __align__(1024) uint8_t ring[ring_bytes(TILE)];
+  uint32_t id = blockIdx.x;
+  if (id < a.dx_groups) return ring_tile<T, TILE, TILE, false, true>(a.dx, id, ring);
+  id -= a.dx_groups;
+  if (id < a.dw_groups) return ring_tile<T, TILE, TILE, true, true>(a.dw, id, ring);
+  column_sum(a.sums, a.sum_rows, a.n, a.db, id - a.dw_groups, reinterpret_cast<double*>(ring));
+}
+
+uint32_t groups_of(const ProductArgs& a, int tile) {
+  return (uint32_t)(((a.m + tile - 1) / tile) * ((a.n + tile - 1) / tile) * a.splits);
+}
+
+template <typename T, int TILE>
+hipError_t layer_for(const ProductArgs& a, hipStream_t s) {
+  layer_ring<T, TILE><<<groups_of(a, TILE), kThreads, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+template <typename T, int TILE>
+hipError_t gradient_for(GradientArgs a, hipStream_t s) {
+  a.dx_groups = a.dx.m > 0 ? groups_of(a.dx, TILE) : 0;
+  a.dw_groups = a.dw.m > 0 ? groups_of(a.dw, TILE) : 0;
+  const uint32_t columns = a.db ? (uint32_t)((a.n + kSumColumns - 1) / kSumColumns) : 0;
+  if (a.dx_groups + a.dw_groups + columns == 0) return hipSuccess;
+  gradient_ring<T, TILE><<<a.dx_groups + a.dw_groups + columns, kThreads, 0, s>>>(a);
   return hipGetLastError();
 }
 
 template <typename T>
-hipError_t ring_type(const ProductArgs& a, int tile, hipStream_t s) {
+hipError_t layer_type(const ProductArgs& a, int tile, hipStream_t s) {
   if constexpr (sizeof(T) == 2) {
-    if (tile == 256) return ring_for<T, 256, 256>(a, s);
+    if (tile == 256) return layer_for<T, 256>(a, s);
   }
-  if (tile == 128) return ring_for<T, 128, 128>(a, s);
-  return ring_for<T, 64, 64>(a, s);
+  if (tile == 128) return layer_for<T, 128>(a, s);
+  return layer_for<T, 64>(a, s);
+}
+
+template <typename T>
+hipError_t gradient_type(const GradientArgs& a, int tile, hipStream_t s) {
+  if constexpr (sizeof(T) == 2) {
+    if (tile == 256) return gradient_for<T, 256>(a, s);
+  }
+  if (tile == 128) return gradient_for<T, 128>(a, s);
+  return gradient_for<T, 64>(a, s);
 }
 
 }  // namespace
 
-hipError_t launch_product_ring(const ProductArgs& a, int tile, hipStream_t s) {
-  if (a.type == kBf16) return ring_type<__bf16>(a, tile, s);
-  if (a.type == kF16) return ring_type<_Float16>(a, tile, s);
-  return ring_type<float>(a, tile, s);
+hipError_t launch_layer_ring(const ProductArgs& a, int tile, hipStream_t s) {
+  if (a.type == kBf16) return layer_type<__bf16>(a, tile, s);
+  if (a.type == kF16) return layer_type<_Float16>(a, tile, s);
+  return layer_type<float>(a, tile, s);
+}
+
+hipError_t launch_gradient_ring(const GradientArgs& a, int type, int tile, hipStream_t s) {
+  if (type == kBf16) return gradient_type<__bf16>(a, tile, s);
+  if (type == kF16) return gradient_type<_Float16>(a, tile, s);
+  return gradient_type<float>(a, tile, s);
 }
 
 }  // namespace xtvxy

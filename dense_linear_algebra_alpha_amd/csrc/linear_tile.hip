@@ -1,6 +1,6 @@
-// Products of any size, alignment, element type and operand order: 64 x 64 tiles, and the kernels
-// around a product (the slope of the activation with its column sums, and the sum of a split
-// contraction's parts).
+// Products of any size, alignment and element type in 64 x 64 tiles, for small or ragged layers, and
+// the kernels around a product: the slope of the activation with its column sums, copies with padded
+// rows, and the sum of a split contraction's parts.
 #include "linear_util.h"
 
 namespace xtvxy {
@@ -17,8 +17,7 @@ template <typename T, bool kContractionMajor>
 struct TileLoad {
   typename Vec<T>::x8 v;
 
-  __device__ __forceinline__ void load(const T* base, int64_t ld, int64_t r0, int64_t rows, int64_t k0, int64_t k_end,
-                                       bool wide) {
+  __device__ __forceinline__ void load(const T* base, int64_t ld, int64_t r0, int64_t rows, int64_t k0, int64_t k_end) {
     const int t = threadIdx.x;
     const int64_t row = kContractionMajor ? r0 + (t & 7) * 8 : r0 + (t >> 2);
     const int64_t k = kContractionMajor ? k0 + (t >> 3) : k0 + (t & 3) * 8;
@@ -26,8 +25,8 @@ struct TileLoad {
     const int64_t outer_end = kContractionMajor ? k_end : rows, inner_end = kContractionMajor ? rows : k_end;
     const int64_t left = outer < outer_end ? inner_end - inner : 0;
     const T* p = base + outer * ld + inner;
-    if (wide && left >= 8) {
-      v = *reinterpret_cast<const typename Vec<T>::x8*>(p);
+    if (left >= 8) {  // memory takes unaligned accesses
+      __builtin_memcpy(&v, p, sizeof(v));
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = i < left ? p[i] : (T)0.0f;
@@ -45,37 +44,69 @@ struct TileLoad {
   }
 };
 
-// One 64 x 64 tile of C per workgroup, four wavefronts of 32 x 32 each. The product is formed
-// transposed (B's rows as the matrix instruction's first operand), so that a lane ends with four
-// neighbouring columns of one row of C. The next step's elements are in flight while the present
-// one's products run.
-template <typename T, bool kAMajor, bool kBMajor>
-__global__ __launch_bounds__(kThreads) void product_tile(ProductArgs a) {
-  __shared__ __align__(16) T sa[kTile * kPitch], sb[kTile * kPitch];
+// d = g act'(z) of 8 elements in fp32.
+template <typename V>
+__device__ __forceinline__ f32x8 slope8(V g, V z, int act) {
+  f32x8 d;
+#pragma unroll
+  for (int c = 0; c < 8; ++c) d[c] = (float)g[c];
+  switch (act) {
+#define XTVXY_SLOPE_CASE(A)                                                                  \
+  case A:                                                                                    \
+    _Pragma("unroll") for (int c = 0; c < 8; ++c) d[c] *= slope<A>((float)z[c]);             \
+    break;
+    XTVXY_SLOPE_CASE(XTVXY_ACT_RELU)
+    XTVXY_SLOPE_CASE(XTVXY_ACT_GELU)
+    XTVXY_SLOPE_CASE(XTVXY_ACT_GELU_TANH)
+    XTVXY_SLOPE_CASE(XTVXY_ACT_SILU)
+#undef XTVXY_SLOPE_CASE
+    default: break;
+  }
+  return d;
+}
+
+// A 64 x 64 tile of C, four wavefronts of 32 x 32 each. The product is formed transposed (B's rows as
+// the matrix instruction's first operand), so that a lane ends with four neighbouring columns of one
+// row of C. The next step's elements are in flight while the present one's products run. With kSlope
+// the first operand is G, and d is formed between its load and its store to LDS; where the
+// contraction runs over d's rows and this is the product's first tile column, its column sums are
+// taken from the unrounded d on the way.
+template <typename T, bool kAMajor, bool kBMajor, bool kSlope>
+__device__ __forceinline__ void tile(const ProductArgs& a, uint32_t id, const GradientArgs* grad, T* sa, T* sb) {
   typedef typename Vec<T>::x8 frag;
-  const int64_t tiles_n = (a.n + kTile - 1) / kTile;
-  const int64_t i0 = (blockIdx.x / tiles_n) * kTile, j0 = (blockIdx.x % tiles_n) * kTile;
-  const int64_t k0 = (int64_t)blockIdx.y * a.k_per_split;
+  const uint32_t tiles_n = (uint32_t)((a.n + kTile - 1) / kTile), tiles = (uint32_t)((a.m + kTile - 1) / kTile) * tiles_n;
+  const uint32_t split = id / tiles, t = id % tiles;
+  const int64_t i0 = (int64_t)(t / tiles_n) * kTile, j0 = (int64_t)(t % tiles_n) * kTile;
+  const int64_t k0 = (int64_t)split * a.k_per_split;
   const int64_t k_end = k0 + a.k_per_split < a.k ? k0 + a.k_per_split : a.k;
   const T* A = static_cast<const T*>(a.A);
   const T* B = static_cast<const T*>(a.B);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int wi = (wave >> 1) * 32, wj = (wave & 1) * 32;
   const int r = lane & 15, g = lane >> 4;
+  const bool with_pre = kSlope && grad->pre, with_sums = kSlope && kAMajor && grad->own_sums && j0 == 0;
 
   f32x4 acc[2][2] = {};
-  TileLoad<T, kAMajor> la;
+  f32x8 sum = {};
+  TileLoad<T, kAMajor> la, lz;
   TileLoad<T, kBMajor> lb;
-  la.load(A, a.lda, i0, a.m, k0, k_end, a.a_wide);
-  lb.load(B, a.ldb, j0, a.n, k0, k_end, a.b_wide);
+  const auto load = [&](int64_t k) {
+    la.load(A, a.lda, i0, a.m, k, k_end);
+    if (with_pre) lz.load(static_cast<const T*>(grad->pre), grad->ldp, i0, a.m, k, k_end);
+    lb.load(B, a.ldb, j0, a.n, k, k_end);
+  };
+  load(k0);
   for (int64_t k = k0; k < k_end; k += kTileDepth) {
+    if (kSlope) {
+      const f32x8 d = slope8(la.v, lz.v, with_pre ? grad->act : XTVXY_ACT_NONE);
+      if (with_sums) sum += d;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) la.v[c] = (T)d[c];
+    }
     la.store(sa);
     lb.store(sb);
     __syncthreads();
-    if (k + kTileDepth < k_end) {
-      la.load(A, a.lda, i0, a.m, k + kTileDepth, k_end, a.a_wide);
-      lb.load(B, a.ldb, j0, a.n, k + kTileDepth, k_end, a.b_wide);
-    }
+    if (k + kTileDepth < k_end) load(k + kTileDepth);
     frag fa[2], fb[2];
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
@@ -95,31 +126,89 @@ __global__ __launch_bounds__(kThreads) void product_tile(ProductArgs a) {
       const int64_t i = i0 + wi + x * 16 + r, j = j0 + wj + y * 16 + g * 4;
       if (i >= a.m || j >= a.n) continue;
       if (a.splits > 1) {
-        float* p = a.partial + ((int64_t)blockIdx.y * a.m + i) * a.n + j;
+        float* p = a.partial + ((int64_t)split * a.m + i) * a.n + j;
         store4<float>(p, acc[x][y], a.n - j >= 4 ? 4 : (int)(a.n - j), a.n % 4 == 0);
       } else {
         epilogue4<T>(a.e, i, j, a.n, acc[x][y]);
       }
     }
+  if (with_sums) {
+    // thread t holds columns 8 (t & 7) + 0..7 of every depth's step t >> 3
+    float* part = reinterpret_cast<float*>(sa);
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      float s = sum[c];
+      s += __shfl_xor(s, 8);
+      s += __shfl_xor(s, 16);
+      s += __shfl_xor(s, 32);
+      if (lane < 8) part[wave * 64 + lane * 8 + c] = s;
+    }
+    __syncthreads();
+    const int64_t i = i0 + threadIdx.x;
+    if (threadIdx.x < 64 && i < a.m)
+      grad->own_sums[(int64_t)split * a.m + i] =
+          part[threadIdx.x] + part[64 + threadIdx.x] + part[128 + threadIdx.x] + part[192 + threadIdx.x];
+  }
+}
+
+template <typename T>
+__global__ __launch_bounds__(kThreads) void layer_tile(ProductArgs a) {
+  __shared__ __align__(16) T sa[kTile * kPitch], sb[kTile * kPitch];
+  tile<T, false, false, false>(a, blockIdx.x, nullptr, sa, sb);
+}
+
+template <typename T>
+__global__ __launch_bounds__(kThreads) void gradient_tile(GradientArgs a) {
+  __shared__ __align__(16) T sa[kTile * kPitch], sb[kTile * kPitch];
+  if (blockIdx.x < a.dx_groups) tile<T, false, true, true>(a.dx, blockIdx.x, &a, sa, sb);
+  else tile<T, true, true, true>(a.dw, blockIdx.x - a.dx_groups, &a, sa, sb);
+}
+
+// Four neighbouring outputs of a split product by four neighbouring lanes: each sums every fourth part
+// in ascending order (its loads are under way together), the lanes' sums join in a fixed order.
+template <typename T>
+__device__ __forceinline__ void finish_quad(const ProductArgs& a, int64_t at) {
+  const int64_t quads = (a.n + 3) / 4, q = at >> 2;
+  const int part = (int)(at & 3);
+  const bool exists = q < a.m * quads;
+  const int64_t i = exists ? q / quads : 0, j = exists ? (q % quads) * 4 : 0;
+  const int count = a.n - j >= 4 ? 4 : (int)(a.n - j);
+  f32x4 z = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (exists) {
+#pragma unroll 4
+    for (int s = part; s < a.splits; s += 4) z += load4<float>(a.partial + ((int64_t)s * a.m + i) * a.n + j, count, a.n % 4 == 0);
+  }
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    z[c] += __shfl_xor(z[c], 1);
+    z[c] += __shfl_xor(z[c], 2);
+  }
+  if (exists && part == 0) epilogue4<T>(a.e, i, j, a.n, z);
 }
 
 template <typename T>
 __global__ __launch_bounds__(kThreads) void product_finish(ProductArgs a) {
-  const int64_t quads = (a.n + 3) / 4, q = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  if (q >= a.m * quads) return;
-  const int64_t i = q / quads, j = (q % quads) * 4;
-  const int count = a.n - j >= 4 ? 4 : (int)(a.n - j);
-  f32x4 z = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int s = 0; s < a.splits; ++s) z += load4<float>(a.partial + ((int64_t)s * a.m + i) * a.n + j, count, a.n % 4 == 0);
-  epilogue4<T>(a.e, i, j, a.n, z);
+  finish_quad<T>(a, (int64_t)blockIdx.x * kThreads + threadIdx.x);
 }
 
-// d = g act'(pre) in fp32, stored in the element type; the column sums db take d before that
-// rounding. A workgroup walks rows_per_group rows; a thread owns 8 neighbouring columns.
-template <typename T, int kAct>
+template <typename T>
+__global__ __launch_bounds__(kThreads) void gradient_finish(GradientArgs a) {
+  __shared__ double lds[16 * kSumColumns];
+  uint32_t id = blockIdx.x;
+  if (id < a.dx_groups) return finish_quad<T>(a.dx, (int64_t)id * kThreads + threadIdx.x);
+  id -= a.dx_groups;
+  if (id < a.dw_groups) return finish_quad<T>(a.dw, (int64_t)id * kThreads + threadIdx.x);
+  column_sum(a.sums, a.sum_rows, a.n, a.db, id - a.dw_groups, lds);
+}
+
+// d = g act'(pre) in fp32, stored in the element type; the column sums db take d before that rounding.
+// A workgroup walks rows_per_group rows of 8 kLanes columns, a thread owns 8 neighbouring columns of
+// every 256 / kLanes-th row.
+template <typename T, int kAct, int kLanes>
 __global__ __launch_bounds__(kThreads) void slope_rows(SlopeArgs a) {
-  const int64_t j = ((int64_t)blockIdx.x * 64 + (threadIdx.x & 63)) * 8;
-  const int part = threadIdx.x >> 6;
+  constexpr int kSlots = kThreads / kLanes;  // rows at once
+  const int slot = threadIdx.x / kLanes, lane = threadIdx.x % kLanes;
+  const int64_t j = ((int64_t)blockIdx.x * kLanes + lane) * 8;
   const int64_t r0 = (int64_t)blockIdx.y * a.rows_per_group;
   const int64_t r1 = r0 + a.rows_per_group < a.m ? r0 + a.rows_per_group : a.m;
   const T* G = static_cast<const T*>(a.g);
@@ -129,49 +218,49 @@ __global__ __launch_bounds__(kThreads) void slope_rows(SlopeArgs a) {
   float sum[8] = {};
   const int count = a.n - j >= 8 ? 8 : (a.n > j ? (int)(a.n - j) : 0);
   if (count > 0) {
-    for (int64_t i = r0 + part; i < r1; i += kThreads / 64) {
-      float x[8];
-      if (a.wide && count == 8) {
-        const v8 g = *reinterpret_cast<const v8*>(G + i * a.ldg + j);
-        v8 z = g, o;
-        if (kAct != XTVXY_ACT_NONE) z = *reinterpret_cast<const v8*>(P + i * a.ldp + j);
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          x[c] = (float)g[c];
-          if (kAct != XTVXY_ACT_NONE) x[c] *= slope<kAct>((float)z[c]);
-          o[c] = (T)x[c];
-        }
-        if (D) *reinterpret_cast<v8*>(D + i * a.ldd + j) = o;
+#pragma unroll 4
+    for (int64_t i = r0 + slot; i < r1; i += kSlots) {
+      v8 g = {}, z = {}, o;
+      if (count == 8) {  // memory takes unaligned accesses
+        __builtin_memcpy(&g, G + i * a.ldg + j, sizeof(g));
+        if (kAct != XTVXY_ACT_NONE) __builtin_memcpy(&z, P + i * a.ldp + j, sizeof(z));
       } else {
-        v8 o = {};
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          x[c] = 0.0f;
+        for (int c = 0; c < 8; ++c)
           if (c < count) {
-            x[c] = (float)G[i * a.ldg + j + c];
-            if (kAct != XTVXY_ACT_NONE) x[c] *= slope<kAct>((float)P[i * a.ldp + j + c]);
-            o[c] = (T)x[c];
+            g[c] = G[i * a.ldg + j + c];
+            if (kAct != XTVXY_ACT_NONE) z[c] = P[i * a.ldp + j + c];
           }
-        }
-        if (D) *reinterpret_cast<v8*>(D + i * a.ldd + j) = o;  // ldd is a multiple of 8
       }
+      float x[8];
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        x[c] = (float)g[c];
+        if (kAct != XTVXY_ACT_NONE) x[c] *= slope<kAct>((float)z[c]);
+        o[c] = (T)x[c];
+      }
+      if (D) *reinterpret_cast<v8*>(D + i * a.ldd + j) = o;  // ldd is a multiple of 8; missing columns are zero
 #pragma unroll
       for (int c = 0; c < 8; ++c) sum[c] += x[c];
     }
   }
   if (!a.sums) return;
-  __shared__ float part_sums[kThreads / 64 - 1][64][9];
-  if (part > 0) {
+  // the row slots' sums: within a wavefront by lane exchanges, then through LDS
+  __shared__ float part[kThreads / 64][kLanes < 64 ? kLanes : 64][9];
+  const int wave = threadIdx.x >> 6;
 #pragma unroll
-    for (int c = 0; c < 8; ++c) part_sums[part - 1][threadIdx.x & 63][c] = sum[c];
+  for (int c = 0; c < 8; ++c) {
+#pragma unroll
+    for (int d = kLanes; d < 64; d *= 2) sum[c] += __shfl_xor(sum[c], d);
+    if ((threadIdx.x & 63) < kLanes) part[wave][lane][c] = sum[c];
   }
   __syncthreads();
-  if (part == 0) {
+  if (threadIdx.x >= kLanes || count == 0) return;
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      for (int p = 0; p < kThreads / 64 - 1; ++p) sum[c] += part_sums[p][threadIdx.x][c];
-      if (c < count) a.sums[(int64_t)blockIdx.y * a.n + j + c] = sum[c];
-    }
+  for (int c = 0; c < 8; ++c) {
+    float s = part[0][lane][c];
+    for (int p = 1; p < kThreads / 64; ++p) s += part[p][lane][c];
+    if (c < count) a.sums[(int64_t)blockIdx.y * a.n + j + c] = s;
   }
 }
 
@@ -197,54 +286,67 @@ __global__ __launch_bounds__(kThreads) void pack_rows(PackArgs a) {
   }
 }
 
-__global__ __launch_bounds__(kThreads) void column_finish(const float* sums, int64_t groups, int64_t n, float* db) {
-  const int64_t j = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  if (j >= n) return;
-  double s = 0.0;
-  for (int64_t g = 0; g < groups; ++g) s += (double)sums[g * n + j];
-  db[j] = (float)s;
-}
-
-template <typename T>
-hipError_t tile_for(const ProductArgs& a, hipStream_t s) {
-  const int64_t tiles = ((a.m + kTile - 1) / kTile) * ((a.n + kTile - 1) / kTile);
-  const dim3 grid((unsigned)tiles, (unsigned)a.splits);
-  if (a.a_contraction_major && a.b_contraction_major)
-    product_tile<T, true, true><<<grid, kThreads, 0, s>>>(a);
-  else if (a.b_contraction_major)
-    product_tile<T, false, true><<<grid, kThreads, 0, s>>>(a);
-  else
-    product_tile<T, false, false><<<grid, kThreads, 0, s>>>(a);
-  return hipGetLastError();
-}
-
-template <typename T>
-hipError_t slope_for(const SlopeArgs& a, hipStream_t s) {
-  const dim3 grid((unsigned)((a.n + 511) / 512), (unsigned)a.groups);
+template <typename T, int kLanes>
+hipError_t slope_lanes(const SlopeArgs& a, hipStream_t s) {
+  const dim3 grid((unsigned)((a.n + 8 * kLanes - 1) / (8 * kLanes)), (unsigned)a.groups);
   switch (a.pre ? a.act : XTVXY_ACT_NONE) {
-    case XTVXY_ACT_RELU: slope_rows<T, XTVXY_ACT_RELU><<<grid, kThreads, 0, s>>>(a); break;
-    case XTVXY_ACT_GELU: slope_rows<T, XTVXY_ACT_GELU><<<grid, kThreads, 0, s>>>(a); break;
-    case XTVXY_ACT_GELU_TANH: slope_rows<T, XTVXY_ACT_GELU_TANH><<<grid, kThreads, 0, s>>>(a); break;
-    case XTVXY_ACT_SILU: slope_rows<T, XTVXY_ACT_SILU><<<grid, kThreads, 0, s>>>(a); break;
-    default: slope_rows<T, XTVXY_ACT_NONE><<<grid, kThreads, 0, s>>>(a); break;
+    case XTVXY_ACT_RELU: slope_rows<T, XTVXY_ACT_RELU, kLanes><<<grid, kThreads, 0, s>>>(a); break;
+    case XTVXY_ACT_GELU: slope_rows<T, XTVXY_ACT_GELU, kLanes><<<grid, kThreads, 0, s>>>(a); break;
+    case XTVXY_ACT_GELU_TANH: slope_rows<T, XTVXY_ACT_GELU_TANH, kLanes><<<grid, kThreads, 0, s>>>(a); break;
+    case XTVXY_ACT_SILU: slope_rows<T, XTVXY_ACT_SILU, kLanes><<<grid, kThreads, 0, s>>>(a); break;
+    default: slope_rows<T, XTVXY_ACT_NONE, kLanes><<<grid, kThreads, 0, s>>>(a); break;
   }
   return hipGetLastError();
 }
 
+// A row's lanes: as many as it has groups of 8 columns, so that narrow layers' rows share a wavefront.
+template <typename T>
+hipError_t slope_for(const SlopeArgs& a, hipStream_t s) {
+  return a.n > kSlopeNarrow ? slope_lanes<T, 64>(a, s) : slope_lanes<T, 16>(a, s);
+}
+
 }  // namespace
 
-hipError_t launch_product_tile(const ProductArgs& a, hipStream_t s) {
-  if (a.type == kBf16) return tile_for<__bf16>(a, s);
-  if (a.type == kF16) return tile_for<_Float16>(a, s);
-  return tile_for<float>(a, s);
+uint32_t tile_groups(const ProductArgs& a) {
+  return (uint32_t)(((a.m + kTile - 1) / kTile) * ((a.n + kTile - 1) / kTile) * a.splits);
+}
+uint32_t quad_groups(const ProductArgs& a) { return (uint32_t)((a.m * ((a.n + 3) / 4) * 4 + kThreads - 1) / kThreads); }
+
+hipError_t launch_layer_tile(const ProductArgs& a, hipStream_t s) {
+  if (a.type == kBf16) layer_tile<__bf16><<<tile_groups(a), kThreads, 0, s>>>(a);
+  else if (a.type == kF16) layer_tile<_Float16><<<tile_groups(a), kThreads, 0, s>>>(a);
+  else layer_tile<float><<<tile_groups(a), kThreads, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+hipError_t launch_gradient_tile(const GradientArgs& args, int type, hipStream_t s) {
+  GradientArgs a = args;
+  a.dx_groups = a.dx.m > 0 ? tile_groups(a.dx) : 0;
+  a.dw_groups = a.dw.m > 0 ? tile_groups(a.dw) : 0;
+  const uint32_t grid = a.dx_groups + a.dw_groups;
+  if (grid == 0) return hipSuccess;
+  if (type == kBf16) gradient_tile<__bf16><<<grid, kThreads, 0, s>>>(a);
+  else if (type == kF16) gradient_tile<_Float16><<<grid, kThreads, 0, s>>>(a);
+  else gradient_tile<float><<<grid, kThreads, 0, s>>>(a);
+  return hipGetLastError();
 }
 
 hipError_t launch_product_finish(const ProductArgs& a, hipStream_t s) {
-  const int64_t quads = a.m * ((a.n + 3) / 4);
-  const unsigned grid = (unsigned)((quads + kThreads - 1) / kThreads);
-  if (a.type == kBf16) product_finish<__bf16><<<grid, kThreads, 0, s>>>(a);
-  else if (a.type == kF16) product_finish<_Float16><<<grid, kThreads, 0, s>>>(a);
-  else product_finish<float><<<grid, kThreads, 0, s>>>(a);
+  if (a.type == kBf16) product_finish<__bf16><<<quad_groups(a), kThreads, 0, s>>>(a);
+  else if (a.type == kF16) product_finish<_Float16><<<quad_groups(a), kThreads, 0, s>>>(a);
+  else product_finish<float><<<quad_groups(a), kThreads, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+hipError_t launch_gradient_finish(const GradientArgs& args, int type, hipStream_t s) {
+  GradientArgs a = args;
+  a.dx_groups = a.dx.m > 0 && a.dx.splits > 1 ? quad_groups(a.dx) : 0;
+  a.dw_groups = a.dw.m > 0 && a.dw.splits > 1 ? quad_groups(a.dw) : 0;
+  const uint32_t grid = a.dx_groups + a.dw_groups + (a.db ? (uint32_t)((a.n + kSumColumns - 1) / kSumColumns) : 0);
+  if (grid == 0) return hipSuccess;
+  if (type == kBf16) gradient_finish<__bf16><<<grid, kThreads, 0, s>>>(a);
+  else if (type == kF16) gradient_finish<_Float16><<<grid, kThreads, 0, s>>>(a);
+  else gradient_finish<float><<<grid, kThreads, 0, s>>>(a);
   return hipGetLastError();
 }
 
@@ -266,9 +368,5 @@ hipError_t launch_pack(const PackArgs& a, int type, hipStream_t s) {
   return hipGetLastError();
 }
 
-hipError_t launch_column_finish(const float* sums, int64_t groups, int64_t n, float* db, hipStream_t s) {
-  column_finish<<<(unsigned)((n + kThreads - 1) / kThreads), kThreads, 0, s>>>(sums, groups, n, db);
-  return hipGetLastError();
-}
 
 }  // namespace xtvxy

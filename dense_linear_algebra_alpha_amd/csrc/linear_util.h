@@ -198,4 +198,24 @@ __device__ __forceinline__ void epilogue4(const LinearEpilogue& e, int64_t i, in
   store4<T>(static_cast<T*>(e.out) + i * e.ldo + j, y, count, wide);
 }
 
+// db[j] = the sum of sums[.][n] over its rows for the 16 columns of workgroup `group` (256 threads): a
+// thread adds every 16th row of a column, the 16 partial sums join in LDS (2 KiB), in fp64 and in a
+// fixed order. 16 loads of a column are under way at once; one thread per column would wait for each.
+constexpr int kSumColumns = 16;
+__device__ __forceinline__ void column_sum(const float* sums, int64_t rows, int64_t n, float* db, int64_t group, double* lds) {
+  const int c = threadIdx.x & 15, slot = threadIdx.x >> 4;
+  const int64_t j = group * kSumColumns + c;
+  double s = 0.0;
+  if (j < n) {
+#pragma unroll 4
+    for (int64_t g = slot; g < rows; g += 16) s += (double)sums[g * n + j];
+  }
+  lds[slot * 16 + c] = s;
+  __syncthreads();
+  if (slot == 0 && j < n) {
+    for (int p = 1; p < 16; ++p) s += lds[p * 16 + c];
+    db[j] = (float)s;
+  }
+}
+
 }  // namespace xtvxy

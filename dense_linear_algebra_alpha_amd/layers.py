@@ -96,6 +96,30 @@ def _suffix(dtype) -> str:
     return s
 
 
+@functools.lru_cache(maxsize=None)
+def _torch():
+    import torch
+    return torch
+
+
+@functools.lru_cache(maxsize=None)
+def _entry(name):
+    """The library's function, looked up once: these helpers are called per token."""
+    return getattr(_abi.load(), name)
+
+
+def _check(status, name):
+    if status:
+        raise _abi.XtvxyError(status, name)
+
+
+def _stream_of(stream, device_index):
+    """Handle of `stream`, or of the device's current stream."""
+    if stream is not None:
+        return stream.cuda_stream or None
+    return _torch()._C._cuda_getCurrentRawStream(device_index) or None
+
+
 @functools.lru_cache(maxsize=4096)
 def _linear_bytes(suffix, m, k, n, aligned) -> int:
     return _size("xtvxy_linear_%s_workspace_size" % suffix, m, k, n, aligned)
@@ -113,40 +137,55 @@ def _activation_code(act) -> int:
     return code
 
 
-def _pitch(name, t, rows, cols, dtype, device) -> int:
+def _pitch(name, t, rows, cols, dtype, dev) -> int:
     """The row stride of a rows x cols matrix argument, checked."""
-    if t.dtype != dtype or t.device != device or t.dim() != 2:
-        raise ValueError("%s must be a 2-D %s tensor on %s" % (name, dtype, device))
-    r, c = t.shape
-    if r != rows or c != cols:
-        raise ValueError("%s must be %d x %d, not %d x %d" % (name, rows, cols, r, c))
+    shape = t.shape
+    if t.dtype is not dtype or t.get_device() != dev or len(shape) != 2:
+        raise ValueError("%s must be a 2-D %s tensor on GPU %d" % (name, dtype, dev))
+    if shape[0] != rows or shape[1] != cols:
+        raise ValueError("%s must be %d x %d, not %d x %d" % (name, rows, cols, shape[0], shape[1]))
     s0, s1 = t.stride()
     if s1 != 1 and cols > 1:
         raise ValueError("%s needs unit column stride" % name)
     if rows <= 1:
-        return max(cols, 1)
+        return cols or 1
     if s0 < cols or s0 < 1:
         raise ValueError("%s needs a row stride of at least its width" % name)
     return s0
 
 
-def _check_bias(name, t, n, device):
-    import torch
-    if t.dtype != torch.float32 or t.device != device or t.dim() != 1 or t.shape[0] != n or (n > 1 and t.stride(0) != 1):
-        raise ValueError("%s must be a contiguous float32 vector of %d elements on %s" % (name, n, device))
+def _check_bias(name, t, n, dev):
+    if (t.dtype is not _torch().float32 or t.get_device() != dev or t.dim() != 1 or t.shape[0] != n
+            or (n > 1 and t.stride(0) != 1)):
+        raise ValueError("%s must be a contiguous float32 vector of %d elements on GPU %d" % (name, n, dev))
 
 
-def _scratch(need, workspace, device):
+def _scratch(need, workspace, like):
     """(tensor made here or None, pointer, bytes) of the workspace of a call that needs `need` bytes."""
     if workspace is not None:
-        if workspace.device != device or not workspace.is_contiguous():
-            raise ValueError("workspace must be a contiguous tensor on %s" % device)
+        if workspace.device != like.device or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on %s" % like.device)
         return None, workspace.data_ptr(), workspace.numel() * workspace.element_size()
     if need == 0:
         return None, None, 0
-    import torch
-    ws = torch.empty(need, dtype=torch.uint8, device=device)
+    ws = like.new_empty(need, dtype=_torch().uint8)
     return ws, ws.data_ptr(), need
+
+
+def _features(X, W):
+    """(device index, type, suffix, m, k, n, ldx, ldw) of a layer's features and weights, checked."""
+    dev = X.get_device()
+    if dev < 0:
+        raise ValueError("X must be on the GPU, not on %s" % X.device)
+    if dev != _torch()._C._cuda_getDevice():
+        raise ValueError("X must be on the current GPU, not on %s" % X.device)
+    dtype = X.dtype
+    suffix = _suffix(dtype)
+    if X.dim() != 2 or W.dim() != 2:
+        raise ValueError("X and W must be 2-D")
+    m, k = X.shape
+    n = W.shape[0]
+    return dev, dtype, suffix, m, k, n, _pitch("X", X, m, k, dtype, dev), _pitch("W", W, n, k, dtype, dev)
 
 
 def linear(X, W, bias=None, residual=None, act="none", *, save_pre=False, out=None, pre=None, workspace=None,
@@ -157,46 +196,39 @@ def linear(X, W, bias=None, residual=None, act="none", *, save_pre=False, out=No
     type: float32, bfloat16 or float16; bias is float32 (n). ``act`` is one of ACTIVATIONS. With
     ``save_pre`` (or ``pre`` given) the call also stores X W^T + bias, which linear_backward takes,
     and returns (out, pre). ``out`` may be the residual."""
-    from . import _keep_for_stream, _stream_handle
-    device, dtype = X.device, X.dtype
-    if device.type != "cuda":
-        raise ValueError("X must be on the GPU, not on %s" % device)
-    suffix = _suffix(dtype)
+    dev, dtype, suffix, m, k, n, ldx, ldw = _features(X, W)
     code = _activation_code(act)
-    if X.dim() != 2 or W.dim() != 2:
-        raise ValueError("X and W must be 2-D")
-    m, k = X.shape
-    n = W.shape[0]
-    ldx, ldw = _pitch("X", X, m, k, dtype, device), _pitch("W", W, n, k, dtype, device)
     bias_ptr = residual_ptr = pre_ptr = None
     ldr = ldp = n
     if bias is not None:
-        _check_bias("bias", bias, n, device)
+        _check_bias("bias", bias, n, dev)
         bias_ptr = bias.data_ptr()
     if residual is not None:
-        ldr = _pitch("residual", residual, m, n, dtype, device)
+        ldr = _pitch("residual", residual, m, n, dtype, dev)
         residual_ptr = residual.data_ptr()
     made_out = out is None
     if made_out:
         out = X.new_empty((m, n))
         ldo = n or 1
     else:
-        ldo = _pitch("out", out, m, n, dtype, device)
+        ldo = _pitch("out", out, m, n, dtype, dev)
     made_pre = save_pre and pre is None
     if made_pre:
         pre = X.new_empty((m, n))
         ldp = n or 1
     elif pre is not None:
-        ldp = _pitch("pre", pre, m, n, dtype, device)
+        ldp = _pitch("pre", pre, m, n, dtype, dev)
     if pre is not None:
         pre_ptr = pre.data_ptr()
     xp, wp = X.data_ptr(), W.data_ptr()
     es = 4 if suffix == "f32" else 2
     aligned = 0 if (xp | wp | ldx * es | ldw * es) & 15 or max(ldx, ldw) * es > _MAX_PITCH else 1
-    made_ws, ws_ptr, ws_bytes = _scratch(_linear_bytes(suffix, m, k, n, aligned), workspace, device)
-    _abi.call("xtvxy_linear_" + suffix, m, k, n, xp, ldx, wp, ldw, bias_ptr, residual_ptr, ldr or 1, code,
-              out.data_ptr(), ldo, pre_ptr, ldp or 1, ws_ptr, ws_bytes, _stream_handle(stream))
+    made_ws, ws_ptr, ws_bytes = _scratch(_linear_bytes(suffix, m, k, n, aligned), workspace, X)
+    name = "xtvxy_linear_" + suffix
+    _check(_entry(name)(m, k, n, xp, ldx, wp, ldw, bias_ptr, residual_ptr, ldr or 1, code,
+                        out.data_ptr(), ldo, pre_ptr, ldp or 1, ws_ptr, ws_bytes, _stream_of(stream, dev)), name)
     if stream is not None:
+        from . import _keep_for_stream
         _keep_for_stream(stream, out if made_out else None, pre if made_pre else None, made_ws)
     return out if pre is None else (out, pre)
 
@@ -208,25 +240,14 @@ def linear_backward(G, X, W, pre=None, act="none", *, need_dX=True, need_dW=True
 
     ``pre`` is what linear stored (required unless act is "none"). Outputs that are not needed are
     not computed and come back as None."""
-    import torch
-
-    from . import _keep_for_stream, _stream_handle
-    device, dtype = X.device, X.dtype
-    if device.type != "cuda":
-        raise ValueError("X must be on the GPU, not on %s" % device)
-    suffix = _suffix(dtype)
+    dev, dtype, suffix, m, k, n, ldx, ldw = _features(X, W)
     code = _activation_code(act)
-    if X.dim() != 2 or W.dim() != 2:
-        raise ValueError("X and W must be 2-D")
-    m, k = X.shape
-    n = W.shape[0]
-    ldx, ldw = _pitch("X", X, m, k, dtype, device), _pitch("W", W, n, k, dtype, device)
-    ldg = _pitch("G", G, m, n, dtype, device)
+    ldg = _pitch("G", G, m, n, dtype, dev)
     ldp, pre_ptr = n or 1, None
     if code != XTVXY_ACT_NONE:
         if pre is None:
             raise ValueError("pre is required for activation %r" % act)
-        ldp = _pitch("pre", pre, m, n, dtype, device)
+        ldp = _pitch("pre", pre, m, n, dtype, dev)
         pre_ptr = pre.data_ptr()
     made = []
     lddx, lddw = k or 1, k or 1
@@ -236,28 +257,30 @@ def linear_backward(G, X, W, pre=None, act="none", *, need_dX=True, need_dW=True
         dX = X.new_empty((m, k))
         made.append(dX)
     else:
-        lddx = _pitch("dX", dX, m, k, dtype, device)
+        lddx = _pitch("dX", dX, m, k, dtype, dev)
     if not need_dW:
         dW = None
     elif dW is None:
         dW = X.new_empty((n, k))
         made.append(dW)
     else:
-        lddw = _pitch("dW", dW, n, k, dtype, device)
+        lddw = _pitch("dW", dW, n, k, dtype, dev)
     if not need_db:
         db = None
     elif db is None:
-        db = torch.empty(n, dtype=torch.float32, device=device)
+        db = X.new_empty(n, dtype=_torch().float32)
         made.append(db)
     else:
-        _check_bias("db", db, n, device)
+        _check_bias("db", db, n, dev)
     gp, xp, wp = G.data_ptr(), X.data_ptr(), W.data_ptr()
     es = 4 if suffix == "f32" else 2
     aligned = 0 if (gp | xp | wp | ldg * es | ldx * es | ldw * es) & 15 or max(ldg, ldx, ldw) * es > _MAX_PITCH else 1
-    made_ws, ws_ptr, ws_bytes = _scratch(_backward_bytes(suffix, m, k, n, code, aligned), workspace, device)
-    _abi.call("xtvxy_linear_backward_" + suffix, m, k, n, gp, ldg, xp, ldx, wp, ldw, pre_ptr, ldp, code,
-              None if dX is None else dX.data_ptr(), lddx, None if dW is None else dW.data_ptr(), lddw,
-              None if db is None else db.data_ptr(), ws_ptr, ws_bytes, _stream_handle(stream))
+    made_ws, ws_ptr, ws_bytes = _scratch(_backward_bytes(suffix, m, k, n, code, aligned), workspace, X)
+    name = "xtvxy_linear_backward_" + suffix
+    _check(_entry(name)(m, k, n, gp, ldg, xp, ldx, wp, ldw, pre_ptr, ldp, code,
+                        None if dX is None else dX.data_ptr(), lddx, None if dW is None else dW.data_ptr(), lddw,
+                        None if db is None else db.data_ptr(), ws_ptr, ws_bytes, _stream_of(stream, dev)), name)
     if stream is not None:
+        from . import _keep_for_stream
         _keep_for_stream(stream, *made, made_ws)
     return dX, dW, db
