@@ -1,6 +1,7 @@
-"""Builds libxtvxy.so (the fused kernels and the C ABI) for gfx950 with hipcc.
+"""Builds libxtvxy.so (the fused kernels and the C ABI) for gfx950 with hipcc, and
+_tensors.so (a small host-only Python extension) with g++.
 
-Objects go to _build/ next to this file and the shared library next to this
+Objects go to _build/ next to this file and the shared libraries next to this
 file, so it travels with the source tree. Usage: ``python -m
 dense_linear_algebra_alpha_amd.build`` or ``build()`` from Python.
 """
@@ -17,6 +18,7 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(HERE, "libxtvxy.so")
+TENSORS_PATH = os.path.join(HERE, "_tensors.so")  # Python extension: checked addresses of tensor lists
 ROCM = os.environ.get("ROCM_PATH", "/opt/rocm")
 HIPCC = os.path.join(ROCM, "bin", "hipcc")
 ARCH = "gfx950"
@@ -25,6 +27,7 @@ SOURCES = ["api.cpp", "model.cpp", "unfused.cpp", "logreg.cpp", "tune.cpp", "csr
            "csr_waves.hip", "csr_rows.hip", "csr_bins.hip",
            "aggregate.hip", "logreg.hip", "probe.hip", "noalloc.hip",
            "linear.cpp", "linear_tile.hip", "linear_ring.hip", "linear_few.hip", "adamw.cpp", "adamw.hip"]
+TENSORS_SOURCE = "tensor_list.cpp"
 HEADERS = ["internal.h", "device_util.h", "csr_common.h", "linear.h", "linear_util.h", "adamw.h"]
 
 COMMON_FLAGS = [
@@ -54,11 +57,32 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _build_tensors() -> None:
+    """The host-only extension module, against the headers of the installed torch."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension
+    tmp = TENSORS_PATH + ".tmp%d" % os.getpid()
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-DUSE_ROCM",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI)]
+    cmd += ["-isystem" + d for d in cpp_extension.include_paths() + [sysconfig.get_paths()["include"]]]
+    # torch's libraries are found by name among those that the process has loaded by importing torch
+    cmd += [os.path.join(CSRC, TENSORS_SOURCE), "-o", tmp, "-L" + os.path.join(os.path.dirname(torch.__file__), "lib"),
+            "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed on %s:\n%s%s" % (TENSORS_SOURCE, r.stdout, r.stderr))
+    os.replace(tmp, TENSORS_PATH)
+
+
 def build(verbose: bool = False) -> str:
-    """Compile every source and link libxtvxy.so; returns the library path."""
+    """Compile every source, link libxtvxy.so and build the extension module; returns the library path."""
     os.makedirs(BUILD_DIR, exist_ok=True)
-    with ThreadPoolExecutor(max_workers=min(len(SOURCES), os.cpu_count() or 1)) as ex:
+    with ThreadPoolExecutor(max_workers=min(len(SOURCES) + 1, os.cpu_count() or 1)) as ex:
+        tensors = ex.submit(_build_tensors)
         objs = list(ex.map(_compile, SOURCES))
+        tensors.result()
     tmp = LIB_PATH + ".tmp%d" % os.getpid()
     cmd = [HIPCC, "--offload-arch=" + ARCH, "-shared", "-fPIC", "-o", tmp] + objs + [
         "-L" + os.path.join(ROCM, "lib"), "-lrocblas", "-lrocsparse", "-Wl,-rpath," + os.path.join(ROCM, "lib")]
@@ -72,11 +96,12 @@ def build(verbose: bool = False) -> str:
 
 
 def sources_newer_than_library() -> bool:
-    if not os.path.exists(LIB_PATH):
+    if not os.path.exists(LIB_PATH) or not os.path.exists(TENSORS_PATH):
         return True
     t = os.path.getmtime(LIB_PATH)
     files = [os.path.join(CSRC, f) for f in SOURCES + HEADERS] + [os.path.join(INCLUDE, "xtvxy.h")]
-    return any(os.path.getmtime(f) > t for f in files)
+    return any(os.path.getmtime(f) > t for f in files) or (
+        os.path.getmtime(os.path.join(CSRC, TENSORS_SOURCE)) > os.path.getmtime(TENSORS_PATH))
 
 
 if __name__ == "__main__":

@@ -3,9 +3,10 @@ optimiser object on torch tensors (argument marshalling only)."""
 from __future__ import annotations
 
 import ctypes
-from operator import attrgetter
+import functools
 
 from . import _abi
+from .layers import _stream_of
 from ._abi import XTVXY_TYPE_BF16, XTVXY_TYPE_F16, XTVXY_TYPE_F32, XTVXY_TYPE_NONE
 
 ADAMW_BLOCK = 128  # elements that share an exponent in 8-bit states
@@ -39,9 +40,19 @@ def xtvxy_adamw_state_values(optimiser, m_out, v_out, type, stream):
 # the optimiser object
 # ---------------------------------------------------------------------------
 
-_dtype_of = attrgetter("dtype")
+@functools.lru_cache(maxsize=None)
+def _addresses():
+    """addresses() of the extension module; a missing one raises."""
+    import torch  # noqa: F401  (the module resolves against it)
+    try:
+        from ._tensors import addresses
+    except ImportError as e:
+        raise RuntimeError("_tensors.so is not built or does not match this torch (%s); run `python -m "
+                           "dense_linear_algebra_alpha_amd.build`" % e) from None
+    return addresses
 
 
+@functools.lru_cache(maxsize=None)
 def _type_code(dtype) -> int:
     import torch
     code = {torch.float32: XTVXY_TYPE_F32, torch.bfloat16: XTVXY_TYPE_BF16, torch.float16: XTVXY_TYPE_F16}.get(dtype)
@@ -95,10 +106,11 @@ class AdamW:
             self._check_list("copies", copies, numel, dtype)
         self.params, self.copies, self.state, self.state_bits, self.steps = params, copies, state, state_bits, int(steps)
         self.lr, self.betas, self.eps, self.weight_decay, self.seed = lr, tuple(betas), eps, weight_decay, seed
-        self._numel, self._device_index = numel, self.device.index
         n = len(params)
+        self._numel = numel
         self._pointers = ctypes.c_void_p * n
-        count = (ctypes.c_int64 * n)(*numel)
+        self._count = count = (ctypes.c_int64 * n)(*numel)
+        self._numel_address = ctypes.addressof(count)
         exps = (self._array(state[2]), self._array(state[3])) if state_bits == 8 else (None, None)
         # fresh states and the caller's tensors may still be in the making on the current stream; steps
         # are ordered after them by the streams that the caller runs them on
@@ -118,42 +130,35 @@ class AdamW:
         return self._pointers(*[t.data_ptr() for t in tensors])
 
     def _like_params(self, name, tensors):
-        """Type code of a list of contiguous tensors of one type and the parameters' sizes. The checks
-        run as whole-list maps: a deep model has hundreds of tensors and this is every step's cost."""
-        import torch
-        T = torch.Tensor
-        if len(tensors) != len(self._numel):
-            raise ValueError("%s has %d tensors, the parameters are %d" % (name, len(tensors), len(self._numel)))
-        if not tensors:
-            return XTVXY_TYPE_F32
-        dtype = tensors[0].dtype
-        if (list(map(T.numel, tensors)) != self._numel or set(map(_dtype_of, tensors)) != {dtype}
-                or set(map(T.get_device, tensors)) != {self._device_index} or not all(map(T.is_contiguous, tensors))):
-            self._check_list(name, tensors, self._numel, dtype)
-        return _type_code(dtype)
+        """(pointers, type code) of a list of contiguous tensors of one type and the parameters' sizes."""
+        tensors = list(tensors)
+        n = len(self._numel)
+        if len(tensors) != n:
+            raise ValueError("%s has %d tensors, the parameters are %d" % (name, len(tensors), n))
+        pointers = self._pointers()
+        if not n:
+            return pointers, XTVXY_TYPE_F32
+        bad = _addresses()(tensors, self._numel_address, ctypes.addressof(pointers), n, self.device.index)
+        if bad >= 0:
+            raise ValueError("%s[%d] must be a contiguous tensor of %d elements on %s, of the list's one type"
+                             % (name, bad, self._numel[bad], self.device))
+        return pointers, _type_code(tensors[0].dtype)
 
     def step(self, grads, *, stream=None):
         """One step with the gradients of the parameters, in their order: contiguous tensors of one type
         (float32, bfloat16 or float16)."""
-        from . import _stream_handle
-        import torch
-        grads = list(grads)
-        code = self._like_params("grads", grads)
-        pointers = self._pointers(*map(torch.Tensor.data_ptr, grads))
+        pointers, code = self._like_params("grads", grads)
         xtvxy_adamw_step(self.handle, pointers, code, self.steps + 1, self.lr, self.betas[0], self.betas[1], self.eps,
-                         self.weight_decay, self.seed & 0xffffffff, _stream_handle(stream))
+                         self.weight_decay, self.seed & 0xffffffff, _stream_of(stream, self.device.index))
         self.steps += 1
 
     def state_values(self, m_out, v_out, *, stream=None):
         """Writes the values that the moments stand for into tensors of the parameters' sizes."""
-        from . import _stream_handle
-        import torch
-        m_out, v_out = list(m_out), list(v_out)
-        code = self._like_params("m_out", m_out)
-        if self._like_params("v_out", v_out) != code:
+        m_pointers, code = self._like_params("m_out", m_out)
+        v_pointers, v_code = self._like_params("v_out", v_out)
+        if v_code != code:
             raise ValueError("m_out and v_out must have one type")
-        xtvxy_adamw_state_values(self.handle, self._pointers(*map(torch.Tensor.data_ptr, m_out)),
-                                 self._pointers(*map(torch.Tensor.data_ptr, v_out)), code, _stream_handle(stream))
+        xtvxy_adamw_state_values(self.handle, m_pointers, v_pointers, code, _stream_of(stream, self.device.index))
 
     def close(self):
         if getattr(self, "handle", 0):
