@@ -47,7 +47,7 @@ hipError_t launch_layer_tile(const ProductArgs& a, hipStream_t s);
 // Operands with 16-byte aligned rows of at most kRingMaxPitch bytes; what lies between a row's end and
 // the next multiple of 16 bytes is zero where the contraction is contiguous, and readable where it is
 // not. tile: 64, 128, or 256 (16-bit elements). k_per_split is a multiple of 32.
-constexpr int64_t kRingMaxPitch = (int64_t)1 << 23;  // 256 rows stay within 32-bit offsets
+constexpr int64_t kRingMaxPitch = (int64_t)1 << 22;  // 256 rows stay within 32-bit offsets
 hipError_t launch_layer_ring(const ProductArgs& a, int tile, hipStream_t s);
 
 // The gradient's products dX = d W (d contraction-contiguous, W strided) and dW = d^T X (both

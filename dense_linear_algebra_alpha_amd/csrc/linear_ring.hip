@@ -25,7 +25,11 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kRing = 4;     // LDS slots
-constexpr uint32_t kNowhere = 0xfffffff0u;  // beyond any tile's extent: such a load returns zero
+constexpr uint32_t kNowhere = 0xc0000000u;  // beyond any tile's extent: such a load returns zero
+// Four loads share a setting of their LDS address: an instruction's own offset (up to 4095) counts for
+// memory and LDS alike. Descriptors begin this far before their data, so that taking those offsets from
+// the lanes' ones leaves none negative.
+constexpr uint32_t kBefore = 4096;
 
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) uint8_t lds_byte;
@@ -45,18 +49,19 @@ struct Stage<float> {
 
 // One operand's tile of R rows of the kept index and one stage of the contraction: its loads into an
 // LDS slot (R * 64 bytes, R / 16 loads of 1 KiB, R / 64 of them by each wavefront) and its fragments.
-template <typename T, int R, bool kMajor>
+template <typename T, int R, bool kMajor, int H>
 struct Operand {
-  static constexpr int kLoads = R / 64;
-  static constexpr int kBytes = R * 64;
-  static constexpr int kSize = sizeof(T), kChunk = Stage<T>::kChunk, kSteps = Stage<T>::kSteps;
+  static constexpr int kLoads = R / 64 * H;
+  static constexpr int kBytes = R * 64 * H;
+  static constexpr int kSize = sizeof(T), kChunk = Stage<T>::kChunk, kSteps = Stage<T>::kSteps * H;
   typedef typename Stage<T>::frag frag;
 
-  const char* base;        // of the next stage to load: its first step, the tile's first row
+  u32x4 rsrc;              // buffer descriptor of the next stage to load: its first step, the tile's first
+                           // row, kBefore bytes earlier, and the bytes that a whole stage may read
   int64_t stage_bytes;     // from one stage to the next
-  int64_t outer_bytes;     // of rows (steps) before the last one of the tile (a step)
+  uint32_t outer_bytes;    // of rows (steps) before the last one of the tile (a step)
   int32_t inner;           // rows of the tile that exist, in whole chunks (steps strided)
-  uint32_t offset[kLoads]; // of this lane, per load, from base
+  uint32_t offset[kLoads]; // of this lane, per load
   int32_t lane_step;       // first contraction step of this lane's chunk (steps contiguous)
 
   // The units that a step's row is permuted in: 32 bytes (16-bit, read 4 steps at a time by a group
@@ -66,22 +71,27 @@ struct Operand {
     return ((k & 3) | ((k >> 3) & 1) << 2) & (R / 16 - 1);
   }
 
+  // What a row's chunks are permuted by (contraction contiguous).
+  static __device__ __forceinline__ int row_key(int row) { return H == 2 ? row & 7 : (row >> 1) & 3; }
+
   // rows: of the kept index from the tile's first on; k0: the first step.
   __device__ __forceinline__ void init(const void* p, int64_t ld, int64_t r0, int64_t rows, int64_t k0) {
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const char* base;
     if (!kMajor) {
       base = static_cast<const char*>(p) + (r0 * ld + k0) * kSize;
       stage_bytes = kSteps * kSize;
-      outer_bytes = ((rows < R ? rows : R) - 1) * ld * kSize;
-      const int chunk = (lane & 3) ^ ((lane >> 3) & 3);
+      outer_bytes = (uint32_t)(((rows < R ? rows : R) - 1) * ld * kSize);
+      constexpr int kRow = 4 * H;  // chunks of a row
+      const int row = lane / kRow, chunk = (lane % kRow) ^ row_key(row);
       lane_step = chunk * kChunk;
 #pragma unroll
       for (int j = 0; j < kLoads; ++j)
-        offset[j] = (uint32_t)(((wave * kLoads + j) * 16 + (lane >> 2)) * ld * kSize) + chunk * 16;
+        offset[j] = (uint32_t)(((wave * kLoads + j) * (64 / kRow) + row) * ld * kSize) + chunk * 16;
     } else {
       base = static_cast<const char*>(p) + (k0 * ld + r0) * kSize;
       stage_bytes = kSteps * ld * kSize;
-      outer_bytes = ld * kSize;
+      outer_bytes = (uint32_t)(ld * kSize);
       inner = ((int32_t)(rows < R ? rows : R) + kChunk - 1) / kChunk * kChunk;
       constexpr int kChunks = R / kChunk;            // of a step's row
       constexpr int kUnit = kSize == 4 ? 4 : 2;      // chunks of a unit
@@ -92,47 +102,81 @@ struct Operand {
         offset[j] = chunk * kChunk < inner ? (uint32_t)(k * ld * kSize) + chunk * 16 : kNowhere;
       }
     }
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) offset[j] += kBefore - (j & 3) * 1024;
+    const uint64_t at = reinterpret_cast<uint64_t>(base) - kBefore;
+    rsrc = u32x4{(uint32_t)at, (uint32_t)(at >> 32) & 0xffffu, extent(kSteps), 0x00027000u};
   }
 
-  // The buffer descriptor of the next stage, of which `left` contraction steps exist.
-  __device__ __forceinline__ u32x4 next(int32_t left) {
-    // bytes from base to the end of what the stage may read: beyond them a load returns zero. In
-    // whole chunks: of a word that straddles the end nothing would be read.
-    const int32_t steps = left < kSteps ? left : kSteps;
-    uint32_t extent = 0;
-    if (left > 0)
-      extent = kMajor ? (uint32_t)(steps - 1) * (uint32_t)outer_bytes + (uint32_t)inner * kSize
-                      : (uint32_t)outer_bytes + (uint32_t)((steps + kChunk - 1) / kChunk * kChunk) * kSize;
-    const uint64_t p = reinterpret_cast<uint64_t>(base);
-    base += stage_bytes;
-    return u32x4{(uint32_t)p, (uint32_t)(p >> 32) & 0xffffu, extent, 0x00027000u};
+  // Bytes from the descriptor's start to the end of what a stage of `steps` may read: beyond them a load
+  // returns zero. In whole chunks: of a word that straddles the end nothing would be read.
+  __device__ __forceinline__ uint32_t extent(int32_t steps) const {
+    if (steps <= 0) return 0;
+    return kBefore + (kMajor ? (uint32_t)(steps - 1) * outer_bytes + (uint32_t)inner * kSize
+                             : outer_bytes + (uint32_t)((steps + kChunk - 1) / kChunk * kChunk) * kSize);
   }
 
-  // Load j of a stage of which `left` steps exist, into the slot at `lds`. Written out because the
-  // compiler makes transposing LDS reads wait for every load to LDS that it knows of; it has no
-  // result register, and the kernel's own waits and barriers order it with the reads of its slot.
-  __device__ __forceinline__ void load(u32x4 rsrc, uint32_t lds, int j, int32_t left) const {
+  // Called before the loads of a stage of which only `left` < kSteps steps exist (none from there on).
+  __device__ __forceinline__ void tail(int32_t left) {
+    rsrc[2] = extent(left);
+    asm volatile("");  // a branch: selecting every lane's offset in every stage would cost as much as 4 products
+    if (!kMajor) {  // the rest of a memory row is the next row's
+#pragma unroll
+      for (int j = 0; j < kLoads; ++j) offset[j] = lane_step < left ? offset[j] : kNowhere;
+    }
+  }
+
+  // After the loads of a stage.
+  __device__ __forceinline__ void advance() {
+    const uint64_t at = ((uint64_t)rsrc[1] << 32 | rsrc[0]) + (uint64_t)stage_bytes;
+    rsrc[0] = (uint32_t)at;
+    rsrc[1] = (uint32_t)(at >> 32);
+  }
+
+  // Where this wavefront's loads j .. j + 3 (j a multiple of 4) go in the slot at `lds`; then load j.
+  // Written out because the compiler makes transposing LDS reads wait for every load to LDS that it
+  // knows of. A load has no result register, and the kernel's own waits and barriers order it with the
+  // reads of its slot. m0 has no other use in these kernels; one instruction has to lie between its
+  // setting and the load.
+  static __device__ __forceinline__ void aim(uint32_t lds, int j) {
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    uint32_t o = offset[j];
-    if (!kMajor) o = lane_step < left ? o : kNowhere;  // the rest of a memory row is the next row's
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-                 :
-                 : "s"(lds + (wave * kLoads + j) * 1024), "v"(o), "s"(rsrc)
-                 : "memory");  // m0 is written next to each use, by the compiler as well
+    asm volatile("s_mov_b32 m0, %0" : : "s"(lds + (wave * kLoads + j) * 1024) : "memory");
+  }
+  __device__ __forceinline__ void load(int j) const {
+    switch (j & 3) {
+      case 0: asm volatile("buffer_load_dwordx4 %0, %1, 0 offen lds" : : "v"(offset[j]), "s"(rsrc) : "memory"); break;
+      case 1: asm volatile("buffer_load_dwordx4 %0, %1, 0 offen offset:1024 lds" : : "v"(offset[j]), "s"(rsrc) : "memory"); break;
+      case 2: asm volatile("buffer_load_dwordx4 %0, %1, 0 offen offset:2048 lds" : : "v"(offset[j]), "s"(rsrc) : "memory"); break;
+      default: asm volatile("buffer_load_dwordx4 %0, %1, 0 offen offset:3072 lds" : : "v"(offset[j]), "s"(rsrc) : "memory"); break;
+    }
+  }
+  // All loads of a stage of which `left` steps exist.
+  __device__ __forceinline__ void load_stage(uint32_t lds, int32_t left) {
+    if (left < kSteps) tail(left);
+#pragma unroll
+    for (int j = 0; j < kLoads; ++j) {
+      if ((j & 3) == 0) {
+        aim(lds, j);
+        asm volatile("s_nop 0");
+      }
+      load(j);
+    }
+    advance();
   }
 
   // This lane's byte offset in a slot for the fragments of a wavefront's rows, from w on.
   static __device__ __forceinline__ uint32_t fragment_base(int w) {
     const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
-    if (!kMajor) return (w + r) * 64 + ((g ^ ((r >> 1) & 3)) << 4);
+    if (!kMajor) return (w + r) * 64 * H + ((g ^ row_key(r)) << 4);
     if (kSize == 4) return g * 4 * R * 4 + (((w >> 4) ^ key(g * 4)) << 6) + r * 4;
     const int k = g * 8 + (r >> 2);
     return k * R * 2 + (((w >> 4) ^ key(k)) << 5) + (r & 3) * 8;
   }
 
-  // Fragment f: rows w + 16 f + 0..15, the stage's steps; lane group g has steps g kSteps / 4 on.
-  static __device__ __forceinline__ frag fragment(lds_byte* slot, uint32_t at, int f) {
-    if (!kMajor) return *(__attribute__((address_space(3))) frag*)(slot + at + f * 1024);
+  // Fragment f: rows w + 16 f + 0..15, half h of the stage's steps; lane group g has a quarter of them.
+  static __device__ __forceinline__ frag fragment(lds_byte* slot, uint32_t at, int f, int h = 0) {
+    if (!kMajor) return *(__attribute__((address_space(3))) frag*)(slot + (at ^ (uint32_t)(h * 64)) + f * 1024 * H);
+    slot += h * (kSteps / H) * R * kSize;
     if constexpr (kSize == 4) {
       lds_byte* p = slot + (at ^ (uint32_t)(f << 6));
       frag v;
@@ -277,115 +321,46 @@ __device__ __forceinline__ void partial_rows(const float* area, const ProductArg
     store4<float>(p + row * a.n, *reinterpret_cast<const f32x4*>(area + staged_at<WN>(row, c4)), count, a.n % 4 == 0);
 }
 
-// Workgroup `id` of a product's tiles x splits, with `ring` of 4 (BM + BN) 64 bytes of LDS.
-template <typename T, int BM, int BN, bool kAMajor, bool kBMajor>
-__device__ __forceinline__ void ring_tile(const ProductArgs& a, uint32_t id, uint8_t* ring) {
-  typedef typename Stage<T>::frag frag;
-  typedef Operand<T, BM, kAMajor> OpA;
-  typedef Operand<T, BN, kBMajor> OpB;
-  constexpr int kStage = Stage<T>::kSteps;
-  constexpr int kSlot = OpA::kBytes + OpB::kBytes;
-  constexpr int FA = BM / 32, FB = BN / 32;  // fragments of a wavefront's BM / 2 x BN / 2
-  constexpr int kLoads = OpA::kLoads + OpB::kLoads;
-  lds_byte* lds = (lds_byte*)ring;
-  const uint32_t lds0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)lds);
-
-  const int64_t tiles_m = (a.m + BM - 1) / BM, tiles_n = (a.n + BN - 1) / BN;
-  const uint32_t tiles = (uint32_t)(tiles_m * tiles_n), split = id / tiles;
-  int64_t tm, tn;
-  tile_of(id % tiles, tiles_m, tiles_n, &tm, &tn);
-  const int64_t i0 = tm * BM, j0 = tn * BN;
-  const int64_t k0 = (int64_t)split * a.k_per_split;
-  const int64_t k_end = k0 + a.k_per_split < a.k ? k0 + a.k_per_split : a.k;
-  int32_t left = (int32_t)(k_end - k0);
-  const int32_t stages = (left + kStage - 1) / kStage;
+// A wavefront's sums in registers: 16 x 16 tiles of the matrix instruction. stage() writes
+// the part-th strip of `rows` rows to the wavefront's staging area.
+template <int FA, int FB>
+struct Sums16 {
+  f32x4 acc[FA][FB];
+  __device__ __forceinline__ void settle() {
+#pragma unroll
+    for (int c = 0; c < FA * FB; ++c) asm volatile("" : "+a"(acc[c / FB][c % FB]));
+  }
+  template <int WN>
+  __device__ __forceinline__ void stage(float* area, int part, int rows) const {
+    const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+#pragma unroll
+    for (int x = 0; x < FA; ++x)
+#pragma unroll
+      for (int y = 0; y < FB; ++y)
+        if (x * 16 / rows == part)
+          *reinterpret_cast<f32x4*>(area + staged_at<WN>(x * 16 % rows + r, y * 4 + g)) = acc[x][y];
+  }
+};
+// The end of a tile: its sums through LDS to memory. `ring` holds at least 256 (BM + BN) bytes.
+template <typename T, int BM, int BN, typename S>
+__device__ __forceinline__ void finish_tile(const ProductArgs& a, uint8_t* ring, S& sums, uint32_t split, int64_t i0,
+                                            int64_t j0) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wi = (wave >> 1) * (BM / 2), wj = (wave & 1) * (BN / 2);
-
-  OpA oa;
-  OpB ob;
-  oa.init(a.A, a.lda, i0, a.m - i0, k0);
-  ob.init(a.B, a.ldb, j0, a.n - j0, k0);
-  const uint32_t at_a = OpA::fragment_base(wi), at_b = OpB::fragment_base(wj);
-  f32x4 acc[FA][FB] = {};
-  frag fa[2][FA], fb[2][FB];
-
-#pragma unroll
-  for (int s = 0; s < kRing; ++s) {
-    const u32x4 ra = oa.next(left), rb = ob.next(left);
-#pragma unroll
-    for (int j = 0; j < OpA::kLoads; ++j) oa.load(ra, lds0 + s * kSlot, j, left);
-#pragma unroll
-    for (int j = 0; j < OpB::kLoads; ++j) ob.load(rb, lds0 + s * kSlot + OpA::kBytes, j, left);
-    left -= kStage;
-  }
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt(waitcnt(3 * kLoads, 15));
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-#pragma unroll
-  for (int f = 0; f < FA; ++f) fa[0][f] = OpA::fragment(lds, at_a, f);
-#pragma unroll
-  for (int f = 0; f < FB; ++f) fb[0][f] = OpB::fragment(lds + OpA::kBytes, at_b, f);
-
-  auto stage = [&](int now, uint32_t slot) {
-    // stage t + 1 has arrived (two younger ones may be on their way), and every wavefront has stage t's
-    // fragments in registers
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt(waitcnt(2 * kLoads, 0));
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-    const uint32_t here = lds0 + slot * kSlot;
-    lds_byte* next = lds + ((slot + 1) & (kRing - 1)) * kSlot;
-    const u32x4 ra = oa.next(left), rb = ob.next(left);
-    // The loads of stage t + 4 and the fragments of stage t + 1 are issued between the products, a few
-    // at a time: the matrix unit is never left waiting behind a queue of them. (Past the last stage the
-    // fragments are zeros or leftovers of the ring that nothing uses.)
-    constexpr int kGroups = FA + FB, kProducts = FA * FB * (sizeof(T) == 4 ? 4 : 1);
-#pragma unroll
-    for (int q = 0; q < kGroups; ++q) {
-      if ((q + 1) * kLoads / kGroups > q * kLoads / kGroups) {
-        const int j = q * kLoads / kGroups;
-        if (j < OpA::kLoads) oa.load(ra, here, j, left);
-        else ob.load(rb, here + OpA::kBytes, j - OpA::kLoads, left);
-      }
-      if (q < FA) fa[now ^ 1][q] = OpA::fragment(next, at_a, q);
-      else fb[now ^ 1][q - FA] = OpB::fragment(next + OpA::kBytes, at_b, q - FA);
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int c = q * kProducts / kGroups; c < (q + 1) * kProducts / kGroups; ++c)
-        mfma_in_place(acc[c / FB % FA][c % FB], fb[now][c % FB], fa[now][c / FB % FA], c / (FA * FB));
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    left -= kStage;
-  };
-  // stages in pairs, so that the two sets of fragments keep their registers; where their number is odd
-  // the last one's loads all lie beyond the extent and its products add zeros
-  for (int32_t t = 0; t < stages; t += 2) {
-    stage(0, t & (kRing - 1));
-    stage(1, (t + 1) & (kRing - 1));
-  }
   // no load to LDS outlives the workgroup, and the last products are through before their sums are read
   asm volatile("s_waitcnt vmcnt(0)\n\ts_nop 15\n\ts_nop 15" ::: "memory");
-#pragma unroll
-  for (int c = 0; c < FA * FB; ++c) asm volatile("" : "+a"(acc[c / FB][c % FB]));
-
+  sums.settle();
   __syncthreads();  // the ring is free: nobody reads fragments any more
 
   // The sums go through LDS, up to 64 rows of a wavefront at a time, so that a lane then has 8 neighbouring
   // columns and a row's lanes its whole width: 16-byte accesses of out, pre and residual.
   constexpr int WN = BN / 2, kRows = BM / 2 < 64 ? BM / 2 : 64;
   constexpr int kArea = kRows * WN * 4;  // bytes of a wavefront
-  static_assert(4 * kArea <= kRing * kSlot, "the staged sums fit the ring");
-  const int lane = threadIdx.x & 63, r = lane & 15, g = lane >> 4;
+  static_assert(4 * kArea <= kRing * (BM + BN) * 64, "the staged sums fit the ring");
   float* area = reinterpret_cast<float*>(ring + wave * kArea);
 #pragma unroll
   for (int part = 0; part < BM / 2 / kRows; ++part) {
-#pragma unroll
-    for (int x = 0; x < kRows / 16; ++x)
-#pragma unroll
-      for (int y = 0; y < FB; ++y)
-        *reinterpret_cast<f32x4*>(area + staged_at<WN>(x * 16 + r, y * 4 + g)) = acc[part * (kRows / 16) + x][y];
+    sums.template stage<WN>(area, part, kRows);
     __builtin_amdgcn_wave_barrier();
     const int64_t i = i0 + wi + part * kRows, j = j0 + wj;
     if (a.splits > 1)
@@ -396,12 +371,231 @@ __device__ __forceinline__ void ring_tile(const ProductArgs& a, uint32_t id, uin
   }
 }
 
+// A tile's place in its product.
+struct TilePlace {
+  uint32_t split;
+  int64_t i0, j0, k0;
+  int32_t steps;
+};
+template <int BM, int BN>
+__device__ __forceinline__ TilePlace place_of(const ProductArgs& a, uint32_t id) {
+  const int64_t tiles_m = (a.m + BM - 1) / BM, tiles_n = (a.n + BN - 1) / BN;
+  const uint32_t tiles = (uint32_t)(tiles_m * tiles_n);
+  TilePlace p;
+  p.split = id / tiles;
+  int64_t tm, tn;
+  tile_of(id % tiles, tiles_m, tiles_n, &tm, &tn);
+  p.i0 = tm * BM;
+  p.j0 = tn * BN;
+  p.k0 = (int64_t)p.split * a.k_per_split;
+  const int64_t k_end = p.k0 + a.k_per_split < a.k ? p.k0 + a.k_per_split : a.k;
+  p.steps = (int32_t)(k_end - p.k0);
+  return p;
+}
+
+// Issue op(0) .. op(ops - 1) between product(0) .. product(products - 1), spread evenly. With one
+// wavefront on a SIMD the matrix unit runs dry where more than about three other instructions stand
+// between two products (16 cycles at a 4-cycle issue), so they are pinned one by one.
+template <int kOps, int kProducts, typename Op, typename Product>
+__device__ __forceinline__ void interleave(Op op, Product product) {
+#pragma unroll
+  for (int c = 0; c < kProducts; ++c) {
+    product(c);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = (c * kOps + kProducts - 1) / kProducts; i * kProducts < (c + 1) * kOps; ++i) {
+      op(i);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+}
+
+// The loads of a stage as a list of instructions: per four loads one setting of their LDS address.
+template <typename OpA, typename OpB>
+struct StageLoads {
+  static constexpr int kA = OpA::kLoads + (OpA::kLoads + 3) / 4, kB = OpB::kLoads + (OpB::kLoads + 3) / 4;
+  static constexpr int kOps = kA + kB;
+  static __device__ __forceinline__ void issue(const OpA& oa, const OpB& ob, uint32_t lds, int i) {
+    if (i < kA) {
+      if (i % 5 == 0) OpA::aim(lds, i / 5 * 4);
+      else oa.load(i / 5 * 4 + i % 5 - 1);
+    } else {
+      i -= kA;
+      if (i % 5 == 0) OpB::aim(lds + OpA::kBytes, i / 5 * 4);
+      else ob.load(i / 5 * 4 + i % 5 - 1);
+    }
+  }
+};
+
+// Workgroup `id` of a product's tiles x splits for 256 x 256 tiles of 16-bit elements. Stages of two
+// halves (128 bytes of a row): a load takes whole 128-byte lines where the contraction is contiguous,
+// which halves the requests to L2 against 64-byte stages, and there is one barrier per two halves. Two
+// slots; stage t's slot is free once its second half's fragments are in registers, at the barrier in
+// the middle of stage t, and takes stage t + 2, which has until the middle of stage t + 1 to arrive.
+template <typename T, int BM, int BN, bool kAMajor, bool kBMajor>
+__device__ __forceinline__ void ring_tile_halves(const ProductArgs& a, uint32_t id, uint8_t* ring) {
+  typedef typename Stage<T>::frag frag;
+  typedef Operand<T, BM, kAMajor, 2> OpA;
+  typedef Operand<T, BN, kBMajor, 2> OpB;
+  typedef StageLoads<OpA, OpB> Loads;
+  constexpr int kStage = OpA::kSteps, kSlot = OpA::kBytes + OpB::kBytes;
+  constexpr int FA = BM / 32, FB = BN / 32, kProducts = FA * FB, kReads = FA + FB;
+  lds_byte* lds = (lds_byte*)ring;
+  const uint32_t lds0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)lds);
+  const TilePlace p = place_of<BM, BN>(a, id);
+  int32_t left = p.steps;
+  const int32_t stages = (left + kStage - 1) / kStage;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wi = (wave >> 1) * (BM / 2), wj = (wave & 1) * (BN / 2);
+
+  OpA oa;
+  OpB ob;
+  oa.init(a.A, a.lda, p.i0, a.m - p.i0, p.k0);
+  ob.init(a.B, a.ldb, p.j0, a.n - p.j0, p.k0);
+  const uint32_t at_a = OpA::fragment_base(wi), at_b = OpB::fragment_base(wj);
+  Sums16<FA, FB> sums = {};
+  frag fa[2][FA], fb[2][FB];
+  // read i of the fragments of a slot's half, into that half's set
+  const auto read = [&](lds_byte* slot, int half, int i) {
+    if (i < FA) fa[half][i] = OpA::fragment(slot, at_a, i, half);
+    else fb[half][i - FA] = OpB::fragment(slot + OpA::kBytes, at_b, i - FA, half);
+  };
+  const auto product = [&](int half, int c) { mfma_in_place(sums.acc[c / FB][c % FB], fb[half][c % FB], fa[half][c / FB], 0); };
+
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    oa.load_stage(lds0 + s * kSlot, left);
+    ob.load_stage(lds0 + s * kSlot + OpA::kBytes, left);
+    left -= kStage;
+  }
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(waitcnt(OpA::kLoads + OpB::kLoads, 15));
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < kReads; ++i) read(lds, 0, i);
+
+  for (int32_t t = 0; t < stages; ++t) {
+    const uint32_t slot = (uint32_t)(t & 1) * kSlot;
+    __builtin_amdgcn_s_waitcnt(waitcnt(63, 0));
+    interleave<kReads, kProducts>([&](int i) { read(lds + slot, 1, i); }, [&](int c) { product(0, c); });
+    // stage t + 1 has arrived, and every wavefront has all of stage t in registers
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(waitcnt(0, 0));
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    if (left < kStage) {
+      oa.tail(left);
+      ob.tail(left);
+    }
+    lds_byte* next = lds + (slot ^ kSlot);
+    // a read and a load in turn (past the last stage the reads are leftovers that nothing uses)
+    constexpr int kOps = kReads > Loads::kOps ? 2 * kReads : 2 * Loads::kOps;
+    interleave<kOps, kProducts>(
+        [&](int i) {
+          if (i % 2 == 0) {
+            if (i / 2 < kReads) read(next, 0, i / 2);
+          } else if (i / 2 < Loads::kOps) {
+            Loads::issue(oa, ob, lds0 + slot, i / 2);
+          }
+        },
+        [&](int c) { product(1, c); });
+    oa.advance();
+    ob.advance();
+    left -= kStage;
+  }
+  finish_tile<T, BM, BN>(a, ring, sums, p.split, p.i0, p.j0);
+}
+
+// The same for smaller tiles and fp32: stages of 64 bytes of a row, a ring of four slots. While the
+// products of stage t run, stage t + 1's fragments are read and stages t + 2 .. t + 4 are on their way.
+template <typename T, int BM, int BN, bool kAMajor, bool kBMajor>
+__device__ __forceinline__ void ring_tile(const ProductArgs& a, uint32_t id, uint8_t* ring) {
+  typedef typename Stage<T>::frag frag;
+  typedef Operand<T, BM, kAMajor, 1> OpA;
+  typedef Operand<T, BN, kBMajor, 1> OpB;
+  typedef StageLoads<OpA, OpB> Loads;
+  constexpr int kStage = OpA::kSteps, kSlot = OpA::kBytes + OpB::kBytes, kLoads = OpA::kLoads + OpB::kLoads;
+  constexpr int FA = BM / 32, FB = BN / 32;  // fragments of a wavefront's BM / 2 x BN / 2
+  constexpr int kReads = FA + FB, kProducts = FA * FB * (sizeof(T) == 4 ? 4 : 1);
+  lds_byte* lds = (lds_byte*)ring;
+  const uint32_t lds0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)lds);
+  const TilePlace p = place_of<BM, BN>(a, id);
+  int32_t left = p.steps;
+  const int32_t stages = (left + kStage - 1) / kStage;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wi = (wave >> 1) * (BM / 2), wj = (wave & 1) * (BN / 2);
+
+  OpA oa;
+  OpB ob;
+  oa.init(a.A, a.lda, p.i0, a.m - p.i0, p.k0);
+  ob.init(a.B, a.ldb, p.j0, a.n - p.j0, p.k0);
+  const uint32_t at_a = OpA::fragment_base(wi), at_b = OpB::fragment_base(wj);
+  Sums16<FA, FB> sums = {};
+  frag fa[2][FA], fb[2][FB];
+  const auto read = [&](lds_byte* slot, int to, int i) {
+    if (i < FA) fa[to][i] = OpA::fragment(slot, at_a, i);
+    else fb[to][i - FA] = OpB::fragment(slot + OpA::kBytes, at_b, i - FA);
+  };
+
+#pragma unroll
+  for (int s = 0; s < kRing; ++s) {
+    oa.load_stage(lds0 + s * kSlot, left);
+    ob.load_stage(lds0 + s * kSlot + OpA::kBytes, left);
+    left -= kStage;
+  }
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(waitcnt(3 * kLoads, 15));
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < kReads; ++i) read(lds, 0, i);
+
+  const auto stage = [&](int now, uint32_t slot) {
+    // stage t + 1 has arrived (two younger ones may be on their way), and every wavefront has stage t's
+    // fragments in registers
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(waitcnt(2 * kLoads, 0));
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+    if (left < kStage) {
+      oa.tail(left);
+      ob.tail(left);
+    }
+    const uint32_t here = lds0 + slot * kSlot;
+    lds_byte* next = lds + ((slot + 1) & (kRing - 1)) * kSlot;
+    constexpr int kOps = kReads > Loads::kOps ? 2 * kReads : 2 * Loads::kOps;
+    interleave<kOps, kProducts>(
+        [&](int i) {
+          if (i % 2 == 0) {
+            if (i / 2 < kReads) read(next, now ^ 1, i / 2);
+          } else if (i / 2 < Loads::kOps) {
+            Loads::issue(oa, ob, here, i / 2);
+          }
+        },
+        [&](int c) {
+          mfma_in_place(sums.acc[c / FB % FA][c % FB], fb[now][c % FB], fa[now][c / FB % FA], c / (FA * FB));
+        });
+    oa.advance();
+    ob.advance();
+    left -= kStage;
+  };
+  // stages in pairs, so that the two sets of fragments keep their registers; where their number is odd
+  // the last one's loads all lie beyond the extent and its products add zeros
+  for (int32_t t = 0; t < stages; t += 2) {
+    stage(0, t & (kRing - 1));
+    stage(1, (t + 1) & (kRing - 1));
+  }
+  finish_tile<T, BM, BN>(a, ring, sums, p.split, p.i0, p.j0);
+}
+
 constexpr int ring_bytes(int tile) { return kRing * 2 * tile * 64; }
 
 template <typename T, int TILE>
 __global__ __launch_bounds__(kThreads, TILE > 128 ? 1 : 2) void layer_ring(ProductArgs a) {
   __shared__ __align__(1024) uint8_t ring[ring_bytes(TILE)];
-  ring_tile<T, TILE, TILE, false, false>(a, blockIdx.x, ring);
+  if constexpr (TILE == 256) ring_tile_halves<T, TILE, TILE, false, false>(a, blockIdx.x, ring);
+  else ring_tile<T, TILE, TILE, false, false>(a, blockIdx.x, ring);
 }
 
 // The gradient's two products in one launch (the second's workgroups fill the CUs that the first's last
@@ -410,9 +604,15 @@ template <typename T, int TILE>
 __global__ __launch_bounds__(kThreads, TILE > 128 ? 1 : 2) void gradient_ring(GradientArgs a) {
   __shared__ __align__(1024) uint8_t ring[ring_bytes(TILE)];
   uint32_t id = blockIdx.x;
-  if (id < a.dx_groups) return ring_tile<T, TILE, TILE, false, true>(a.dx, id, ring);
-  id -= a.dx_groups;
-  if (id < a.dw_groups) return ring_tile<T, TILE, TILE, true, true>(a.dw, id, ring);
+  if constexpr (TILE == 256) {
+    if (id < a.dx_groups) return ring_tile_halves<T, TILE, TILE, false, true>(a.dx, id, ring);
+    id -= a.dx_groups;
+    if (id < a.dw_groups) return ring_tile_halves<T, TILE, TILE, true, true>(a.dw, id, ring);
+  } else {
+    if (id < a.dx_groups) return ring_tile<T, TILE, TILE, false, true>(a.dx, id, ring);
+    id -= a.dx_groups;
+    if (id < a.dw_groups) return ring_tile<T, TILE, TILE, true, true>(a.dw, id, ring);
+  }
   column_sum(a.sums, a.sum_rows, a.n, a.db, id - a.dw_groups, reinterpret_cast<double*>(ring));
 }
 

@@ -10,7 +10,7 @@ from ._abi import (XTVXY_ACT_GELU, XTVXY_ACT_GELU_TANH, XTVXY_ACT_NONE, XTVXY_AC
 
 ACTIVATIONS = {"none": XTVXY_ACT_NONE, "relu": XTVXY_ACT_RELU, "gelu": XTVXY_ACT_GELU,
                "gelu_tanh": XTVXY_ACT_GELU_TANH, "silu": XTVXY_ACT_SILU}
-_MAX_PITCH = 8 << 20  # bytes between rows up to which a matrix counts as aligned for the workspace queries
+_MAX_PITCH = 4 << 20  # bytes between rows up to which a matrix counts as aligned for the workspace queries
 
 
 # ---------------------------------------------------------------------------

@@ -711,7 +711,7 @@ enum {
 };
 
 /* Workspace bytes of the layer for this shape; aligned16 states whether X, W and their rows are
- * 16-byte aligned (pointers and strides), with strides of at most 8 MiB. Matrices whose rows are not,
+ * 16-byte aligned (pointers and strides), with strides of at most 4 MiB. Matrices whose rows are not,
  * or are no whole multiples of 16 bytes, are copied into the workspace, except for small products. */
 xtvxy_status xtvxy_linear_f32_workspace_size(int64_t m, int64_t k, int64_t n, int aligned16, size_t *bytes);
 xtvxy_status xtvxy_linear_bf16_workspace_size(int64_t m, int64_t k, int64_t n, int aligned16, size_t *bytes);
