@@ -24,7 +24,6 @@ struct Matrix {
   int es;
   size_t extent() const { return rows > 0 && cols > 0 ? (size_t)((rows - 1) * ld + cols) * es : 0; }
   bool aligned16() const { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * es % 16 == 0; }
-  bool aligned(int elems) const { return reinterpret_cast<uintptr_t>(p) % (elems * es) == 0 && ld % elems == 0; }
 };
 
 // Whether two matrices share an element (rows of equal pitch: exact; else by their extents).
@@ -277,8 +276,7 @@ xtvxy_status linear_impl(int type, int64_t m, int64_t k, int64_t n, const void* 
     a.ldb = padded(k, es);
   }
   if (pack.jobs > 0 && launch_pack(pack, type, stream) != hipSuccess) return XTVXY_ERROR_LAUNCH;
-  const auto wide = [&](int c) { return mo.aligned(c) && (!residual || mr.aligned(c)) && (!pre || mp.aligned(c)); };
-  a.e = {bias, residual, ldr, pre, ldp, out, ldo, act, wide(4), wide(8)};
+  a.e = {bias, residual, ldr, pre, ldp, out, ldo, act};
   if (plan.few) {
     a.splits = (int32_t)plan.product.splits;
     a.k_per_split = plan.product.k_per_split;
@@ -318,11 +316,11 @@ BackwardPlan plan_backward(int type, int64_t m, int64_t k, int64_t n, int act, b
   p.pack_x = want_dw && ring && !x_whole;
   p.form_d = ring && (act != XTVXY_ACT_NONE || !g_whole);
   p.ldd = cdiv(n, 8) * 8;
-  // row groups: about four workgroups per CU, at least 8 rows for each row that a workgroup takes at once
+  // row groups: about four workgroups per CU, at least 2 rows for each row that a workgroup takes at once
   const bool narrow = n <= kSlopeNarrow;
   const int64_t column_groups = std::max<int64_t>(1, cdiv(n, narrow ? 128 : 512));
   const int64_t groups = std::max<int64_t>(1, 4 * kComputeUnits / column_groups);
-  p.rows_per_group = std::max<int64_t>(narrow ? 64 : 32, cdiv(m, groups));
+  p.rows_per_group = std::max<int64_t>(narrow ? 32 : 8, cdiv(m, groups));
   p.groups = std::max<int64_t>(1, cdiv(m, p.rows_per_group));
   plan_gradient(type, m, k, n, want_dx, want_dw, ring, &p.dx, &p.dw);
   const auto take = [&](bool want, size_t bytes) {
@@ -402,7 +400,7 @@ xtvxy_status backward_impl(int type, int64_t m, int64_t k, int64_t n, const void
     a.dx.splits = (int32_t)p.dx.splits;
     a.dx.k_per_split = p.dx.k_per_split;
     a.dx.partial = reinterpret_cast<float*>(base + p.dx_off);
-    a.dx.e = {nullptr, nullptr, 0, nullptr, 0, dX, lddx, XTVXY_ACT_NONE, mdx.aligned(4), mdx.aligned(8)};
+    a.dx.e = {nullptr, nullptr, 0, nullptr, 0, dX, lddx, XTVXY_ACT_NONE};
   }
   if (dW && k > 0) {
     a.dw.B = X;
@@ -413,7 +411,7 @@ xtvxy_status backward_impl(int type, int64_t m, int64_t k, int64_t n, const void
     a.dw.splits = (int32_t)p.dw.splits;
     a.dw.k_per_split = p.dw.k_per_split;
     a.dw.partial = reinterpret_cast<float*>(base + p.dw_off);
-    a.dw.e = {nullptr, nullptr, 0, nullptr, 0, dW, lddw, XTVXY_ACT_NONE, mdw.aligned(4), mdw.aligned(8)};
+    a.dw.e = {nullptr, nullptr, 0, nullptr, 0, dW, lddw, XTVXY_ACT_NONE};
   }
   a.dx.type = a.dw.type = type;
   a.dx.A = a.dw.A = G;

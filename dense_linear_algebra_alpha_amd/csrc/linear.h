@@ -21,8 +21,6 @@ struct LinearEpilogue {
   void* out;
   int64_t ldo;
   int32_t act;     // XTVXY_ACT_*
-  int32_t wide;    // rows of out, pre and residual allow 4-element (16 or 8 byte) accesses
-  int32_t wide8;   // and 8-element ones
 };
 
 // C[i][j] = sum over k of A(i, k) B(j, k), i < m, j < n, followed by the epilogue. Where

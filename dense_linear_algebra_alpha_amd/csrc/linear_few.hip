@@ -126,7 +126,7 @@ __global__ __launch_bounds__(KW * 64) void product_few(ProductArgs a) {
     const int64_t i = c / NT * 16 + r, j = j0 + c % NT * 16 + g * 4;
     if (i >= a.m || j >= a.n) continue;
     if (a.splits > 1)
-      store4<float>(a.partial + ((int64_t)blockIdx.y * a.m + i) * a.n + j, z, a.n - j >= 4 ? 4 : (int)(a.n - j), a.n % 4 == 0);
+      store4<float>(a.partial + ((int64_t)blockIdx.y * a.m + i) * a.n + j, z, a.n - j >= 4 ? 4 : (int)(a.n - j));
     else
       epilogue4<T>(a.e, i, j, a.n, z);
   }

@@ -24,7 +24,6 @@ namespace xtvxy {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kRing = 4;     // LDS slots
 constexpr uint32_t kNowhere = 0xc0000000u;  // beyond any tile's extent: such a load returns zero
 // Four loads share a setting of their LDS address: an instruction's own offset (up to 4095) counts for
 // memory and LDS alike. Descriptors begin this far before their data, so that taking those offsets from
@@ -240,58 +239,62 @@ __device__ __forceinline__ f32x8 staged8(const float* area, int row, int c8) {
   return {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
 }
 
-// The epilogue of a wavefront's staged rows from (i0, j0) on, 8 columns a lane.
-template <typename T, int kAct, int WN, int kRows>
+// The epilogue of a wavefront's staged rows from (i0, j0) on, 8 columns a lane. kPlain: the sums alone.
+template <typename T, int kAct, int WN, int kRows, bool kPlain>
 __device__ __forceinline__ void epilogue_rows(const float* area, const ProductArgs& a, int64_t i0, int64_t j0) {
-  typedef typename Vec<T>::x8 v8;
   constexpr int kLanes = WN / 8, kStep = 64 / kLanes;  // lanes of a row, rows at once
-  const LinearEpilogue& e = a.e;
+  const LinearEpilogue e = kPlain ? LinearEpilogue{nullptr, nullptr, 0, nullptr, 0, a.e.out, a.e.ldo, kAct} : a.e;
   const int lane = threadIdx.x & 63, c8 = lane % kLanes;
   const int64_t j = j0 + c8 * 8;
   const int count = a.n - j >= 8 ? 8 : (a.n > j ? (int)(a.n - j) : 0);
   if (count == 0) return;
-  const bool wide = e.wide8 && count == 8;
-  f32x8 bias = {};
-  if (e.bias)
-#pragma unroll
-    for (int c = 0; c < 8; ++c)
-      if (c < count) bias[c] = e.bias[j + c];
+  float bias[8] = {};
+  if (e.bias) load_elems<float, 8>(e.bias + j, count, bias);
   const int rows = a.m - i0 >= kRows ? kRows : (int)(a.m - i0);
-  if (wide) {
-    const T* res = static_cast<const T*>(e.residual) + (e.residual ? i0 * e.ldr + j : 0);
-    T* pre = static_cast<T*>(e.pre) + (e.pre ? i0 * e.ldp + j : 0);
-    T* out = static_cast<T*>(e.out) + i0 * e.ldo + j;
-#pragma unroll 4
-    for (int row = lane / kLanes; row < rows; row += kStep) {
-      v8 rv = {};
-      if (e.residual) rv = *reinterpret_cast<const v8*>(res + row * e.ldr);
-      f32x8 z = staged8<WN>(area, row, c8) + bias;
-      v8 o;
-      if (e.pre) {
+  const T* res = static_cast<const T*>(e.residual) + (e.residual ? i0 * e.ldr + j : 0);
+  T* pre = static_cast<T*>(e.pre) + (e.pre ? i0 * e.ldp + j : 0);
+  T* out = static_cast<T*>(e.out) + i0 * e.ldo + j;
+  const auto run = [&](int row, int count, const T (&rv)[8]) {
+    T o[8];
+    const f32x8 s = staged8<WN>(area, row, c8);
+    float z[8];
 #pragma unroll
-        for (int c = 0; c < 8; ++c) o[c] = (T)z[c];
-        *reinterpret_cast<v8*>(pre + row * e.ldp) = o;
-      }
+    for (int c = 0; c < 8; ++c) z[c] = s[c] + bias[c];
+    if (e.pre) {
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        float y = activation<sizeof(T) == 2, kAct>(z[c]);
-        if (e.residual) y += (float)rv[c];
-        o[c] = (T)y;
-      }
-      *reinterpret_cast<v8*>(out + row * e.ldo) = o;
+      for (int c = 0; c < 8; ++c) o[c] = (T)z[c];
+      store_elems<T, 8>(pre + row * e.ldp, count, o);
+    }
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      float y = activation<sizeof(T) == 2, kAct>(z[c]);
+      if (e.residual) y += (float)rv[c];
+      o[c] = (T)y;
+    }
+    store_elems<T, 8>(out + row * e.ldo, count, o);
+  };
+  if (count == 8) {
+    // The residual of several rows is loaded before the first of them is stored (out may be the residual,
+    // so the compiler keeps loads behind stores): one wait instead of one per row.
+    constexpr int kBatch = kRows / kStep < 4 ? kRows / kStep : 4;
+#pragma unroll 1
+    for (int row = lane / kLanes; row < rows; row += kStep * kBatch) {
+      T rv[kBatch][8] = {};
+      if (e.residual)
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+          const int at = row + b * kStep;
+          load_elems<T, 8>(res + (at < rows ? at : row) * e.ldr, 8, rv[b]);
+        }
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b)
+        if (row + b * kStep < rows) run(row + b * kStep, 8, rv[b]);
     }
   } else {
     for (int row = lane / kLanes; row < rows; row += kStep) {
-      const f32x8 z = staged8<WN>(area, row, c8) + bias;
-      const int64_t i = i0 + row;
-#pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        if (c >= count) break;
-        if (e.pre) static_cast<T*>(e.pre)[i * e.ldp + j + c] = (T)z[c];
-        float y = activation<sizeof(T) == 2, kAct>(z[c]);
-        if (e.residual) y += (float)static_cast<const T*>(e.residual)[i * e.ldr + j + c];
-        static_cast<T*>(e.out)[i * e.ldo + j + c] = (T)y;
-      }
+      T rv[8] = {};
+      if (e.residual) load_elems<T, 8>(res + row * e.ldr, count, rv);
+      run(row, count, rv);
     }
   }
 }
@@ -299,11 +302,11 @@ __device__ __forceinline__ void epilogue_rows(const float* area, const ProductAr
 template <typename T, int WN, int kRows>
 __device__ __forceinline__ void epilogue_any(const float* area, const ProductArgs& a, int64_t i0, int64_t j0) {
   switch (a.e.act) {
-    case XTVXY_ACT_RELU: epilogue_rows<T, XTVXY_ACT_RELU, WN, kRows>(area, a, i0, j0); break;
-    case XTVXY_ACT_GELU: epilogue_rows<T, XTVXY_ACT_GELU, WN, kRows>(area, a, i0, j0); break;
-    case XTVXY_ACT_GELU_TANH: epilogue_rows<T, XTVXY_ACT_GELU_TANH, WN, kRows>(area, a, i0, j0); break;
-    case XTVXY_ACT_SILU: epilogue_rows<T, XTVXY_ACT_SILU, WN, kRows>(area, a, i0, j0); break;
-    default: epilogue_rows<T, XTVXY_ACT_NONE, WN, kRows>(area, a, i0, j0); break;
+    case XTVXY_ACT_RELU: epilogue_rows<T, XTVXY_ACT_RELU, WN, kRows, false>(area, a, i0, j0); break;
+    case XTVXY_ACT_GELU: epilogue_rows<T, XTVXY_ACT_GELU, WN, kRows, false>(area, a, i0, j0); break;
+    case XTVXY_ACT_GELU_TANH: epilogue_rows<T, XTVXY_ACT_GELU_TANH, WN, kRows, false>(area, a, i0, j0); break;
+    case XTVXY_ACT_SILU: epilogue_rows<T, XTVXY_ACT_SILU, WN, kRows, false>(area, a, i0, j0); break;
+    default: epilogue_rows<T, XTVXY_ACT_NONE, WN, kRows, false>(area, a, i0, j0); break;
   }
 }
 
@@ -318,7 +321,7 @@ __device__ __forceinline__ void partial_rows(const float* area, const ProductArg
   const int rows = a.m - i0 >= kRows ? kRows : (int)(a.m - i0);
   float* p = a.partial + ((int64_t)split * a.m + i0) * a.n + j;
   for (int row = lane / kLanes; row < rows; row += kStep)
-    store4<float>(p + row * a.n, *reinterpret_cast<const f32x4*>(area + staged_at<WN>(row, c4)), count, a.n % 4 == 0);
+    store4<float>(p + row * a.n, *reinterpret_cast<const f32x4*>(area + staged_at<WN>(row, c4)), count);
 }
 
 // A wavefront's sums in registers: 16 x 16 tiles of the matrix instruction. stage() writes
@@ -341,8 +344,8 @@ struct Sums16 {
           *reinterpret_cast<f32x4*>(area + staged_at<WN>(x * 16 % rows + r, y * 4 + g)) = acc[x][y];
   }
 };
-// The end of a tile: its sums through LDS to memory. `ring` holds at least 256 (BM + BN) bytes.
-template <typename T, int BM, int BN, typename S>
+// The end of a tile (kPlain: of the gradient's products, which have no epilogue): its sums through LDS to memory. `ring` holds at least 256 (BM + BN) bytes.
+template <typename T, int BM, int BN, bool kPlain, typename S>
 __device__ __forceinline__ void finish_tile(const ProductArgs& a, uint8_t* ring, S& sums, uint32_t split, int64_t i0,
                                             int64_t j0) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -356,7 +359,7 @@ __device__ __forceinline__ void finish_tile(const ProductArgs& a, uint8_t* ring,
   // columns and a row's lanes its whole width: 16-byte accesses of out, pre and residual.
   constexpr int WN = BN / 2, kRows = BM / 2 < 64 ? BM / 2 : 64;
   constexpr int kArea = kRows * WN * 4;  // bytes of a wavefront
-  static_assert(4 * kArea <= kRing * (BM + BN) * 64, "the staged sums fit the ring");
+  static_assert(4 * kArea <= 4 * (BM + BN) * 64, "the staged sums fit four slots");
   float* area = reinterpret_cast<float*>(ring + wave * kArea);
 #pragma unroll
   for (int part = 0; part < BM / 2 / kRows; ++part) {
@@ -365,6 +368,8 @@ __device__ __forceinline__ void finish_tile(const ProductArgs& a, uint8_t* ring,
     const int64_t i = i0 + wi + part * kRows, j = j0 + wj;
     if (a.splits > 1)
       partial_rows<WN, kRows>(area, a, split, i, j);
+    else if (kPlain)
+      epilogue_rows<T, XTVXY_ACT_NONE, WN, kRows, true>(area, a, i, j);
     else
       epilogue_any<T, WN, kRows>(area, a, i, j);
     __builtin_amdgcn_wave_barrier();
@@ -504,12 +509,12 @@ __device__ __forceinline__ void ring_tile_halves(const ProductArgs& a, uint32_t 
     ob.advance();
     left -= kStage;
   }
-  finish_tile<T, BM, BN>(a, ring, sums, p.split, p.i0, p.j0);
+  finish_tile<T, BM, BN, kBMajor>(a, ring, sums, p.split, p.i0, p.j0);
 }
 
 // The same for smaller tiles and fp32: stages of 64 bytes of a row, a ring of four slots. While the
 // products of stage t run, stage t + 1's fragments are read and stages t + 2 .. t + 4 are on their way.
-template <typename T, int BM, int BN, bool kAMajor, bool kBMajor>
+template <typename T, int BM, int BN, int kRing, bool kAMajor, bool kBMajor>
 __device__ __forceinline__ void ring_tile(const ProductArgs& a, uint32_t id, uint8_t* ring) {
   typedef typename Stage<T>::frag frag;
   typedef Operand<T, BM, kAMajor, 1> OpA;
@@ -545,7 +550,7 @@ __device__ __forceinline__ void ring_tile(const ProductArgs& a, uint32_t id, uin
     left -= kStage;
   }
   asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt(waitcnt(3 * kLoads, 15));
+  __builtin_amdgcn_s_waitcnt(waitcnt((kRing - 1) * kLoads, 15));
   __builtin_amdgcn_s_barrier();
   asm volatile("" ::: "memory");
 #pragma unroll
@@ -555,7 +560,7 @@ __device__ __forceinline__ void ring_tile(const ProductArgs& a, uint32_t id, uin
     // stage t + 1 has arrived (two younger ones may be on their way), and every wavefront has stage t's
     // fragments in registers
     asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt(waitcnt(2 * kLoads, 0));
+    __builtin_amdgcn_s_waitcnt(waitcnt((kRing - 2) * kLoads, 0));
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
     if (left < kStage) {
@@ -586,32 +591,37 @@ __device__ __forceinline__ void ring_tile(const ProductArgs& a, uint32_t id, uin
     stage(0, t & (kRing - 1));
     stage(1, (t + 1) & (kRing - 1));
   }
-  finish_tile<T, BM, BN>(a, ring, sums, p.split, p.i0, p.j0);
+  finish_tile<T, BM, BN, kBMajor>(a, ring, sums, p.split, p.i0, p.j0);
 }
 
-constexpr int ring_bytes(int tile) { return kRing * 2 * tile * 64; }
+// LDS slots of a launch: where it is few workgroups, those that a CU can hold with eight slots each (two
+// of 64 x 64, one of 128 x 128), a load has seven stages to arrive instead of three. A lone 64 x 64
+// workgroup's stage then takes DEEP64 us instead of 0.18, a lone 128 x 128 one's DEEP128 instead of 0.33.
+constexpr int kSlots = 4, kDeepSlots = 8;
+constexpr int ring_bytes(int tile, int slots) { return (tile == 256 ? 4 : slots) * 2 * tile * 64; }
+bool few_groups(int tile, int64_t groups) { return groups <= 256 * (tile == 64 ? 2 : 1); }
 
-template <typename T, int TILE>
-__global__ __launch_bounds__(kThreads, TILE > 128 ? 1 : 2) void layer_ring(ProductArgs a) {
-  __shared__ __align__(1024) uint8_t ring[ring_bytes(TILE)];
+template <typename T, int TILE, int RING>
+__global__ __launch_bounds__(kThreads, TILE > 128 || RING * TILE > 512 ? 1 : 2) void layer_ring(ProductArgs a) {
+  __shared__ __align__(1024) uint8_t ring[ring_bytes(TILE, RING)];
   if constexpr (TILE == 256) ring_tile_halves<T, TILE, TILE, false, false>(a, blockIdx.x, ring);
-  else ring_tile<T, TILE, TILE, false, false>(a, blockIdx.x, ring);
+  else ring_tile<T, TILE, TILE, RING, false, false>(a, blockIdx.x, ring);
 }
 
 // The gradient's two products in one launch (the second's workgroups fill the CUs that the first's last
 // round leaves), and the sum of the row groups' column sums.
-template <typename T, int TILE>
-__global__ __launch_bounds__(kThreads, TILE > 128 ? 1 : 2) void gradient_ring(GradientArgs a) {
-  __shared__ __align__(1024) uint8_t ring[ring_bytes(TILE)];
+template <typename T, int TILE, int RING>
+__global__ __launch_bounds__(kThreads, TILE > 128 || RING * TILE > 512 ? 1 : 2) void gradient_ring(GradientArgs a) {
+  __shared__ __align__(1024) uint8_t ring[ring_bytes(TILE, RING)];
   uint32_t id = blockIdx.x;
   if constexpr (TILE == 256) {
     if (id < a.dx_groups) return ring_tile_halves<T, TILE, TILE, false, true>(a.dx, id, ring);
     id -= a.dx_groups;
     if (id < a.dw_groups) return ring_tile_halves<T, TILE, TILE, true, true>(a.dw, id, ring);
   } else {
-    if (id < a.dx_groups) return ring_tile<T, TILE, TILE, false, true>(a.dx, id, ring);
+    if (id < a.dx_groups) return ring_tile<T, TILE, TILE, RING, false, true>(a.dx, id, ring);
     id -= a.dx_groups;
-    if (id < a.dw_groups) return ring_tile<T, TILE, TILE, true, true>(a.dw, id, ring);
+    if (id < a.dw_groups) return ring_tile<T, TILE, TILE, RING, true, true>(a.dw, id, ring);
   }
   column_sum(a.sums, a.sum_rows, a.n, a.db, id - a.dw_groups, reinterpret_cast<double*>(ring));
 }
@@ -622,7 +632,14 @@ uint32_t groups_of(const ProductArgs& a, int tile) {
 
 template <typename T, int TILE>
 hipError_t layer_for(const ProductArgs& a, hipStream_t s) {
-  layer_ring<T, TILE><<<groups_of(a, TILE), kThreads, 0, s>>>(a);
+  const uint32_t groups = groups_of(a, TILE);
+  if constexpr (TILE < 256) {
+    if (few_groups(TILE, groups)) {
+      layer_ring<T, TILE, kDeepSlots><<<groups, kThreads, 0, s>>>(a);
+      return hipGetLastError();
+    }
+  }
+  layer_ring<T, TILE, kSlots><<<groups, kThreads, 0, s>>>(a);
   return hipGetLastError();
 }
 
@@ -631,8 +648,15 @@ hipError_t gradient_for(GradientArgs a, hipStream_t s) {
   a.dx_groups = a.dx.m > 0 ? groups_of(a.dx, TILE) : 0;
   a.dw_groups = a.dw.m > 0 ? groups_of(a.dw, TILE) : 0;
   const uint32_t columns = a.db ? (uint32_t)((a.n + kSumColumns - 1) / kSumColumns) : 0;
-  if (a.dx_groups + a.dw_groups + columns == 0) return hipSuccess;
-  gradient_ring<T, TILE><<<a.dx_groups + a.dw_groups + columns, kThreads, 0, s>>>(a);
+  const uint32_t groups = a.dx_groups + a.dw_groups + columns;
+  if (groups == 0) return hipSuccess;
+  if constexpr (TILE < 256) {
+    if (few_groups(TILE, a.dx_groups + a.dw_groups)) {
+      gradient_ring<T, TILE, kDeepSlots><<<groups, kThreads, 0, s>>>(a);
+      return hipGetLastError();
+    }
+  }
+  gradient_ring<T, TILE, kSlots><<<groups, kThreads, 0, s>>>(a);
   return hipGetLastError();
 }
 

@@ -127,7 +127,7 @@ __device__ __forceinline__ void tile(const ProductArgs& a, uint32_t id, const Gr
       if (i >= a.m || j >= a.n) continue;
       if (a.splits > 1) {
         float* p = a.partial + ((int64_t)split * a.m + i) * a.n + j;
-        store4<float>(p, acc[x][y], a.n - j >= 4 ? 4 : (int)(a.n - j), a.n % 4 == 0);
+        store4<float>(p, acc[x][y], a.n - j >= 4 ? 4 : (int)(a.n - j));
       } else {
         epilogue4<T>(a.e, i, j, a.n, acc[x][y]);
       }
@@ -176,7 +176,7 @@ __device__ __forceinline__ void finish_quad(const ProductArgs& a, int64_t at) {
   f32x4 z = {0.0f, 0.0f, 0.0f, 0.0f};
   if (exists) {
 #pragma unroll 4
-    for (int s = part; s < a.splits; s += 4) z += load4<float>(a.partial + ((int64_t)s * a.m + i) * a.n + j, count, a.n % 4 == 0);
+    for (int s = part; s < a.splits; s += 4) z += load4<float>(a.partial + ((int64_t)s * a.m + i) * a.n + j, count);
   }
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
@@ -217,19 +217,25 @@ __global__ __launch_bounds__(kThreads) void slope_rows(SlopeArgs a) {
   typedef typename Vec<T>::x8 v8;
   float sum[8] = {};
   const int count = a.n - j >= 8 ? 8 : (a.n > j ? (int)(a.n - j) : 0);
+  // The lane of a row's last, partial eight loads the eight that end with the row and shifts: a branch
+  // around its loads would make every row wait for them (1501 x 501: 13.8 us against 5).
+  const int shift = a.n >= 8 ? 8 - count : 0;
+  const bool shifts = __any(count > 0 && shift > 0);
+  const T* Gj = G + j - shift;
+  const T* Pj = P + j - shift;
   if (count > 0) {
 #pragma unroll 4
     for (int64_t i = r0 + slot; i < r1; i += kSlots) {
       v8 g = {}, z = {}, o;
-      if (count == 8) {  // memory takes unaligned accesses
-        __builtin_memcpy(&g, G + i * a.ldg + j, sizeof(g));
-        if (kAct != XTVXY_ACT_NONE) __builtin_memcpy(&z, P + i * a.ldp + j, sizeof(z));
+      if (a.n >= 8) {  // memory takes unaligned accesses
+        __builtin_memcpy(&g, Gj + i * a.ldg, sizeof(g));
+        if (kAct != XTVXY_ACT_NONE) __builtin_memcpy(&z, Pj + i * a.ldp, sizeof(z));
       } else {
 #pragma unroll
         for (int c = 0; c < 8; ++c)
           if (c < count) {
-            g[c] = G[i * a.ldg + j + c];
-            if (kAct != XTVXY_ACT_NONE) z[c] = P[i * a.ldp + j + c];
+            g[c] = Gj[i * a.ldg + c];
+            if (kAct != XTVXY_ACT_NONE) z[c] = Pj[i * a.ldp + c];
           }
       }
       float x[8];
@@ -237,8 +243,15 @@ __global__ __launch_bounds__(kThreads) void slope_rows(SlopeArgs a) {
       for (int c = 0; c < 8; ++c) {
         x[c] = (float)g[c];
         if (kAct != XTVXY_ACT_NONE) x[c] *= slope<kAct>((float)z[c]);
-        o[c] = (T)x[c];
       }
+      if (shifts) {  // zeros come in from the right
+#pragma unroll
+        for (int by = 4; by > 0; by /= 2)
+#pragma unroll
+          for (int c = 0; c < 8; ++c) x[c] = shift & by ? (c + by < 8 ? x[c + by] : 0.0f) : x[c];
+      }
+#pragma unroll
+      for (int c = 0; c < 8; ++c) o[c] = (T)x[c];
       if (D) *reinterpret_cast<v8*>(D + i * a.ldd + j) = o;  // ldd is a multiple of 8; missing columns are zero
 #pragma unroll
       for (int c = 0; c < 8; ++c) sum[c] += x[c];
@@ -265,6 +278,7 @@ __global__ __launch_bounds__(kThreads) void slope_rows(SlopeArgs a) {
 }
 
 // 16 bytes of a row at a time; the source may have any alignment (memory takes unaligned accesses).
+// Positions are 32-bit where they fit: two 64-bit divisions cost as much as the copy of a chunk.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void pack_rows(PackArgs a) {
   constexpr int kChunk = 16 / sizeof(T);
@@ -272,16 +286,15 @@ __global__ __launch_bounds__(kThreads) void pack_rows(PackArgs a) {
   const PackJob& job = a.job[blockIdx.y];
   const int64_t chunks = job.ldd / kChunk, total = job.rows * chunks;
   for (int64_t at = (int64_t)blockIdx.x * kThreads + threadIdx.x; at < total; at += (int64_t)gridDim.x * kThreads) {
-    const int64_t i = at / chunks, c = (at % chunks) * kChunk;
+    const bool fits = total <= INT32_MAX;
+    const int64_t i = fits ? (uint32_t)at / (uint32_t)chunks : at / chunks, c = (at - i * chunks) * kChunk;
     const T* p = static_cast<const T*>(job.src) + i * job.ld + c;
-    chunk v = {};
-    if (job.cols - c >= kChunk) {
-      __builtin_memcpy(&v, p, 16);
-    } else {
+    const int64_t left = job.cols - c;
+    T x[kChunk];
+    load_elems<T, kChunk>(p, left >= kChunk ? kChunk : (int)left, x);
+    chunk v;
 #pragma unroll
-      for (int x = 0; x < kChunk; ++x)
-        if (c + x < job.cols) v[x] = p[x];
-    }
+    for (int e = 0; e < kChunk; ++e) v[e] = x[e];
     *reinterpret_cast<chunk*>(static_cast<T*>(job.dst) + i * job.ldd + c) = v;
   }
 }

@@ -132,34 +132,65 @@ __device__ __forceinline__ float slope(float z) {
   return 1.0f;
 }
 
-// Four elements of a row, from j0, of which `count` exist.
-template <typename T>
-__device__ __forceinline__ f32x4 load4(const T* p, int count, bool wide) {
-  f32x4 r = {0.0f, 0.0f, 0.0f, 0.0f};
-  if (wide) {
-    const typename Vec<T>::x4 v = *reinterpret_cast<const typename Vec<T>::x4*>(p);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) r[i] = (float)v[i];
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i < count) r[i] = (float)p[i];
+// N = 4 or 8 elements of a row of which the first `count` exist (the rest come out as zero). Memory takes
+// vector accesses of any alignment, so only a row's last elements go piecewise, in at most three accesses:
+// with one access per element the ends of rows of odd length cost more than the rest of the epilogue.
+template <typename T, int N>
+__device__ __forceinline__ void load_elems(const T* p, int count, T (&x)[N]) {
+  if (count >= N) {
+    __builtin_memcpy(x, p, sizeof(T) * N);
+    return;
   }
-  return r;
+#pragma unroll
+  for (int i = 0; i < N; ++i) x[i] = (T)0.0f;
+  T four[4] = {}, two[2] = {}, one = (T)0.0f;
+  if (N == 8 && (count & 4)) __builtin_memcpy(four, p, sizeof(four));
+  const T* q = p + (count & (N == 8 ? 4 : 0));
+  if (count & 2) __builtin_memcpy(two, q, sizeof(two));
+  if (count & 1) one = q[count & 2];
+  const int at = N == 8 ? count & 4 : 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    if (N == 8 && i < 4 && at) x[i] = four[i];
+    if (i >= at && i < at + 2 && (count & 2)) x[i] = two[(i - at) & 1];
+    if ((count & 1) && i == count - 1) x[i] = one;
+  }
+}
+
+template <typename T, int N>
+__device__ __forceinline__ void store_elems(T* p, int count, const T (&x)[N]) {
+  if (count >= N) {
+    __builtin_memcpy(p, x, sizeof(T) * N);
+    return;
+  }
+  T* q = p;
+  T y[4] = {x[0], x[1], x[2], x[3]};
+  if (N == 8 && (count & 4)) {
+    __builtin_memcpy(q, y, sizeof(y));
+    q += 4;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = x[(i + 4) % N];
+  }
+  T z = y[0];
+  if (count & 2) {
+    __builtin_memcpy(q, y, 2 * sizeof(T));
+    q += 2;
+    z = y[2];
+  }
+  if (count & 1) *q = z;
 }
 
 template <typename T>
-__device__ __forceinline__ void store4(T* p, f32x4 v, int count, bool wide) {
-  if (wide) {
-    typename Vec<T>::x4 o;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = (T)v[i];
-    *reinterpret_cast<typename Vec<T>::x4*>(p) = o;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i < count) p[i] = (T)v[i];
-  }
+__device__ __forceinline__ f32x4 load4(const T* p, int count) {
+  T x[4];
+  load_elems<T, 4>(p, count, x);
+  return {(float)x[0], (float)x[1], (float)x[2], (float)x[3]};
+}
+
+template <typename T>
+__device__ __forceinline__ void store4(T* p, f32x4 v, int count) {
+  const T x[4] = {(T)v[0], (T)v[1], (T)v[2], (T)v[3]};
+  store_elems<T, 4>(p, count, x);
 }
 
 template <bool kFast>
@@ -186,16 +217,11 @@ template <typename T>
 __device__ __forceinline__ void epilogue4(const LinearEpilogue& e, int64_t i, int64_t j, int64_t n, f32x4 z) {
   const int count = n - j >= 4 ? 4 : (int)(n - j);
   if (count <= 0) return;
-  const bool wide = e.wide && count == 4;
-  if (e.bias) {
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-      if (c < count) z[c] += e.bias[j + c];
-  }
-  if (e.pre) store4<T>(static_cast<T*>(e.pre) + i * e.ldp + j, z, count, wide);
+  if (e.bias) z += load4<float>(e.bias + j, count);
+  if (e.pre) store4<T>(static_cast<T*>(e.pre) + i * e.ldp + j, z, count);
   f32x4 y = activation4<sizeof(T) == 2>(z, e.act);
-  if (e.residual) y += load4<T>(static_cast<const T*>(e.residual) + i * e.ldr + j, count, wide);
-  store4<T>(static_cast<T*>(e.out) + i * e.ldo + j, y, count, wide);
+  if (e.residual) y += load4<T>(static_cast<const T*>(e.residual) + i * e.ldr + j, count);
+  store4<T>(static_cast<T*>(e.out) + i * e.ldo + j, y, count);
 }
 
 // db[j] = the sum of sums[.][n] over its rows for the 16 columns of workgroup `group` (256 threads): a
