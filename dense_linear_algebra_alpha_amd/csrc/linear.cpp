@@ -43,55 +43,89 @@ Matrix vec(const float* p, int64_t n) { return {p, 1, n, n > 0 ? n : 1, 4}; }
 
 xtvxy_status status_of(hipError_t e) { return e == hipSuccess ? XTVXY_SUCCESS : XTVXY_ERROR_LAUNCH; }
 
-// How one product is computed: by which kernel, and in how many parts of the contraction.
+// How one product is computed: by which kernel, which of its tiles whole and which in how many parts of
+// the contraction.
 struct ProductPlan {
   int tile = 0;  // 0: the kernel for any alignment; 64, 128, 256: the ring kernel's tile
-  int64_t splits = 1, k_per_split = 0;
+  int64_t whole = 0, splits = 1, k_per_split = 0;
   size_t bytes = 0;  // partial sums
 };
 
-// Microseconds per stage of a CU that runs `groups` workgroups of a tile in all, of which several are
-// resident at once (one of 256, two of 128, five of 64). Measured on products of 2^28 .. 2^40
-// multiplications: 256 x 256 0.88 (the matrix unit is busy), 128 x 128 0.33 for a lone workgroup and
-// 0.57 for two, 64 x 64 0.18 alone and 0.13 each from two on; fp32 stages take the matrix unit 3.4, 0.84
-// (128, 64; half the contraction steps of a 16-bit stage).
-double stage_us(int type, int tile, int64_t groups) {
-  if (type == kF32) return tile == 128 ? 1.18 * groups : (groups <= 1 ? 0.36 : 0.28 * groups);
-  if (tile == 256) return 0.88 * groups;
-  if (tile == 128) return groups <= 1 ? 0.33 : 0.285 * groups;
-  return groups <= 1 ? 0.18 : 0.13 * groups;
+// The estimate of a launch's time: its workgroups are jobs on slots, 1 (256), 2 (128) or 5 (64) of them on
+// each CU. A job takes its stages of 32 steps (fp32: 16) and a start and end (first loads, epilogue).
+// Measured, us a stage: 256 x 256 0.71 (8192^3: 733 us); 128 x 128 0.33 alone on its CU, 0.57 two; 64 x 64
+// 0.18 alone, 0.13 more for each other; fp32 takes the matrix unit 1.18 (128) and 0.28 (64; alone 0.36).
+int residents(int tile) { return tile == 256 ? 1 : tile == 128 ? 2 : 5; }
+double stage_us(int type, int tile, int64_t on_cu) {
+  if (type == kF32) return tile == 128 ? 1.18 * on_cu : on_cu <= 1 ? 0.36 : 0.28 * on_cu;
+  if (tile == 256) return 0.71;
+  if (tile == 128) return on_cu <= 1 ? 0.33 : 0.285 * on_cu;
+  return on_cu <= 1 ? 0.18 : 0.13 * on_cu;
 }
+double start_and_end_us(int type, int tile) { return tile == 256 ? 9.0 : tile == 128 ? 3.5 : type == kF32 ? 2.5 : 2.0; }
 
-// Times and sizes of one product with a tile and a number of parts. Estimated: the stages (launch and
-// first loads are not counted), the epilogue's stores (a CU stores a tile at about 8 bytes a cycle),
-// and for parts the sums written and read back at 8 TB/s (they stay in the last-level cache).
-struct ProductCost {
-  int64_t groups = 0, stages = 0, per = 0;
-  double extra_us = 0;
+struct Jobs {
+  int64_t count = 0;
+  double us = 0;
 };
-bool product_cost(int type, int tile, int64_t splits, int64_t m, int64_t n, int64_t k, ProductCost* c) {
-  *c = {};
-  c->per = std::max<int64_t>(kTileDepth, cdiv(cdiv(k, splits), kTileDepth) * kTileDepth);
-  const int64_t tiles = cdiv(m, tile) * cdiv(n, tile);
-  if (splits > 1 && (c->per < 64 || tiles * splits > 16 * kComputeUnits || cdiv(k, c->per) != splits)) return false;
-  c->groups = tiles * splits;
-  c->stages = cdiv(c->per, type == kF32 ? 16 : 32);
-  c->extra_us = (double)cdiv(c->groups, kComputeUnits) * tile * tile * (splits > 1 ? 4 : elem_size(type)) / 8 / 2200 +
-                (tile == 256 ? 2.0 : 0.0) + (splits > 1 ? 2.0 * splits * m * n * 4 / 8e6 : 0.0);
-  return true;
+// When the last of the jobs ends, each in turn given to the slot that is free first.
+double makespan(int64_t slots, const Jobs* jobs, int kinds) {
+  struct Class {  // slots that are free from the same time on
+    double at;
+    int64_t count;
+  } free_at[8] = {{0.0, slots}};
+  int classes = 1;
+  double last = 0;
+  for (int j = 0; j < kinds; ++j) {
+    int64_t left = jobs[j].count;
+    while (left > 0) {
+      int first = 0;
+      for (int c = 1; c < classes; ++c)
+        if (free_at[c].at < free_at[first].at) first = c;
+      const int64_t rounds = classes == 1 ? std::max<int64_t>(1, left / free_at[first].count) : 1;
+      const int64_t n = std::min(left, free_at[first].count * rounds);
+      const double end = free_at[first].at + rounds * jobs[j].us;
+      left -= n;
+      last = std::max(last, end);
+      const int64_t used = std::min(n, free_at[first].count);
+      if ((free_at[first].count -= used) == 0) free_at[first] = free_at[--classes];
+      int same = 0;
+      while (same < classes && free_at[same].at != end) ++same;
+      if (same < classes) free_at[same].count += used;
+      else free_at[classes++] = {end, used};  // at most one class more per kind of job
+    }
+  }
+  return last;
 }
 
 constexpr int64_t kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64};
+constexpr int64_t kMostParts = 5 * kComputeUnits;  // workgroups of split tiles
 
-void set_product(ProductPlan* p, int tile, int64_t splits, const ProductCost& c, int64_t m, int64_t n) {
-  p->tile = tile;
+// A product with a tile, `whole` of its tiles not split. False where the split makes no sense.
+bool set_product(ProductPlan* p, int type, int tile, bool ring, int64_t whole, int64_t splits, int64_t m, int64_t n, int64_t k) {
+  const int64_t tiles = cdiv(m, tile) * cdiv(n, tile);
+  p->tile = ring ? tile : 0;
   p->splits = splits;
-  p->k_per_split = c.per;
-  p->bytes = splits > 1 ? align_up((size_t)splits * m * n * 4) : 0;
+  p->whole = splits > 1 ? whole : tiles;
+  p->k_per_split = std::max<int64_t>(kTileDepth, cdiv(cdiv(k, splits), kTileDepth) * kTileDepth);
+  p->bytes = splits == 1 ? 0 : align_up((size_t)splits * (ring ? (tiles - whole) * tile * tile : m * n) * 4);
+  return splits == 1 || (p->k_per_split >= 64 && (tiles - whole) * splits <= kMostParts && cdiv(k, p->k_per_split) == splits);
 }
 
-// The layer's tile and number of parts with the least estimated time (2 us for the second launch of a
-// split product).
+// The jobs of a product, and the time of writing its parts' sums and of reading them back at 8 TB/s
+// (they stay in the last-level cache).
+double product_jobs(const ProductPlan& p, int type, int tile, int64_t m, int64_t n, int64_t k, double stage, Jobs* jobs) {
+  const int64_t tiles = cdiv(m, tile) * cdiv(n, tile), whole = p.splits > 1 ? p.whole : tiles;
+  const int64_t depth = type == kF32 ? 16 : 32;
+  const double ends = start_and_end_us(type, tile);
+  jobs[0] = {whole, cdiv(k, depth) * stage + ends};
+  jobs[1] = {(tiles - whole) * p.splits, cdiv(p.k_per_split, depth) * stage + ends};
+  return p.splits > 1 ? 2.0 * p.splits * (tiles - whole) * tile * tile * 4 / 8e6 : 0.0;
+}
+
+constexpr double kFinishUs = 3.0;  // the launch that sums the parts
+
+// The layer's tile, split tiles and parts with the least estimated time.
 ProductPlan plan_product(int type, int64_t m, int64_t n, int64_t k, bool ring) {
   ProductPlan best;
   best.k_per_split = kTileDepth;
@@ -99,13 +133,23 @@ ProductPlan plan_product(int type, int64_t m, int64_t n, int64_t k, bool ring) {
   double least = 0;
   for (int tile : {64, 128, 256}) {
     if (!ring ? tile != 64 : (tile == 256 && type == kF32)) continue;
-    for (int64_t splits : kSplits) {
-      ProductCost c;
-      if (!product_cost(type, tile, splits, m, n, k, &c)) continue;
-      const double us = c.stages * stage_us(type, tile, cdiv(c.groups, kComputeUnits)) + c.extra_us + (splits > 1 ? 2.0 : 0.0);
-      if (least == 0 || us < least) {
-        least = us;
-        set_product(&best, ring ? tile : 0, splits, c, m, n);
+    const int64_t tiles = cdiv(m, tile) * cdiv(n, tile), slots = kComputeUnits * residents(tile);
+    // what a last, incomplete round of the CUs would hold may be split instead of everything
+    const int64_t whole[] = {0, tiles / kComputeUnits * kComputeUnits, tiles / slots * slots};
+    for (int w = 0; w < (ring ? 3 : 1); ++w) {
+      if (w > 0 && (whole[w] == 0 || whole[w] == tiles)) continue;
+      for (int64_t splits : kSplits) {
+        ProductPlan p;
+        if ((w > 0 && splits == 1) || !set_product(&p, type, tile, ring, whole[w], splits, m, n, k)) continue;
+        const int64_t groups = whole[w] + (tiles - whole[w]) * splits;
+        const int64_t on_cu = std::min<int64_t>(residents(tile), cdiv(groups, kComputeUnits));
+        Jobs jobs[2];
+        double us = product_jobs(p, type, tile, m, n, k, stage_us(type, tile, on_cu), jobs);
+        us += makespan(kComputeUnits * on_cu, jobs, 2) + (splits > 1 ? kFinishUs : 0.0);
+        if (least == 0 || us < least) {
+          least = us;
+          best = p;
+        }
       }
     }
   }
@@ -113,43 +157,83 @@ ProductPlan plan_product(int type, int64_t m, int64_t n, int64_t k, bool ring) {
 }
 
 // The gradient's products dX (m x k, contraction n) and dW (n x k, contraction m) share a tile and a
-// launch: the CUs' stages are those of both, and at least the longer product's.
+// launch, the one with the longer contraction first.
 void plan_gradient(int type, int64_t m, int64_t k, int64_t n, bool want_dx, bool want_dw, bool ring, ProductPlan* dx,
                    ProductPlan* dw) {
   dx->k_per_split = dw->k_per_split = kTileDepth;
   if (m == 0 || k == 0 || n == 0) return;
+  const bool dw_first = m > n;
   double least = 0;
   for (int tile : {64, 128, 256}) {
     if (!ring ? tile != 64 : (tile == 256 && type == kF32)) continue;
-    for (int64_t sx : kSplits) {
-      ProductCost cx, cw;
-      if (want_dx ? !product_cost(type, tile, sx, m, k, n, &cx) : sx > 1) continue;
-      for (int64_t sw : kSplits) {
-        if (want_dw ? !product_cost(type, tile, sw, n, k, m, &cw) : sw > 1) continue;
-        const int64_t groups = cx.groups + cw.groups, rounds = cdiv(groups, kComputeUnits);
-        const double mean = (double)(cx.groups * cx.stages + cw.groups * cw.stages) / groups;
-        const double longest = (double)std::max(cx.stages, cw.stages) * stage_us(type, tile, 1);
-        const double us = std::max(longest, mean * stage_us(type, tile, rounds)) + cx.extra_us + cw.extra_us +
-                          (sx > 1 || sw > 1 ? 2.0 : 0.0);
-        if (least == 0 || us < least) {
-          least = us;
-          if (want_dx) set_product(dx, ring ? tile : 0, sx, cx, m, k);
-          if (want_dw) set_product(dw, ring ? tile : 0, sw, cw, n, k);
+    const int64_t tx = want_dx ? cdiv(m, tile) * cdiv(k, tile) : 0, tw = want_dw ? cdiv(n, tile) * cdiv(k, tile) : 0;
+    // of the product that runs last, those tiles that its last, incomplete round would hold
+    const int64_t last = dw_first ? tx : tw, full = (tx + tw) / kComputeUnits * kComputeUnits - (tx + tw - last);
+    for (int rest = 0; rest < (ring && full > 0 && full < last ? 2 : 1); ++rest)
+      for (int64_t sx : kSplits) {
+        ProductPlan px, pw;
+        if (!want_dx ? sx > 1 : !set_product(&px, type, tile, ring, rest && dw_first ? full : 0, sx, m, k, n)) continue;
+        for (int64_t sw : kSplits) {
+          if (rest && (dw_first ? sx : sw) == 1) continue;
+          if (!want_dw ? sw > 1 : !set_product(&pw, type, tile, ring, rest && !dw_first ? full : 0, sw, n, k, m)) continue;
+          Jobs jobs[4];
+          double us = 0;
+          const auto both = [&](double stage) {
+            us = sx > 1 || sw > 1 ? kFinishUs : 0.0;
+            if (want_dx) us += product_jobs(px, type, tile, m, k, n, stage, jobs + (dw_first ? 2 : 0));
+            if (want_dw) us += product_jobs(pw, type, tile, n, k, m, stage, jobs + (dw_first ? 0 : 2));
+          };
+          both(0.0);
+          const int64_t groups = jobs[0].count + jobs[1].count + jobs[2].count + jobs[3].count;
+          const int64_t on_cu = std::max<int64_t>(1, std::min<int64_t>(residents(tile), cdiv(groups, kComputeUnits)));
+          both(stage_us(type, tile, on_cu));
+          us += makespan(kComputeUnits * on_cu, jobs, 4);
+          if (least == 0 || us < least) {
+            least = us;
+            *dx = want_dx ? px : ProductPlan{};
+            *dw = want_dw ? pw : ProductPlan{};
+          }
         }
       }
-    }
   }
 }
+
+// Plans of the shapes of a thread's latest calls: the search takes 10 to 100 us, a call 5.
+template <typename Plan>
+struct PlanCache {
+  struct Entry {
+    int64_t key[4] = {-1, -1, -1, -1};
+    Plan plan;
+  } entries[64];
+  template <typename Make>
+  const Plan& get(int64_t m, int64_t k, int64_t n, int64_t what, Make make) {
+    const uint64_t h = (uint64_t)m * 0x9E3779B97F4A7C15u ^ (uint64_t)k * 0xC2B2AE3D27D4EB4Fu ^ (uint64_t)n * 0x165667B19E3779F9u ^
+                       (uint64_t)what * 0x27D4EB2F165667C5u;
+    Entry& e = entries[(h >> 40) % 64];
+    const int64_t key[4] = {m, k, n, what};
+    if (!std::equal(key, key + 4, e.key)) {
+      e.plan = make();
+      std::copy(key, key + 4, e.key);
+    }
+    return e.plan;
+  }
+};
 
 bool product_fits(int64_t m, int64_t n) {
   return cdiv(m, 64) * cdiv(n, 64) <= kMaxGroups;
 }
 
+void take_plan(ProductArgs* a, const ProductPlan& p, void* ws) {
+  a->tile = p.tile;
+  a->whole = p.tile ? p.whole : 0;
+  a->splits = (int32_t)p.splits;
+  a->k_per_split = p.k_per_split;
+  a->partial = static_cast<float*>(ws);
+}
+
 hipError_t run_layer(ProductArgs a, const ProductPlan& p, void* ws, hipStream_t s) {
-  a.splits = (int32_t)p.splits;
-  a.k_per_split = p.k_per_split;
-  a.partial = static_cast<float*>(ws);
-  hipError_t e = p.tile ? launch_layer_ring(a, p.tile, s) : launch_layer_tile(a, s);
+  take_plan(&a, p, ws);
+  hipError_t e = p.tile ? launch_layer_ring(a, s) : launch_layer_tile(a, s);
   if (e == hipSuccess && a.splits > 1) e = launch_product_finish(a, s);
   return e;
 }
@@ -178,7 +262,7 @@ struct LinearPlan {
   size_t x_off = 0, w_off = 0, partial_off = 0, bytes = 0;
 };
 
-LinearPlan plan_linear(int type, int64_t m, int64_t k, int64_t n, bool x_whole, bool w_whole) {
+LinearPlan make_linear_plan(int type, int64_t m, int64_t k, int64_t n, bool x_whole, bool w_whole) {
   LinearPlan p;
   const int es = elem_size(type);
   if (m <= kFewRows) {
@@ -216,6 +300,11 @@ LinearPlan plan_linear(int type, int64_t m, int64_t k, int64_t n, bool x_whole, 
   return p;
 }
 
+const LinearPlan& plan_linear(int type, int64_t m, int64_t k, int64_t n, bool x_whole, bool w_whole) {
+  thread_local PlanCache<LinearPlan> cache;
+  return cache.get(m, k, n, type * 4 + x_whole * 2 + w_whole, [&] { return make_linear_plan(type, m, k, n, x_whole, w_whole); });
+}
+
 xtvxy_status linear_workspace(int type, int64_t m, int64_t k, int64_t n, int aligned16, size_t* bytes) {
   if (!bytes) return XTVXY_ERROR_NULL_POINTER;
   if (m < 0 || k < 0 || n < 0) return XTVXY_ERROR_INVALID_VALUE;
@@ -251,7 +340,7 @@ xtvxy_status linear_impl(int type, int64_t m, int64_t k, int64_t n, const void* 
       overlap(mp, mb) || overlap(mp, mr))
     return XTVXY_ERROR_ALIASING;
   if (residual && !(residual == out && ldr == ldo) && overlap(mo, mr)) return XTVXY_ERROR_ALIASING;
-  const LinearPlan plan = plan_linear(type, m, k, n, whole_chunks(mx), whole_chunks(mw));
+  const LinearPlan& plan = plan_linear(type, m, k, n, whole_chunks(mx), whole_chunks(mw));
   if (plan.bytes > 0 && (!ws || ws_bytes < plan.bytes || reinterpret_cast<uintptr_t>(ws) % kAlign != 0))
     return XTVXY_ERROR_WORKSPACE;
   char* base = static_cast<char*>(ws);
@@ -300,8 +389,8 @@ struct BackwardPlan {
   size_t x_off = 0, w_off = 0, d_off = 0, sums_off = 0, dx_off = 0, dw_off = 0, bytes = 0;
 };
 
-BackwardPlan plan_backward(int type, int64_t m, int64_t k, int64_t n, int act, bool g_whole, bool x_whole, bool w_whole,
-                           bool want_dx, bool want_dw) {
+BackwardPlan make_backward_plan(int type, int64_t m, int64_t k, int64_t n, int act, bool g_whole, bool x_whole, bool w_whole,
+                                bool want_dx, bool want_dw) {
   BackwardPlan p;
   const int es = elem_size(type);
   want_dx = want_dx && k > 0;
@@ -322,7 +411,17 @@ BackwardPlan plan_backward(int type, int64_t m, int64_t k, int64_t n, int act, b
   const int64_t groups = std::max<int64_t>(1, 4 * kComputeUnits / column_groups);
   p.rows_per_group = std::max<int64_t>(narrow ? 32 : 8, cdiv(m, groups));
   p.groups = std::max<int64_t>(1, cdiv(m, p.rows_per_group));
-  plan_gradient(type, m, k, n, want_dx, want_dw, ring, &p.dx, &p.dw);
+  struct Products {
+    ProductPlan dx, dw;
+  };
+  thread_local PlanCache<Products> cache;  // the search does not depend on the matrices' alignment
+  const Products& products = cache.get(m, k, n, type * 8 + want_dx * 4 + want_dw * 2 + ring, [&] {
+    Products both;
+    plan_gradient(type, m, k, n, want_dx, want_dw, ring, &both.dx, &both.dw);
+    return both;
+  });
+  p.dx = products.dx;
+  p.dw = products.dw;
   const auto take = [&](bool want, size_t bytes) {
     const size_t at = p.bytes;
     if (want) p.bytes += bytes;
@@ -335,6 +434,15 @@ BackwardPlan plan_backward(int type, int64_t m, int64_t k, int64_t n, int act, b
   p.dx_off = take(want_dx, p.dx.bytes);
   p.dw_off = take(want_dw, p.dw.bytes);
   return p;
+}
+
+const BackwardPlan& plan_backward(int type, int64_t m, int64_t k, int64_t n, int act, bool g_whole, bool x_whole,
+                                  bool w_whole, bool want_dx, bool want_dw) {
+  thread_local PlanCache<BackwardPlan> cache;
+  const int64_t what = (((((type * 8 + act) * 2 + g_whole) * 2 + x_whole) * 2 + w_whole) * 2 + want_dx) * 2 + want_dw;
+  return cache.get(m, k, n, what, [&] {
+    return make_backward_plan(type, m, k, n, act, g_whole, x_whole, w_whole, want_dx, want_dw);
+  });
 }
 
 bool backward_fits(int64_t m, int64_t k, int64_t n) {
@@ -355,7 +463,9 @@ xtvxy_status backward_workspace(int type, int64_t m, int64_t k, int64_t n, int a
   for (int c = 0; c < 8; ++c) {
     const bool g = c & 1, x = c & 2, w = c & 4;
     if (aligned16 && !(g == nc && x == kc && w == kc)) continue;
-    *bytes = std::max(*bytes, plan_backward(type, m, k, n, act, nc && g, kc && x, kc && w, true, true).bytes);
+    // a product alone may be split further than the two together
+    for (int want = 1; want < 4; ++want)
+      *bytes = std::max(*bytes, make_backward_plan(type, m, k, n, act, nc && g, kc && x, kc && w, want & 1, want & 2).bytes);
   }
   return XTVXY_SUCCESS;
 }
@@ -382,7 +492,7 @@ xtvxy_status backward_impl(int type, int64_t m, int64_t k, int64_t n, const void
       if (overlap(*o, *i)) return XTVXY_ERROR_ALIASING;
   if (overlap(mdx, mdw) || overlap(mdx, mdb) || overlap(mdw, mdb)) return XTVXY_ERROR_ALIASING;
 
-  const BackwardPlan p = plan_backward(type, m, k, n, act, whole_chunks(mg), whole_chunks(mx), whole_chunks(mw),
+  const BackwardPlan& p = plan_backward(type, m, k, n, act, whole_chunks(mg), whole_chunks(mx), whole_chunks(mw),
                                        dX != nullptr, dW != nullptr);
   if (reads && p.bytes > 0 && (!ws || ws_bytes < p.bytes || reinterpret_cast<uintptr_t>(ws) % kAlign != 0))
     return XTVXY_ERROR_WORKSPACE;
@@ -397,9 +507,7 @@ xtvxy_status backward_impl(int type, int64_t m, int64_t k, int64_t n, const void
     a.dx.m = m;
     a.dx.n = k;
     a.dx.k = n;
-    a.dx.splits = (int32_t)p.dx.splits;
-    a.dx.k_per_split = p.dx.k_per_split;
-    a.dx.partial = reinterpret_cast<float*>(base + p.dx_off);
+    take_plan(&a.dx, p.dx, base + p.dx_off);
     a.dx.e = {nullptr, nullptr, 0, nullptr, 0, dX, lddx, XTVXY_ACT_NONE};
   }
   if (dW && k > 0) {
@@ -408,12 +516,11 @@ xtvxy_status backward_impl(int type, int64_t m, int64_t k, int64_t n, const void
     a.dw.m = n;
     a.dw.n = k;
     a.dw.k = m;
-    a.dw.splits = (int32_t)p.dw.splits;
-    a.dw.k_per_split = p.dw.k_per_split;
-    a.dw.partial = reinterpret_cast<float*>(base + p.dw_off);
+    take_plan(&a.dw, p.dw, base + p.dw_off);
     a.dw.e = {nullptr, nullptr, 0, nullptr, 0, dW, lddw, XTVXY_ACT_NONE};
   }
   a.dx.type = a.dw.type = type;
+  a.dw_first = m > n;
   a.dx.A = a.dw.A = G;
   a.dx.lda = a.dw.lda = ldg;
   if (!reads) {  // no rows or no outputs: db is zero, and so are the products' empty sums

@@ -32,9 +32,15 @@ struct ProductArgs {
   int64_t m, n, k;
   int32_t type;
   int32_t a_contraction_major, b_contraction_major;
-  int32_t splits;           // parts of the contraction, each with sums of its own in `partial`
+  int32_t tile;             // edge of the ring kernel's tiles, 0 for the other kernels
+  // The first `whole` tiles (in the order of tile_of) run over the whole contraction; the others are
+  // split into parts of it, each with sums of its own in `partial`: [splits][other tiles][tile][tile].
+  // The other kernels split everything (whole 0): [splits][m][n].
+  int32_t splits;
+  int64_t whole;
   int64_t k_per_split;      // a multiple of the tile's depth; splits * k_per_split >= k
-  float* partial;           // [splits][m][n] when splits > 1
+  float* partial;           // used when splits > 1
+  __host__ __device__ int64_t tiles() const { return ((m + tile - 1) / tile) * ((n + tile - 1) / tile); }
   LinearEpilogue e;
 };
 
@@ -44,9 +50,9 @@ hipError_t launch_layer_tile(const ProductArgs& a, hipStream_t s);
 
 // Operands with 16-byte aligned rows of at most kRingMaxPitch bytes; what lies between a row's end and
 // the next multiple of 16 bytes is zero where the contraction is contiguous, and readable where it is
-// not. tile: 64, 128, or 256 (16-bit elements). k_per_split is a multiple of 32.
+// not. a.tile: 64, 128, or 256 (16-bit elements). k_per_split is a multiple of 32.
 constexpr int64_t kRingMaxPitch = (int64_t)1 << 22;  // 256 rows stay within 32-bit offsets
-hipError_t launch_layer_ring(const ProductArgs& a, int tile, hipStream_t s);
+hipError_t launch_layer_ring(const ProductArgs& a, hipStream_t s);
 
 // The gradient's products dX = d W (d contraction-contiguous, W strided) and dW = d^T X (both
 // strided), either with m == 0 where it is not wanted, and db[j] = the sum over sum_rows of
@@ -54,6 +60,7 @@ hipError_t launch_layer_ring(const ProductArgs& a, int tile, hipStream_t s);
 struct GradientArgs {
   ProductArgs dx, dw;
   uint32_t dx_groups, dw_groups;  // workgroups (set by the launcher)
+  int32_t dw_first;               // the ring kernel starts dw's workgroups first
   const float* sums;
   int64_t sum_rows, n;
   float* db;

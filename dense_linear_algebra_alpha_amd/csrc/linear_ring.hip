@@ -24,6 +24,7 @@ namespace xtvxy {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kRing = 4;     // LDS slots (eight gain nothing, not even for a lone 64 x 64 workgroup)
 constexpr uint32_t kNowhere = 0xc0000000u;  // beyond any tile's extent: such a load returns zero
 // Four loads share a setting of their LDS address: an instruction's own offset (up to 4095) counts for
 // memory and LDS alike. Descriptors begin this far before their data, so that taking those offsets from
@@ -212,19 +213,6 @@ __device__ __forceinline__ void mfma_in_place(f32x4& acc, f32x4 a, f32x4 b, int 
 // The s_waitcnt operand that waits until at most `vm` memory and `lgkm` LDS operations are under way.
 constexpr int waitcnt(int vm, int lgkm) { return (vm & 15) | (7 << 4) | (lgkm << 8) | ((vm >> 4) << 14); }
 
-// Tile of a workgroup: workgroups go to the 8 XCDs in turn, each of which has an L2 of its own, so
-// each XCD takes a contiguous range of the tiles, ordered in bands of kBand tile rows.
-__device__ __forceinline__ void tile_of(uint32_t id, int64_t tiles_m, int64_t tiles_n, int64_t* tm, int64_t* tn) {
-  constexpr int kXcds = 8, kBand = 4;
-  const uint32_t tiles = (uint32_t)(tiles_m * tiles_n);
-  const uint32_t x = id % kXcds, q = tiles / kXcds, r = tiles % kXcds;
-  const uint32_t t = x * q + (x < r ? x : r) + id / kXcds;
-  const uint32_t band_tiles = kBand * (uint32_t)tiles_n, band = t / band_tiles, in = t % band_tiles;
-  const uint32_t rows = (uint32_t)tiles_m - band * kBand < kBand ? (uint32_t)tiles_m - band * kBand : kBand;
-  *tm = band * kBand + in % rows;
-  *tn = in / rows;
-}
-
 // Where the four columns from 4 c on of a staged row lie (in floats): the rows' pitch is a multiple of
 // the banks, so the chunks are permuted by the row.
 template <int WN>
@@ -310,18 +298,14 @@ __device__ __forceinline__ void epilogue_any(const float* area, const ProductArg
   }
 }
 
-// The staged rows as one part of a split product.
-template <int WN, int kRows>
-__device__ __forceinline__ void partial_rows(const float* area, const ProductArgs& a, uint32_t split, int64_t i0, int64_t j0) {
+// The staged rows as one part of a split tile: row-major in the tile's own area.
+template <int WN, int kRows, int BN>
+__device__ __forceinline__ void partial_rows(const float* area, float* p) {
   constexpr int kLanes = WN / 4, kStep = 64 / kLanes;
   const int lane = threadIdx.x & 63, c4 = lane % kLanes;
-  const int64_t j = j0 + c4 * 4;
-  if (j >= a.n) return;
-  const int count = a.n - j >= 4 ? 4 : (int)(a.n - j);
-  const int rows = a.m - i0 >= kRows ? kRows : (int)(a.m - i0);
-  float* p = a.partial + ((int64_t)split * a.m + i0) * a.n + j;
-  for (int row = lane / kLanes; row < rows; row += kStep)
-    store4<float>(p + row * a.n, *reinterpret_cast<const f32x4*>(area + staged_at<WN>(row, c4)), count);
+#pragma unroll 4
+  for (int row = lane / kLanes; row < kRows; row += kStep)
+    *reinterpret_cast<f32x4*>(p + row * BN + c4 * 4) = *reinterpret_cast<const f32x4*>(area + staged_at<WN>(row, c4));
 }
 
 // A wavefront's sums in registers: 16 x 16 tiles of the matrix instruction. stage() writes
@@ -344,10 +328,38 @@ struct Sums16 {
           *reinterpret_cast<f32x4*>(area + staged_at<WN>(x * 16 % rows + r, y * 4 + g)) = acc[x][y];
   }
 };
-// The end of a tile (kPlain: of the gradient's products, which have no epilogue): its sums through LDS to memory. `ring` holds at least 256 (BM + BN) bytes.
+// A tile's place in its product.
+struct TilePlace {
+  float* part;  // where its sums go if it is one part of a split tile, else null
+  int64_t i0, j0, k0;
+  int32_t steps;
+};
+template <int BM, int BN>
+__device__ __forceinline__ TilePlace place_of(const ProductArgs& a, uint32_t id) {
+  TilePlace p;
+  int64_t tm, tn, k_end = a.k;
+  const uint32_t whole = (uint32_t)a.whole;
+  p.part = nullptr;
+  p.k0 = 0;
+  if (id < whole) {
+    tile_of(a, spread(id, whole), &tm, &tn);
+  } else {
+    const uint32_t rest = (uint32_t)a.tiles() - whole, split = (id - whole) / rest, r = (id - whole) % rest;
+    tile_of(a, whole + spread(r, rest), &tm, &tn);
+    if (a.splits > 1) p.part = a.partial + ((int64_t)split * rest + r) * (BM * BN);
+    p.k0 = (int64_t)split * a.k_per_split;
+    k_end = p.k0 + a.k_per_split < a.k ? p.k0 + a.k_per_split : a.k;
+  }
+  p.i0 = tm * BM;
+  p.j0 = tn * BN;
+  p.steps = (int32_t)(k_end - p.k0);
+  return p;
+}
+
+// The end of a tile (kPlain: of the gradient's products, which have no epilogue): its sums through LDS
+// to memory. `ring` holds at least 256 (BM + BN) bytes.
 template <typename T, int BM, int BN, bool kPlain, typename S>
-__device__ __forceinline__ void finish_tile(const ProductArgs& a, uint8_t* ring, S& sums, uint32_t split, int64_t i0,
-                                            int64_t j0) {
+__device__ __forceinline__ void finish_tile(const ProductArgs& a, uint8_t* ring, S& sums, const TilePlace& p) {
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wi = (wave >> 1) * (BM / 2), wj = (wave & 1) * (BN / 2);
   // no load to LDS outlives the workgroup, and the last products are through before their sums are read
@@ -359,43 +371,21 @@ __device__ __forceinline__ void finish_tile(const ProductArgs& a, uint8_t* ring,
   // columns and a row's lanes its whole width: 16-byte accesses of out, pre and residual.
   constexpr int WN = BN / 2, kRows = BM / 2 < 64 ? BM / 2 : 64;
   constexpr int kArea = kRows * WN * 4;  // bytes of a wavefront
-  static_assert(4 * kArea <= 4 * (BM + BN) * 64, "the staged sums fit four slots");
+  static_assert(4 * kArea <= kRing * (BM + BN) * 64, "the staged sums fit the ring");
   float* area = reinterpret_cast<float*>(ring + wave * kArea);
 #pragma unroll
   for (int part = 0; part < BM / 2 / kRows; ++part) {
     sums.template stage<WN>(area, part, kRows);
     __builtin_amdgcn_wave_barrier();
-    const int64_t i = i0 + wi + part * kRows, j = j0 + wj;
-    if (a.splits > 1)
-      partial_rows<WN, kRows>(area, a, split, i, j);
+    const int i = wi + part * kRows;
+    if (p.part)
+      partial_rows<WN, kRows, BN>(area, p.part + i * BN + wj);
     else if (kPlain)
-      epilogue_rows<T, XTVXY_ACT_NONE, WN, kRows, true>(area, a, i, j);
+      epilogue_rows<T, XTVXY_ACT_NONE, WN, kRows, true>(area, a, p.i0 + i, p.j0 + wj);
     else
-      epilogue_any<T, WN, kRows>(area, a, i, j);
+      epilogue_any<T, WN, kRows>(area, a, p.i0 + i, p.j0 + wj);
     __builtin_amdgcn_wave_barrier();
   }
-}
-
-// A tile's place in its product.
-struct TilePlace {
-  uint32_t split;
-  int64_t i0, j0, k0;
-  int32_t steps;
-};
-template <int BM, int BN>
-__device__ __forceinline__ TilePlace place_of(const ProductArgs& a, uint32_t id) {
-  const int64_t tiles_m = (a.m + BM - 1) / BM, tiles_n = (a.n + BN - 1) / BN;
-  const uint32_t tiles = (uint32_t)(tiles_m * tiles_n);
-  TilePlace p;
-  p.split = id / tiles;
-  int64_t tm, tn;
-  tile_of(id % tiles, tiles_m, tiles_n, &tm, &tn);
-  p.i0 = tm * BM;
-  p.j0 = tn * BN;
-  p.k0 = (int64_t)p.split * a.k_per_split;
-  const int64_t k_end = p.k0 + a.k_per_split < a.k ? p.k0 + a.k_per_split : a.k;
-  p.steps = (int32_t)(k_end - p.k0);
-  return p;
 }
 
 // Issue op(0) .. op(ops - 1) between product(0) .. product(products - 1), spread evenly. With one
@@ -509,12 +499,12 @@ __device__ __forceinline__ void ring_tile_halves(const ProductArgs& a, uint32_t 
     ob.advance();
     left -= kStage;
   }
-  finish_tile<T, BM, BN, kBMajor>(a, ring, sums, p.split, p.i0, p.j0);
+  finish_tile<T, BM, BN, kBMajor>(a, ring, sums, p);
 }
 
 // The same for smaller tiles and fp32: stages of 64 bytes of a row, a ring of four slots. While the
 // products of stage t run, stage t + 1's fragments are read and stages t + 2 .. t + 4 are on their way.
-template <typename T, int BM, int BN, int kRing, bool kAMajor, bool kBMajor>
+template <typename T, int BM, int BN, bool kAMajor, bool kBMajor>
 __device__ __forceinline__ void ring_tile(const ProductArgs& a, uint32_t id, uint8_t* ring) {
   typedef typename Stage<T>::frag frag;
   typedef Operand<T, BM, kAMajor, 1> OpA;
@@ -591,81 +581,61 @@ __device__ __forceinline__ void ring_tile(const ProductArgs& a, uint32_t id, uin
     stage(0, t & (kRing - 1));
     stage(1, (t + 1) & (kRing - 1));
   }
-  finish_tile<T, BM, BN, kBMajor>(a, ring, sums, p.split, p.i0, p.j0);
+  finish_tile<T, BM, BN, kBMajor>(a, ring, sums, p);
 }
 
-// LDS slots of a launch: where it is few workgroups, those that a CU can hold with eight slots each (two
-// of 64 x 64, one of 128 x 128), a load has seven stages to arrive instead of three. A lone 64 x 64
-// workgroup's stage then takes DEEP64 us instead of 0.18, a lone 128 x 128 one's DEEP128 instead of 0.33.
-constexpr int kSlots = 4, kDeepSlots = 8;
-constexpr int ring_bytes(int tile, int slots) { return (tile == 256 ? 4 : slots) * 2 * tile * 64; }
-bool few_groups(int tile, int64_t groups) { return groups <= 256 * (tile == 64 ? 2 : 1); }
+constexpr int ring_bytes(int tile) { return kRing * 2 * tile * 64; }
 
-template <typename T, int TILE, int RING>
-__global__ __launch_bounds__(kThreads, TILE > 128 || RING * TILE > 512 ? 1 : 2) void layer_ring(ProductArgs a) {
-  __shared__ __align__(1024) uint8_t ring[ring_bytes(TILE, RING)];
+template <typename T, int TILE>
+__global__ __launch_bounds__(kThreads, TILE > 128 ? 1 : 2) void layer_ring(ProductArgs a) {
+  __shared__ __align__(1024) uint8_t ring[ring_bytes(TILE)];
   if constexpr (TILE == 256) ring_tile_halves<T, TILE, TILE, false, false>(a, blockIdx.x, ring);
-  else ring_tile<T, TILE, TILE, RING, false, false>(a, blockIdx.x, ring);
+  else ring_tile<T, TILE, TILE, false, false>(a, blockIdx.x, ring);
 }
 
-// The gradient's two products in one launch (the second's workgroups fill the CUs that the first's last
-// round leaves), and the sum of the row groups' column sums.
-template <typename T, int TILE, int RING>
-__global__ __launch_bounds__(kThreads, TILE > 128 || RING * TILE > 512 ? 1 : 2) void gradient_ring(GradientArgs a) {
-  __shared__ __align__(1024) uint8_t ring[ring_bytes(TILE, RING)];
+template <typename T, int TILE, bool kAMajor>
+__device__ __forceinline__ void gradient_product(const ProductArgs& a, uint32_t id, uint8_t* ring) {
+  if constexpr (TILE == 256) ring_tile_halves<T, TILE, TILE, kAMajor, true>(a, id, ring);
+  else ring_tile<T, TILE, TILE, kAMajor, true>(a, id, ring);
+}
+
+// The gradient's two products in one launch, the one with the longer contraction first (the other's
+// workgroups fill the CUs that its last round leaves), and the sum of the row groups' column sums.
+template <typename T, int TILE>
+__global__ __launch_bounds__(kThreads, TILE > 128 ? 1 : 2) void gradient_ring(GradientArgs a) {
+  __shared__ __align__(1024) uint8_t ring[ring_bytes(TILE)];
+  const uint32_t products = a.dx_groups + a.dw_groups;
   uint32_t id = blockIdx.x;
-  if constexpr (TILE == 256) {
-    if (id < a.dx_groups) return ring_tile_halves<T, TILE, TILE, false, true>(a.dx, id, ring);
-    id -= a.dx_groups;
-    if (id < a.dw_groups) return ring_tile_halves<T, TILE, TILE, true, true>(a.dw, id, ring);
-  } else {
-    if (id < a.dx_groups) return ring_tile<T, TILE, TILE, RING, false, true>(a.dx, id, ring);
-    id -= a.dx_groups;
-    if (id < a.dw_groups) return ring_tile<T, TILE, TILE, RING, true, true>(a.dw, id, ring);
-  }
-  column_sum(a.sums, a.sum_rows, a.n, a.db, id - a.dw_groups, reinterpret_cast<double*>(ring));
+  if (id >= products) return column_sum(a.sums, a.sum_rows, a.n, a.db, id - products, reinterpret_cast<double*>(ring));
+  if (a.dw_first) id = id < a.dw_groups ? id + a.dx_groups : id - a.dw_groups;
+  if (id < a.dx_groups) gradient_product<T, TILE, false>(a.dx, id, ring);
+  else gradient_product<T, TILE, true>(a.dw, id - a.dx_groups, ring);
 }
 
-uint32_t groups_of(const ProductArgs& a, int tile) {
-  return (uint32_t)(((a.m + tile - 1) / tile) * ((a.n + tile - 1) / tile) * a.splits);
-}
+uint32_t groups_of(const ProductArgs& a) { return (uint32_t)(a.whole + (a.tiles() - a.whole) * a.splits); }
 
 template <typename T, int TILE>
 hipError_t layer_for(const ProductArgs& a, hipStream_t s) {
-  const uint32_t groups = groups_of(a, TILE);
-  if constexpr (TILE < 256) {
-    if (few_groups(TILE, groups)) {
-      layer_ring<T, TILE, kDeepSlots><<<groups, kThreads, 0, s>>>(a);
-      return hipGetLastError();
-    }
-  }
-  layer_ring<T, TILE, kSlots><<<groups, kThreads, 0, s>>>(a);
+  layer_ring<T, TILE><<<groups_of(a), kThreads, 0, s>>>(a);
   return hipGetLastError();
 }
 
 template <typename T, int TILE>
 hipError_t gradient_for(GradientArgs a, hipStream_t s) {
-  a.dx_groups = a.dx.m > 0 ? groups_of(a.dx, TILE) : 0;
-  a.dw_groups = a.dw.m > 0 ? groups_of(a.dw, TILE) : 0;
+  a.dx_groups = a.dx.m > 0 ? groups_of(a.dx) : 0;
+  a.dw_groups = a.dw.m > 0 ? groups_of(a.dw) : 0;
   const uint32_t columns = a.db ? (uint32_t)((a.n + kSumColumns - 1) / kSumColumns) : 0;
-  const uint32_t groups = a.dx_groups + a.dw_groups + columns;
-  if (groups == 0) return hipSuccess;
-  if constexpr (TILE < 256) {
-    if (few_groups(TILE, a.dx_groups + a.dw_groups)) {
-      gradient_ring<T, TILE, kDeepSlots><<<groups, kThreads, 0, s>>>(a);
-      return hipGetLastError();
-    }
-  }
-  gradient_ring<T, TILE, kSlots><<<groups, kThreads, 0, s>>>(a);
+  if (a.dx_groups + a.dw_groups + columns == 0) return hipSuccess;
+  gradient_ring<T, TILE><<<a.dx_groups + a.dw_groups + columns, kThreads, 0, s>>>(a);
   return hipGetLastError();
 }
 
 template <typename T>
-hipError_t layer_type(const ProductArgs& a, int tile, hipStream_t s) {
+hipError_t layer_type(const ProductArgs& a, hipStream_t s) {
   if constexpr (sizeof(T) == 2) {
-    if (tile == 256) return layer_for<T, 256>(a, s);
+    if (a.tile == 256) return layer_for<T, 256>(a, s);
   }
-  if (tile == 128) return layer_for<T, 128>(a, s);
+  if (a.tile == 128) return layer_for<T, 128>(a, s);
   return layer_for<T, 64>(a, s);
 }
 
@@ -680,10 +650,10 @@ hipError_t gradient_type(const GradientArgs& a, int tile, hipStream_t s) {
 
 }  // namespace
 
-hipError_t launch_layer_ring(const ProductArgs& a, int tile, hipStream_t s) {
-  if (a.type == kBf16) return layer_type<__bf16>(a, tile, s);
-  if (a.type == kF16) return layer_type<_Float16>(a, tile, s);
-  return layer_type<float>(a, tile, s);
+hipError_t launch_layer_ring(const ProductArgs& a, hipStream_t s) {
+  if (a.type == kBf16) return layer_type<__bf16>(a, s);
+  if (a.type == kF16) return layer_type<_Float16>(a, s);
+  return layer_type<float>(a, s);
 }
 
 hipError_t launch_gradient_ring(const GradientArgs& a, int type, int tile, hipStream_t s) {

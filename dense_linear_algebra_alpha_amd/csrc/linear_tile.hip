@@ -168,15 +168,32 @@ __global__ __launch_bounds__(kThreads) void gradient_tile(GradientArgs a) {
 // in ascending order (its loads are under way together), the lanes' sums join in a fixed order.
 template <typename T>
 __device__ __forceinline__ void finish_quad(const ProductArgs& a, int64_t at) {
-  const int64_t quads = (a.n + 3) / 4, q = at >> 2;
   const int part = (int)(at & 3);
-  const bool exists = q < a.m * quads;
-  const int64_t i = exists ? q / quads : 0, j = exists ? (q % quads) * 4 : 0;
+  int64_t q = at >> 2, i, j, stride;
+  const float* p = a.partial;
+  if (a.tile) {  // split tiles in areas of their own
+    const int edge = 31 - __builtin_clz(a.tile), r = (int)(q >> (2 * edge - 2));
+    const int row = (int)(q >> (edge - 2)) & (a.tile - 1), quad = (int)q & (a.tile / 4 - 1);
+    const uint32_t rest = (uint32_t)(a.tiles() - a.whole);
+    int64_t tm, tn;
+    tile_of(a, (uint32_t)a.whole + spread((uint32_t)r, rest), &tm, &tn);
+    i = tm * a.tile + row;
+    j = tn * a.tile + quad * 4;
+    p += q * 4;
+    stride = (int64_t)rest << (2 * edge);
+  } else {
+    const int64_t quads = (a.n + 3) / 4;
+    i = q / quads;
+    j = (q - i * quads) * 4;
+    p += i * a.n + j;
+    stride = a.m * a.n;
+  }
+  const bool exists = i < a.m && j < a.n;
   const int count = a.n - j >= 4 ? 4 : (int)(a.n - j);
   f32x4 z = {0.0f, 0.0f, 0.0f, 0.0f};
   if (exists) {
 #pragma unroll 4
-    for (int s = part; s < a.splits; s += 4) z += load4<float>(a.partial + ((int64_t)s * a.m + i) * a.n + j, count);
+    for (int s = part; s < a.splits; s += 4) z += load4<float>(p + s * stride, count);
   }
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
@@ -323,7 +340,10 @@ hipError_t slope_for(const SlopeArgs& a, hipStream_t s) {
 uint32_t tile_groups(const ProductArgs& a) {
   return (uint32_t)(((a.m + kTile - 1) / kTile) * ((a.n + kTile - 1) / kTile) * a.splits);
 }
-uint32_t quad_groups(const ProductArgs& a) { return (uint32_t)((a.m * ((a.n + 3) / 4) * 4 + kThreads - 1) / kThreads); }
+uint32_t quad_groups(const ProductArgs& a) {
+  const int64_t quads = a.tile ? (a.tiles() - a.whole) * a.tile * (a.tile / 4) : a.m * ((a.n + 3) / 4);
+  return (uint32_t)((quads * 4 + kThreads - 1) / kThreads);
+}
 
 hipError_t launch_layer_tile(const ProductArgs& a, hipStream_t s) {
   if (a.type == kBf16) layer_tile<__bf16><<<tile_groups(a), kThreads, 0, s>>>(a);

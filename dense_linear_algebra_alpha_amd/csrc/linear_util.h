@@ -224,6 +224,25 @@ __device__ __forceinline__ void epilogue4(const LinearEpilogue& e, int64_t i, in
   store4<T>(static_cast<T*>(e.out) + i * e.ldo + j, y, count);
 }
 
+// Place of the t-th tile of a product: tiles are ordered in bands of kBand tile rows, so that
+// neighbours in the order share operands.
+__device__ __forceinline__ void tile_of(const ProductArgs& a, uint32_t t, int64_t* tm, int64_t* tn) {
+  constexpr uint32_t kBand = 4;
+  const uint32_t tiles_m = (uint32_t)((a.m + a.tile - 1) / a.tile), tiles_n = (uint32_t)((a.n + a.tile - 1) / a.tile);
+  const uint32_t band_tiles = kBand * tiles_n, band = t / band_tiles, in = t % band_tiles;
+  const uint32_t rows = tiles_m - band * kBand < kBand ? tiles_m - band * kBand : kBand;
+  *tm = band * kBand + in % rows;
+  *tn = in / rows;
+}
+
+// Workgroups go to the 8 XCDs in turn, each of which has an L2 of its own: of `count` positions, workgroup
+// id takes one of its XCD's contiguous range.
+__device__ __forceinline__ uint32_t spread(uint32_t id, uint32_t count) {
+  constexpr uint32_t kXcds = 8;
+  const uint32_t x = id % kXcds, q = count / kXcds, r = count % kXcds;
+  return x * q + (x < r ? x : r) + id / kXcds;
+}
+
 // db[j] = the sum of sums[.][n] over its rows for the 16 columns of workgroup `group` (256 threads): a
 // thread adds every 16th row of a column, the 16 partial sums join in LDS (2 KiB), in fp64 and in a
 // fixed order. 16 loads of a column are under way at once; one thread per column would wait for each.
