@@ -51,29 +51,36 @@ struct ProductPlan {
   size_t bytes = 0;  // partial sums
 };
 
-// The estimate of a launch's time: its workgroups are jobs on slots, 1 (256), 2 (128) or 5 (64) of them on
-// each CU. A job takes its stages of 32 steps (fp32: 16) and a start and end (first loads, epilogue).
-// Measured, us a stage: 256 x 256 0.71 (8192^3: 733 us); 128 x 128 0.33 alone on its CU, 0.57 two; 64 x 64
-// 0.18 alone, 0.13 more for each other; fp32 takes the matrix unit 1.18 (128) and 0.28 (64; alone 0.36).
+// The estimate of a launch's time. Its workgroups are jobs of so many stages (32 steps; fp32: 16). A CU
+// holds one of 256 x 256, two of 128 x 128 or five of 64 x 64 at a time, and works off a stage in
+// stage_us of the matrix unit and LDS; a smaller tile alone on its CU waits instead, alone_us a stage.
+// The constants were fitted to 1900 measured choices of tile and parts for 64 products and gradients of
+// 2^23 to 2^36 multiplications: what the estimate picks is 1.1% slower than the best one in the geometric
+// mean, 12% at most (one tile for all: 256 x 256 up to 2.9 times slower, 64 x 64 up to 2.6).
 int residents(int tile) { return tile == 256 ? 1 : tile == 128 ? 2 : 5; }
-double stage_us(int type, int tile, int64_t on_cu) {
-  if (type == kF32) return tile == 128 ? 1.18 * on_cu : on_cu <= 1 ? 0.36 : 0.28 * on_cu;
-  if (tile == 256) return 0.71;
-  if (tile == 128) return on_cu <= 1 ? 0.33 : 0.285 * on_cu;
-  return on_cu <= 1 ? 0.18 : 0.13 * on_cu;
+double stage_us(int type, int tile) {
+  if (type == kF32) return tile == 128 ? 1.12 : 0.28;
+  return tile == 256 ? 0.70 : tile == 128 ? 0.27 : 0.125;
 }
-double start_and_end_us(int type, int tile) { return tile == 256 ? 9.0 : tile == 128 ? 3.5 : type == kF32 ? 2.5 : 2.0; }
+double alone_us(int type, int tile) {
+  if (type == kF32) return tile == 128 ? 1.15 : 0.36;
+  return tile == 256 ? 0.70 : tile == 128 ? 0.33 : 0.18;
+}
+// First loads and epilogue; those of a CU's further workgroups are hidden but for next_us.
+double ends_us(int tile) { return tile == 256 ? 9.0 : tile == 128 ? 4.5 : 5.5; }
+double next_us(int tile) { return tile == 128 ? 1.5 : 0.7; }
+// A split: the launch that sums the parts, their sums written and read back.
+constexpr double kFinishUs = 8.0, kPartsBytesPerUs = 4e6;
 
 struct Jobs {
-  int64_t count = 0;
-  double us = 0;
+  int64_t count = 0, stages = 0;
 };
-// When the last of the jobs ends, each in turn given to the slot that is free first.
-double makespan(int64_t slots, const Jobs* jobs, int kinds) {
-  struct Class {  // slots that are free from the same time on
+// When the last of the jobs ends, each in turn given to the CU that is free first.
+double makespan(const Jobs* jobs, int kinds, double us_per_stage, double us_per_job) {
+  struct Class {  // CUs that are free from the same time on
     double at;
     int64_t count;
-  } free_at[8] = {{0.0, slots}};
+  } free_at[8] = {{0.0, kComputeUnits}};
   int classes = 1;
   double last = 0;
   for (int j = 0; j < kinds; ++j) {
@@ -84,7 +91,7 @@ double makespan(int64_t slots, const Jobs* jobs, int kinds) {
         if (free_at[c].at < free_at[first].at) first = c;
       const int64_t rounds = classes == 1 ? std::max<int64_t>(1, left / free_at[first].count) : 1;
       const int64_t n = std::min(left, free_at[first].count * rounds);
-      const double end = free_at[first].at + rounds * jobs[j].us;
+      const double end = free_at[first].at + rounds * (jobs[j].stages * us_per_stage + us_per_job);
       left -= n;
       last = std::max(last, end);
       const int64_t used = std::min(n, free_at[first].count);
@@ -96,6 +103,42 @@ double makespan(int64_t slots, const Jobs* jobs, int kinds) {
     }
   }
   return last;
+}
+
+// When the last of the jobs ends where CUs share themselves among several.
+double shared_end(int type, int tile, const Jobs* jobs, int kinds) {
+  const double us = stage_us(type, tile), ends = ends_us(tile);
+  int64_t total = 0, stages = 0, longest = 0, last = 0, upto[5] = {0};
+  for (int j = 0; j < kinds; ++j) {
+    total += jobs[j].count;
+    stages += jobs[j].count * jobs[j].stages;
+    upto[j + 1] = total;
+    if (jobs[j].count > 0) longest = std::max(longest, last = jobs[j].stages);
+  }
+  if (total > kComputeUnits * residents(tile)) {
+    // later jobs go where there is room, so the loads are even but for the last jobs; a job that is longer
+    // than its CU's load goes on alone
+    const double load = stages * us / kComputeUnits, all = us * residents(tile);
+    const double even = load + 0.3 * last * all + next_us(tile) * ((double)total / kComputeUnits - 1);
+    return std::max(even, load + (longest - load / all) * alone_us(type, tile)) + ends;
+  }
+  double latest = longest * alone_us(type, tile) + ends;
+  for (int b = 0; b < 2 * kinds + 2; ++b) {  // the CUs in turn: the loads change where a kind of job ends
+    const int64_t cu = (upto[b / 2] + kComputeUnits - b % 2) % kComputeUnits;
+    int64_t load = 0, held = 0;
+    for (int j = 0; j < kinds; ++j) {
+      const auto before = [&](int64_t n) { return n > cu ? (n - cu + kComputeUnits - 1) / kComputeUnits : 0; };
+      const int64_t mine = before(upto[j + 1]) - before(upto[j]);
+      load += mine * jobs[j].stages;
+      held += mine;
+    }
+    latest = std::max(latest, load * us + ends + next_us(tile) * std::max<int64_t>(0, held - 1));
+  }
+  return latest;
+}
+
+double launch_us(int type, int tile, const Jobs* jobs, int kinds) {
+  return tile == 256 ? makespan(jobs, kinds, stage_us(type, tile), ends_us(tile)) : shared_end(type, tile, jobs, kinds);
 }
 
 constexpr int64_t kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64};
@@ -112,18 +155,14 @@ bool set_product(ProductPlan* p, int type, int tile, bool ring, int64_t whole, i
   return splits == 1 || (p->k_per_split >= 64 && (tiles - whole) * splits <= kMostParts && cdiv(k, p->k_per_split) == splits);
 }
 
-// The jobs of a product, and the time of writing its parts' sums and of reading them back at 8 TB/s
-// (they stay in the last-level cache).
-double product_jobs(const ProductPlan& p, int type, int tile, int64_t m, int64_t n, int64_t k, double stage, Jobs* jobs) {
+// The jobs of a product; returns the time of its parts' sums.
+double product_jobs(const ProductPlan& p, int type, int tile, int64_t m, int64_t n, int64_t k, Jobs* jobs) {
   const int64_t tiles = cdiv(m, tile) * cdiv(n, tile), whole = p.splits > 1 ? p.whole : tiles;
   const int64_t depth = type == kF32 ? 16 : 32;
-  const double ends = start_and_end_us(type, tile);
-  jobs[0] = {whole, cdiv(k, depth) * stage + ends};
-  jobs[1] = {(tiles - whole) * p.splits, cdiv(p.k_per_split, depth) * stage + ends};
-  return p.splits > 1 ? 2.0 * p.splits * (tiles - whole) * tile * tile * 4 / 8e6 : 0.0;
+  jobs[0] = {whole, cdiv(k, depth)};
+  jobs[1] = {(tiles - whole) * p.splits, cdiv(p.k_per_split, depth)};
+  return p.splits > 1 ? 2.0 * p.splits * (tiles - whole) * tile * tile * 4 / kPartsBytesPerUs : 0.0;
 }
-
-constexpr double kFinishUs = 3.0;  // the launch that sums the parts
 
 // The layer's tile, split tiles and parts with the least estimated time.
 ProductPlan plan_product(int type, int64_t m, int64_t n, int64_t k, bool ring) {
@@ -141,11 +180,9 @@ ProductPlan plan_product(int type, int64_t m, int64_t n, int64_t k, bool ring) {
       for (int64_t splits : kSplits) {
         ProductPlan p;
         if ((w > 0 && splits == 1) || !set_product(&p, type, tile, ring, whole[w], splits, m, n, k)) continue;
-        const int64_t groups = whole[w] + (tiles - whole[w]) * splits;
-        const int64_t on_cu = std::min<int64_t>(residents(tile), cdiv(groups, kComputeUnits));
         Jobs jobs[2];
-        double us = product_jobs(p, type, tile, m, n, k, stage_us(type, tile, on_cu), jobs);
-        us += makespan(kComputeUnits * on_cu, jobs, 2) + (splits > 1 ? kFinishUs : 0.0);
+        double us = product_jobs(p, type, tile, m, n, k, jobs) + (splits > 1 ? kFinishUs : 0.0);
+        us += launch_us(type, tile, jobs, 2);
         if (least == 0 || us < least) {
           least = us;
           best = p;
@@ -177,17 +214,10 @@ void plan_gradient(int type, int64_t m, int64_t k, int64_t n, bool want_dx, bool
           if (rest && (dw_first ? sx : sw) == 1) continue;
           if (!want_dw ? sw > 1 : !set_product(&pw, type, tile, ring, rest && !dw_first ? full : 0, sw, n, k, m)) continue;
           Jobs jobs[4];
-          double us = 0;
-          const auto both = [&](double stage) {
-            us = sx > 1 || sw > 1 ? kFinishUs : 0.0;
-            if (want_dx) us += product_jobs(px, type, tile, m, k, n, stage, jobs + (dw_first ? 2 : 0));
-            if (want_dw) us += product_jobs(pw, type, tile, n, k, m, stage, jobs + (dw_first ? 0 : 2));
-          };
-          both(0.0);
-          const int64_t groups = jobs[0].count + jobs[1].count + jobs[2].count + jobs[3].count;
-          const int64_t on_cu = std::max<int64_t>(1, std::min<int64_t>(residents(tile), cdiv(groups, kComputeUnits)));
-          both(stage_us(type, tile, on_cu));
-          us += makespan(kComputeUnits * on_cu, jobs, 4);
+          double us = sx > 1 || sw > 1 ? kFinishUs : 0.0;
+          if (want_dx) us += product_jobs(px, type, tile, m, k, n, jobs + (dw_first ? 2 : 0));
+          if (want_dw) us += product_jobs(pw, type, tile, n, k, m, jobs + (dw_first ? 0 : 2));
+          us += launch_us(type, tile, jobs, 4);
           if (least == 0 || us < least) {
             least = us;
             *dx = want_dx ? px : ProductPlan{};
