@@ -122,7 +122,8 @@ double shared_end(int type, int tile, const Jobs* jobs, int kinds) {
     const double even = load + 0.3 * last * all + next_us(tile) * ((double)total / kComputeUnits - 1);
     return std::max(even, load + (longest - load / all) * alone_us(type, tile)) + ends;
   }
-  double latest = longest * alone_us(type, tile) + ends;
+  // the epilogue of a lone 128 x 128 tile is on nobody's cover
+  double latest = longest * alone_us(type, tile) + ends + (tile == 128 && total <= kComputeUnits ? 2.0 : 0.0);
   for (int b = 0; b < 2 * kinds + 2; ++b) {  // the CUs in turn: the loads change where a kind of job ends
     const int64_t cu = (upto[b / 2] + kComputeUnits - b % 2) % kComputeUnits;
     int64_t load = 0, held = 0;
@@ -233,7 +234,7 @@ template <typename Plan>
 struct PlanCache {
   struct Entry {
     int64_t key[4] = {-1, -1, -1, -1};
-    Plan plan;
+    Plan plan{};
   } entries[64];
   template <typename Make>
   const Plan& get(int64_t m, int64_t k, int64_t n, int64_t what, Make make) {
@@ -480,6 +481,20 @@ bool backward_fits(int64_t m, int64_t k, int64_t n) {
   return cdiv(m, 64) * cdiv(k, 64) + cdiv(n, 64) * cdiv(k, 64) + cdiv(n, 16) <= kMaxGroups;
 }
 
+size_t most_backward_bytes(int type, int64_t m, int64_t k, int64_t n, int act, int aligned16) {
+  size_t bytes = 0;
+  const int es = elem_size(type);
+  const bool kc = k * es % 16 == 0, nc = n * es % 16 == 0;
+  for (int c = 0; c < 8; ++c) {
+    const bool g = c & 1, x = c & 2, w = c & 4;
+    if (aligned16 && !(g == nc && x == kc && w == kc)) continue;
+    // a product alone may be split further than the two together
+    for (int want = 1; want < 4; ++want)
+      bytes = std::max(bytes, make_backward_plan(type, m, k, n, act, nc && g, kc && x, kc && w, want & 1, want & 2).bytes);
+  }
+  return bytes;
+}
+
 xtvxy_status backward_workspace(int type, int64_t m, int64_t k, int64_t n, int act, int aligned16, size_t* bytes) {
   if (!bytes) return XTVXY_ERROR_NULL_POINTER;
   if (m < 0 || k < 0 || n < 0 || !valid_act(act)) return XTVXY_ERROR_INVALID_VALUE;
@@ -488,15 +503,8 @@ xtvxy_status backward_workspace(int type, int64_t m, int64_t k, int64_t n, int a
   if (m == 0 || n == 0) return XTVXY_SUCCESS;
   if (!backward_fits(m, k, n)) return XTVXY_ERROR_UNSUPPORTED;
   // any of G, X and W may turn out to need its copy where aligned16 is 0: the largest of the plans
-  const int es = elem_size(type);
-  const bool kc = k * es % 16 == 0, nc = n * es % 16 == 0;
-  for (int c = 0; c < 8; ++c) {
-    const bool g = c & 1, x = c & 2, w = c & 4;
-    if (aligned16 && !(g == nc && x == kc && w == kc)) continue;
-    // a product alone may be split further than the two together
-    for (int want = 1; want < 4; ++want)
-      *bytes = std::max(*bytes, make_backward_plan(type, m, k, n, act, nc && g, kc && x, kc && w, want & 1, want & 2).bytes);
-  }
+  thread_local PlanCache<size_t> cache;
+  *bytes = cache.get(m, k, n, (type * 8 + act) * 2 + (aligned16 != 0), [&] { return most_backward_bytes(type, m, k, n, act, aligned16); });
   return XTVXY_SUCCESS;
 }
 

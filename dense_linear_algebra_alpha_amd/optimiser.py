@@ -6,7 +6,7 @@ import ctypes
 import functools
 
 from . import _abi
-from .layers import _stream_of
+from .layers import _extension, _stream_of
 from ._abi import XTVXY_TYPE_BF16, XTVXY_TYPE_F16, XTVXY_TYPE_F32, XTVXY_TYPE_NONE
 
 ADAMW_BLOCK = 128  # elements that share an exponent in 8-bit states
@@ -39,18 +39,6 @@ def xtvxy_adamw_state_values(optimiser, m_out, v_out, type, stream):
 # ---------------------------------------------------------------------------
 # the optimiser object
 # ---------------------------------------------------------------------------
-
-@functools.lru_cache(maxsize=None)
-def _addresses():
-    """addresses() of the extension module; a missing one raises."""
-    import torch  # noqa: F401  (the module resolves against it)
-    try:
-        from ._tensors import addresses
-    except ImportError as e:
-        raise RuntimeError("_tensors.so is not built or does not match this torch (%s); run `python -m "
-                           "dense_linear_algebra_alpha_amd.build`" % e) from None
-    return addresses
-
 
 @functools.lru_cache(maxsize=None)
 def _type_code(dtype) -> int:
@@ -138,7 +126,7 @@ class AdamW:
         pointers = self._pointers()
         if not n:
             return pointers, XTVXY_TYPE_F32
-        bad = _addresses()(tensors, self._numel_address, ctypes.addressof(pointers), n, self.device.index)
+        bad = _extension().addresses(tensors, self._numel_address, ctypes.addressof(pointers), n, self.device.index)
         if bad >= 0:
             raise ValueError("%s[%d] must be a contiguous tensor of %d elements on %s, of the list's one type"
                              % (name, bad, self._numel[bad], self.device))
