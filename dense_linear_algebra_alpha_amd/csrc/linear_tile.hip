@@ -67,11 +67,10 @@ __device__ __forceinline__ f32x8 slope8(V g, V z, int act) {
 
 // A 64 x 64 tile of C, four wavefronts of 32 x 32 each. The product is formed transposed (B's rows as
 // the matrix instruction's first operand), so that a lane ends with four neighbouring columns of one
-// row of C. The next step's elements are in flight while the present one's products run. With kSlope
-// the first operand is G, and d is formed between its load and its store to LDS; where the
-// contraction runs over d's rows and this is the product's first tile column, its column sums are
-// taken from the unrounded d on the way.
-template <typename T, bool kAMajor, bool kBMajor, bool kSlope>
+// row of C. The next step's elements are in flight while the present one's products run. The first operand
+// is G, and d is formed between its load and its store to LDS; where the contraction runs over d's rows
+// and this is the product's first tile column, its column sums are taken from the unrounded d on the way.
+template <typename T, bool kAMajor, bool kBMajor>
 __device__ __forceinline__ void tile(const ProductArgs& a, uint32_t id, const GradientArgs* grad, T* sa, T* sb) {
   typedef typename Vec<T>::x8 frag;
   const uint32_t tiles_n = (uint32_t)((a.n + kTile - 1) / kTile), tiles = (uint32_t)((a.m + kTile - 1) / kTile) * tiles_n;
@@ -84,7 +83,7 @@ __device__ __forceinline__ void tile(const ProductArgs& a, uint32_t id, const Gr
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int wi = (wave >> 1) * 32, wj = (wave & 1) * 32;
   const int r = lane & 15, g = lane >> 4;
-  const bool with_pre = kSlope && grad->pre, with_sums = kSlope && kAMajor && grad->own_sums && j0 == 0;
+  const bool with_pre = grad->pre, with_sums = kAMajor && grad->own_sums && j0 == 0;
 
   f32x4 acc[2][2] = {};
   f32x8 sum = {};
@@ -97,12 +96,10 @@ __device__ __forceinline__ void tile(const ProductArgs& a, uint32_t id, const Gr
   };
   load(k0);
   for (int64_t k = k0; k < k_end; k += kTileDepth) {
-    if (kSlope) {
-      const f32x8 d = slope8(la.v, lz.v, with_pre ? grad->act : XTVXY_ACT_NONE);
-      if (with_sums) sum += d;
+    const f32x8 d = slope8(la.v, lz.v, with_pre ? grad->act : XTVXY_ACT_NONE);
+    if (with_sums) sum += d;
 #pragma unroll
-      for (int c = 0; c < 8; ++c) la.v[c] = (T)d[c];
-    }
+    for (int c = 0; c < 8; ++c) la.v[c] = (T)d[c];
     la.store(sa);
     lb.store(sb);
     __syncthreads();
@@ -151,17 +148,98 @@ __device__ __forceinline__ void tile(const ProductArgs& a, uint32_t id, const Gr
   }
 }
 
-template <typename T>
+// The layer's tile for rows of any length and alignment: the same 64 x 64 outputs by four wavefronts, with
+// four steps of both operands in flight in registers and two LDS buffers, so that a step has one barrier.
+// A row's end needs no branch: its last 8 elements are loaded as they lie and shifted so that zeros stand
+// beyond the end; rows that do not exist are loaded as the last one and not stored. kShort: rows of fewer
+// than 8 elements, loaded one by one (in a kernel of its own: a branch makes every load wait).
+template <typename T, bool kShort>
 __global__ __launch_bounds__(kThreads) void layer_tile(ProductArgs a) {
-  __shared__ __align__(16) T sa[kTile * kPitch], sb[kTile * kPitch];
-  tile<T, false, false, false>(a, blockIdx.x, nullptr, sa, sb);
+  typedef typename Vec<T>::x8 frag;
+  constexpr int kAhead = 4, kBuffer = 2 * kTile * kPitch;
+  __shared__ __align__(16) T lds[2 * kBuffer];
+  const uint32_t tiles_n = (uint32_t)((a.n + kTile - 1) / kTile), tiles = (uint32_t)((a.m + kTile - 1) / kTile) * tiles_n;
+  const uint32_t split = blockIdx.x / tiles, t = blockIdx.x % tiles;
+  const int64_t i0 = (int64_t)(t / tiles_n) * kTile, j0 = (int64_t)(t % tiles_n) * kTile;
+  const int64_t k0 = (int64_t)split * a.k_per_split;
+  const int64_t k_end = k0 + a.k_per_split < a.k ? k0 + a.k_per_split : a.k;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int wi = (wave >> 1) * 32, wj = (wave & 1) * 32, r = lane & 15, g = lane >> 4;
+  const int row = threadIdx.x >> 2, chunk = (threadIdx.x & 3) * 8;
+  const T* pa = static_cast<const T*>(a.A) + (i0 + row < a.m ? i0 + row : a.m - 1) * a.lda;
+  const T* pb = static_cast<const T*>(a.B) + (j0 + row < a.n ? j0 + row : a.n - 1) * a.ldb;
+  frag va[kAhead], vb[kAhead];
+  const auto load = [&](frag& v, const T* p, int64_t k) {
+    k += chunk;
+    if (!kShort) {
+      __builtin_memcpy(&v, p + (k <= k_end - 8 ? k : k_end - 8), sizeof(v));  // memory takes unaligned accesses
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = k + i < k_end ? p[k + i] : (T)0.0f;
+    }
+  };
+  const auto trim = [&](frag& v, int64_t k) {
+    const int64_t over = k + chunk + 8 - k_end;  // elements beyond the end
+    if (kShort) return;
+    const int shift = over <= 0 ? 0 : over < 8 ? (int)over : 8;
+#pragma unroll
+    for (int by = 8; by > 0; by /= 2)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = shift & by ? (i + by < 8 ? v[(i + by) & 7] : (T)0.0f) : v[i];
+  };
+  // Steps in fours without a branch around a load: where its number is not known the compiler waits for
+  // all of them. Steps beyond the end load the row's last elements again and multiply zeros.
+  if (k0 < k_end) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      load(va[u], pa, k0 + u * kTileDepth);
+      load(vb[u], pb, k0 + u * kTileDepth);
+    }
+  }
+  f32x4 acc[2][2] = {};
+  for (int64_t k4 = k0; k4 < k_end; k4 += kAhead * kTileDepth) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int64_t k = k4 + u * kTileDepth;
+      if (k + kTileDepth > k_end) {
+        trim(va[u], k);
+        trim(vb[u], k);
+      }
+      T* sa = lds + (u & 1) * kBuffer;
+      T* sb = sa + kTile * kPitch;
+      *reinterpret_cast<frag*>(sa + row * kPitch + chunk) = va[u];
+      *reinterpret_cast<frag*>(sb + row * kPitch + chunk) = vb[u];
+      __syncthreads();  // the buffer's last readers have passed the barrier of the step between
+      load(va[u], pa, k + kAhead * kTileDepth);
+      load(vb[u], pb, k + kAhead * kTileDepth);
+      frag fa[2], fb[2];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        fa[x] = *reinterpret_cast<const frag*>(sa + (wi + x * 16 + r) * kPitch + g * 8);
+        fb[x] = *reinterpret_cast<const frag*>(sb + (wj + x * 16 + r) * kPitch + g * 8);
+      }
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+#pragma unroll
+        for (int y = 0; y < 2; ++y) acc[x][y] = mfma_16x16(fb[y], fa[x], acc[x][y]);
+    }
+  }
+#pragma unroll
+  for (int x = 0; x < 2; ++x)
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      const int64_t i = i0 + wi + x * 16 + r, j = j0 + wj + y * 16 + g * 4;
+      if (i >= a.m || j >= a.n) continue;
+      if (a.splits > 1) store4<float>(a.partial + ((int64_t)split * a.m + i) * a.n + j, acc[x][y], a.n - j >= 4 ? 4 : (int)(a.n - j));
+      else epilogue4<T>(a.e, i, j, a.n, acc[x][y]);
+    }
 }
 
 template <typename T>
 __global__ __launch_bounds__(kThreads) void gradient_tile(GradientArgs a) {
   __shared__ __align__(16) T sa[kTile * kPitch], sb[kTile * kPitch];
-  if (blockIdx.x < a.dx_groups) tile<T, false, true, true>(a.dx, blockIdx.x, &a, sa, sb);
-  else tile<T, true, true, true>(a.dw, blockIdx.x - a.dx_groups, &a, sa, sb);
+  if (blockIdx.x < a.dx_groups) tile<T, false, true>(a.dx, blockIdx.x, &a, sa, sb);
+  else tile<T, true, true>(a.dw, blockIdx.x - a.dx_groups, &a, sa, sb);
 }
 
 // Four neighbouring outputs of a split product by four neighbouring lanes: each sums every fourth part
@@ -335,20 +413,27 @@ hipError_t slope_for(const SlopeArgs& a, hipStream_t s) {
   return a.n > kSlopeNarrow ? slope_lanes<T, 64>(a, s) : slope_lanes<T, 16>(a, s);
 }
 
-}  // namespace
-
 uint32_t tile_groups(const ProductArgs& a) {
   return (uint32_t)(((a.m + kTile - 1) / kTile) * ((a.n + kTile - 1) / kTile) * a.splits);
 }
+
+template <typename T>
+void layer_tile_for(const ProductArgs& a, hipStream_t s) {
+  if (a.k < 8) layer_tile<T, true><<<tile_groups(a), kThreads, 0, s>>>(a);
+  else layer_tile<T, false><<<tile_groups(a), kThreads, 0, s>>>(a);
+}
+
+}  // namespace
+
 uint32_t quad_groups(const ProductArgs& a) {
   const int64_t quads = a.tile ? (a.tiles() - a.whole) * a.tile * (a.tile / 4) : a.m * ((a.n + 3) / 4);
   return (uint32_t)((quads * 4 + kThreads - 1) / kThreads);
 }
 
 hipError_t launch_layer_tile(const ProductArgs& a, hipStream_t s) {
-  if (a.type == kBf16) layer_tile<__bf16><<<tile_groups(a), kThreads, 0, s>>>(a);
-  else if (a.type == kF16) layer_tile<_Float16><<<tile_groups(a), kThreads, 0, s>>>(a);
-  else layer_tile<float><<<tile_groups(a), kThreads, 0, s>>>(a);
+  if (a.type == kBf16) layer_tile_for<__bf16>(a, s);
+  else if (a.type == kF16) layer_tile_for<_Float16>(a, s);
+  else layer_tile_for<float>(a, s);
   return hipGetLastError();
 }
 
