@@ -272,9 +272,10 @@ hipError_t run_layer(ProductArgs a, const ProductPlan& p, void* ws, hipStream_t 
 // A product's operand as the ring kernel takes it: the caller's matrix where its rows are 16-byte
 // aligned and whole 16-byte chunks, else a copy in the workspace with rows padded by zeros. Small
 // products take any operand as it is. us, direct against copied, fp16: 300 x 301 x 303 7.5, 10.1;
-// 100 x 5001 x 900 12.6, 18.6; 1023 x 1111 x 777 13.7, 15.6; 2000 x 1001 x 1000 19.3, 21.3;
-// 2000 x 501 x 3001 30.9, 32.0; 2000 x 2001 x 2001 59, 44; fp32 at the same four 31.5, 33.6; 45.4, 46.5; 65, 64; 145, 137.
-constexpr int64_t kSmallProduct = (int64_t)1 << 31;  // multiplications
+// 100 x 5001 x 900 12.6, 18.6; 1023 x 1111 x 777 13.3, 15.6; 2000 x 1001 x 1000 18.2, 21.3;
+// 2000 x 501 x 3001 28.4, 32.0; 2000 x 2001 x 2001 43.3, 43.7; 4000 x 2001 x 4000 80, 79; fp32 at the last
+// four 45, 47; 64, 64; 140, 137; 520, 507.
+constexpr int64_t kSmallProduct = (int64_t)1 << 33;  // multiplications
 constexpr int64_t kSmallGradient = (int64_t)1 << 26;
 
 int64_t padded(int64_t cols, int es) { return cdiv(cols, 16 / es) * (16 / es); }

