@@ -301,16 +301,24 @@ LinearPlan make_linear_plan(int type, int64_t m, int64_t k, int64_t n, bool x_wh
   const int es = elem_size(type);
   if (m <= kFewRows) {
     // W cold, us: 16 outputs a workgroup against 32: 1 x 4096 x 4096 bf16 8.9, 11.9; 13 x 2048 x 8192 11.2, 10.5
-    // (X is loaded once per workgroup); 4 wavefronts against 8: bf16 8.9, 9.5, fp32 18.1, 16.9. Where the
-    // outputs are too few for the CUs the contraction is split: 1 x 8192 x 1024 12.1 to 9.7, 1 x 16384 x 256
-    // 20.1 to 9.0. The ring kernel with its best split: 13.9, 14.8, 13.9, 27.4, 13.2, 15.4; at 32 rows of
+    // (X is loaded once per workgroup); 20 x 8192 x 14336 74, 60; but where 32 leave more CUs without work in
+    // the last round 12 x 8192 x 10000 45, 50, 6 x 7296 x 9958 fp32 70, 79. 4 wavefronts against 8: bf16 8.9, 9.5,
+    // fp32 18.1, 16.9. The ring kernel with its best split: 13.9, 14.8, 13.9, 27.4, 13.2, 15.4; at 32 rows of
     // 4096 x 4096 15.6 against 14.7, at 48 14.9 against 21.
-    p.few_outputs = m > 4 && n >= 8192 ? 32 : 16;
+    const auto busy = [](int64_t groups) { return (double)groups / (cdiv(groups, kComputeUnits) * kComputeUnits); };
+    const bool wide = m > 4 && n >= 8192 && 1.15 * busy(cdiv(n, 32)) >= busy(cdiv(n, 16));
+    p.few_outputs = wide ? 32 : 16;
     const int64_t groups = cdiv(n, p.few_outputs);
     p.few = k >= 4096 && (type == kF32 || groups < kComputeUnits) ? 8 : 4;
+    // Where the outputs are too few for the CUs the contraction is split, into the fewest parts that keep them
+    // busy: 1 x 8192 x 1024 12.1 to 9.7, 1 x 16384 x 256 20.1 to 9.0, 23 x 11392 x 2528 (158 groups) 30.1 in one part,
+    // 33.3 in two, 25.7 in three; 9 x 10368 x 3046 fp32 (191 groups) 38 in one part, 42 in two.
     int64_t splits = 1;
-    if (groups <= kComputeUnits / 2 && k * es >= 16384)
-      splits = std::max<int64_t>(1, std::min<int64_t>({8, kComputeUnits / groups, k / (p.few * 256)}));
+    if (groups < kComputeUnits && busy(groups) < 0.7 && k * es >= 16384) {
+      const int64_t most = std::max<int64_t>(1, std::min<int64_t>(8, k / (p.few * 256)));
+      for (int64_t s = 2; s <= most && busy(groups * splits) < 0.9; ++s)
+        if (busy(groups * s) > busy(groups * splits)) splits = s;
+    }
     p.product.k_per_split = std::max<int64_t>(32, cdiv(cdiv(k, p.few * splits), 32) * 32);
     p.product.splits = std::max<int64_t>(1, cdiv(k, p.few * p.product.k_per_split));
     if (p.product.splits > 1) p.bytes = p.product.bytes = align_up((size_t)p.product.splits * m * n * 4);

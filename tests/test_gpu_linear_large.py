@@ -22,7 +22,8 @@ def inputs(m, k, n, dtype, seed):
 
 
 FORWARD = [("bf16", (2308, 1288, 6800)), ("f16", (4100, 520, 4104)), ("bf16", (2307, 333, 6801)), ("f16", (256, 4096, 256)),
-           ("f32", (1030, 524, 2056)), ("f32", (1500, 1000, 3001)), ("bf16", (1856, 1512, 3200)), ("f16", (900, 6000, 1801))]
+           ("f32", (1030, 524, 2056)), ("f32", (1500, 1000, 3001)), ("bf16", (1856, 1512, 3200)), ("f16", (900, 6000, 1801)),
+           ("bf16", (23, 11392, 2528)), ("f32", (6, 7297, 9958)), ("f16", (9, 2000, 8200))]
 
 
 @pytest.mark.parametrize("dtype,size", FORWARD, ids=lambda v: v if isinstance(v, str) else "%dx%dx%d" % v)
