@@ -96,7 +96,7 @@ __device__ __forceinline__ uint32_t encode_m(float m, int exponent, uint32_t rnd
 __device__ __forceinline__ uint32_t encode_v(float v, int exponent, uint32_t rnd) {
   const float x = ldexpf(v, 127 - exponent - 112);
   uint32_t code = (__float_as_uint(x) + (rnd & 0x7ffffu)) >> 19;
-  code = code > 255u ? 255u : code;  // NaN and infinities: the largest (m's code says NaN)
+  code = code > 255u ? 255u : code;  // NaN, infinities and what no exponent holds: the largest
   return v > 0.0f && code < 1u ? 1u : code;  // what is not zero is not stored as zero: m / sqrt(v) stays bounded
 }
 
@@ -163,7 +163,8 @@ __global__ __launch_bounds__(kThreads) void adamw_step(AdamStep a) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     m[i] = fmaf(gr[i], a.one_minus_beta1, m[i] * a.beta1);
-    v[i] = fmaf(gr[i] * gr[i], a.one_minus_beta2, v[i] * a.beta2);
+    // not through g^2, which leaves fp32 from 1.9e19 on
+    v[i] = fmaf(gr[i] * a.one_minus_beta2, gr[i], v[i] * a.beta2);
   }
   if (exact) {
 #pragma unroll
@@ -184,6 +185,10 @@ __global__ __launch_bounds__(kThreads) void adamw_step(AdamStep a) {
     uint32_t mt = 0, vt = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
+      // A finite gradient whose square leaves fp32: m / sqrt(v) is zero in this step, but v's code cannot say
+      // infinity (and its block's exponent goes by the others), so m is dropped: the next step would take it
+      // over the square root of a far smaller v.
+      if (v[i] == INFINITY && fabsf(m[i]) < INFINITY) m[i] = 0.0f;
       mt = max(mt, finite_bits(m[i]));
       vt = max(vt, finite_bits(v[i]));
     }

@@ -764,7 +764,8 @@ enum { XTVXY_TYPE_NONE = 0, XTVXY_TYPE_F32 = 1, XTVXY_TYPE_BF16 = 2, XTVXY_TYPE_
 /* The AdamW step over many tensors in one launch per 400 tensors. Step t = 1, 2, ... of an element:
  *     m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2,
  *     p = p (1 - lr weight_decay) - lr / (1 - beta1^t) m / (sqrt(v) / sqrt(1 - beta2^t) + eps),
- * in fp32 with fp32 parameters; then the 16-bit copy of p, if the optimiser has copies. Each tensor
+ * in fp32 with fp32 parameters; then the 16-bit copy of p, if the optimiser has copies. A v beyond fp32
+ * is infinite and leaves p alone. Each tensor
  * is contiguous; its pointers may have any alignment that its types allow (16 bytes: fast).
  *
  * state_bits 32: m and v fp32. state_bits 8: m and v are codes, one byte per element, in blocks of 128
@@ -777,7 +778,9 @@ enum { XTVXY_TYPE_NONE = 0, XTVXY_TYPE_F32 = 1, XTVXY_TYPE_BF16 = 2, XTVXY_TYPE_
  * the remainder (m's in steps of 2^-13, v's of 2^-19). A nonzero v is never stored as zero. The random
  * bits are a hash of the element's number (through all tensors, each beginning at the next
  * multiple of 128, mod 2^32), the seed and t, so a step is bitwise reproducible. A NaN or infinite m
- * is stored as NaN, a NaN or infinite v as the largest code; the others of the block keep theirs.
+ * is stored as NaN, a NaN or infinite v as the largest code; the others of the block keep theirs. Where
+ * v is infinite and m finite (gradients from about 1e20 on), m is stored as zero, so that the following
+ * steps are as small as after any other; a finite v beyond 1.9375 2^126 is stored as that.
  * Fresh 8-bit states are zero codes with any exponents.
  *
  * xtvxy_adamw_create is a set-up call: it allocates and fills a table of the tensors in device memory
