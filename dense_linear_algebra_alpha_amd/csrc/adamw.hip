@@ -100,10 +100,10 @@ __device__ __forceinline__ uint32_t encode_v(float v, int exponent, uint32_t rnd
   return v > 0.0f && code < 1u ? 1u : code;  // what is not zero is not stored as zero: m / sqrt(v) stays bounded
 }
 
-// The smallest biased exponent e in 1..253 with top <= limit 2^(e - 127), limit 1.mantissa.
-__device__ __forceinline__ int block_exponent(uint32_t top_bits, uint32_t limit_mantissa) {
-  const int e = (int)(top_bits >> 23) + ((top_bits & 0x7fffffu) > limit_mantissa ? 1 : 0);
-  return top_bits == 0 ? 1 : min(max(e, 1), 253);
+// The smallest biased exponent e in 1..253 with top <= limit 2^(e - 127 + shift), limit 1.mantissa.
+__device__ __forceinline__ int block_exponent(uint32_t top_bits, uint32_t limit_mantissa, int shift) {
+  const int e = (int)(top_bits >> 23) + ((top_bits & 0x7fffffu) > limit_mantissa ? 1 : 0) - shift;
+  return min(max(e, 1), 253);
 }
 
 // The largest of x over the 16 lanes of a row.
@@ -193,8 +193,8 @@ __global__ __launch_bounds__(kThreads) void adamw_step(AdamStep a) {
       vt = max(vt, finite_bits(v[i]));
     }
     // elements that do not exist are zero and change no maximum
-    const int me = max(block_exponent(row_max(mt), 0x600000u) - 8, 1);  // 448 = 1.75 * 2^8
-    const int ve = block_exponent(row_max(vt), 0x780000u);              // 1.9375
+    const int me = block_exponent(row_max(mt), 0x600000u, 8);  // 448 = 1.75 * 2^8: holds all of fp32
+    const int ve = block_exponent(row_max(vt), 0x780000u, 0);  // 1.9375
     u32x2 mo = {0, 0}, vo = {0, 0};
     uint32_t h = (t.first + (uint32_t)at) * 0x9E3779B1u + a.salt;
 #pragma unroll

@@ -3,6 +3,7 @@ import numpy as np
 import pytest
 import torch
 
+import adamw_oracle as O
 import dense_linear_algebra_alpha_amd as xt
 from gpu_util import dev, note
 
@@ -61,3 +62,29 @@ def test_one_large_finite_gradient(bits, big, grad):
         keep = torch.arange(384) != 5
         if true_v > 3.5e38 or bits == 32:
             assert all(torch.equal(a[keep], b[keep]) for a, b in zip(steps, clean_steps))
+
+
+def test_first_moments_next_to_the_end_of_fp32():
+    """8-bit first moments of up to 2^128 keep their sign and size; only NaN and infinity become NaN."""
+    codes = np.arange(256, dtype=np.int64)
+    codes = codes[(codes & 127) < 127]
+    n = 254
+    for exponent, beta1 in ((245, 0.999), (246, 0.999), (246, 0.9), (247, 0.5)):
+        exps = np.full(2, exponent, np.int64)
+        m0 = O.decode(codes, exps, O.m_value)
+        fits = np.abs(m0) < 2.0 ** 127 * (2 - 2.0 ** -23)
+        held = np.where(fits, codes, 0)
+        m0 = np.where(fits, m0, 0.0)
+        state = [torch.from_numpy(x.astype(np.uint8)).to(dev()) for x in (held, np.zeros(n), exps, np.ones(2))]
+        note("adamw first moments with exponent %d, beta1 %g" % (exponent, beta1))
+        opt = xt.AdamW([torch.zeros(n, device=dev())], lr=0.0, betas=(beta1, 0.99), weight_decay=0.0, state_bits=8,
+                       state=tuple([s] for s in state), steps=3)
+        opt.step([torch.zeros(n, device=dev())])
+        m, v = torch.zeros(n, device=dev()), torch.zeros(n, device=dev())
+        opt.state_values([m], [v])
+        got, want = m.double().cpu().numpy(), beta1 * m0
+        # a code's step is 2^-3 of its value, or 2^-9 of the block's unit (448 units at most)
+        top = np.repeat([np.abs(want[:128]).max(), np.abs(want[128:]).max()], 128)[:n]
+        assert np.isfinite(got).all()
+        assert (np.abs(got - want) <= np.maximum(2.0 ** -3 * np.abs(want), 2.0 ** -9 * top / 224)).all()
+        assert (np.sign(got) * np.sign(want) >= 0).all()
