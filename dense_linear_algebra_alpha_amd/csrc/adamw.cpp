@@ -183,7 +183,7 @@ xtvxy_status xtvxy_adamw_step(xtvxy_adamw h, const void* const* grads, int grad_
   if (!on_its_device(h)) return XTVXY_ERROR_INVALID_VALUE;
   AdamStep a;
   a.tensors = h->d_tensors;
-  a.decay = (float)(1.0 - lr * weight_decay);
+  a.decay = (float)(lr * weight_decay);
   a.rate = (float)(lr / (1.0 - std::pow(beta1, (double)step)));
   a.root_scale = (float)(1.0 / std::sqrt(1.0 - std::pow(beta2, (double)step)));
   a.beta1 = (float)beta1;

@@ -30,7 +30,7 @@ struct AdamStep {
   const AdamTensor* tensors;
   const AdamChunk* chunks;   // of this launch's tensors
   int32_t first_tensor;
-  float decay;               // 1 - lr weight_decay
+  float decay;               // lr weight_decay
   float rate;                // lr / (1 - beta1^t)
   float root_scale;          // 1 / sqrt(1 - beta2^t)
   float beta1, one_minus_beta1, beta2, one_minus_beta2, eps;

@@ -118,6 +118,12 @@ __device__ __forceinline__ uint32_t finite_bits(float x) {
   return b < 0x7f800000u ? b : 0u;
 }
 
+// p - (decay p + update). A factor 1 - decay would be kept to steps of 6e-8 only: a decay of 2e-8 a step would be
+// none, the same way for every element and step. An infinite p stays infinite.
+__device__ __forceinline__ float moved(float p, float decay, float update) {
+  return p - (fabsf(p) < INFINITY ? fmaf(decay, p, update) : update);
+}
+
 struct NoCopy {};
 template <typename C>
 struct CopyOut {
@@ -168,12 +174,12 @@ __global__ __launch_bounds__(kThreads) void adamw_step(AdamStep a) {
   }
   if (exact) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) p[i] = p[i] * a.decay - a.rate * m[i] / (sqrtf(v[i]) * a.root_scale + a.eps);
+    for (int i = 0; i < 8; ++i) p[i] = moved(p[i], a.decay, a.rate * m[i] / (sqrtf(v[i]) * a.root_scale + a.eps));
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float root = __builtin_amdgcn_sqrtf(v[i]);
-      p[i] = fmaf(p[i], a.decay, -(a.rate * m[i]) * fast_rcp(fmaf(root, a.root_scale, a.eps)));
+      p[i] = moved(p[i], a.decay, a.rate * m[i] * fast_rcp(fmaf(root, a.root_scale, a.eps)));
     }
   }
   store8<float>(t.p + at, count, wide, p);

@@ -88,3 +88,44 @@ def test_first_moments_next_to_the_end_of_fp32():
         assert np.isfinite(got).all()
         assert (np.abs(got - want) <= np.maximum(2.0 ** -3 * np.abs(want), 2.0 ** -9 * top / 224)).all()
         assert (np.sign(got) * np.sign(want) >= 0).all()
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+@pytest.mark.parametrize("lr", [2e-6, 1e-5])
+def test_weight_decay_below_the_spacing_of_fp32(lr, bits):
+    """lr weight_decay of 2e-8 and 1e-7: the mean decay over many elements, whose updates of many units of p
+    spread the rounding of the sum evenly."""
+    n, wd, b1, b2, t = 1 << 20, 0.01, 0.9, 0.99, 7
+    gen = torch.Generator().manual_seed(8)
+    p0 = 1.0 + torch.rand(n, generator=gen)
+    g = torch.randn(n, generator=gen)
+    p = p0.to(dev())
+    note("adamw %d bits, lr %g and weight decay %g" % (bits, lr, wd))
+    if bits == 32:
+        m0, v0 = torch.randn(n, generator=gen) * 0.3, torch.rand(n, generator=gen) + 0.5
+        state = ([m0.to(dev())], [v0.to(dev())])
+        md, vd = m0.double(), v0.double()
+    else:
+        qm = (torch.randint(0, 0x60, (n,), generator=gen) + 128 * torch.randint(0, 2, (n,), generator=gen)).numpy()
+        qv = torch.randint(0xa0, 0x100, (n,), generator=gen).numpy()
+        em, ev = np.full(n // 128, 122), np.full(n // 128, 127)
+        state = tuple([torch.from_numpy(x.astype(np.uint8)).to(dev())] for x in (qm, qv, em, ev))
+        md, vd = torch.from_numpy(O.decode(qm, em, O.m_value)), torch.from_numpy(O.decode(qv, ev, O.v_value))
+    opt = xt.AdamW([p], lr=lr, betas=(b1, b2), weight_decay=wd, state_bits=bits, state=state, steps=t - 1)
+    opt.step([g.to(dev())])
+    m1, v1 = b1 * md + (1 - b1) * g.double(), b2 * vd + (1 - b2) * g.double() ** 2
+    update = lr / (1 - b1 ** t) * m1 / (v1.sqrt() / (1 - b2 ** t) ** 0.5 + opt.eps)
+    assert update.std() > 2.0 ** -23  # of several units: the sum is rounded evenly to 1e-8 of a unit
+    decay = (p0.double() - update - p.double().cpu()).mean().item()
+    want = lr * wd * p0.double().mean().item()
+    # the sum's rounding is off by at most half of 2^-23, evenly; five standard deviations of its mean, and the
+    # update's own few units
+    assert abs(decay - want) <= 5 * 2.0 ** -23 / 12 ** 0.5 / n ** 0.5 + 16 * 2.0 ** -24 * update.abs().mean().item()
+
+
+def test_infinite_parameters_stay():
+    p = torch.tensor([float("inf"), -float("inf"), 1.0], device=dev())
+    for wd in (0.0, 0.01):
+        note("adamw infinite parameters, weight decay %g" % wd)
+        xt.AdamW([p], lr=1e-3, weight_decay=wd).step([torch.ones(3, device=dev())])
+        assert p[0] == float("inf") and p[1] == -float("inf") and torch.isfinite(p[2])
