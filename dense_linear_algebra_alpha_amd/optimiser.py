@@ -6,7 +6,7 @@ import ctypes
 import functools
 
 from . import _abi
-from .layers import _extension, _stream_of
+from .layers import _extension, _stream_of, _torch
 from ._abi import XTVXY_TYPE_BF16, XTVXY_TYPE_F16, XTVXY_TYPE_F32, XTVXY_TYPE_NONE
 
 ADAMW_BLOCK = 128  # elements that share an exponent in 8-bit states
@@ -58,7 +58,8 @@ class AdamW:
     rounds them at random from ``seed`` (formats in include/xtvxy.h). ``state`` resumes from (m, v), or
     (m, v, m_exp, v_exp) for 8 bits, lists of tensors that the object goes on using (uint8 for 8 bits);
     None starts from zeros. ``steps`` is the number of steps taken before. The object keeps its tensors:
-    they must not be resized or moved. lr, betas, eps, weight_decay and seed are plain attributes."""
+    they must not be resized or moved, and their GPU has to be the current one in every call. lr, betas,
+    eps, weight_decay and seed are plain attributes."""
 
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, *, copies=None, state_bits=32,
                  state=None, steps=0, seed=0):
@@ -73,6 +74,7 @@ class AdamW:
             if p.dtype != torch.float32 or p.device.type != "cuda" or p.device != params[0].device or not p.is_contiguous():
                 raise ValueError("params[%d] must be a contiguous float32 tensor on the GPU of the others" % i)
         self.device = params[0].device if params else torch.device("cuda", torch.cuda.current_device())
+        self._check_device()
         numel = [p.numel() for p in params]
         blocks = [(n + ADAMW_BLOCK - 1) // ADAMW_BLOCK for n in numel]
         st = torch.float32 if state_bits == 32 else torch.uint8
@@ -106,6 +108,12 @@ class AdamW:
                                          self._array(state[1]), *exps, copy_type,
                                          None if copies is None else self._array(copies))
 
+    def _check_device(self):
+        current = _torch()._C._cuda_getDevice()
+        if self.device.index != current:
+            raise ValueError("the optimiser's tensors are on %s, which must be the current GPU, not cuda:%d"
+                             % (self.device, current))
+
     def _check_list(self, name, tensors, lengths, dtype):
         if len(tensors) != len(lengths):
             raise ValueError("%s has %d tensors, the parameters are %d" % (name, len(tensors), len(lengths)))
@@ -135,6 +143,7 @@ class AdamW:
     def step(self, grads, *, stream=None):
         """One step with the gradients of the parameters, in their order: contiguous tensors of one type
         (float32, bfloat16 or float16)."""
+        self._check_device()
         pointers, code = self._like_params("grads", grads)
         xtvxy_adamw_step(self.handle, pointers, code, self.steps + 1, self.lr, self.betas[0], self.betas[1], self.eps,
                          self.weight_decay, self.seed & 0xffffffff, _stream_of(stream, self.device.index))
@@ -142,6 +151,7 @@ class AdamW:
 
     def state_values(self, m_out, v_out, *, stream=None):
         """Writes the values that the moments stand for into tensors of the parameters' sizes."""
+        self._check_device()
         m_pointers, code = self._like_params("m_out", m_out)
         v_pointers, v_code = self._like_params("v_out", v_out)
         if v_code != code:
