@@ -471,22 +471,25 @@ def _check_vec(name, t, length, device, required=True):
         raise ValueError("%s must be a contiguous float32 tensor of %d elements on %s" % (name, length, device))
 
 
-def _workspace(nbytes: int, device):
+def _make(stream, fn, *args, returned=True, **kw):
+    """fn(*args, **kw): a tensor for a call on `stream` to write, allocated there. A block of the current
+    stream could be one that a kernel there still reads. One that goes back to the caller, who uses it on
+    the current stream, is not handed out again before that stream is done with it."""
+    if stream is None:
+        return fn(*args, **kw)
+    torch = _torch()
+    with torch.cuda.stream(stream):
+        t = fn(*args, **kw)
+    if returned:
+        t.record_stream(torch.cuda.current_stream(t.device))
+    return t
+
+
+def _workspace(nbytes: int, device, stream):
     torch = _torch()
     if nbytes == 0:
         return None
-    return torch.empty(int(nbytes), dtype=torch.uint8, device=device)
-
-
-def _keep_for_stream(stream, *tensors):
-    """Tensors allocated here on the current stream but used by kernels launched on `stream`: tell
-    the caching allocator, so that their memory is not handed out again before that stream has
-    passed the call (it would otherwise be reusable as soon as the helper returns)."""
-    if stream is None:
-        return
-    for t in tensors:
-        if t is not None:
-            t.record_stream(stream)
+    return _make(stream, torch.empty, int(nbytes), dtype=torch.uint8, device=device, returned=False)
 
 
 def dense_plan(m, n, ldx=None, aligned=True, dev=None, bf16=False) -> xtvxy_launch_params:
@@ -523,17 +526,15 @@ def dense(X, y, v=None, z=None, alpha=1.0, beta=0.0, out=None, *, m=None, n=None
     _check_vec("y", y, n, device)
     _check_vec("v", v, m, device, required=False)
     _check_vec("z", z, n, device, required=beta != 0)
-    made_out = out is None
-    if made_out:
-        out = torch.empty(n, dtype=torch.float32, device=device)
+    if out is None:
+        out = _make(stream, torch.empty, n, dtype=torch.float32, device=device)
     _check_vec("out", out, n, device)
     if plan is None:
         need = (xtvxy_dense_bf16_workspace_size if bf16 or f16 else xtvxy_dense_f32_workspace_size)(m, n, ldx)
     else:
         need = int(plan.workspace_bytes)
-    made_ws = workspace is None
-    if made_ws:
-        workspace = _workspace(need, device)
+    if workspace is None:
+        workspace = _workspace(need, device, stream)
     ws_ptr, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
     args = (m, n, float(alpha), X.data_ptr(), ldx, _ptr(v), y.data_ptr(), float(beta), _ptr(z), out.data_ptr(),
             ws_ptr, ws_bytes, _stream_handle(stream))
@@ -541,7 +542,6 @@ def dense(X, y, v=None, z=None, alpha=1.0, beta=0.0, out=None, *, m=None, n=None
         (xtvxy_dense_f16 if f16 else xtvxy_dense_bf16 if bf16 else xtvxy_dense_f32)(*args)
     else:
         (xtvxy_dense_f16_ex if f16 else xtvxy_dense_bf16_ex if bf16 else xtvxy_dense_f32_ex)(*args, plan)
-    _keep_for_stream(stream, out if made_out else None, workspace if made_ws else None)
     return out
 
 
@@ -563,14 +563,12 @@ def csr(row_ptr, col_idx, values, n, y, v=None, z=None, alpha=1.0, beta=0.0, out
     _check_vec("y", y, n, device)
     _check_vec("v", v, m, device, required=False)
     _check_vec("z", z, n, device, required=beta != 0)
-    made_out = out is None
-    if made_out:
-        out = torch.empty(n, dtype=torch.float32, device=device)
+    if out is None:
+        out = _make(stream, torch.empty, n, dtype=torch.float32, device=device)
     _check_vec("out", out, n, device)
     need = xtvxy_csr_f32_workspace_size(m, n, nnz) if plan is None else int(plan.workspace_bytes)
-    made_ws = workspace is None
-    if made_ws:
-        workspace = _workspace(need, device)
+    if workspace is None:
+        workspace = _workspace(need, device, stream)
     ws_ptr, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
     args = (m, n, nnz, float(alpha), row_ptr.data_ptr(), _ptr(col_idx) if nnz else None,
             _ptr(values) if nnz else None, _ptr(v), y.data_ptr(), float(beta), _ptr(z), out.data_ptr(), ws_ptr,
@@ -579,7 +577,6 @@ def csr(row_ptr, col_idx, values, n, y, v=None, z=None, alpha=1.0, beta=0.0, out
         (xtvxy_csr_bf16 if bf16 else xtvxy_csr_f32)(*args)
     else:
         (xtvxy_csr_bf16_ex if bf16 else xtvxy_csr_f32_ex)(*args, plan)
-    _keep_for_stream(stream, out if made_out else None, workspace if made_ws else None)
     return out
 
 
@@ -625,9 +622,8 @@ def csr_rowdot(row_ptr, col_idx, values, n, y, v=None, t0=None, alpha=1.0, beta=
     _check_vec("y", y, n, device)
     _check_vec("v", v, m, device, required=False)
     _check_vec("t0", t0, m, device, required=beta != 0)
-    made_out = out is None
-    if made_out:
-        out = torch.empty(m, dtype=torch.float32, device=device)
+    if out is None:
+        out = _make(stream, torch.empty, m, dtype=torch.float32, device=device)
     _check_vec("out", out, m, device)
     args = (m, n, nnz, float(alpha), row_ptr.data_ptr(), _ptr(col_idx) if nnz else None,
             _ptr(values) if nnz else None, _ptr(v), y.data_ptr(), float(beta), _ptr(t0), out.data_ptr(),
@@ -636,7 +632,6 @@ def csr_rowdot(row_ptr, col_idx, values, n, y, v=None, t0=None, alpha=1.0, beta=
         (xtvxy_csr_bf16_rowdot if bf16 else xtvxy_csr_f32_rowdot)(*args)
     else:
         (xtvxy_csr_bf16_rowdot_ex if bf16 else xtvxy_csr_f32_rowdot_ex)(*args, plan)
-    _keep_for_stream(stream, out if made_out else None)
     return out
 
 
@@ -649,14 +644,12 @@ def csr_tmv(row_ptr, col_idx, values, n, u, z=None, alpha=1.0, beta=0.0, out=Non
     bf16 = _is_bf16(values)
     _check_vec("u", u, m, device)
     _check_vec("z", z, n, device, required=beta != 0)
-    made_out = out is None
-    if made_out:
-        out = torch.empty(n, dtype=torch.float32, device=device)
+    if out is None:
+        out = _make(stream, torch.empty, n, dtype=torch.float32, device=device)
     _check_vec("out", out, n, device)
     need = xtvxy_csr_f32_workspace_size(m, n, nnz) if plan is None else int(plan.workspace_bytes)
-    made_ws = workspace is None
-    if made_ws:
-        workspace = _workspace(need, device)
+    if workspace is None:
+        workspace = _workspace(need, device, stream)
     ws_ptr, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
     args = (m, n, nnz, float(alpha), row_ptr.data_ptr(), _ptr(col_idx) if nnz else None,
             _ptr(values) if nnz else None, u.data_ptr(), float(beta), _ptr(z), out.data_ptr(), ws_ptr, ws_bytes,
@@ -665,14 +658,13 @@ def csr_tmv(row_ptr, col_idx, values, n, u, z=None, alpha=1.0, beta=0.0, out=Non
         (xtvxy_csr_bf16_tmv if bf16 else xtvxy_csr_f32_tmv)(*args)
     else:
         (xtvxy_csr_bf16_tmv_ex if bf16 else xtvxy_csr_f32_tmv_ex)(*args, plan)
-    _keep_for_stream(stream, out if made_out else None, workspace if made_ws else None)
     return out
 
 
 def csr_check(row_ptr, col_idx, n, stream=None) -> int:
     """Device-side structure check; returns 0 for a well-formed matrix (synchronizes)."""
     torch = _torch()
-    flag = torch.zeros(1, dtype=torch.int32, device=row_ptr.device)
+    flag = _make(stream, torch.zeros, 1, dtype=torch.int32, device=row_ptr.device)
     xtvxy_csr_check(row_ptr.numel() - 1, n, col_idx.numel(), row_ptr.data_ptr(),
                     col_idx.data_ptr() if col_idx.numel() else None, flag.data_ptr(), _stream_handle(stream))
     if stream is not None:  # the check ran on `stream`; .item() below waits for the current stream only
@@ -685,9 +677,8 @@ def dense_transpose(X, stream=None):
     torch = _torch()
     m, n = X.shape
     ldx = max(X.stride(0) if m > 1 else n, n, 1)
-    Xt = torch.empty((n, m), dtype=torch.float32, device=X.device)
+    Xt = _make(stream, torch.empty, (n, m), dtype=torch.float32, device=X.device)
     xtvxy_dense_f32_transpose(m, n, X.data_ptr(), ldx, Xt.data_ptr(), max(m, 1), _stream_handle(stream))
-    _keep_for_stream(stream, Xt)
     return Xt
 
 
@@ -701,12 +692,10 @@ def dense_unfused(X, y, v=None, z=None, alpha=1.0, beta=0.0, out=None, *, Xt=Non
     _check_vec("y", y, n, device)
     _check_vec("v", v, m, device, required=False)
     _check_vec("z", z, n, device, required=beta != 0)
-    made_out = out is None
-    if made_out:
-        out = torch.empty(n, dtype=torch.float32, device=device)
-    made_ws = workspace is None
-    if made_ws:
-        workspace = _workspace(xtvxy_dense_f32_unfused_reference_workspace_size(m, n), device)
+    if out is None:
+        out = _make(stream, torch.empty, n, dtype=torch.float32, device=device)
+    if workspace is None:
+        workspace = _workspace(xtvxy_dense_f32_unfused_reference_workspace_size(m, n), device, stream)
     ws_ptr, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
     if Xt is None:
         xtvxy_dense_f32_unfused_reference(m, n, float(alpha), X.data_ptr(), ldx, _ptr(v), y.data_ptr(), float(beta),
@@ -718,7 +707,6 @@ def dense_unfused(X, y, v=None, z=None, alpha=1.0, beta=0.0, out=None, *, Xt=Non
         xtvxy_dense_f32_unfused_reference_explicit(m, n, float(alpha), X.data_ptr(), ldx, Xt.data_ptr(), ldxt, _ptr(v),
                                                    y.data_ptr(), float(beta), _ptr(z), out.data_ptr(), ws_ptr,
                                                    ws_bytes, _stream_handle(stream))
-    _keep_for_stream(stream, out if made_out else None, workspace if made_ws else None)
     return out
 
 
@@ -754,14 +742,12 @@ class CsrAnalysis:
         _check_vec("y", y, self.n, self.device)
         _check_vec("v", v, self.m, self.device, required=False)
         _check_vec("z", z, self.n, self.device, required=beta != 0)
-        made_out = out is None
-        if made_out:
-            out = torch.empty(self.n, dtype=torch.float32, device=self.device)
+        if out is None:
+            out = _make(stream, torch.empty, self.n, dtype=torch.float32, device=self.device)
         _check_vec("out", out, self.n, self.device)
         need = xtvxy_csr_f32_analysed_workspace_size(self.handle) if plan is None else int(plan.workspace_bytes)
-        made_ws = workspace is None
-        if made_ws:
-            workspace = _workspace(need, self.device)
+        if workspace is None:
+            workspace = _workspace(need, self.device, stream)
         ws_ptr, ws_bytes = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
         args = (self.handle, float(alpha), _ptr(values) if self.nnz else None, _ptr(v), y.data_ptr(), float(beta),
                 _ptr(z), out.data_ptr(), ws_ptr, ws_bytes, _stream_handle(stream))
@@ -769,7 +755,6 @@ class CsrAnalysis:
             (xtvxy_csr_bf16_analysed if bf16 else xtvxy_csr_f32_analysed)(*args)
         else:
             (xtvxy_csr_bf16_analysed_ex if bf16 else xtvxy_csr_f32_analysed_ex)(*args, plan)
-        _keep_for_stream(stream, out if made_out else None, workspace if made_ws else None)
         return out
 
     def close(self):
@@ -801,12 +786,10 @@ class CsrUnfusedPlan:
 
     def __call__(self, y, v=None, z=None, alpha=1.0, beta=0.0, out=None, stream=None):
         torch = _torch()
-        made_out = out is None
-        if made_out:
-            out = torch.empty(self.n, dtype=torch.float32, device=y.device)
+        if out is None:
+            out = _make(stream, torch.empty, self.n, dtype=torch.float32, device=y.device)
         xtvxy_csr_f32_unfused_reference(self.handle, float(alpha), _ptr(v), y.data_ptr(), float(beta), _ptr(z),
                                         out.data_ptr(), _stream_handle(stream))
-        _keep_for_stream(stream, out if made_out else None)
         return out
 
     def close(self):
@@ -839,7 +822,7 @@ def logreg_newton_cg(row_ptr, col_idx, values, n, labels, lam, w=None, *, max_ne
     bf16 = _is_bf16(values)
     _check_vec("labels", labels, m, device)
     if w is None:
-        w = torch.zeros(n, dtype=torch.float32, device=device)
+        w = _make(stream, torch.zeros, n, dtype=torch.float32, device=device)
     _check_vec("w", w, n, device)
     if engine not in ("fused", "unfused"):
         raise ValueError("engine must be 'fused' or 'unfused'")
@@ -855,7 +838,7 @@ def logreg_newton_cg(row_ptr, col_idx, values, n, labels, lam, w=None, *, max_ne
                                XTVXY_LOGREG_FUSED if engine == "fused" else XTVXY_LOGREG_UNFUSED)
     need = xtvxy_logreg_newton_cg_f32_workspace_size(m, n, nnz)
     if workspace is None:
-        workspace = _workspace(need, device)
+        workspace = _workspace(need, device, stream)
     rows = int(max_newton) + 1
     hist = (ctypes.c_double * (rows * len(_HISTORY_KEYS)))()
     rep = xtvxy_logreg_report()
@@ -879,7 +862,7 @@ def dense_tune(X, y, v=None, z=None, alpha=1.0, beta=0.0, out=None, *, repeats=1
     m, n = X.shape
     ldx = max(X.stride(0) if m > 1 else n, n, 1)
     if out is None:
-        out = torch.empty(n, dtype=torch.float32, device=X.device)
+        out = _make(stream, torch.empty, n, dtype=torch.float32, device=X.device)
     fn = (xtvxy_dense_f16_tune if X.dtype == torch.float16 else
           xtvxy_dense_bf16_tune if X.dtype in (torch.bfloat16, torch.uint16) else xtvxy_dense_f32_tune)
     return fn(m, n, float(alpha), X.data_ptr(), ldx, _ptr(v), y.data_ptr(), float(beta), _ptr(z),
@@ -893,7 +876,7 @@ def csr_tune(row_ptr, col_idx, values, n, y, v=None, z=None, alpha=1.0, beta=0.0
     torch = _torch()
     m, nnz, device = _check_csr_arrays(row_ptr, col_idx, values, bf16_ok=True)
     if out is None:
-        out = torch.empty(n, dtype=torch.float32, device=device)
+        out = _make(stream, torch.empty, n, dtype=torch.float32, device=device)
     return (xtvxy_csr_bf16_tune if _is_bf16(values) else xtvxy_csr_f32_tune)(m, n, nnz, float(alpha), row_ptr.data_ptr(), _ptr(col_idx), _ptr(values), _ptr(v),
                               y.data_ptr(), float(beta), _ptr(z), out.data_ptr(), repeats,
                               _stream_handle(stream)).as_dict()

@@ -179,7 +179,12 @@ def _check_bias(name, t, n, dev):
         raise ValueError("%s must be a contiguous float32 vector of %d elements on GPU %d" % (name, n, dev))
 
 
-def _scratch(need, workspace, like):
+def _new(like, shape, stream, dtype=None, returned=True):
+    from . import _make  # the package's rule for tensors of a call on `stream`
+    return _make(stream, like.new_empty, shape, dtype=dtype or like.dtype, returned=returned)
+
+
+def _scratch(need, workspace, like, stream):
     """(tensor made here or None, pointer, bytes) of the workspace of a call that needs `need` bytes."""
     if workspace is not None:
         if workspace.device != like.device or not workspace.is_contiguous():
@@ -187,7 +192,7 @@ def _scratch(need, workspace, like):
         return None, workspace.data_ptr(), workspace.numel() * workspace.element_size()
     if need == 0:
         return None, None, 0
-    ws = like.new_empty(need, dtype=_torch().uint8)
+    ws = _new(like, need, stream, _torch().uint8, returned=False)
     return ws, ws.data_ptr(), need
 
 
@@ -234,15 +239,13 @@ def linear(X, W, bias=None, residual=None, act="none", *, save_pre=False, out=No
     if residual is not None:
         ldr = _pitch("residual", residual, m, n, dtype, dev)
         residual_ptr = residual.data_ptr()
-    made_out = out is None
-    if made_out:
-        out = X.new_empty((m, n))
+    if out is None:
+        out = _new(X, (m, n), stream)
         ldo = n or 1
     else:
         ldo = _pitch("out", out, m, n, dtype, dev)
-    made_pre = save_pre and pre is None
-    if made_pre:
-        pre = X.new_empty((m, n))
+    if save_pre and pre is None:
+        pre = _new(X, (m, n), stream)
         ldp = n or 1
     elif pre is not None:
         ldp = _pitch("pre", pre, m, n, dtype, dev)
@@ -251,13 +254,10 @@ def linear(X, W, bias=None, residual=None, act="none", *, save_pre=False, out=No
     xp, wp = X.data_ptr(), W.data_ptr()
     es = 4 if suffix == "f32" else 2
     aligned = 0 if (xp | wp | ldx * es | ldw * es) & 15 or max(ldx, ldw) * es > _MAX_PITCH else 1
-    made_ws, ws_ptr, ws_bytes = _scratch(_linear_bytes(suffix, m, k, n, aligned), workspace, X)
+    ws, ws_ptr, ws_bytes = _scratch(_linear_bytes(suffix, m, k, n, aligned), workspace, X, stream)
     name = "xtvxy_linear_" + suffix
     _check(_entry(name)(m, k, n, xp, ldx, wp, ldw, bias_ptr, residual_ptr, ldr or 1, code,
                         out.data_ptr(), ldo, pre_ptr, ldp or 1, ws_ptr, ws_bytes, _stream_of(stream, dev)), name)
-    if stream is not None:
-        from . import _keep_for_stream
-        _keep_for_stream(stream, out if made_out else None, pre if made_pre else None, made_ws)
     return out if pre is None else (out, pre)
 
 
@@ -287,38 +287,31 @@ def linear_backward(G, X, W, pre=None, act="none", *, need_dX=True, need_dW=True
             raise ValueError("pre is required for activation %r" % act)
         ldp = _pitch("pre", pre, m, n, dtype, dev)
         pre_ptr = pre.data_ptr()
-    made = []
     lddx, lddw = k or 1, k or 1
     if not need_dX:
         dX = None
     elif dX is None:
-        dX = X.new_empty((m, k))
-        made.append(dX)
+        dX = _new(X, (m, k), stream)
     else:
         lddx = _pitch("dX", dX, m, k, dtype, dev)
     if not need_dW:
         dW = None
     elif dW is None:
-        dW = X.new_empty((n, k))
-        made.append(dW)
+        dW = _new(X, (n, k), stream)
     else:
         lddw = _pitch("dW", dW, n, k, dtype, dev)
     if not need_db:
         db = None
     elif db is None:
-        db = X.new_empty(n, dtype=_torch().float32)
-        made.append(db)
+        db = _new(X, n, stream, _torch().float32)
     else:
         _check_bias("db", db, n, dev)
     gp, xp, wp = G.data_ptr(), X.data_ptr(), W.data_ptr()
     es = 4 if suffix == "f32" else 2
     aligned = 0 if (gp | xp | wp | ldg * es | ldx * es | ldw * es) & 15 or max(ldg, ldx, ldw) * es > _MAX_PITCH else 1
-    made_ws, ws_ptr, ws_bytes = _scratch(_backward_bytes(suffix, m, k, n, code, aligned), workspace, X)
+    ws, ws_ptr, ws_bytes = _scratch(_backward_bytes(suffix, m, k, n, code, aligned), workspace, X, stream)
     name = "xtvxy_linear_backward_" + suffix
     _check(_entry(name)(m, k, n, gp, ldg, xp, ldx, wp, ldw, pre_ptr, ldp, code,
                         None if dX is None else dX.data_ptr(), lddx, None if dW is None else dW.data_ptr(), lddw,
                         None if db is None else db.data_ptr(), ws_ptr, ws_bytes, _stream_of(stream, dev)), name)
-    if stream is not None:
-        from . import _keep_for_stream
-        _keep_for_stream(stream, *made, made_ws)
     return dX, dW, db
