@@ -81,6 +81,7 @@ class AdamW:
         lengths = (numel, numel) if state_bits == 32 else (numel, numel, blocks, blocks)
         if state is None:
             state = tuple([torch.zeros(n, dtype=st, device=self.device) for n in ls] for ls in lengths)
+            torch.cuda.current_stream().synchronize()  # the first step may run on any stream
         if len(state) != len(lengths):
             raise ValueError("state of %d-bit states has %d lists" % (state_bits, len(lengths)))
         state = tuple(list(s) for s in state)
@@ -102,8 +103,8 @@ class AdamW:
         self._count = count = (ctypes.c_int64 * n)(*numel)
         self._numel_address = ctypes.addressof(count)
         exps = (self._array(state[2]), self._array(state[3])) if state_bits == 8 else (None, None)
-        # fresh states and the caller's tensors may still be in the making on the current stream; steps
-        # are ordered after them by the streams that the caller runs them on
+        # the caller's tensors may still be in the making: steps are ordered after that by the streams that the
+        # caller runs them on
         self.handle = xtvxy_adamw_create(n, count, self._array(params), state_bits, self._array(state[0]),
                                          self._array(state[1]), *exps, copy_type,
                                          None if copies is None else self._array(copies))

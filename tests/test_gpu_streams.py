@@ -101,3 +101,19 @@ def test_check_on_another_stream_behind_a_busy_one():
     assert want != 0
     torch.cuda._sleep(50_000_000)
     assert xt.csr_check(rp, ci, 4, stream=s) == want
+
+
+def test_fresh_optimiser_states_behind_a_busy_stream():
+    """Fresh states are zero when the object is there, whatever stream its first step runs on."""
+    n = 4096
+    g, p = normal(n, 1), normal(n, 2)
+    made, used = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    note("fresh states on another stream")
+    with torch.cuda.stream(made):
+        torch.cuda._sleep(50_000_000)
+        opt = xt.AdamW([p], betas=(0.9, 0.99))
+    opt.step([g], stream=used)
+    torch.cuda.synchronize()
+    assert torch.equal(opt.state[0][0], g * torch.tensor(1 - 0.9, device=dev()))
+    assert (opt.state[1][0] > 0).all()
