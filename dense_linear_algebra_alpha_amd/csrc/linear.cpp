@@ -181,6 +181,7 @@ ProductPlan plan_product(int type, int64_t m, int64_t n, int64_t k, bool ring) {
       for (int64_t splits : kSplits) {
         ProductPlan p;
         if ((w > 0 && splits == 1) || !set_product(&p, type, tile, ring, whole[w], splits, m, n, k)) continue;
+        if (splits > 1 && tiles + kMostParts > kMaxGroups) continue;  // beyond one launch
         Jobs jobs[2];
         double us = product_jobs(p, type, tile, m, n, k, jobs) + (splits > 1 ? kFinishUs : 0.0);
         us += launch_us(type, tile, jobs, 2);
@@ -214,6 +215,7 @@ void plan_gradient(int type, int64_t m, int64_t k, int64_t n, bool want_dx, bool
         for (int64_t sw : kSplits) {
           if (rest && (dw_first ? sx : sw) == 1) continue;
           if (!want_dw ? sw > 1 : !set_product(&pw, type, tile, ring, rest && !dw_first ? full : 0, sw, n, k, m)) continue;
+          if ((sx > 1 || sw > 1) && tx + tw + cdiv(n, 16) + 2 * kMostParts > kMaxGroups) continue;
           Jobs jobs[4];
           double us = sx > 1 || sw > 1 ? kFinishUs : 0.0;
           if (want_dx) us += product_jobs(px, type, tile, m, k, n, jobs + (dw_first ? 2 : 0));
@@ -307,22 +309,26 @@ LinearPlan make_linear_plan(int type, int64_t m, int64_t k, int64_t n, bool x_wh
     // 4096 x 4096 15.6 against 14.7, at 48 14.9 against 21.
     const auto busy = [](int64_t groups) { return (double)groups / (cdiv(groups, kComputeUnits) * kComputeUnits); };
     const bool wide = m > 4 && n >= 8192 && 1.15 * busy(cdiv(n, 32)) >= busy(cdiv(n, 16));
-    p.few_outputs = wide ? 32 : 16;
-    const int64_t groups = cdiv(n, p.few_outputs);
-    p.few = k >= 4096 && (type == kF32 || groups < kComputeUnits) ? 8 : 4;
-    // Where the outputs are too few for the CUs the contraction is split, into the fewest parts that keep them
-    // busy: 1 x 8192 x 1024 12.1 to 9.7, 1 x 16384 x 256 20.1 to 9.0, 23 x 11392 x 2528 (158 groups) 30.1 in one part,
-    // 33.3 in two, 25.7 in three; 9 x 10368 x 3046 fp32 (191 groups) 38 in one part, 42 in two.
-    int64_t splits = 1;
-    if (groups < kComputeUnits && busy(groups) < 0.7 && k * es >= 16384) {
-      const int64_t most = std::max<int64_t>(1, std::min<int64_t>(8, k / (p.few * 256)));
-      for (int64_t s = 2; s <= most && busy(groups * splits) < 0.9; ++s)
-        if (busy(groups * s) > busy(groups * splits)) splits = s;
+    const int outputs = wide ? 32 : 16;
+    const int64_t groups = cdiv(n, outputs);
+    const int waves = k >= 4096 && (type == kF32 || groups < kComputeUnits) ? 8 : 4;
+    if (groups * (waves / 4) <= kMaxGroups) {  // else the kernels below, whose workgroups take 64 outputs or more
+      p.few = waves;
+      p.few_outputs = outputs;
+      // Where the outputs are too few for the CUs the contraction is split, into the fewest parts that keep them
+      // busy: 1 x 8192 x 1024 12.1 to 9.7, 1 x 16384 x 256 20.1 to 9.0, 23 x 11392 x 2528 (158 groups) 30.1 in one part,
+      // 33.3 in two, 25.7 in three; 9 x 10368 x 3046 fp32 (191 groups) 38 in one part, 42 in two.
+      int64_t splits = 1;
+      if (groups < kComputeUnits && busy(groups) < 0.7 && k * es >= 16384) {
+        const int64_t most = std::max<int64_t>(1, std::min<int64_t>(8, k / (waves * 256)));
+        for (int64_t s = 2; s <= most && busy(groups * splits) < 0.9; ++s)
+          if (busy(groups * s) > busy(groups * splits)) splits = s;
+      }
+      p.product.k_per_split = std::max<int64_t>(32, cdiv(cdiv(k, waves * splits), 32) * 32);
+      p.product.splits = std::max<int64_t>(1, cdiv(k, waves * p.product.k_per_split));
+      if (p.product.splits > 1) p.bytes = p.product.bytes = align_up((size_t)p.product.splits * m * n * 4);
+      return p;
     }
-    p.product.k_per_split = std::max<int64_t>(32, cdiv(cdiv(k, p.few * splits), 32) * 32);
-    p.product.splits = std::max<int64_t>(1, cdiv(k, p.few * p.product.k_per_split));
-    if (p.product.splits > 1) p.bytes = p.product.bytes = align_up((size_t)p.product.splits * m * n * 4);
-    return p;
   }
   const bool small = (double)m * n * k < (double)kSmallProduct;
   const bool ring = (x_whole && w_whole) || (!small && k > 0 && padded(k, es) * es <= kRingMaxPitch);
