@@ -32,3 +32,22 @@ def test_few_rows_of_more_outputs_than_their_kernel_can_launch(m, k):
         big = b[at:at + (1 << 25)].abs() + sum(X[:, i:i + 1].float().abs() * w[:, i].abs() for i in range(k))
         assert ((out[:, at:at + (1 << 25)].float() - z.clamp_min(0)).abs()
                 <= L.half_step(torch.bfloat16) * z.abs() + 2 * (k + 4) * 2.0 ** -23 * big).all()
+
+
+ROWS, FEATURES, OUTPUTS = (1 << 22) + 300, 520, 520  # 2^31 elements lie before row 4129776
+BORDER = (1 << 31) // FEATURES
+LIVE = torch.cat([torch.arange(0, 300), torch.arange(BORDER - 300, BORDER + 300), torch.arange(ROWS - 300, ROWS)])
+
+
+def test_weight_gradient_over_offsets_beyond_32_bits():
+    """dW sums rows on both sides of element 2^31 of G and X, and the last ones. Its bound is that of the rows that
+    are not zero: adding an exact zero rounds nothing. The slope is one, so d is G, unrounded."""
+    rows = LIVE.to(dev())
+    X = torch.zeros(ROWS, FEATURES, dtype=torch.bfloat16, device=dev())
+    X[rows] = rand((len(rows), FEATURES), 1, torch.bfloat16)
+    W = rand((OUTPUTS, FEATURES), 2, torch.bfloat16, FEATURES ** -0.5)
+    pre = torch.ones(ROWS, OUTPUTS, dtype=torch.bfloat16, device=dev())
+    note("linear_backward beyond 2^31 elements: dW")
+    _, dW, _ = xt.linear_backward(X, X, W, pre, "relu", need_dX=False)  # G is X
+    torch.cuda.synchronize()
+    L.check(dW, *L.backward(X[rows], X[rows], W, None, "none")["dW"], what="dW")
