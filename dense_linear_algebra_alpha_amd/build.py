@@ -1,5 +1,6 @@
 """Builds libxtvxy.so (the fused kernels and the C ABI) for gfx950 with hipcc, and
-_tensors.so (a small host-only Python extension) with g++.
+_tensors.so (a small host-only Python extension of the torch helpers) with g++.
+The library does not need the extension: without torch or g++ it is built alone.
 
 Objects go to _build/ next to this file and the shared libraries next to this
 file, so it travels with the source tree. Usage: ``python -m
@@ -7,7 +8,9 @@ dense_linear_algebra_alpha_amd.build`` or ``build()`` from Python.
 """
 from __future__ import annotations
 
+import importlib.util
 import os
+import shutil
 import subprocess
 import sys
 from concurrent.futures import ThreadPoolExecutor
@@ -57,6 +60,13 @@ def _compile(src: str) -> str:
     return obj
 
 
+def _extension_lacks() -> str:
+    """What the extension module cannot be built without and is not there, or an empty string."""
+    if importlib.util.find_spec("torch") is None:
+        return "torch"
+    return "" if shutil.which("g++") else "g++"
+
+
 def _build_tensors() -> None:
     """The host-only extension module, against the headers of the installed torch."""
     import sysconfig
@@ -77,12 +87,13 @@ def _build_tensors() -> None:
 
 
 def build(verbose: bool = False) -> str:
-    """Compile every source, link libxtvxy.so and build the extension module; returns the library path."""
+    """Compile every source, link libxtvxy.so and build the extension module; returns the library path. The
+    library is there also where the extension's build fails."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     with ThreadPoolExecutor(max_workers=min(len(SOURCES) + 1, os.cpu_count() or 1)) as ex:
-        tensors = ex.submit(_build_tensors)
+        lacks = _extension_lacks()
+        tensors = None if lacks else ex.submit(_build_tensors)
         objs = list(ex.map(_compile, SOURCES))
-        tensors.result()
     tmp = LIB_PATH + ".tmp%d" % os.getpid()
     cmd = [HIPCC, "--offload-arch=" + ARCH, "-shared", "-fPIC", "-o", tmp] + objs + [
         "-L" + os.path.join(ROCM, "lib"), "-lrocblas", "-lrocsparse", "-Wl,-rpath," + os.path.join(ROCM, "lib")]
@@ -92,16 +103,22 @@ def build(verbose: bool = False) -> str:
     os.replace(tmp, LIB_PATH)
     if verbose:
         print("built", LIB_PATH)
+    if lacks:
+        print("_tensors.so is not built without %s: the torch helpers work, with more host time a call" % lacks,
+              file=sys.stderr)
+    else:
+        tensors.result()
     return LIB_PATH
 
 
 def sources_newer_than_library() -> bool:
-    if not os.path.exists(LIB_PATH) or not os.path.exists(TENSORS_PATH):
+    extension = not _extension_lacks()
+    if not os.path.exists(LIB_PATH) or (extension and not os.path.exists(TENSORS_PATH)):
         return True
     t = os.path.getmtime(LIB_PATH)
     files = [os.path.join(CSRC, f) for f in SOURCES + HEADERS] + [os.path.join(INCLUDE, "xtvxy.h")]
     return any(os.path.getmtime(f) > t for f in files) or (
-        os.path.getmtime(os.path.join(CSRC, TENSORS_SOURCE)) > os.path.getmtime(TENSORS_PATH))
+        extension and os.path.getmtime(os.path.join(CSRC, TENSORS_SOURCE)) > os.path.getmtime(TENSORS_PATH))
 
 
 if __name__ == "__main__":

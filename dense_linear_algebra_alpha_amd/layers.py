@@ -132,13 +132,16 @@ def _backward_bytes(suffix, m, k, n, act, aligned) -> int:
 
 @functools.lru_cache(maxsize=None)
 def _extension():
-    """The extension module, with the layer's entry points bound; a missing one raises."""
+    """The extension module, with the layer's entry points bound; None, with a warning, where it is missing:
+    what it does is then done here, in more host time."""
     import torch  # noqa: F401  (the module resolves against it)
     try:
         from . import _tensors
     except ImportError as e:
-        raise RuntimeError("_tensors.so is not built or does not match this torch (%s); run `python -m "
-                           "dense_linear_algebra_alpha_amd.build`" % e) from None
+        import warnings
+        warnings.warn("_tensors.so is not built or does not match this torch (%s): calls take more host time; run "
+                      "`python -m dense_linear_algebra_alpha_amd.build`" % e, RuntimeWarning)
+        return None
     names = ("xtvxy_linear_%s_workspace_size", "xtvxy_linear_%s", "xtvxy_linear_backward_%s_workspace_size",
              "xtvxy_linear_backward_%s")
     _tensors.bind(*[ctypes.cast(_entry(f % s), ctypes.c_void_p).value for s in ("f32", "bf16", "f16") for f in names])
@@ -220,11 +223,12 @@ def linear(X, W, bias=None, residual=None, act="none", *, save_pre=False, out=No
     type: float32, bfloat16 or float16; bias is float32 (n). ``act`` is one of ACTIVATIONS. With
     ``save_pre`` (or ``pre`` given) the call also stores X W^T + bias, which linear_backward takes,
     and returns (out, pre). ``out`` may be the residual."""
-    if stream is None:  # the usual call in compiled code; None: what follows says what is wrong
+    if stream is None:  # the usual call in compiled code; None: what follows says what is wrong, or makes the call
         c = _torch()._C
         dev = c._cuda_getDevice() if X.is_cuda else -1
-        got = None if dev < 0 else _extension().linear(X, W, bias, residual, ACTIVATIONS.get(act, -1), save_pre, out, pre,
-                                                       workspace, dev, c._cuda_getCurrentRawStream(dev))
+        e = _extension() if dev >= 0 else None
+        got = e and e.linear(X, W, bias, residual, ACTIVATIONS.get(act, -1), save_pre, out, pre, workspace, dev,
+                             c._cuda_getCurrentRawStream(dev))
         if type(got) is int:
             _raise(got, "xtvxy_linear", X)
         if got is not None:
@@ -271,9 +275,9 @@ def linear_backward(G, X, W, pre=None, act="none", *, need_dX=True, need_dW=True
     if stream is None:  # as in linear
         c = _torch()._C
         dev = c._cuda_getDevice() if X.is_cuda else -1
-        got = None if dev < 0 else _extension().linear_backward(G, X, W, pre, ACTIVATIONS.get(act, -1), need_dX, need_dW,
-                                                                need_db, dX, dW, db, workspace, dev,
-                                                                c._cuda_getCurrentRawStream(dev))
+        e = _extension() if dev >= 0 else None
+        got = e and e.linear_backward(G, X, W, pre, ACTIVATIONS.get(act, -1), need_dX, need_dW, need_db, dX, dW, db,
+                                      workspace, dev, c._cuda_getCurrentRawStream(dev))
         if type(got) is int:
             _raise(got, "xtvxy_linear_backward", X)
         if got is not None:

@@ -135,11 +135,23 @@ class AdamW:
         pointers = self._pointers()
         if not n:
             return pointers, XTVXY_TYPE_F32
-        bad = _extension().addresses(tensors, self._numel_address, ctypes.addressof(pointers), n, self.device.index)
+        e = _extension()
+        bad = (e.addresses(tensors, self._numel_address, ctypes.addressof(pointers), n, self.device.index) if e else
+               self._addresses(tensors, pointers))
         if bad >= 0:
             raise ValueError("%s[%d] must be a contiguous tensor of %d elements on %s, of the list's one type"
                              % (name, bad, self._numel[bad], self.device))
         return pointers, _type_code(tensors[0].dtype)
+
+    def _addresses(self, tensors, pointers) -> int:
+        """What the extension's addresses() does."""
+        strided = _torch().strided
+        for i, (t, n) in enumerate(zip(tensors, self._numel)):
+            if (getattr(t, "layout", None) is not strided or t.get_device() != self.device.index
+                    or t.dtype is not tensors[0].dtype or t.numel() != n or not t.is_contiguous()):
+                return i
+            pointers[i] = t.data_ptr()
+        return -1
 
     def step(self, grads, *, stream=None):
         """One step with the gradients of the parameters, in their order: contiguous tensors of one type
