@@ -11,7 +11,8 @@ Two layers, both argument marshalling only:
     as ints, the stream as an int handle);
   * tensor helpers (``dense``, ``csr``, ``dense_unfused``, ``CsrUnfusedPlan``)
     that take torch CUDA tensors, allocate the workspace with torch, and call
-    the C entry points on the current torch stream.
+    the C entry points on the current torch stream. They take no part in autograd:
+    results carry no graph.
 Every computation happens in the library's kernels; a missing library raises.
 """
 from __future__ import annotations

@@ -222,7 +222,11 @@ def linear(X, W, bias=None, residual=None, act="none", *, save_pre=False, out=No
     X (m x k), W (n x k), residual and out (m x n) are 2-D tensors with unit column stride, of one
     type: float32, bfloat16 or float16; bias is float32 (n). ``act`` is one of ACTIVATIONS. With
     ``save_pre`` (or ``pre`` given) the call also stores X W^T + bias, which linear_backward takes,
-    and returns (out, pre). ``out`` may be the residual."""
+    and returns (out, pre). ``out`` may be the residual.
+
+    Nothing here is recorded by autograd: results carry no graph, whether or not the arguments require
+    gradients, and tensors given as outputs are written without moving their version counters. The
+    gradient is linear_backward's."""
     if stream is None:  # the usual call in compiled code; None: what follows says what is wrong, or makes the call
         c = _torch()._C
         dev = c._cuda_getDevice() if X.is_cuda else -1

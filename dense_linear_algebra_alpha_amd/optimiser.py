@@ -58,8 +58,9 @@ class AdamW:
     rounds them at random from ``seed`` (formats in include/xtvxy.h). ``state`` resumes from (m, v), or
     (m, v, m_exp, v_exp) for 8 bits, lists of tensors that the object goes on using (uint8 for 8 bits);
     None starts from zeros. ``steps`` is the number of steps taken before. The object keeps its tensors:
-    they must not be resized or moved, and their GPU has to be the current one in every call. lr, betas,
-    eps, weight_decay and seed are plain attributes."""
+    they must not be resized or moved, and their GPU has to be the current one in every call. To autograd a
+    step is a write in place: a backward pass through what it saved of params or copies before raises. lr,
+    betas, eps, weight_decay and seed are plain attributes."""
 
     def __init__(self, params, lr=1e-3, betas=(0.9, 0.999), eps=1e-8, weight_decay=0.01, *, copies=None, state_bits=32,
                  state=None, steps=0, seed=0):
@@ -99,6 +100,7 @@ class AdamW:
         self.lr, self.betas, self.eps, self.weight_decay, self.seed = lr, tuple(betas), eps, weight_decay, seed
         n = len(params)
         self._numel = numel
+        self._written = params + (copies or [])
         self._pointers = ctypes.c_void_p * n
         self._count = count = (ctypes.c_int64 * n)(*numel)
         self._numel_address = ctypes.addressof(count)
@@ -161,6 +163,11 @@ class AdamW:
         xtvxy_adamw_step(self.handle, pointers, code, self.steps + 1, self.lr, self.betas[0], self.betas[1], self.eps,
                          self.weight_decay, self.seed & 0xffffffff, _stream_of(stream, self.device.index))
         self.steps += 1
+        e = _extension()
+        if e:
+            e.written(self._written)
+        else:
+            _torch().autograd.graph.increment_version([t for t in self._written if not t.is_inference()])
 
     def state_values(self, m_out, v_out, *, stream=None):
         """Writes the values that the moments stand for into tensors of the parameters' sizes."""
