@@ -17,6 +17,8 @@ constexpr int64_t kMaxGroups = ((int64_t)1 << 24) - 1;  // workgroups of 256 thr
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 bool bytes_overflow(int64_t rows, int64_t ld) { return rows > 0 && ld > INT64_MAX / 16 / rows; }
+// The same for rows of cols elements padded by up to 8.
+bool padded_overflow(int64_t rows, int64_t cols) { return rows > 0 && cols > INT64_MAX / 16 / rows - 8; }
 
 struct Matrix {
   const void* p;
@@ -356,7 +358,7 @@ const LinearPlan& plan_linear(int type, int64_t m, int64_t k, int64_t n, bool x_
 xtvxy_status linear_workspace(int type, int64_t m, int64_t k, int64_t n, int aligned16, size_t* bytes) {
   if (!bytes) return XTVXY_ERROR_NULL_POINTER;
   if (m < 0 || k < 0 || n < 0) return XTVXY_ERROR_INVALID_VALUE;
-  if (bytes_overflow(m, n) || bytes_overflow(m, k + 8) || bytes_overflow(n, k + 8)) return XTVXY_ERROR_INVALID_VALUE;
+  if (bytes_overflow(m, n) || padded_overflow(m, k) || padded_overflow(n, k)) return XTVXY_ERROR_INVALID_VALUE;
   *bytes = 0;
   if (m == 0 || n == 0) return XTVXY_SUCCESS;
   if (!product_fits(m, n)) return XTVXY_ERROR_UNSUPPORTED;
@@ -515,7 +517,7 @@ size_t most_backward_bytes(int type, int64_t m, int64_t k, int64_t n, int act, i
 xtvxy_status backward_workspace(int type, int64_t m, int64_t k, int64_t n, int act, int aligned16, size_t* bytes) {
   if (!bytes) return XTVXY_ERROR_NULL_POINTER;
   if (m < 0 || k < 0 || n < 0 || !valid_act(act)) return XTVXY_ERROR_INVALID_VALUE;
-  if (bytes_overflow(m, n + 8) || bytes_overflow(m, k + 8) || bytes_overflow(n, k + 8)) return XTVXY_ERROR_INVALID_VALUE;
+  if (padded_overflow(m, n) || padded_overflow(m, k) || padded_overflow(n, k)) return XTVXY_ERROR_INVALID_VALUE;
   *bytes = 0;
   if (m == 0 || n == 0) return XTVXY_SUCCESS;
   if (!backward_fits(m, k, n)) return XTVXY_ERROR_UNSUPPORTED;
@@ -530,7 +532,7 @@ xtvxy_status backward_impl(int type, int64_t m, int64_t k, int64_t n, const void
                            int64_t lddx, void* dW, int64_t lddw, float* db, void* ws, size_t ws_bytes,
                            hipStream_t stream) {
   if (m < 0 || k < 0 || n < 0 || !valid_act(act)) return XTVXY_ERROR_INVALID_VALUE;
-  if (bytes_overflow(m, n + 8)) return XTVXY_ERROR_INVALID_VALUE;
+  if (padded_overflow(m, n)) return XTVXY_ERROR_INVALID_VALUE;
   if (bad_ld(ldg, n, m) || bad_ld(ldx, k, m) || bad_ld(ldw, k, n) || (dX && bad_ld(lddx, k, m)) ||
       (dW && bad_ld(lddw, k, n)) || (act != XTVXY_ACT_NONE && bad_ld(ldp, n, m)))
     return XTVXY_ERROR_INVALID_VALUE;
