@@ -94,7 +94,8 @@ xtvxy_status create(int32_t tensors, const int64_t* numel, float* const* params,
     const uintptr_t states = reinterpret_cast<uintptr_t>(t.m) | reinterpret_cast<uintptr_t>(t.v);
     t.wide = (reinterpret_cast<uintptr_t>(t.p) | reinterpret_cast<uintptr_t>(t.copy)) % 16 == 0 &&
              states % (q ? 8 : 16) == 0;
-    if (((reinterpret_cast<uintptr_t>(t.p) | (q ? 0 : states)) % 4) != 0) return XTVXY_ERROR_INVALID_VALUE;
+    if ((reinterpret_cast<uintptr_t>(t.p) | (q ? 0 : states)) % 4 != 0 || reinterpret_cast<uintptr_t>(t.copy) % 2 != 0)
+      return XTVXY_ERROR_INVALID_VALUE;
     const int64_t blocks = (n + kAdamBlock - 1) / kAdamBlock;
     number += (uint64_t)blocks * kAdamBlock;
     for (int64_t c = 0; c * kAdamChunk < n; ++c) chunks.push_back({i, (int32_t)c});
