@@ -163,9 +163,9 @@ __global__ __launch_bounds__(kThreads) void adamw_step(AdamStep a) {
       v[i] = decode_v((vc[i / 4] >> (8 * (i & 3))) & 0xff, ve);
     }
   }
-  // The hardware's square root takes subnormals as zero (1e-19 at most), which only an eps next to
-  // that would show; such an eps takes the library's square root and division.
-  const bool exact = a.eps < 1e-12f;
+  // The hardware's square root takes subnormals as zero (roots of up to 1.1e-19), half a unit of an eps of
+  // 1.8e-12 times the root's factor; a smaller eps takes the library's square root and division.
+  const bool exact = a.eps < 2e-12f * a.root_scale;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     m[i] = fmaf(gr[i], a.one_minus_beta1, m[i] * a.beta1);

@@ -129,3 +129,21 @@ def test_infinite_parameters_stay():
         note("adamw infinite parameters, weight decay %g" % wd)
         xt.AdamW([p], lr=1e-3, weight_decay=wd).step([torch.ones(3, device=dev())])
         assert p[0] == float("inf") and p[1] == -float("inf") and torch.isfinite(p[2])
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+@pytest.mark.parametrize("beta2,eps", [(0.999999, 1e-12), (0.999, 1e-12), (0.99, 1e-13), (0.999999, 1e-8)])
+def test_second_moments_below_fp32s_normal_range(beta2, eps, bits):
+    """Gradients whose v is subnormal: its root counts next to eps, as the formula says."""
+    n = 512
+    # from 2^-140 to 2^-126: 2^-9 of the value at the least, halved by the root
+    v = 2.0 ** torch.linspace(-140, -126, n, dtype=torch.float64)
+    g = (v / (1 - beta2)).sqrt().float()
+    p = torch.zeros(n, device=dev())
+    note("adamw %d bits, subnormal second moments, beta2 %g, eps %g" % (bits, beta2, eps))
+    xt.AdamW([p], lr=1e-2, betas=(0.9, beta2), eps=eps, weight_decay=0.0, state_bits=bits).step([g.to(dev())])
+    want = -1e-2 * g.double() / (g.double().abs() + eps)
+    root = g.double() / (g.double() + eps)  # share of the root in the denominator
+    # v is kept to 2^-149; 32 units for the rest
+    tol = 32 * 2.0 ** -24 + root * 2.0 ** -149 / v
+    assert ((p.double().cpu() / want - 1).abs() <= tol).all()
