@@ -52,6 +52,14 @@ bool on_its_device(const xtvxy_adamw_s* h) {
   return hipGetDevice(&dev) == hipSuccess && dev == h->device;
 }
 
+// Whether any two of the [begin, end) ranges overlap; sorts them.
+bool overlap_within(std::vector<std::pair<uintptr_t, uintptr_t>>* ranges) {
+  std::sort(ranges->begin(), ranges->end());
+  for (size_t i = 1; i < ranges->size(); ++i)
+    if ((*ranges)[i].first < (*ranges)[i - 1].second) return true;
+  return false;
+}
+
 xtvxy_status create(int32_t tensors, const int64_t* numel, float* const* params, int state_bits, void* const* m,
                     void* const* v, uint8_t* const* m_exp, uint8_t* const* v_exp, int copy_type, void* const* copies,
                     xtvxy_adamw* out) {
@@ -111,9 +119,7 @@ xtvxy_status create(int32_t tensors, const int64_t* numel, float* const* params,
     add(t.v_exp, blocks);
     add(t.copy, n * 2);
   }
-  std::sort(h->written.begin(), h->written.end());
-  for (size_t i = 1; i < h->written.size(); ++i)
-    if (h->written[i].first < h->written[i - 1].second) return XTVXY_ERROR_ALIASING;
+  if (overlap_within(&h->written)) return XTVXY_ERROR_ALIASING;
   h->tensors = tensors;
   h->state_bits = state_bits;
   h->copy_type = copy_type;
@@ -142,6 +148,41 @@ xtvxy_status for_runs(const xtvxy_adamw_s* h, int most, F fn) {
     t0 = t1;
   }
   return XTVXY_SUCCESS;
+}
+
+xtvxy_status state_values(const xtvxy_adamw_s* h, void* const* m_out, void* const* v_out, int type, hipStream_t stream) {
+  if (!h) return XTVXY_ERROR_NULL_POINTER;
+  if (!valid_type(type)) return XTVXY_ERROR_INVALID_VALUE;
+  if (h->first_chunk.back() == 0) return XTVXY_SUCCESS;
+  if (!m_out || !v_out) return XTVXY_ERROR_NULL_POINTER;
+  const int es = type_size(type);
+  std::vector<std::pair<uintptr_t, uintptr_t>> out;
+  out.reserve(2 * h->numel.size());
+  size_t at = 0;
+  for (int32_t i = 0; i < h->tensors; ++i) {
+    if (h->numel[i] == 0) continue;
+    for (const void* p : {m_out[i], v_out[i]}) {
+      const uintptr_t o = reinterpret_cast<uintptr_t>(p);
+      if (!o) return XTVXY_ERROR_NULL_POINTER;
+      if (o % es != 0) return XTVXY_ERROR_INVALID_VALUE;
+      const uintptr_t end = o + (uintptr_t)h->numel[i] * es;
+      if (h->writes(o, end, &at)) return XTVXY_ERROR_ALIASING;
+      out.emplace_back(o, end);
+    }
+  }
+  if (overlap_within(&out)) return XTVXY_ERROR_ALIASING;
+  if (!on_its_device(h)) return XTVXY_ERROR_INVALID_VALUE;
+  AdamValues a;
+  a.tensors = h->d_tensors;
+  return for_runs(h, kAdamPointers / 2, [&](int32_t t0, int32_t t1, int64_t c0, int64_t chunks) {
+    a.chunks = h->d_chunks + c0;
+    a.first_tensor = t0;
+    for (int32_t i = t0; i < t1; ++i) {
+      a.out[2 * (i - t0)] = m_out[i];
+      a.out[2 * (i - t0) + 1] = v_out[i];
+    }
+    return launch_adamw_values(a, chunks, h->state_bits, elem_type(type), stream);
+  });
 }
 
 }  // namespace
@@ -202,35 +243,13 @@ xtvxy_status xtvxy_adamw_step(xtvxy_adamw h, const void* const* grads, int grad_
   });
 }
 
-xtvxy_status xtvxy_adamw_state_values(xtvxy_adamw h, void* const* m_out, void* const* v_out, int type,
+xtvxy_status xtvxy_adamw_state_values(xtvxy_adamw optimiser, void* const* m_out, void* const* v_out, int type,
                                       hipStream_t stream) {
-  if (!h) return XTVXY_ERROR_NULL_POINTER;
-  if (!valid_type(type)) return XTVXY_ERROR_INVALID_VALUE;
-  if (h->first_chunk.back() == 0) return XTVXY_SUCCESS;
-  if (!m_out || !v_out) return XTVXY_ERROR_NULL_POINTER;
-  const int es = type_size(type);
-  size_t at = 0;
-  for (int32_t i = 0; i < h->tensors; ++i) {
-    if (h->numel[i] == 0) continue;
-    for (const void* p : {m_out[i], v_out[i]}) {
-      const uintptr_t o = reinterpret_cast<uintptr_t>(p);
-      if (!o) return XTVXY_ERROR_NULL_POINTER;
-      if (o % es != 0) return XTVXY_ERROR_INVALID_VALUE;
-      if (h->writes(o, o + (uintptr_t)h->numel[i] * es, &at)) return XTVXY_ERROR_ALIASING;
-    }
+  try {
+    return state_values(optimiser, m_out, v_out, type, stream);
+  } catch (const std::exception&) {  // host memory
+    return XTVXY_ERROR_LAUNCH;
   }
-  if (!on_its_device(h)) return XTVXY_ERROR_INVALID_VALUE;
-  AdamValues a;
-  a.tensors = h->d_tensors;
-  return for_runs(h, kAdamPointers / 2, [&](int32_t t0, int32_t t1, int64_t c0, int64_t chunks) {
-    a.chunks = h->d_chunks + c0;
-    a.first_tensor = t0;
-    for (int32_t i = t0; i < t1; ++i) {
-      a.out[2 * (i - t0)] = m_out[i];
-      a.out[2 * (i - t0) + 1] = v_out[i];
-    }
-    return launch_adamw_values(a, chunks, h->state_bits, elem_type(type), stream);
-  });
 }
 
 }  // extern "C"

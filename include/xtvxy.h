@@ -802,7 +802,8 @@ xtvxy_status xtvxy_adamw_step(xtvxy_adamw optimiser, const void *const *grads, i
                               double beta1, double beta2, double eps, double weight_decay, uint32_t seed,
                               hipStream_t stream);
 /* Writes the values that m and v stand for into fp32, bf16 or fp16 tensors (host arrays of device
- * pointers; those of 8-bit states are exact in bf16 unless below its normal range). */
+ * pointers; those of 8-bit states are exact in bf16 unless below its normal range). The tensors may overlap
+ * neither each other nor the optimiser's. */
 xtvxy_status xtvxy_adamw_state_values(xtvxy_adamw optimiser, void *const *m_out, void *const *v_out, int type,
                                       hipStream_t stream);
 

@@ -147,3 +147,19 @@ def test_second_moments_below_fp32s_normal_range(beta2, eps, bits):
     # v is kept to 2^-149; 32 units for the rest
     tol = 32 * 2.0 ** -24 + root * 2.0 ** -149 / v
     assert ((p.double().cpu() / want - 1).abs() <= tol).all()
+
+
+def test_values_of_states_do_not_share_memory():
+    p, x = torch.ones(300, device=dev()), torch.zeros(700, device=dev())
+    for bits in (8, 32):
+        note("adamw %d bits, values into overlapping tensors" % bits)
+        opt = xt.AdamW([p, p.clone()], state_bits=bits)
+        opt.step([p.clone(), p.clone()])
+        a, b, c, d = [torch.zeros(300, device=dev()) for _ in range(4)]
+        opt.state_values([a, b], [c, d])
+        for m, v in (([a, b], [a, d]), ([a, a], [c, d]), ([a, b], [c, c]), ([x[:300], b], [c, x[299:599]])):
+            with pytest.raises(xt.XtvxyError, match="ALIASING"):
+                opt.state_values(m, v)
+        opt.state_values([x[:300], b], [c, x[300:600]])
+        torch.cuda.synchronize()
+        assert torch.equal(x[:300], a) and torch.equal(x[300:600], d)
