@@ -51,3 +51,72 @@ def test_weight_gradient_over_offsets_beyond_32_bits():
     _, dW, _ = xt.linear_backward(X, X, W, pre, "relu", need_dX=False)  # G is X
     torch.cuda.synchronize()
     L.check(dW, *L.backward(X[rows], X[rows], W, None, "none")["dW"], what="dW")
+
+
+def check(got, ref, bound, what):
+    """layer_oracle.check() of finite references, without copies to the host."""
+    assert got.shape == ref.shape, what
+    assert ((got.double() - ref).abs() <= bound).all(), what
+
+
+LONG = (1 << 21) + 9  # rows of more than 4 MiB in every type
+SOME = torch.cat([torch.arange(0, 130), torch.arange(LONG // 2 - 130, LONG // 2 + 130), torch.arange(LONG - 130, LONG)])
+
+
+@pytest.mark.parametrize("dtype", list(L.DTYPES))
+@pytest.mark.parametrize("m", [5, 40, 130])
+def test_forward_over_long_rows(m, dtype):
+    """A contraction of over 2^21 features, which only the kernels for rows of any length take; zeros in all but some
+    of them, so that the bound is theirs."""
+    n, cols = 24, SOME.to(dev())
+    X, W = torch.zeros(m, LONG, dtype=L.DTYPES[dtype], device=dev()), rand((n, LONG), 2, L.DTYPES[dtype], 0.05)
+    X[:, cols] = rand((m, len(cols)), 1, X.dtype)
+    b, R = rand((n,), 3, torch.float32), rand((m, n), 4, X.dtype)
+    note("linear over long rows %s m=%d" % (dtype, m))
+    out, pre = xt.linear(X, W, b, R, "gelu", save_pre=True)
+    torch.cuda.synchronize()
+    y, ey, z, ez = L.forward(X[:, cols], W[:, cols], b, R, "gelu")
+    L.check(out, y, ey, "out")
+    L.check(pre, z, ez, "pre")
+
+
+@pytest.mark.parametrize("dtype", list(L.DTYPES))
+@pytest.mark.parametrize("act", ["none", "silu"])
+@pytest.mark.parametrize("size", [(40, LONG, 24), (70, LONG, 9), (130, LONG - 1, 33)], ids=lambda s: "%dx%dx%d" % s)
+def test_backward_over_long_rows(size, act, dtype):
+    """Rows of X and W too long for the ring kernel: the tile kernel forms d itself, in 16 bits too."""
+    m, k, n = size
+    X, W = rand((m, k), 1, L.DTYPES[dtype]), rand((n, k), 2, L.DTYPES[dtype])
+    G, pre = rand((m, n), 3, X.dtype), rand((m, n), 4, X.dtype)
+    for need in ((True, True, True), (True, False, True), (False, True, False)):
+        note("linear_backward over long rows %s %s %s %s" % (size, act, dtype, need))
+        got = xt.linear_backward(G, X, W, None if act == "none" else pre, act, need_dX=need[0], need_dW=need[1],
+                                 need_db=need[2])
+        torch.cuda.synchronize()
+        ref = L.backward(G, X, W, pre, act)
+        for t, name, wanted in zip(got, ("dX", "dW", "db"), need):
+            assert (t is not None) == wanted
+            if wanted:
+                check(t, *ref[name], what=name)
+        del got, ref
+
+
+@pytest.mark.parametrize("dtype", list(L.DTYPES))
+@pytest.mark.parametrize("act", ["none", "gelu_tanh"])
+def test_backward_over_many_outputs(act, dtype):
+    """Rows of G and pre too long for the ring kernel, zeros in all but some of G's columns."""
+    m, k, n = 70, 33, LONG
+    cols = SOME.to(dev())
+    X, W, pre = rand((m, k), 1, L.DTYPES[dtype]), rand((n, k), 2, L.DTYPES[dtype]), rand((m, n), 4, L.DTYPES[dtype])
+    G = torch.zeros(m, n, dtype=X.dtype, device=dev())
+    G[:, cols] = rand((m, len(cols)), 3, X.dtype)
+    note("linear_backward over many outputs %s %s" % (act, dtype))
+    dX, dW, db = xt.linear_backward(G, X, W, None if act == "none" else pre, act)
+    torch.cuda.synchronize()
+    ref = L.backward(G[:, cols], X, W[cols], pre[:, cols], act)
+    check(dX, *ref["dX"], what="dX")
+    check(dW[cols], *ref["dW"], what="dW")
+    check(db[cols], *ref["db"], what="db")
+    others = torch.ones(n, dtype=torch.bool, device=dev())
+    others[cols] = False
+    assert not dW[others].any() and not db[others].any()
