@@ -783,15 +783,16 @@ enum { XTVXY_TYPE_NONE = 0, XTVXY_TYPE_F32 = 1, XTVXY_TYPE_BF16 = 2, XTVXY_TYPE_
  * steps are as small as after any other; a finite v beyond 1.9375 2^126 is stored as that.
  * Fresh 8-bit states are zero codes with any exponents.
  *
- * xtvxy_adamw_create is a set-up call: it allocates and fills a table of the tensors in device memory
- * (synchronising) and keeps the pointers to params, states and copies, which must stay valid until
- * xtvxy_adamw_destroy. numel, params, m, v, m_exp, v_exp and copies are HOST arrays of `tensors`
- * entries (m_exp and v_exp NULL for 32 bits, copies NULL for copy_type XTVXY_TYPE_NONE); entries of
- * empty tensors may be NULL. Overlapping buffers give XTVXY_ERROR_ALIASING. Gradients (host
- * array of device pointers, one type for all) are passed at each step and may be other tensors each
- * time; they may not overlap what a step writes. The object is used on the device that was current when
- * it was made (XTVXY_ERROR_INVALID_VALUE otherwise); steps of one object run in stream order.
- * A captured step replays with the t and rates that it was captured with. */
+ * xtvxy_adamw_create is a set-up call (not during a stream capture): it allocates and fills a table of
+ * the tensors in device memory (synchronising) and keeps the pointers to params, states and copies, which
+ * must stay valid until xtvxy_adamw_destroy. numel, params, m, v, m_exp, v_exp and copies are HOST arrays of
+ * `tensors` entries (m_exp and v_exp NULL for 32 bits, copies NULL for copy_type XTVXY_TYPE_NONE); entries
+ * of empty tensors may be NULL. Overlapping buffers give XTVXY_ERROR_ALIASING. Gradients (host array of
+ * device pointers, one type for all) are passed at each step and may be other tensors each time; they may
+ * not overlap what a step writes. The object is used on the device that was current when it was made, where
+ * its tensors have to be (XTVXY_ERROR_INVALID_VALUE on another one); steps of one object run in stream
+ * order. A captured step replays with the t and rates that it was captured with, and the object must outlive
+ * the graph. */
 typedef struct xtvxy_adamw_s *xtvxy_adamw;
 xtvxy_status xtvxy_adamw_create(int32_t tensors, const int64_t *numel, float *const *params, int state_bits,
                                 void *const *m, void *const *v, uint8_t *const *m_exp, uint8_t *const *v_exp,

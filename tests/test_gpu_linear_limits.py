@@ -120,3 +120,21 @@ def test_backward_over_many_outputs(act, dtype):
     others = torch.ones(n, dtype=torch.bool, device=dev())
     others[cols] = False
     assert not dW[others].any() and not db[others].any()
+
+
+@pytest.mark.parametrize("dtype", list(L.DTYPES))
+@pytest.mark.parametrize("m", [3, 40, 300])
+def test_no_features(m, dtype):
+    """k = 0: the layer is act(bias) + residual, the gradient db alone."""
+    n, dt = 264, L.DTYPES[dtype]
+    X, W = torch.empty(m, 0, dtype=dt, device=dev()), torch.empty(n, 0, dtype=dt, device=dev())
+    b, R, pre = rand((n,), 3, torch.float32), rand((m, n), 4, dt), rand((m, n), 5, dt)
+    note("no features %s m=%d" % (dtype, m))
+    out, z = xt.linear(X, W, b, R, "silu", save_pre=True)
+    dX, dW, db = xt.linear_backward(R, X, W, pre, "silu")
+    torch.cuda.synchronize()
+    y, ey, z64, ez = L.forward(X, W, b, R, "silu")
+    check(out, y, ey, "out")
+    check(z, z64, ez, "pre")
+    assert dX.shape == (m, 0) and dW.shape == (n, 0)
+    check(db, *L.backward(R, X, W, pre, "silu")["db"], what="db")
