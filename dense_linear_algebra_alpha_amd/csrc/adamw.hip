@@ -4,8 +4,8 @@
 // 2 + 2 (and 4 / 128) of 8-bit ones, and 2 of a 16-bit copy. A workgroup takes 2048 elements of one
 // tensor, a thread 8 neighbours: 16-byte accesses of every operand but the 8-bit states (8 bytes), and
 // a block of 128 elements, which shares an exponent, lies in 16 lanes. 100 M elements with bf16 gradients and
-// copies: 515 us with 32-bit states (5.4 TB/s; a copy of 4 GiB reaches 4.7), 295 us with 8-bit ones
-// (5.4 TB/s), and 110 us to write the values of both (5.5 TB/s).
+// copies: 518 us with 32-bit states (5.4 TB/s; a copy of 4 GiB reaches 4.7), 306 us with 8-bit ones
+// (5.2 TB/s), and 113 us to write the values of both (5.3 TB/s).
 #include "adamw.h"
 #include "linear_util.h"
 

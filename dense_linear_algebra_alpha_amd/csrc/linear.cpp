@@ -56,9 +56,9 @@ struct ProductPlan {
 // The estimate of a launch's time. Its workgroups are jobs of so many stages (32 steps; fp32: 16). A CU
 // holds one of 256 x 256, two of 128 x 128 or five of 64 x 64 at a time, and works off a stage in
 // stage_us of the matrix unit and LDS; a smaller tile alone on its CU waits instead, alone_us a stage.
-// The constants were fitted to 1900 measured choices of tile and parts for 64 products and gradients of
-// 2^23 to 2^36 multiplications: what the estimate picks is 1.1% slower than the best one in the geometric
-// mean, 12% at most (one tile for all: 256 x 256 up to 2.9 times slower, 64 x 64 up to 2.6).
+// The constants were fitted to 1842 measured choices of tile and parts for 62 products and gradients of
+// 2^23 to 2^36 multiplications: what the estimate picks is 1.0% slower than the best one in the geometric
+// mean, 12% at most (one tile for all: 256 x 256 up to 3.2 times slower, 128 x 128 2.0, 64 x 64 2.6).
 int residents(int tile) { return tile == 256 ? 1 : tile == 128 ? 2 : 5; }
 double stage_us(int type, int tile) {
   if (type == kF32) return tile == 128 ? 1.12 : 0.28;
@@ -233,7 +233,8 @@ void plan_gradient(int type, int64_t m, int64_t k, int64_t n, bool want_dx, bool
   }
 }
 
-// Plans of the shapes of a thread's latest calls: the search takes 10 to 100 us, a call 5.
+// Plans of the shapes of a thread's latest calls. The search takes 1.2 us for a layer (15 at most over 600 shapes)
+// and 8 for a gradient (26), and a gradient's workspace query looks at up to 24 of them; a call takes 4.
 template <typename Plan>
 struct PlanCache {
   struct Entry {

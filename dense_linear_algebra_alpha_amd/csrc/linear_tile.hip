@@ -3,7 +3,7 @@
 // copies with padded rows, and the sum of a split contraction's parts.
 //
 // These are bound by latency: a launch, the first loads, a step's barrier and the end of the tile. fp16
-// 1023 x 1111 x 777 (35 steps) takes 12 us, the slope of 4096 x 4096 in bf16 20.5 us (4.9 TB/s), of
+// 1023 x 1111 x 777 (35 steps) takes 13.8 us, the slope of 4096 x 4096 in bf16 21 us (4.8 TB/s), of
 // 1501 x 501 5.
 #include "linear_util.h"
 
@@ -72,7 +72,7 @@ __device__ __forceinline__ f32x8 slope8(V g, V z, int act) {
 // A 64 x 64 tile of C, four wavefronts of 32 x 32 each. The product is formed transposed (B's rows as
 // the matrix instruction's first operand), so that a lane ends with four neighbouring columns of one
 // row of C. The next step's elements are in flight while the present one's products run. The first operand
-// is G, and d is formed between its load and its store to LDS; where the contraction runs over d's rows
+// is G, and d is formed between its load and its store to LDS, in the element type (as slope_rows does); where the contraction runs over d's rows
 // and this is the product's first tile column, its column sums are taken from the unrounded d on the way.
 template <typename T, bool kAMajor, bool kBMajor>
 __device__ __forceinline__ void tile(const ProductArgs& a, uint32_t id, const GradientArgs* grad, T* sa, T* sb) {
@@ -301,7 +301,10 @@ __global__ __launch_bounds__(kThreads) void gradient_finish(GradientArgs a) {
   column_sum(a.sums, a.sum_rows, a.n, a.db, id - a.dw_groups, lds);
 }
 
-// d = g act'(pre) in fp32, stored in the element type; the column sums db take d before that rounding.
+// d = g act'(pre) in fp32, stored in the element type, which is what the products' instructions take; the
+// column sums db take d before that rounding. It makes the error of 16-bit dX and dW 1.41 times what rounding
+// them alone costs (bf16 2.35e-3 against 1.66e-3 in the 2-norm, fp16 2.94e-4 against 2.08e-4); d as the sum of
+// two 16-bit parts would take twice the products.
 // A workgroup walks rows_per_group rows of 8 kLanes columns, a thread owns 8 neighbouring columns of
 // every 256 / kLanes-th row.
 template <typename T, int kAct, int kLanes>
