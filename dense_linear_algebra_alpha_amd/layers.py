@@ -272,7 +272,8 @@ def linear(X, W, bias=None, residual=None, act="none", *, save_pre=False, out=No
 def linear_backward(G, X, W, pre=None, act="none", *, need_dX=True, need_dW=True, need_db=True, dX=None, dW=None,
                     db=None, workspace=None, stream=None):
     """The gradient of linear: (dX, dW, db) for G = d loss / d out, with d = G * act'(pre),
-    dX = d W, dW = d^T X and db the column sums of d (float32). The residual's gradient is G.
+    dX = d W, dW = d^T X and db the column sums of d (float32). The residual's gradient is G. d is formed
+    in float32; the products take it in the tensors' type, db sums it unrounded.
 
     ``pre`` is what linear stored (required unless act is "none"). Outputs that are not needed are
     not computed and come back as None."""
