@@ -117,3 +117,32 @@ def test_fresh_optimiser_states_behind_a_busy_stream():
     torch.cuda.synchronize()
     assert torch.equal(opt.state[0][0], g * torch.tensor(1 - 0.9, device=dev()))
     assert (opt.state[1][0] > 0).all()
+
+
+def test_calls_on_a_side_stream_of_a_captured_graph():
+    X, W, G = normal((300, 520), 1, torch.bfloat16), normal((264, 520), 2, torch.bfloat16), normal((300, 264), 3, torch.bfloat16)
+    y, v = normal(520, 4), normal(300, 5)
+    side = torch.cuda.Stream()
+
+    def step(stream):
+        out, pre = xt.linear(X, W, act="silu", save_pre=True, stream=stream)
+        return (out, pre) + xt.linear_backward(G, X, W, pre, "silu", stream=stream) + (xt.dense(X, y, v, stream=stream),)
+
+    note("side stream of a captured graph")
+    step(None)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        held = step(side)
+        here.wait_stream(side)
+    for seed in (10, 20, 30):
+        for i, t in enumerate((X, W, G)):
+            t.copy_(normal(t.shape, seed + i, torch.bfloat16))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in held]
+        want = step(None)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
