@@ -57,16 +57,30 @@ __all__ = [
     "xtvxy_linear_backward_f16_workspace_size", "xtvxy_linear_backward_f32", "xtvxy_linear_backward_bf16",
     "xtvxy_linear_backward_f16", "AdamW", "xtvxy_adamw_create", "xtvxy_adamw_destroy", "xtvxy_adamw_step",
     "xtvxy_adamw_state_values",
+    "embedding", "embedding_backward", "xtvxy_embedding_f32", "xtvxy_embedding_bf16", "xtvxy_embedding_f16",
+    "xtvxy_embedding_backward_f32", "xtvxy_embedding_backward_bf16", "xtvxy_embedding_backward_f16",
+    "xtvxy_embedding_backward_f32_workspace_size", "xtvxy_embedding_backward_bf16_workspace_size",
+    "xtvxy_embedding_backward_f16_workspace_size", "layer_norm", "layer_norm_backward",
+    "xtvxy_layer_norm_backward_workspace_size", "xtvxy_layer_norm_f32", "xtvxy_layer_norm_bf16",
+    "xtvxy_layer_norm_f16", "xtvxy_layer_norm_backward_f32", "xtvxy_layer_norm_backward_bf16",
+    "xtvxy_layer_norm_backward_f16",
 ]
 
 load = _abi.load
 
+from .embeddings import (embedding, embedding_backward, xtvxy_embedding_f32, xtvxy_embedding_bf16,  # noqa: E402,F401
+                         xtvxy_embedding_f16, xtvxy_embedding_backward_f32, xtvxy_embedding_backward_bf16,
+                         xtvxy_embedding_backward_f16, xtvxy_embedding_backward_f32_workspace_size,
+                         xtvxy_embedding_backward_bf16_workspace_size, xtvxy_embedding_backward_f16_workspace_size)
 from .layers import (ACTIVATIONS, linear, linear_backward, xtvxy_linear_backward_bf16,  # noqa: E402,F401
                      xtvxy_linear_backward_bf16_workspace_size, xtvxy_linear_backward_f16,
                      xtvxy_linear_backward_f16_workspace_size, xtvxy_linear_backward_f32,
                      xtvxy_linear_backward_f32_workspace_size, xtvxy_linear_bf16, xtvxy_linear_bf16_workspace_size,
                      xtvxy_linear_f16, xtvxy_linear_f16_workspace_size, xtvxy_linear_f32,
                      xtvxy_linear_f32_workspace_size)
+from .norm import (layer_norm, layer_norm_backward, xtvxy_layer_norm_backward_workspace_size,  # noqa: E402,F401
+                   xtvxy_layer_norm_f32, xtvxy_layer_norm_bf16, xtvxy_layer_norm_f16, xtvxy_layer_norm_backward_f32,
+                   xtvxy_layer_norm_backward_bf16, xtvxy_layer_norm_backward_f16)
 from .optimiser import (AdamW, xtvxy_adamw_create, xtvxy_adamw_destroy, xtvxy_adamw_state_values,  # noqa: E402,F401
                         xtvxy_adamw_step)
 

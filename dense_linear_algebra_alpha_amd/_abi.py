@@ -201,6 +201,14 @@ for _t in ("f32", "bf16", "f16"):
     SIGNATURES["xtvxy_linear_backward_%s_workspace_size" % _t] = [_i64, _i64, _i64, _i32, _i32, _P(_sz)]
     SIGNATURES["xtvxy_linear_backward_%s" % _t] = [_i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _i32,
                                                    _vp, _i64, _vp, _i64, _vp, _vp, _sz, _vp]
+    SIGNATURES["xtvxy_layer_norm_" + _t] = [_i64, _i64, _vp, _i64, _vp, _vp, _f32, _vp, _i64, _vp, _vp, _vp]
+    SIGNATURES["xtvxy_layer_norm_backward_" + _t] = [_i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _i64, _vp, _vp,
+                                                     _vp, _sz, _vp]
+    SIGNATURES["xtvxy_embedding_" + _t] = [_i64, _i64, _i64, _vp, _i32, _vp, _i64, _f32, _vp, _i64, _vp]
+    SIGNATURES["xtvxy_embedding_backward_%s_workspace_size" % _t] = [_i64, _i64, _i64, _P(_sz)]
+    SIGNATURES["xtvxy_embedding_backward_" + _t] = [_i64, _i64, _i64, _vp, _i64, _vp, _i32, _f32, _i32, _vp, _i64, _vp,
+                                                    _sz, _vp]
+SIGNATURES["xtvxy_layer_norm_backward_workspace_size"] = [_i64, _i64, _P(_sz)]
 _vpp, _f64 = _P(_vp), ctypes.c_double
 SIGNATURES.update({
     "xtvxy_adamw_create": [ctypes.c_int32, _P(_i64), _vpp, _i32, _vpp, _vpp, _vpp, _vpp, _i32, _vpp, _vpp],

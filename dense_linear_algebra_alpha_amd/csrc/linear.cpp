@@ -6,6 +6,7 @@
 #include <cstdint>
 
 #include "linear.h"
+#include "matrix.h"
 
 using namespace xtvxy;
 
@@ -14,36 +15,6 @@ namespace {
 constexpr int64_t kComputeUnits = 256;           // the plans are for this chip whatever runs the query
 constexpr int64_t kMaxGroups = ((int64_t)1 << 24) - 1;  // workgroups of 256 threads in one launch: below 2^32 threads
 
-int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
-
-bool bytes_overflow(int64_t rows, int64_t ld) { return rows > 0 && ld > INT64_MAX / 16 / rows; }
-// The same for rows of cols elements padded by up to 8.
-bool padded_overflow(int64_t rows, int64_t cols) { return rows > 0 && cols > INT64_MAX / 16 / rows - 8; }
-
-struct Matrix {
-  const void* p;
-  int64_t rows, cols, ld;
-  int es;
-  size_t extent() const { return rows > 0 && cols > 0 ? (size_t)((rows - 1) * ld + cols) * es : 0; }
-  bool aligned16() const { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * es % 16 == 0; }
-};
-
-// Whether two matrices share an element (rows of equal pitch: exact; else by their extents).
-bool overlap(const Matrix& a, const Matrix& b) {
-  if (!a.p || !b.p) return false;
-  const size_t an = a.extent(), bn = b.extent();
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
-  if (an == 0 || bn == 0 || x >= y + bn || y >= x + an) return false;
-  const int64_t pitch = a.ld * a.es;
-  if (pitch != b.ld * b.es) return true;
-  int64_t d = (int64_t)(y - x) % pitch;  // of b's first column past a's, around the pitch
-  if (d < 0) d += pitch;
-  return !(d >= a.cols * a.es && d + b.cols * b.es <= pitch);
-}
-
-Matrix vec(const float* p, int64_t n) { return {p, 1, n, n > 0 ? n : 1, 4}; }
-
-xtvxy_status status_of(hipError_t e) { return e == hipSuccess ? XTVXY_SUCCESS : XTVXY_ERROR_LAUNCH; }
 
 // How one product is computed: by which kernel, which of its tiles whole and which in how many parts of
 // the contraction.
@@ -372,7 +343,6 @@ xtvxy_status linear_workspace(int type, int64_t m, int64_t k, int64_t n, int ali
   return XTVXY_SUCCESS;
 }
 
-bool bad_ld(int64_t ld, int64_t cols, int64_t rows) { return ld < std::max<int64_t>(cols, 1) || bytes_overflow(rows, ld); }
 
 xtvxy_status linear_impl(int type, int64_t m, int64_t k, int64_t n, const void* X, int64_t ldx, const void* W,
                          int64_t ldw, const float* bias, const void* residual, int64_t ldr, int act, void* out,

@@ -1,0 +1,442 @@
+// Layer norm over the rows of a matrix, and its gradient.
+//
+//     mean_i = sum_j x_ij / n,  rstd_i = 1 / sqrt(sum_j (x_ij - mean_i)^2 / n + eps),  xhat = (x - mean) rstd,
+//     out = xhat weight + bias;
+//     h = g weight,  dX = rstd (h - sum_j h_ij / n - xhat sum_j h_ij xhat_ij / n),
+//     dweight = sum_i g_ij xhat_ij,  dbias = sum_i g_ij.
+//
+// Both are bound by memory: the forward pass reads and writes each element once, the gradient reads two and
+// writes one. A row stays in the registers of the threads that share it (a wavefront, 4 or 16) between its
+// sums and its output. Threads keep their columns from row to row, so weight and bias are loaded once per
+// workgroup and the gradient's column sums stay in registers; the next row is loaded before the sums of the
+// current one are joined.
+//
+// A row's last chunk of 16 bytes, where n is no multiple of one, is the last 16 bytes of the row: memory
+// takes any alignment, a branch around its loads would make every row wait for them. What it shares with
+// the chunk before counts once in the sums and is stored twice with the same value.
+#include "linear_util.h"
+#include "norm.h"
+
+namespace xtvxy {
+namespace {
+
+template <typename T>
+constexpr int kChunkOf = 16 / sizeof(T);  // elements of a chunk
+
+// The chunks of a row that a thread owns: chunk c begins at column at[c]; the first skip[c] of its elements
+// belong to another chunk (all of them where the chunk is beyond the row).
+template <typename T, int L, int C>
+struct Columns {
+  static constexpr int V = kChunkOf<T>;
+  int32_t at[C], skip[C];
+  __device__ __forceinline__ Columns(int64_t n, int t) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int64_t j = (int64_t)(c * L + t) * V, last = n - V;
+      at[c] = (int32_t)(j < last ? j : last);
+      skip[c] = j < last ? 0 : j - last < V ? (int32_t)(j - last) : V;
+    }
+  }
+};
+
+template <typename T, int C>
+struct Chunks {
+  static constexpr int V = kChunkOf<T>;
+  T e[C][V];
+  template <typename K>
+  __device__ __forceinline__ void load(const T* row, const K& k) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) __builtin_memcpy(e[c], row + k.at[c], 16);
+  }
+};
+
+template <int V, typename K, int C>
+__device__ __forceinline__ void load_vector(const float* p, const K& k, float otherwise, float (&v)[C][V]) {
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    if (p) {
+      __builtin_memcpy(v[c], p + k.at[c], 4 * V);
+    } else {
+#pragma unroll
+      for (int e = 0; e < V; ++e) v[c][e] = otherwise;
+    }
+  }
+}
+
+// x over the wavefronts of a row (waves of them, slots of `lds` from `first` on), in a fixed order.
+template <int kWaves>
+__device__ __forceinline__ float row_sum(const float* lds, int first) {
+  float s = lds[first];
+#pragma unroll
+  for (int w = 1; w < kWaves; ++w) s += lds[first + w];
+  return s;
+}
+
+// A row's mean and sum of squared distances from it. Each wavefront forms its own mean first and takes
+// distances from that (no cancellation); the wavefronts' (mean, distances) join as
+//     mean = sum n_w mean_w / n,  sum = sum_w (sum_w + n_w (mean_w - mean)^2).
+template <typename T, int L, int C>
+__global__ __launch_bounds__(L < 256 ? 256 : L) void norm_rows(NormArgs a) {
+  constexpr int V = kChunkOf<T>, kBlock = L < 256 ? 256 : L, kRows = kBlock / L, kWaves = L / 64;
+  __shared__ float part[2][2][kBlock / 64];
+  const int t = threadIdx.x % L, sub = threadIdx.x / L, lane = threadIdx.x & 63;
+  const Columns<T, L, C> k(a.n, t);
+  float w[C][V], b[C][V];
+  load_vector<V>(a.weight, k, 1.0f, w);
+  load_vector<V>(a.bias, k, 0.0f, b);
+  const float n = (float)a.n;
+  int own = 0;  // elements of the row that this thread counts
+#pragma unroll
+  for (int c = 0; c < C; ++c) own += V - k.skip[c];
+  const float mine = group_sum((float)own, 64);
+  float counts[kWaves];  // of each wavefront of the row
+  if constexpr (kWaves > 1) {
+    if (lane == 0) part[0][0][threadIdx.x / 64] = mine;
+    __syncthreads();
+#pragma unroll
+    for (int v = 0; v < kWaves; ++v) counts[v] = part[0][0][sub * kWaves + v];
+    __syncthreads();
+  }
+  const T* X = static_cast<const T*>(a.x);
+  const int64_t step = (int64_t)gridDim.x * kRows;
+  int64_t i = (int64_t)blockIdx.x * kRows + sub;
+  Chunks<T, C> next;
+  next.load(X + (i < a.m ? i : a.m - 1) * a.ldx, k);
+  int turn = 0;
+  for (int64_t i0 = (int64_t)blockIdx.x * kRows; i0 < a.m; i0 += step, i += step, turn ^= 1) {
+    float x[C][V];
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int e = 0; e < V; ++e) x[c][e] = (float)next.e[c][e];
+    if (i0 + step < a.m) next.load(X + (i + step < a.m ? i + step : a.m - 1) * a.ldx, k);
+    float s = 0.0f;
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int e = 0; e < V; ++e) s += e >= k.skip[c] ? x[c][e] : 0.0f;
+    // divided: the mean of a constant row is that constant
+    float mean = mine > 0.0f ? group_sum(s, 64) / mine : 0.0f, q = 0.0f;
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const float d = x[c][e] - mean;
+        q += e >= k.skip[c] ? d * d : 0.0f;
+      }
+    q = group_sum(q, 64);
+    if constexpr (kWaves > 1) {
+      if (lane == 0) {
+        part[turn][0][threadIdx.x / 64] = mean;
+        part[turn][1][threadIdx.x / 64] = q;
+      }
+      __syncthreads();
+      const float* means = &part[turn][0][sub * kWaves];
+      const float* squares = &part[turn][1][sub * kWaves];
+      float total = 0.0f;
+#pragma unroll
+      for (int v = 0; v < kWaves; ++v) total += counts[v] * means[v];
+      mean = total / n;
+      q = 0.0f;
+#pragma unroll
+      for (int v = 0; v < kWaves; ++v) {
+        const float d = means[v] - mean;
+        q += squares[v] + counts[v] * d * d;
+      }
+    }
+    const float rstd = 1.0f / sqrtf(q / n + a.eps);
+    if (i >= a.m) continue;
+    if (t == 0) {
+      if (a.mean) a.mean[i] = mean;
+      if (a.rstd) a.rstd[i] = rstd;
+    }
+    T* out = static_cast<T*>(a.out) + i * a.ldo;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      if (k.skip[c] == V) continue;
+      T o[V];
+#pragma unroll
+      for (int e = 0; e < V; ++e) o[e] = (T)fmaf((x[c][e] - mean) * rstd, w[c][e], b[c][e]);
+      __builtin_memcpy(out + k.at[c], o, 16);
+    }
+  }
+}
+
+// The sum over a workgroup of kThreads, the same in every thread; `lds` has kThreads / 64 floats.
+template <int kThreads>
+__device__ __forceinline__ float block_sum(float x, float* lds) {
+  x = group_sum(x, 64);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = x;
+  __syncthreads();
+  return row_sum<kThreads / 64>(lds, 0);
+}
+
+// Rows shorter than a chunk or longer than the registers of 1024 threads: a workgroup walks the row once for
+// the mean, once for the distances and once for the output (the second and third time out of L2).
+template <typename T, int kThreads>
+__global__ __launch_bounds__(kThreads) void norm_any(NormArgs a) {
+  __shared__ float lds[kThreads / 64];
+  for (int64_t i = blockIdx.x; i < a.m; i += gridDim.x) {
+    const T* x = static_cast<const T*>(a.x) + i * a.ldx;
+    T* out = static_cast<T*>(a.out) + i * a.ldo;
+    float s = 0.0f, q = 0.0f;
+    for (int64_t j = threadIdx.x; j < a.n; j += kThreads) s += (float)x[j];
+    const float mean = block_sum<kThreads>(s, lds) / (float)a.n;
+    for (int64_t j = threadIdx.x; j < a.n; j += kThreads) {
+      const float d = (float)x[j] - mean;
+      q += d * d;
+    }
+    const float rstd = 1.0f / sqrtf(block_sum<kThreads>(q, lds) / (float)a.n + a.eps);
+    if (threadIdx.x == 0) {
+      if (a.mean) a.mean[i] = mean;
+      if (a.rstd) a.rstd[i] = rstd;
+    }
+    for (int64_t j = threadIdx.x; j < a.n; j += kThreads)
+      out[j] = (T)fmaf(((float)x[j] - mean) * rstd, a.weight ? a.weight[j] : 1.0f, a.bias ? a.bias[j] : 0.0f);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// the gradient
+// ---------------------------------------------------------------------------
+
+constexpr int kGradientThreads = 1024;
+
+// A workgroup takes 1024 / L rows at a time. Its rows' column sums join in LDS at the end.
+template <typename T, int L, int C>
+__global__ __launch_bounds__(kGradientThreads) void norm_gradient_rows(NormGradientArgs a) {
+  constexpr int V = kChunkOf<T>, kRows = kGradientThreads / L, kWaves = L / 64;
+  __shared__ float part[2][2][kGradientThreads / 64];
+  __shared__ __align__(16) float join[kRows][L * V];
+  const int t = threadIdx.x % L, sub = threadIdx.x / L, lane = threadIdx.x & 63;
+  const Columns<T, L, C> k(a.n, t);
+  float w[C][V], dw[C][V] = {}, db[C][V] = {};
+  load_vector<V>(a.weight, k, 1.0f, w);
+  const float inv_n = 1.0f / (float)a.n;
+  const T* X = static_cast<const T*>(a.x);
+  const T* G = static_cast<const T*>(a.g);
+  const int64_t step = (int64_t)gridDim.x * kRows;
+  int64_t i = (int64_t)blockIdx.x * kRows + sub;
+  Chunks<T, C> x, g;
+  float mean = 0.0f, rstd = 0.0f;
+  const auto load = [&](int64_t row) {
+    row = row < a.m ? row : a.m - 1;
+    x.load(X + row * a.ldx, k);
+    g.load(G + row * a.ldg, k);
+    mean = a.mean[row];
+    rstd = a.rstd[row];
+  };
+  load(i);
+  int turn = 0;
+  for (int64_t i0 = (int64_t)blockIdx.x * kRows; i0 < a.m; i0 += step, i += step, turn ^= 1) {
+    float xhat[C][V], h[C][V], s = 0.0f, q = 0.0f;
+    const float r = rstd;
+    const bool there = i < a.m;
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        const float ge = (float)g.e[c][e];
+        xhat[c][e] = ((float)x.e[c][e] - mean) * rstd;
+        h[c][e] = ge * w[c][e];
+        s += e >= k.skip[c] ? h[c][e] : 0.0f;
+        q += e >= k.skip[c] ? h[c][e] * xhat[c][e] : 0.0f;
+        if (there) {  // the same for a wavefront
+          dw[c][e] = fmaf(ge, xhat[c][e], dw[c][e]);
+          db[c][e] += ge;
+        }
+      }
+    if (i0 + step < a.m) load(i + step);
+    s = group_sum(s, 64);
+    q = group_sum(q, 64);
+    if constexpr (kWaves > 1) {
+      if (lane == 0) {
+        part[turn][0][threadIdx.x / 64] = s;
+        part[turn][1][threadIdx.x / 64] = q;
+      }
+      __syncthreads();
+      s = row_sum<kWaves>(part[turn][0], sub * kWaves);
+      q = row_sum<kWaves>(part[turn][1], sub * kWaves);
+    }
+    if (!there || !a.dx) continue;
+    s *= inv_n;
+    q *= inv_n;
+    T* dx = static_cast<T*>(a.dx) + i * a.lddx;
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      if (k.skip[c] == V) continue;
+      T o[V];
+#pragma unroll
+      for (int e = 0; e < V; ++e) o[e] = (T)(r * (h[c][e] - s - xhat[c][e] * q));
+      __builtin_memcpy(dx + k.at[c], o, 16);
+    }
+  }
+  if (!a.sums) return;
+  // columns of chunk c: L V neighbours from c L V on, V of each of the first row's threads
+  float* sums = a.sums + (int64_t)blockIdx.x * 2 * a.n;
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+      __syncthreads();
+#pragma unroll
+      for (int e = 0; e < V; ++e) join[sub][t * V + e] = which ? db[c][e] : dw[c][e];
+      __syncthreads();
+      for (int col = threadIdx.x; col < L * V; col += kGradientThreads) {
+        const int64_t j = (int64_t)c * L * V + col;
+        if (j >= a.n) break;
+        // the last, shifted chunk: column j lies skip elements further into it
+        const int64_t last = a.n - V, first = j / V * V;
+        const int from = first > last ? col + (int)(first - last) : col;
+        float s = join[0][from];
+#pragma unroll
+        for (int r = 1; r < kRows; ++r) s += join[r][from];
+        sums[which * a.n + j] = s;
+      }
+    }
+}
+
+// Rows of any length: the sums and dX of a row by one workgroup, which walks it twice.
+template <typename T, int kThreads>
+__global__ __launch_bounds__(kThreads) void norm_gradient_any(NormGradientArgs a) {
+  __shared__ float lds[kThreads / 64];
+  for (int64_t i = blockIdx.x; i < a.m; i += gridDim.x) {
+    const T* x = static_cast<const T*>(a.x) + i * a.ldx;
+    const T* g = static_cast<const T*>(a.g) + i * a.ldg;
+    T* dx = static_cast<T*>(a.dx) + i * a.lddx;
+    const float mean = a.mean[i], rstd = a.rstd[i];
+    float s = 0.0f, q = 0.0f;
+    for (int64_t j = threadIdx.x; j < a.n; j += kThreads) {
+      const float h = (float)g[j] * (a.weight ? a.weight[j] : 1.0f);
+      s += h;
+      q += h * (((float)x[j] - mean) * rstd);
+    }
+    s = block_sum<kThreads>(s, lds) / (float)a.n;
+    q = block_sum<kThreads>(q, lds) / (float)a.n;
+    for (int64_t j = threadIdx.x; j < a.n; j += kThreads) {
+      const float h = (float)g[j] * (a.weight ? a.weight[j] : 1.0f);
+      dx[j] = (T)(rstd * (h - s - ((float)x[j] - mean) * rstd * q));
+    }
+  }
+}
+
+// Their column sums: a thread owns a column over every groups-th row.
+template <typename T>
+__global__ __launch_bounds__(256) void norm_columns_any(NormGradientArgs a) {
+  const int64_t j = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (j >= a.n) return;
+  const T* X = static_cast<const T*>(a.x) + j;
+  const T* G = static_cast<const T*>(a.g) + j;
+  float dw = 0.0f, db = 0.0f;
+#pragma unroll 4
+  for (int64_t i = blockIdx.y; i < a.m; i += a.groups) {
+    const float g = (float)G[i * a.ldg];
+    dw = fmaf(g, ((float)X[i * a.ldx] - a.mean[i]) * a.rstd[i], dw);
+    db += g;
+  }
+  a.sums[(int64_t)blockIdx.y * 2 * a.n + j] = dw;
+  a.sums[((int64_t)blockIdx.y * 2 + 1) * a.n + j] = db;
+}
+
+// dweight and dbias from the workgroups' sums [groups][2][n], in fp64 and in a fixed order: 16 columns of the
+// 2 n a workgroup, as in column_sum.
+__global__ __launch_bounds__(256) void norm_gradient_finish(NormGradientArgs a) {
+  __shared__ double lds[256];
+  const int c = threadIdx.x & 15, slot = threadIdx.x >> 4;
+  const int64_t j = (int64_t)blockIdx.x * 16 + c;
+  double s = 0.0;
+  if (j < 2 * a.n) {
+#pragma unroll 4
+    for (int64_t g = slot; g < a.groups; g += 16) s += (double)a.sums[g * 2 * a.n + j];
+  }
+  lds[threadIdx.x] = s;
+  __syncthreads();
+  if (slot != 0 || j >= 2 * a.n) return;
+  for (int p = 1; p < 16; ++p) s += lds[p * 16 + c];
+  float* out = j < a.n ? a.dweight : a.dbias;
+  if (out) out[j < a.n ? j : j - a.n] = (float)s;
+}
+
+constexpr int64_t kMostGroups = 256;  // one workgroup per CU
+
+template <typename T, int L>
+void norm_for(const NormArgs& a, hipStream_t s) {
+  constexpr int kBlock = L < 256 ? 256 : L, kRows = kBlock / L;
+  const int64_t chunks = (a.n + kChunkOf<T> - 1) / kChunkOf<T>;
+  const int64_t most = 8192 * 64 / kBlock / (kBlock / 64);
+  const int64_t rows = (a.m + kRows - 1) / kRows;
+  const unsigned grid = (unsigned)(rows < most ? rows : most);
+  if (chunks <= L) norm_rows<T, L, 1><<<grid, kBlock, 0, s>>>(a);
+  else if (chunks <= 2 * L) norm_rows<T, L, 2><<<grid, kBlock, 0, s>>>(a);
+  else norm_rows<T, L, 4><<<grid, kBlock, 0, s>>>(a);
+}
+
+template <typename T>
+void norm_type(const NormArgs& a, hipStream_t s) {
+  constexpr int V = kChunkOf<T>;
+  if (a.n < V || a.n > 1024 * 4 * V) {
+    const unsigned grid = (unsigned)(a.m < 4096 ? a.m : 4096);
+    if (a.n < V) norm_any<T, 64><<<grid, 64, 0, s>>>(a);
+    else norm_any<T, 1024><<<grid, 1024, 0, s>>>(a);
+  } else if (a.n <= 64 * 4 * V) {
+    norm_for<T, 64>(a, s);
+  } else if (a.n <= 256 * 4 * V) {
+    norm_for<T, 256>(a, s);
+  } else {
+    norm_for<T, 1024>(a, s);
+  }
+}
+
+template <typename T, int L>
+void norm_gradient_for(const NormGradientArgs& a, hipStream_t s) {
+  constexpr int V = kChunkOf<T>;
+  const int64_t chunks = (a.n + V - 1) / V;
+  const unsigned grid = (unsigned)a.groups;
+  if (chunks <= L) norm_gradient_rows<T, L, 1><<<grid, kGradientThreads, 0, s>>>(a);
+  else if (V == 8 || chunks <= 2 * L) norm_gradient_rows<T, L, 2><<<grid, kGradientThreads, 0, s>>>(a);
+  else if constexpr (V == 4) norm_gradient_rows<T, L, 4><<<grid, kGradientThreads, 0, s>>>(a);
+}
+
+template <typename T>
+void norm_gradient_type(const NormGradientArgs& a, hipStream_t s) {
+  constexpr int V = kChunkOf<T>;
+  if (a.n < V || a.n > kNormGradientMost) {
+    const unsigned grid = (unsigned)(a.m < 4096 ? a.m : 4096);
+    if (a.dx && a.n < V) norm_gradient_any<T, 64><<<grid, 64, 0, s>>>(a);
+    else if (a.dx) norm_gradient_any<T, 1024><<<grid, 1024, 0, s>>>(a);
+    if (a.sums) norm_columns_any<T><<<dim3((unsigned)((a.n + 255) / 256), (unsigned)a.groups), 256, 0, s>>>(a);
+  } else if (a.n <= 64 * 16) {
+    norm_gradient_for<T, 64>(a, s);
+  } else if (a.n <= 256 * 16) {
+    norm_gradient_for<T, 256>(a, s);
+  } else {
+    norm_gradient_for<T, 1024>(a, s);
+  }
+  if (a.sums) norm_gradient_finish<<<(unsigned)((2 * a.n + 15) / 16), 256, 0, s>>>(a);
+}
+
+}  // namespace
+
+int64_t norm_gradient_groups(int64_t m, int64_t n) {
+  // rows that a workgroup takes at once; the kernels for any length take one
+  const int64_t rows = n > kNormGradientMost || n < 8 ? 1 : n <= 64 * 16 ? 16 : n <= 256 * 16 ? 4 : 1;
+  const int64_t groups = (m + rows - 1) / rows;
+  return groups < kMostGroups ? groups : kMostGroups;
+}
+
+hipError_t launch_norm(const NormArgs& a, int type, hipStream_t s) {
+  if (type == kBf16) norm_type<__bf16>(a, s);
+  else if (type == kF16) norm_type<_Float16>(a, s);
+  else norm_type<float>(a, s);
+  return hipGetLastError();
+}
+
+hipError_t launch_norm_gradient(const NormGradientArgs& a, int type, hipStream_t s) {
+  if (type == kBf16) norm_gradient_type<__bf16>(a, s);
+  else if (type == kF16) norm_gradient_type<_Float16>(a, s);
+  else norm_gradient_type<float>(a, s);
+  return hipGetLastError();
+}
+
+}  // namespace xtvxy

@@ -808,6 +808,82 @@ xtvxy_status xtvxy_adamw_step(xtvxy_adamw optimiser, const void *const *grads, i
 xtvxy_status xtvxy_adamw_state_values(xtvxy_adamw optimiser, void *const *m_out, void *const *v_out, int type,
                                       hipStream_t stream);
 
+/* ------------------------------------------------------------------------ */
+/* Layer norm and embedding, with their gradients                           */
+/* ------------------------------------------------------------------------ */
+
+/* Layer norm of each row of X (m x n, row stride ldx >= max(1, n)):
+ *     mean_i = sum_j x_ij / n,   rstd_i = 1 / sqrt(sum_j (x_ij - mean_i)^2 / n + eps),
+ *     out_ij = (x_ij - mean_i) rstd_i weight_j + bias_j.
+ * X and out share one element type (fp32, or bf16 / fp16 bit patterns); weight, bias (n floats, NULL: ones,
+ * zeros) and the statistics mean and rstd (m floats, NULL: not stored) are fp32. Everything is computed in
+ * fp32, the squares as distances from the mean, and rounded once as it is stored. NaN and infinities spread
+ * over their row as the formulas say. eps finite and >= 0. m == 0 or n == 0 is a no-op. An output that
+ * overlaps an input or another output gives XTVXY_ERROR_ALIASING. Pointers and strides of any alignment;
+ * results are bitwise reproducible. */
+xtvxy_status xtvxy_layer_norm_f32(int64_t m, int64_t n, const float *X, int64_t ldx, const float *weight,
+                                 const float *bias, float eps, float *out, int64_t ldo, float *mean, float *rstd,
+                                 hipStream_t stream);
+xtvxy_status xtvxy_layer_norm_bf16(int64_t m, int64_t n, const uint16_t *X, int64_t ldx, const float *weight,
+                                 const float *bias, float eps, uint16_t *out, int64_t ldo, float *mean, float *rstd,
+                                 hipStream_t stream);
+xtvxy_status xtvxy_layer_norm_f16(int64_t m, int64_t n, const uint16_t *X, int64_t ldx, const float *weight,
+                                 const float *bias, float eps, uint16_t *out, int64_t ldo, float *mean, float *rstd,
+                                 hipStream_t stream);
+
+/* Its gradient from G = d loss / d out and the forward call's mean and rstd: with xhat = (x - mean) rstd and
+ * h = g weight,
+ *     dX = rstd (h - sum_j h_ij / n - xhat sum_j h_ij xhat_ij / n),
+ *     dweight_j = sum_i g_ij xhat_ij,   dbias_j = sum_i g_ij   (n floats, fp32).
+ * weight may be NULL (ones). dX, dweight and dbias may each be NULL (not computed). m == 0 gives zero
+ * dweight and dbias. The workspace is needed for dweight and dbias alone. Otherwise as the forward call. */
+xtvxy_status xtvxy_layer_norm_backward_workspace_size(int64_t m, int64_t n, size_t *bytes);
+xtvxy_status xtvxy_layer_norm_backward_f32(int64_t m, int64_t n, const float *G, int64_t ldg, const float *X,
+                                          int64_t ldx, const float *mean, const float *rstd, const float *weight,
+                                          float *dX, int64_t lddx, float *dweight, float *dbias, void *workspace,
+                                          size_t workspace_bytes, hipStream_t stream);
+xtvxy_status xtvxy_layer_norm_backward_bf16(int64_t m, int64_t n, const uint16_t *G, int64_t ldg, const uint16_t *X,
+                                          int64_t ldx, const float *mean, const float *rstd, const float *weight,
+                                          uint16_t *dX, int64_t lddx, float *dweight, float *dbias, void *workspace,
+                                          size_t workspace_bytes, hipStream_t stream);
+xtvxy_status xtvxy_layer_norm_backward_f16(int64_t m, int64_t n, const uint16_t *G, int64_t ldg, const uint16_t *X,
+                                          int64_t ldx, const float *mean, const float *rstd, const float *weight,
+                                          uint16_t *dX, int64_t lddx, float *dweight, float *dbias, void *workspace,
+                                          size_t workspace_bytes, hipStream_t stream);
+
+/* Embedding: row i of out is scale times row ids[i] of the table (rows x k, row stride ldt >= max(1, k)),
+ * i < count. ids (device) are int32_t or int64_t by index_bits (32 or 64). Table and out share one element type;
+ * the product with scale is taken in fp32 and rounded once. A negative id is padding: its row of out is zero. An id
+ * >= rows, which the host cannot see, gives a row of NaN. count == 0 or k == 0 is a no-op. out may
+ * overlap neither table nor ids (XTVXY_ERROR_ALIASING). Pointers and strides of any alignment. */
+xtvxy_status xtvxy_embedding_f32(int64_t count, int64_t k, int64_t rows, const void *ids, int index_bits,
+                                const float *table, int64_t ldt, float scale, float *out, int64_t ldo, hipStream_t stream);
+xtvxy_status xtvxy_embedding_bf16(int64_t count, int64_t k, int64_t rows, const void *ids, int index_bits,
+                                const uint16_t *table, int64_t ldt, float scale, uint16_t *out, int64_t ldo, hipStream_t stream);
+xtvxy_status xtvxy_embedding_f16(int64_t count, int64_t k, int64_t rows, const void *ids, int index_bits,
+                                const uint16_t *table, int64_t ldt, float scale, uint16_t *out, int64_t ldo, hipStream_t stream);
+
+/* Its gradient from G = d loss / d out (count x k):
+ *     dtable_r = scale sum over ids[i] = r of G_i   (+ dtable_r, where accumulate is nonzero),
+ * each row summed in fp32 in the order of the tokens (up to 32 at a time, then those sums) and rounded once, so
+ * that results are bitwise reproducible. Without accumulate every element of dtable (rows x k) is written, zero
+ * where no id points; with it only the rows that occur are read and written: so the gradient of a table that is
+ * also an output layer's weight is added to that layer's. Negative ids and ids >= rows take no part.
+ * dtable may overlap neither G nor ids. count up to 2^30, rows below 2^31 - 1, and count / 32 times the KiB of
+ * a row below 2^24 (XTVXY_ERROR_UNSUPPORTED beyond). */
+xtvxy_status xtvxy_embedding_backward_f32_workspace_size(int64_t count, int64_t k, int64_t rows, size_t *bytes);
+xtvxy_status xtvxy_embedding_backward_f32(int64_t count, int64_t k, int64_t rows, const float *G, int64_t ldg,
+                                         const void *ids, int index_bits, float scale, int accumulate, float *dtable,
+                                         int64_t lddt, void *workspace, size_t workspace_bytes, hipStream_t stream);
+xtvxy_status xtvxy_embedding_backward_bf16_workspace_size(int64_t count, int64_t k, int64_t rows, size_t *bytes);
+xtvxy_status xtvxy_embedding_backward_bf16(int64_t count, int64_t k, int64_t rows, const uint16_t *G, int64_t ldg,
+                                         const void *ids, int index_bits, float scale, int accumulate, uint16_t *dtable,
+                                         int64_t lddt, void *workspace, size_t workspace_bytes, hipStream_t stream);
+xtvxy_status xtvxy_embedding_backward_f16_workspace_size(int64_t count, int64_t k, int64_t rows, size_t *bytes);
+xtvxy_status xtvxy_embedding_backward_f16(int64_t count, int64_t k, int64_t rows, const uint16_t *G, int64_t ldg,
+                                         const void *ids, int index_bits, float scale, int accumulate, uint16_t *dtable,
+                                         int64_t lddt, void *workspace, size_t workspace_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,141 @@
+"""Refusals of layer norm and embedding without a GPU: every call returns before a kernel is launched."""
+import pytest
+import torch
+
+import dense_linear_algebra_alpha_amd as xt
+from dense_linear_algebra_alpha_amd import _abi, build
+
+A = 1 << 40  # never dereferenced
+MB = 1 << 20
+SUFFIXES = ("f32", "bf16", "f16")
+BAD, NULL, ALIAS = _abi.XTVXY_ERROR_INVALID_VALUE, _abi.XTVXY_ERROR_NULL_POINTER, _abi.XTVXY_ERROR_ALIASING
+WORKSPACE, UNSUPPORTED = _abi.XTVXY_ERROR_WORKSPACE, _abi.XTVXY_ERROR_UNSUPPORTED
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    if build.sources_newer_than_library():
+        build.build()
+    return _abi.load()
+
+
+def norm_status(s, m=8, n=8, X=A, ldx=8, weight=A + MB, bias=A + 2 * MB, eps=1e-5, out=A + 3 * MB, ldo=8, mean=A + 4 * MB,
+                rstd=A + 5 * MB):
+    return getattr(_abi.load(), "xtvxy_layer_norm_" + s)(m, n, X, ldx, weight, bias, eps, out, ldo, mean, rstd, None)
+
+
+@pytest.mark.parametrize("s", SUFFIXES)
+def test_layer_norm_errors(s):
+    for kw in ({"m": -1}, {"n": -1}, {"ldx": 7}, {"ldo": 7}, {"eps": -1e-9}, {"eps": float("nan")}, {"eps": float("inf")},
+               {"m": 1 << 60}):
+        assert norm_status(s, **kw) == BAD, kw
+    for kw in ({"X": None}, {"out": None}):
+        assert norm_status(s, **kw) == NULL, kw
+    for kw in ({"out": A}, {"out": A + 16}, {"out": A + MB + 4}, {"mean": A + 4}, {"rstd": A + 2 * MB}, {"rstd": A + 4 * MB + 28},
+               {"mean": A + 3 * MB}):
+        assert norm_status(s, **kw) == ALIAS, kw
+    assert norm_status(s, m=0) == 0 and norm_status(s, n=0) == 0
+    assert norm_status(s, m=1, n=1 << 31, ldx=1 << 31, ldo=1 << 31, X=A << 1, out=A << 2, weight=None, bias=None) == UNSUPPORTED
+
+
+def norm_backward_status(s, m=8, n=8, G=A, ldg=8, X=A + MB, ldx=8, mean=A + 2 * MB, rstd=A + 3 * MB, weight=A + 4 * MB,
+                         dX=A + 5 * MB, lddx=8, dweight=A + 6 * MB, dbias=A + 7 * MB, ws=None, wsb=0):
+    return getattr(_abi.load(), "xtvxy_layer_norm_backward_" + s)(m, n, G, ldg, X, ldx, mean, rstd, weight, dX, lddx,
+                                                                  dweight, dbias, ws, wsb, None)
+
+
+@pytest.mark.parametrize("s", SUFFIXES)
+def test_layer_norm_backward_errors(s):
+    for kw in ({"m": -1}, {"n": -1}, {"ldg": 7}, {"ldx": 7}, {"lddx": 7}, {"m": 1 << 60}):
+        assert norm_backward_status(s, **kw) == BAD, kw
+    for kw in ({"G": None}, {"X": None}, {"mean": None}, {"rstd": None}):
+        assert norm_backward_status(s, **kw) == NULL, kw
+    for kw in ({"dX": A}, {"dX": A + MB + 8}, {"dweight": A + 2 * MB}, {"dbias": A + 4 * MB + 4}, {"dweight": A + 5 * MB + 4},
+               {"dbias": A + 6 * MB + 28}):
+        assert norm_backward_status(s, **kw) == ALIAS, kw
+    need = xt.xtvxy_layer_norm_backward_workspace_size(8, 8)
+    assert need > 0
+    for ws, b in ((None, 0), (A << 1, need - 1), ((A << 1) + 4, need)):
+        assert norm_backward_status(s, ws=ws, wsb=b) == WORKSPACE
+    assert norm_backward_status(s, n=0) == 0
+    assert norm_backward_status(s, dX=None, dweight=None, dbias=None) == 0
+    assert xt.xtvxy_layer_norm_backward_workspace_size(0, 8) == 0
+    for args in ((-1, 5), (1 << 40, 1 << 40)):
+        with pytest.raises(xt.XtvxyError):
+            xt.xtvxy_layer_norm_backward_workspace_size(*args)
+
+
+def embedding_status(s, count=8, k=8, rows=16, ids=A, bits=64, table=A + MB, ldt=8, scale=1.0, out=A + 2 * MB, ldo=8):
+    return getattr(_abi.load(), "xtvxy_embedding_" + s)(count, k, rows, ids, bits, table, ldt, scale, out, ldo, None)
+
+
+def embedding_backward_status(s, count=8, k=8, rows=16, G=A, ldg=8, ids=A + MB, bits=64, scale=1.0, acc=0, dtable=A + 2 * MB,
+                              lddt=8, ws=None, wsb=0):
+    return getattr(_abi.load(), "xtvxy_embedding_backward_" + s)(count, k, rows, G, ldg, ids, bits, scale, acc, dtable, lddt,
+                                                                 ws, wsb, None)
+
+
+@pytest.mark.parametrize("s", SUFFIXES)
+def test_embedding_errors(s):
+    for kw in ({"count": -1}, {"k": -1}, {"rows": -1}, {"bits": 16}, {"ldt": 7}, {"ldo": 7}, {"count": 1 << 60}):
+        assert embedding_status(s, **kw) == BAD, kw
+    for kw in ({"ids": None}, {"table": None}, {"out": None}):
+        assert embedding_status(s, **kw) == NULL, kw
+    for kw in ({"out": A}, {"out": A + 56}, {"out": A + MB + 16}):
+        assert embedding_status(s, **kw) == ALIAS, kw
+    assert embedding_status(s, count=0) == 0 and embedding_status(s, k=0) == 0
+
+
+@pytest.mark.parametrize("s", SUFFIXES)
+def test_embedding_backward_errors(s):
+    for kw in ({"count": -1}, {"k": -1}, {"rows": -1}, {"bits": 0}, {"ldg": 7}, {"lddt": 7}, {"count": 1 << 60}):
+        assert embedding_backward_status(s, **kw) == BAD, kw
+    for kw in ({"ids": None}, {"G": None}, {"dtable": None}):
+        assert embedding_backward_status(s, **kw) == NULL, kw
+    for kw in ({"dtable": A}, {"dtable": A + 16}, {"dtable": A + MB + 16}):
+        assert embedding_backward_status(s, **kw) == ALIAS, kw
+    size = getattr(xt, "xtvxy_embedding_backward_%s_workspace_size" % s)
+    need = size(8, 8, 16)
+    for ws, b in ((None, 0), (A << 1, need - 1), ((A << 1) + 4, need)):
+        assert embedding_backward_status(s, ws=ws, wsb=b) == WORKSPACE
+    assert embedding_backward_status(s, k=0) == 0 and embedding_backward_status(s, rows=0) == 0
+    assert size(0, 8, 16) == 0 and size(40000, 8, 16) > size(16384, 8, 16) > need
+    for args in ((-1, 5, 5), (1 << 31, 8, 8), (8, 8, 1 << 31), (1 << 29, 1 << 12, 8)):
+        with pytest.raises(xt.XtvxyError):
+            size(*args)
+    assert embedding_backward_status(s, count=1 << 31, ldg=8, dtable=A << 2) == UNSUPPORTED
+
+
+def test_helpers_refuse_host_tensors():
+    X, v = torch.zeros(4, 8), torch.zeros(4)
+    ids = torch.zeros(4, dtype=torch.int64)
+    for call in (lambda: xt.layer_norm(X), lambda: xt.layer_norm_backward(X, X, v, v), lambda: xt.embedding(ids, X),
+                 lambda: xt.embedding_backward(X, ids, 5)):
+        with pytest.raises(ValueError, match="GPU"):
+            call()
+
+
+@pytest.mark.gpu
+def test_helpers_refuse_what_the_kernels_cannot_take():
+    d = "cuda"
+    X, v, w = torch.zeros(4, 8, device=d), torch.zeros(4, device=d), torch.zeros(8, device=d)
+    ids = torch.zeros(4, dtype=torch.int64, device=d)
+    for call in (lambda: xt.layer_norm(X.double()), lambda: xt.layer_norm(X.t()), lambda: xt.layer_norm(X[0]),
+                 lambda: xt.layer_norm(X, v), lambda: xt.layer_norm(X, w.half()), lambda: xt.layer_norm(X, w, w.cpu()),
+                 lambda: xt.layer_norm(X, out=X.half()), lambda: xt.layer_norm(X, mean=w),
+                 lambda: xt.layer_norm(torch.zeros(1, 8, device=d).expand(4, 8)),
+                 lambda: xt.layer_norm_backward(X, X, v, None), lambda: xt.layer_norm_backward(X, X, w, v),
+                 lambda: xt.layer_norm_backward(X.half(), X, v, v), lambda: xt.layer_norm_backward(X, X, v, v, v),
+                 lambda: xt.layer_norm_backward(X, X, v, v, w, dweight=v),
+                 lambda: xt.embedding(ids.float(), X), lambda: xt.embedding(ids[None], X), lambda: xt.embedding(ids.cpu(), X),
+                 lambda: xt.embedding(ids[::2], X), lambda: xt.embedding(ids, X[0]), lambda: xt.embedding(ids, X, out=X[:, :4]),
+                 lambda: xt.embedding_backward(X, ids[:3], 9), lambda: xt.embedding_backward(X, ids, 9, accumulate=True),
+                 lambda: xt.embedding_backward(X, ids, -1), lambda: xt.embedding_backward(X, ids, 9, dtable=X),
+                 lambda: xt.embedding_backward(X, ids, 4, dtable=X.half())):
+        with pytest.raises(ValueError):
+            call()
+    for call in (lambda: xt.layer_norm(X, eps=-1.0), lambda: xt.layer_norm(X, out=X),
+                 lambda: xt.layer_norm_backward(X, X, v, v, workspace=torch.zeros(16, device=d)),
+                 lambda: xt.embedding(ids, X, out=X), lambda: xt.embedding_backward(X, ids, 4, dtable=X)):
+        with pytest.raises(xt.XtvxyError):
+            call()
