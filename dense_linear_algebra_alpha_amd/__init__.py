@@ -64,6 +64,20 @@ __all__ = [
     "xtvxy_layer_norm_backward_workspace_size", "xtvxy_layer_norm_f32", "xtvxy_layer_norm_bf16",
     "xtvxy_layer_norm_f16", "xtvxy_layer_norm_backward_f32", "xtvxy_layer_norm_backward_bf16",
     "xtvxy_layer_norm_backward_f16",
+    "linear_cross_entropy", "linear_cross_entropy_backward", "linear_distillation", "linear_distillation_backward",
+    "xtvxy_linear_cross_entropy_f32_workspace_size", "xtvxy_linear_cross_entropy_bf16_workspace_size",
+    "xtvxy_linear_cross_entropy_f16_workspace_size", "xtvxy_linear_cross_entropy_f32",
+    "xtvxy_linear_cross_entropy_bf16", "xtvxy_linear_cross_entropy_f16",
+    "xtvxy_linear_cross_entropy_backward_f32_workspace_size",
+    "xtvxy_linear_cross_entropy_backward_bf16_workspace_size",
+    "xtvxy_linear_cross_entropy_backward_f16_workspace_size", "xtvxy_linear_cross_entropy_backward_f32",
+    "xtvxy_linear_cross_entropy_backward_bf16", "xtvxy_linear_cross_entropy_backward_f16",
+    "xtvxy_linear_distillation_f32_workspace_size", "xtvxy_linear_distillation_bf16_workspace_size",
+    "xtvxy_linear_distillation_f16_workspace_size", "xtvxy_linear_distillation_f32", "xtvxy_linear_distillation_bf16",
+    "xtvxy_linear_distillation_f16", "xtvxy_linear_distillation_backward_f32_workspace_size",
+    "xtvxy_linear_distillation_backward_bf16_workspace_size", "xtvxy_linear_distillation_backward_f16_workspace_size",
+    "xtvxy_linear_distillation_backward_f32", "xtvxy_linear_distillation_backward_bf16",
+    "xtvxy_linear_distillation_backward_f16",
 ]
 
 load = _abi.load
@@ -78,6 +92,21 @@ from .layers import (ACTIVATIONS, linear, linear_backward, xtvxy_linear_backward
                      xtvxy_linear_backward_f32_workspace_size, xtvxy_linear_bf16, xtvxy_linear_bf16_workspace_size,
                      xtvxy_linear_f16, xtvxy_linear_f16_workspace_size, xtvxy_linear_f32,
                      xtvxy_linear_f32_workspace_size)
+from .losses import (linear_cross_entropy, linear_cross_entropy_backward, linear_distillation,  # noqa: E402,F401
+                     linear_distillation_backward, xtvxy_linear_cross_entropy_f32_workspace_size,
+                     xtvxy_linear_cross_entropy_bf16_workspace_size, xtvxy_linear_cross_entropy_f16_workspace_size,
+                     xtvxy_linear_cross_entropy_f32, xtvxy_linear_cross_entropy_bf16, xtvxy_linear_cross_entropy_f16,
+                     xtvxy_linear_cross_entropy_backward_f32_workspace_size,
+                     xtvxy_linear_cross_entropy_backward_bf16_workspace_size,
+                     xtvxy_linear_cross_entropy_backward_f16_workspace_size, xtvxy_linear_cross_entropy_backward_f32,
+                     xtvxy_linear_cross_entropy_backward_bf16, xtvxy_linear_cross_entropy_backward_f16,
+                     xtvxy_linear_distillation_f32_workspace_size, xtvxy_linear_distillation_bf16_workspace_size,
+                     xtvxy_linear_distillation_f16_workspace_size, xtvxy_linear_distillation_f32,
+                     xtvxy_linear_distillation_bf16, xtvxy_linear_distillation_f16,
+                     xtvxy_linear_distillation_backward_f32_workspace_size,
+                     xtvxy_linear_distillation_backward_bf16_workspace_size,
+                     xtvxy_linear_distillation_backward_f16_workspace_size, xtvxy_linear_distillation_backward_f32,
+                     xtvxy_linear_distillation_backward_bf16, xtvxy_linear_distillation_backward_f16)
 from .norm import (layer_norm, layer_norm_backward, xtvxy_layer_norm_backward_workspace_size,  # noqa: E402,F401
                    xtvxy_layer_norm_f32, xtvxy_layer_norm_bf16, xtvxy_layer_norm_f16, xtvxy_layer_norm_backward_f32,
                    xtvxy_layer_norm_backward_bf16, xtvxy_layer_norm_backward_f16)

@@ -208,6 +208,19 @@ for _t in ("f32", "bf16", "f16"):
     SIGNATURES["xtvxy_embedding_backward_%s_workspace_size" % _t] = [_i64, _i64, _i64, _P(_sz)]
     SIGNATURES["xtvxy_embedding_backward_" + _t] = [_i64, _i64, _i64, _vp, _i64, _vp, _i32, _f32, _i32, _vp, _i64, _vp,
                                                     _sz, _vp]
+    SIGNATURES["xtvxy_linear_cross_entropy_%s_workspace_size" % _t] = [_i64, _i64, _i64, _i32, _P(_sz)]
+    SIGNATURES["xtvxy_linear_cross_entropy_" + _t] = [_i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _vp, _i32, _vp, _vp, _vp,
+                                                      _sz, _vp]
+    SIGNATURES["xtvxy_linear_cross_entropy_backward_%s_workspace_size" % _t] = [_i64, _i64, _i64, _i32, _P(_sz)]
+    SIGNATURES["xtvxy_linear_cross_entropy_backward_" + _t] = [_i64, _i64, _i64, _vp, _vp, _i64, _vp, _i64, _vp, _vp, _i32,
+                                                               _vp, _vp, _i64, _vp, _i64, _vp, _vp, _sz, _vp]
+    SIGNATURES["xtvxy_linear_distillation_%s_workspace_size" % _t] = [_i64, _i64, _i64, _i64, _i32, _P(_sz)]
+    SIGNATURES["xtvxy_linear_distillation_" + _t] = [_i64, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _i32, _vp,
+                                                     _i64, _i32, _f32, _vp, _vp, _vp, _vp, _sz, _vp]
+    SIGNATURES["xtvxy_linear_distillation_backward_%s_workspace_size" % _t] = [_i64, _i64, _i64, _i64, _i32, _P(_sz)]
+    SIGNATURES["xtvxy_linear_distillation_backward_" + _t] = [_i64, _i64, _i64, _vp, _vp, _i64, _vp, _i64, _vp, _i64, _vp,
+                                                              _i64, _i32, _vp, _f32, _vp, _vp, _i64, _vp, _i64, _vp, _vp,
+                                                              _sz, _vp]
 SIGNATURES["xtvxy_layer_norm_backward_workspace_size"] = [_i64, _i64, _P(_sz)]
 _vpp, _f64 = _P(_vp), ctypes.c_double
 SIGNATURES.update({

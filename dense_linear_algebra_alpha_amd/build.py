@@ -30,9 +30,11 @@ SOURCES = ["api.cpp", "model.cpp", "unfused.cpp", "logreg.cpp", "tune.cpp", "csr
            "csr_waves.hip", "csr_rows.hip", "csr_bins.hip",
            "aggregate.hip", "logreg.hip", "probe.hip", "noalloc.hip",
            "linear.cpp", "linear_tile.hip", "linear_ring.hip", "linear_few.hip", "adamw.cpp", "adamw.hip",
-           "norm.cpp", "norm.hip", "embedding.cpp", "embedding.hip"]
+           "norm.cpp", "norm.hip", "embedding.cpp", "embedding.hip",
+           "loss.cpp", "loss.hip"]
 TENSORS_SOURCE = "tensor_list.cpp"
-HEADERS = ["internal.h", "device_util.h", "csr_common.h", "linear.h", "linear_util.h", "adamw.h", "matrix.h", "norm.h", "embedding.h"]
+HEADERS = ["internal.h", "device_util.h", "csr_common.h", "linear.h", "linear_util.h", "adamw.h", "matrix.h", "norm.h", "embedding.h",
+           "loss.h", "linear_plan.h", "linear_ring.h"]
 
 COMMON_FLAGS = [
     "-O3", "-std=c++17", "-fPIC", "-Wall", "-Wno-unused-function",

@@ -5,24 +5,11 @@
 #include <algorithm>
 #include <cstdint>
 
-#include "linear.h"
-#include "matrix.h"
+#include "linear_plan.h"
 
 using namespace xtvxy;
 
 namespace {
-
-constexpr int64_t kComputeUnits = 256;           // the plans are for this chip whatever runs the query
-constexpr int64_t kMaxGroups = ((int64_t)1 << 24) - 1;  // workgroups of 256 threads in one launch: below 2^32 threads
-
-
-// How one product is computed: by which kernel, which of its tiles whole and which in how many parts of
-// the contraction.
-struct ProductPlan {
-  int tile = 0;  // 0: the kernel for any alignment; 64, 128, 256: the ring kernel's tile
-  int64_t whole = 0, splits = 1, k_per_split = 0;
-  size_t bytes = 0;  // partial sums
-};
 
 // The estimate of a launch's time. Its workgroups are jobs of so many stages (32 steps; fp32: 16). A CU
 // holds one of 256 x 256, two of 128 x 128 or five of 64 x 64 at a time, and works off a stage in
@@ -138,8 +125,9 @@ double product_jobs(const ProductPlan& p, int type, int tile, int64_t m, int64_t
   return p.splits > 1 ? 2.0 * p.splits * (tiles - whole) * tile * tile * 4 / kPartsBytesPerUs : 0.0;
 }
 
-// The layer's tile, split tiles and parts with the least estimated time.
-ProductPlan plan_product(int type, int64_t m, int64_t n, int64_t k, bool ring) {
+}  // namespace
+
+ProductPlan xtvxy::plan_product(int type, int64_t m, int64_t n, int64_t k, bool ring, bool split) {
   ProductPlan best;
   best.k_per_split = kTileDepth;
   if (m == 0 || n == 0) return best;
@@ -153,6 +141,7 @@ ProductPlan plan_product(int type, int64_t m, int64_t n, int64_t k, bool ring) {
       if (w > 0 && (whole[w] == 0 || whole[w] == tiles)) continue;
       for (int64_t splits : kSplits) {
         ProductPlan p;
+        if (splits > 1 && !split) break;
         if ((w > 0 && splits == 1) || !set_product(&p, type, tile, ring, whole[w], splits, m, n, k)) continue;
         if (splits > 1 && tiles + kMostParts > kMaxGroups) continue;  // beyond one launch
         Jobs jobs[2];
@@ -168,20 +157,20 @@ ProductPlan plan_product(int type, int64_t m, int64_t n, int64_t k, bool ring) {
   return best;
 }
 
-// The gradient's products dX (m x k, contraction n) and dW (n x k, contraction m) share a tile and a
-// launch, the one with the longer contraction first.
-void plan_gradient(int type, int64_t m, int64_t k, int64_t n, bool want_dx, bool want_dw, bool ring, ProductPlan* dx,
-                   ProductPlan* dw) {
+// Of the gradient's products the one with the longer contraction goes first.
+void xtvxy::plan_gradient(int type, int64_t m, int64_t k, int64_t n, bool want_dx, bool want_dw, bool ring, ProductPlan* dx,
+                          ProductPlan* dw, int only_tile, bool dx_in_parts) {
   dx->k_per_split = dw->k_per_split = kTileDepth;
   if (m == 0 || k == 0 || n == 0) return;
   const bool dw_first = m > n;
   double least = 0;
   for (int tile : {64, 128, 256}) {
-    if (!ring ? tile != 64 : (tile == 256 && type == kF32)) continue;
+    if (only_tile ? tile != only_tile : !ring ? tile != 64 : (tile == 256 && type == kF32)) continue;
     const int64_t tx = want_dx ? cdiv(m, tile) * cdiv(k, tile) : 0, tw = want_dw ? cdiv(n, tile) * cdiv(k, tile) : 0;
     // of the product that runs last, those tiles that its last, incomplete round would hold
     const int64_t last = dw_first ? tx : tw, full = (tx + tw) / kComputeUnits * kComputeUnits - (tx + tw - last);
-    for (int rest = 0; rest < (ring && full > 0 && full < last ? 2 : 1); ++rest)
+    const bool uneven = ring && full > 0 && full < last && !(dw_first && dx_in_parts);
+    for (int rest = 0; rest < (uneven ? 2 : 1); ++rest)
       for (int64_t sx : kSplits) {
         ProductPlan px, pw;
         if (!want_dx ? sx > 1 : !set_product(&px, type, tile, ring, rest && dw_first ? full : 0, sx, m, k, n)) continue;
@@ -204,39 +193,7 @@ void plan_gradient(int type, int64_t m, int64_t k, int64_t n, bool want_dx, bool
   }
 }
 
-// Plans of the shapes of a thread's latest calls. The search takes 1.2 us for a layer (15 at most over 600 shapes)
-// and 8 for a gradient (26), and a gradient's workspace query looks at up to 24 of them; a call takes 4.
-template <typename Plan>
-struct PlanCache {
-  struct Entry {
-    int64_t key[4] = {-1, -1, -1, -1};
-    Plan plan{};
-  } entries[64];
-  template <typename Make>
-  const Plan& get(int64_t m, int64_t k, int64_t n, int64_t what, Make make) {
-    const uint64_t h = (uint64_t)m * 0x9E3779B97F4A7C15u ^ (uint64_t)k * 0xC2B2AE3D27D4EB4Fu ^ (uint64_t)n * 0x165667B19E3779F9u ^
-                       (uint64_t)what * 0x27D4EB2F165667C5u;
-    Entry& e = entries[(h >> 40) % 64];
-    const int64_t key[4] = {m, k, n, what};
-    if (!std::equal(key, key + 4, e.key)) {
-      e.plan = make();
-      std::copy(key, key + 4, e.key);
-    }
-    return e.plan;
-  }
-};
-
-bool product_fits(int64_t m, int64_t n) {
-  return cdiv(m, 64) * cdiv(n, 64) <= kMaxGroups;
-}
-
-void take_plan(ProductArgs* a, const ProductPlan& p, void* ws) {
-  a->tile = p.tile;
-  a->whole = p.tile ? p.whole : 0;
-  a->splits = (int32_t)p.splits;
-  a->k_per_split = p.k_per_split;
-  a->partial = static_cast<float*>(ws);
-}
+namespace {
 
 hipError_t run_layer(ProductArgs a, const ProductPlan& p, void* ws, hipStream_t s) {
   take_plan(&a, p, ws);
@@ -253,14 +210,6 @@ hipError_t run_layer(ProductArgs a, const ProductPlan& p, void* ws, hipStream_t 
 // four 45, 47; 64, 64; 140, 137; 520, 507.
 constexpr int64_t kSmallProduct = (int64_t)1 << 33;  // multiplications
 constexpr int64_t kSmallGradient = (int64_t)1 << 26;
-
-int64_t padded(int64_t cols, int es) { return cdiv(cols, 16 / es) * (16 / es); }
-
-bool whole_chunks(const Matrix& x) {
-  return x.aligned16() && x.cols * x.es % 16 == 0 && x.ld * x.es <= kRingMaxPitch;
-}
-
-size_t packed_bytes(int64_t rows, int64_t cols, int es) { return align_up((size_t)rows * padded(cols, es) * es); }
 
 bool valid_act(int a) { return a >= XTVXY_ACT_NONE && a <= XTVXY_ACT_SILU; }
 
@@ -464,11 +413,6 @@ const BackwardPlan& plan_backward(int type, int64_t m, int64_t k, int64_t n, int
   return cache.get(m, k, n, what, [&] {
     return make_backward_plan(type, m, k, n, act, g_whole, x_whole, w_whole, want_dx, want_dw);
   });
-}
-
-bool backward_fits(int64_t m, int64_t k, int64_t n) {
-  // both products are one launch
-  return cdiv(m, 64) * cdiv(k, 64) + cdiv(n, 64) * cdiv(k, 64) + cdiv(n, 16) <= kMaxGroups;
 }
 
 size_t most_backward_bytes(int type, int64_t m, int64_t k, int64_t n, int act, int aligned16) {

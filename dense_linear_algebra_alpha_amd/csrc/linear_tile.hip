@@ -283,6 +283,7 @@ __device__ __forceinline__ void finish_quad(const ProductArgs& a, int64_t at) {
     z[c] += __shfl_xor(z[c], 1);
     z[c] += __shfl_xor(z[c], 2);
   }
+  if (a.scale) z *= *a.scale;
   if (exists && part == 0) epilogue4<T>(a.e, i, j, a.n, z);
 }
 

@@ -1,0 +1,87 @@
+// Internal declarations of the losses over an output layer's logits: softmax cross entropy and distillation from a
+// teacher's top logits (loss.cpp, loss.hip).
+#pragma once
+
+#include "linear.h"
+
+namespace xtvxy {
+
+// Classes of each row that a loss looks at: labels (one a row) or a teacher's (per_row of them).
+struct ClassList {
+  const void* p;
+  int64_t ld;
+  int32_t bits, per_row;
+};
+
+// A piece of the logits t = (X W^T + bias) / T of which only statistics are kept: product.A is X, product.B the
+// piece's rows of W, product.n its classes from `first_class` on.
+struct LossForwardArgs {
+  ProductArgs product;
+  const float* bias;     // of the piece; null: zeros
+  float inv_temperature;
+  int64_t first_class;
+  ClassList list;
+  float* listed;         // [m][per_row]: t of the listed classes of this piece
+  float* stats;          // [2 tiles of columns][m][2]: largest t and sum of exp(t - largest) over half a tile
+};
+hipError_t launch_loss_forward(const LossForwardArgs& a, hipStream_t s);
+
+// Joins a piece's statistics into each row's running ones and, after the last piece, forms lse and loss.
+struct LossFinishArgs {
+  const float* stats;
+  int64_t parts, m, n;
+  float* run;            // [m][2], null: one piece
+  int32_t first, last;
+  ClassList list;
+  const float* listed;
+  const float* weights;  // [m][per_row], null: labels
+  float* loss;
+  float* lse;
+};
+hipError_t launch_loss_finish(const LossFinishArgs& a, hipStream_t s);
+
+// Target weights from a teacher's logits: softmax(teacher / T) over a row's classes, equal classes' in the first.
+constexpr int64_t kMostListed = 1024;
+struct TeacherArgs {
+  ClassList list;
+  const void* teacher;
+  int64_t ldt;
+  int32_t type;
+  float inv_temperature;
+  int64_t m, n;
+  float* weights;
+};
+hipError_t launch_teacher_weights(const TeacherArgs& a, hipStream_t s);
+
+// factor_i of d_ij = factor_i (softmax_ij - target_ij): grad_i / T, 0 for rows that do not count, NaN for bad ones; and,
+// for fp16, powers of two scale[0] and scale[1] = 1 / scale[0] with which the largest |factor| is in [2^13, 2^14).
+struct LossFactorArgs {
+  const float* grad;
+  ClassList list;
+  const float* weights;  // null: labels
+  float inv_temperature;
+  int64_t m, n;
+  float* factor;
+  float* scale;          // null: not wanted
+};
+hipError_t launch_loss_factor(const LossFactorArgs& a, hipStream_t s);
+
+// d of a piece, rounded to the product's type (times scale[0]) in rows of ldd elements, zero beyond the piece; and
+// the column sums of each half tile of rows, unrounded and not scaled.
+struct LossGradientArgs {
+  ProductArgs product;
+  const float* bias;
+  float inv_temperature;
+  int64_t first_class;
+  ClassList list;
+  const float* weights;
+  const float* factor;
+  const float* lse;
+  const float* scale;    // null: 1
+  void* d;               // null: not wanted
+  int64_t ldd;
+  float* sums;           // [2 tiles of rows][n], null: not wanted
+};
+hipError_t launch_loss_gradient(const LossGradientArgs& a, hipStream_t s);
+
+}  // namespace xtvxy

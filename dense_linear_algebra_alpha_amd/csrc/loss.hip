@@ -1,0 +1,407 @@
+// Softmax cross entropy and distillation over the classes of an output layer, without keeping its logits.
+//
+//     t_ij = (sum_k x_ik w_jk + bias_j) / T,  lse_i = log sum_j exp(t_ij),
+//     labels y:             loss_i = lse_i - t_i,y                                    target_ij = [j = y_i]
+//     a teacher's weights P: loss_i = sum_c P_ic (log P_ic - t_ic + lse_i)            target_ij = P_ij
+//     d_ij = grad_i / T (exp(t_ij - lse_i) - target_ij),  dX = d W,  dW = d^T X,  dbias_j = sum_i d_ij.
+//
+// The products run through the ring kernel (linear_ring.h) and are what bounds both directions; what happens to the
+// logits happens in a tile's registers. Forward: each wavefront reduces its half of a tile's columns to the largest t
+// and the sum of exp(t - largest) per row, and writes down t of the classes that its rows list; the sums of all tiles
+// are joined in a fixed order. Gradient: the logits are formed once more, piece by piece of the vocabulary (a
+// fourth product; keeping them costs as much memory as the vocabulary is wide), turned into d, and the piece's d,
+// in the element type, goes through the layer's gradient kernel.
+#include "linear_ring.h"
+#include "loss.h"
+
+namespace xtvxy {
+namespace {
+
+__device__ __forceinline__ int64_t class_at(const ClassList& l, int64_t i, int e) {
+  const int64_t at = i * l.ld + e;
+  return l.bits == 32 ? static_cast<const int32_t*>(l.p)[at] : static_cast<const int64_t*>(l.p)[at];
+}
+
+// For every class that a strip's rows list within its columns: fn(row of the strip, its place in the list, place of its
+// value in the staging area). Lanes take the lists' entries in turn.
+template <int WN, typename Fn>
+__device__ __forceinline__ void for_listed(const ClassList& list, int64_t i0, int rows, int64_t first_class, int columns, Fn fn) {
+  const int lane = threadIdx.x & 63;
+  const uint32_t total = (uint32_t)rows * (uint32_t)list.per_row;
+  for (uint32_t at = lane; at < total; at += 64) {
+    const uint32_t row = list.per_row == 1 ? at : at / (uint32_t)list.per_row, e = at - row * (uint32_t)list.per_row;
+    const int64_t c = class_at(list, i0 + row, (int)e) - first_class;
+    if (c >= 0 && c < columns) fn((int)row, (int)e, staged_at<WN>((int)row, (int)c >> 2) + ((int)c & 3));
+  }
+}
+
+// The bias of a lane's columns: four neighbours of each of the FB groups of 16.
+template <int FB>
+__device__ __forceinline__ void lane_bias(const float* bias, int64_t j, int64_t n, f32x4 (&b)[FB]) {
+#pragma unroll
+  for (int y = 0; y < FB; ++y) {
+    const int64_t at = j + y * 16;
+    b[y] = bias && at < n ? load4<float>(bias + at, n - at >= 4 ? 4 : (int)(n - at)) : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  }
+}
+
+// t of one row's columns of a lane: -infinity where there is no column.
+template <int FB>
+__device__ __forceinline__ void lane_logits(f32x4 (&z)[FB], const f32x4 (&bias)[FB], float inv_temperature, int64_t j, int64_t n) {
+#pragma unroll
+  for (int y = 0; y < FB; ++y)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float t = (z[y][e] + bias[y][e]) * inv_temperature;
+      z[y][e] = j + y * 16 + e < n ? t : -__builtin_inff();
+    }
+}
+
+struct StatsEnd {
+  const LossForwardArgs& l;
+  template <typename T, int BM, int BN, typename S>
+  __device__ __forceinline__ void finish(const ProductArgs& a, uint8_t* ring, S& sums, const TilePlace& p) const {
+    constexpr int FA = BM / 32, FB = BN / 32;
+    typedef Strips<BM, BN> Strip;
+    constexpr int WN = Strip::kWidth, kRows = Strip::kRows;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int wi = (wave >> 1) * (BM / 2), wj = (wave & 1) * (BN / 2), r = lane & 15, g = lane >> 4;
+    end_of_products(sums);
+    const int64_t j = p.j0 + wj + g * 4;
+    f32x4 bias[FB];
+    lane_bias<FB>(l.bias, j, a.n, bias);
+    float* stats = l.stats + (p.j0 / BN * 2 + (wave & 1)) * a.m * 2;
+#pragma unroll
+    for (int x = 0; x < FA; ++x) {
+      lane_logits<FB>(sums.acc[x], bias, l.inv_temperature, j, a.n);
+      float top = sums.acc[x][0][0];
+#pragma unroll
+      for (int y = 0; y < FB; ++y)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) top = fmaxf(top, sums.acc[x][y][e]);
+      top = fmaxf(top, __shfl_xor(top, 16));
+      top = fmaxf(top, __shfl_xor(top, 32));
+      // a row without a finite logit here has no distances from its largest one
+      const float from = top == -__builtin_inff() ? 0.0f : top;
+      float s = 0.0f;
+#pragma unroll
+      for (int y = 0; y < FB; ++y)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s += fast_exp(sums.acc[x][y][e] - from);
+      s = add_xor32(add_xor16(s));
+      const int64_t i = p.i0 + wi + x * 16 + r;
+      if (g == 0 && i < a.m) *reinterpret_cast<f32x2*>(stats + i * 2) = f32x2{top, s};
+    }
+    if (l.list.per_row == 0) return;
+    float* area = reinterpret_cast<float*>(ring + wave * Strip::kArea);
+    const int64_t width = a.n - p.j0 - wj;
+#pragma unroll
+    for (int part = 0; part < BM / 2 / kRows; ++part) {
+      const int64_t i0 = p.i0 + wi + part * kRows;
+      if (i0 >= a.m) break;
+      sums.template stage<WN>(area, part, kRows);
+      __builtin_amdgcn_wave_barrier();
+      for_listed<WN>(l.list, i0, a.m - i0 < kRows ? (int)(a.m - i0) : kRows, l.first_class + p.j0 + wj,
+                     width < WN ? (int)width : WN,
+                     [&](int row, int e, int at) { l.listed[(i0 + row) * l.list.per_row + e] = area[at]; });
+      __builtin_amdgcn_wave_barrier();
+    }
+  }
+};
+
+struct GradientEnd {
+  const LossGradientArgs& l;
+  template <typename T, int BM, int BN, typename S>
+  __device__ __forceinline__ void finish(const ProductArgs& a, uint8_t* ring, S& sums, const TilePlace& p) const {
+    constexpr int FA = BM / 32, FB = BN / 32;
+    typedef Strips<BM, BN> Strip;
+    constexpr int WN = Strip::kWidth, kRows = Strip::kRows, kLanes = WN / 8, kStep = 64 / kLanes;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int wi = (wave >> 1) * (BM / 2), wj = (wave & 1) * (BN / 2), r = lane & 15, g = lane >> 4;
+    end_of_products(sums);
+    const int64_t j = p.j0 + wj + g * 4;
+    f32x4 bias[FB];
+    lane_bias<FB>(l.bias, j, a.n, bias);
+#pragma unroll
+    for (int x = 0; x < FA; ++x) {
+      const int64_t i = p.i0 + wi + x * 16 + r;
+      const float factor = i < a.m ? l.factor[i] : 0.0f, lse = i < a.m ? l.lse[i] : 0.0f;
+      lane_logits<FB>(sums.acc[x], bias, l.inv_temperature, j, a.n);
+#pragma unroll
+      for (int y = 0; y < FB; ++y)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {  // a row that does not count is zero whatever its logits are
+          const float d = factor * fast_exp(sums.acc[x][y][e] - lse);
+          sums.acc[x][y][e] = factor == 0.0f ? 0.0f : d;
+        }
+    }
+    float* area = reinterpret_cast<float*>(ring + wave * Strip::kArea);
+    const int64_t width = a.n - p.j0 - wj;
+    const int c8 = lane % kLanes;
+    const int64_t column = p.j0 + wj + c8 * 8;  // of this lane's eight
+    const float scale = l.scale ? *l.scale : 1.0f;
+    float column_sums[8] = {};
+#pragma unroll
+    for (int part = 0; part < BM / 2 / kRows; ++part) {
+      const int64_t i0 = p.i0 + wi + part * kRows;
+      if (i0 >= a.m) break;
+      const int rows = a.m - i0 < kRows ? (int)(a.m - i0) : kRows;
+      sums.template stage<WN>(area, part, kRows);
+      __builtin_amdgcn_wave_barrier();
+      for_listed<WN>(l.list, i0, rows, l.first_class + p.j0 + wj, width < WN ? (int)width : WN, [&](int row, int e, int at) {
+        const float factor = l.factor[i0 + row], w = l.weights ? l.weights[(i0 + row) * l.list.per_row + e] : 1.0f;
+        // a class that is listed twice comes here twice, maybe at once
+        if (factor != 0.0f && w != 0.0f) __hip_atomic_fetch_add(area + at, -factor * w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+      });
+      __builtin_amdgcn_wave_barrier();
+      if (column < l.ldd) {
+        T* d = static_cast<T*>(l.d) + (l.d ? i0 * l.ldd + column : 0);
+#pragma unroll 4
+        for (int row = lane / kLanes; row < rows; row += kStep) {
+          const f32x8 v = staged8<WN>(area, row, c8);
+          typename Vec<T>::x8 o;
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            column_sums[c] += v[c];
+            o[c] = (T)(v[c] * scale);
+          }
+          if (l.d) *reinterpret_cast<typename Vec<T>::x8*>(d + row * l.ldd) = o;
+        }
+      }
+      __builtin_amdgcn_wave_barrier();
+    }
+    if (!l.sums) return;
+    float* out = l.sums + (p.i0 / BM * 2 + (wave >> 1)) * a.n;
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+#pragma unroll
+      for (int by = kLanes; by < 64; by *= 2) column_sums[c] += __shfl_xor(column_sums[c], by);
+    }
+    const int count = a.n - column >= 8 ? 8 : (a.n > column ? (int)(a.n - column) : 0);
+    if (lane < kLanes && count > 0) store_elems<float, 8>(out + column, count, column_sums);
+  }
+};
+
+template <typename T, int TILE, typename End>
+__device__ __forceinline__ void loss_tile(const ProductArgs& a, uint8_t* ring, const End& end) {
+  if constexpr (TILE == 256) ring_tile_halves<T, TILE, TILE, false, false>(a, blockIdx.x, ring, end);
+  else ring_tile<T, TILE, TILE, false, false>(a, blockIdx.x, ring, end);
+}
+
+template <typename T, int TILE>
+__global__ __launch_bounds__(kThreads, TILE > 128 ? 1 : 2) void loss_forward(LossForwardArgs a) {
+  __shared__ __align__(1024) uint8_t ring[ring_bytes(TILE)];
+  loss_tile<T, TILE>(a.product, ring, StatsEnd{a});
+}
+
+template <typename T, int TILE>
+__global__ __launch_bounds__(kThreads, TILE > 128 ? 1 : 2) void loss_gradient(LossGradientArgs a) {
+  __shared__ __align__(1024) uint8_t ring[ring_bytes(TILE)];
+  loss_tile<T, TILE>(a.product, ring, GradientEnd{a});
+}
+
+// (largest, sum of exp(t - largest)) of two sets of logits joined. Either may be empty: (-infinity, 0).
+__device__ __forceinline__ void join_stats(float* top, float* sum, float top2, float sum2) {
+  const float t = fmaxf(*top, top2), from = t == -__builtin_inff() ? 0.0f : t;
+  *sum = *sum * fast_exp(*top - from) + sum2 * fast_exp(top2 - from);
+  *top = t;
+}
+
+// 16 rows a workgroup: of each row a thread joins every 16th part's statistics, the 16 join in order; the terms of a
+// teacher's classes likewise.
+__global__ __launch_bounds__(256) void loss_finish(LossFinishArgs a) {
+  __shared__ float tops[16][17], sums[16][17], terms[16][17], norms[16];
+  const int c = threadIdx.x & 15, slot = threadIdx.x >> 4;
+  const int64_t i = (int64_t)blockIdx.x * 16 + c;
+  const bool there = i < a.m;
+  float top = -__builtin_inff(), sum = 0.0f;
+  if (there) {
+#pragma unroll 4
+    for (int64_t p = slot; p < a.parts; p += 16) {
+      const f32x2 v = *reinterpret_cast<const f32x2*>(a.stats + (p * a.m + i) * 2);
+      join_stats(&top, &sum, v[0], v[1]);
+    }
+  }
+  tops[slot][c] = top;
+  sums[slot][c] = sum;
+  __syncthreads();
+  if (slot == 0 && there) {
+    for (int s = 1; s < 16; ++s) join_stats(&top, &sum, tops[s][c], sums[s][c]);
+    if (a.run && !a.first) join_stats(&top, &sum, a.run[i * 2], a.run[i * 2 + 1]);
+    if (a.run && !a.last) {
+      a.run[i * 2] = top;
+      a.run[i * 2 + 1] = sum;
+    }
+    norms[c] = top + logf(sum);
+  }
+  if (!a.last) return;
+  __syncthreads();
+  const float lse = there ? norms[c] : 0.0f;
+  if (a.weights) {
+    float s = 0.0f;
+    if (there) {
+      for (int e = slot; e < a.list.per_row; e += 16) {
+        const float w = a.weights[i * a.list.per_row + e];
+        if (w != 0.0f) s += w * (logf(w) - a.listed[i * a.list.per_row + e] + lse);
+      }
+    }
+    terms[slot][c] = s;
+    __syncthreads();
+    if (slot != 0 || !there) return;
+    for (int q = 1; q < 16; ++q) s += terms[q][c];
+    a.loss[i] = s;
+  } else {
+    if (slot != 0 || !there) return;
+    const int64_t y = class_at(a.list, i, 0);
+    a.loss[i] = y < 0 ? 0.0f : y < a.n ? lse - a.listed[i] : __builtin_nanf("");
+  }
+  a.lse[i] = lse;
+}
+
+// A wavefront a row.
+template <typename T>
+__global__ __launch_bounds__(256) void teacher_weights(TeacherArgs a) {
+  __shared__ int32_t classes[4][kMostListed];
+  __shared__ float weights[4][kMostListed];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, count = a.list.per_row;
+  const int64_t i = (int64_t)blockIdx.x * 4 + wave;
+  if (i >= a.m) return;
+  const T* teacher = static_cast<const T*>(a.teacher) + i * a.ldt;
+  bool bad = false;
+  float top = -__builtin_inff();
+  for (int e = lane; e < count; e += 64) {
+    const int64_t c = class_at(a.list, i, e);
+    bad |= c >= a.n;
+    const bool valid = c >= 0 && c < a.n;
+    const float t = valid ? (float)teacher[e] * a.inv_temperature : -__builtin_inff();
+    classes[wave][e] = valid ? (int32_t)c : -1;
+    weights[wave][e] = t;
+    bad |= t != t;
+    top = fmaxf(top, t);
+  }
+#pragma unroll
+  for (int by = 1; by < 64; by *= 2) top = fmaxf(top, __shfl_xor(top, by));
+  bad = __any(bad);
+  const float from = top == -__builtin_inff() ? 0.0f : top;
+  float sum = 0.0f;
+  for (int e = lane; e < count; e += 64) {
+    const float w = expf(weights[wave][e] - from);
+    weights[wave][e] = w;
+    sum += w;
+  }
+  sum = group_sum(sum, 64);
+  __builtin_amdgcn_wave_barrier();
+  for (int e = lane; e < count; e += 64) {
+    const int32_t c = classes[wave][e];
+    float w = 0.0f;
+    bool first = true;
+    for (int f = 0; f < count; ++f) {
+      const bool same = classes[wave][f] == c;
+      if (same && f < e) first = false;
+      if (same && f >= e) w += weights[wave][f];
+    }
+    w = first && c >= 0 && sum > 0.0f ? w / sum : 0.0f;
+    // a class beyond the vocabulary or an infinite or missing logit: the whole row is no distribution
+    a.weights[i * count + e] = bad || !(sum < __builtin_inff()) ? __builtin_nanf("") : w;
+  }
+}
+
+__global__ __launch_bounds__(256) void loss_factor(LossFactorArgs a) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= a.m) return;
+  float f;
+  if (a.weights) {
+    float s = 0.0f;
+    for (int e = 0; e < a.list.per_row; ++e) s += a.weights[i * a.list.per_row + e];
+    f = s == 0.0f ? 0.0f : s == s ? a.grad[i] * a.inv_temperature : s;
+  } else {
+    const int64_t y = class_at(a.list, i, 0);
+    f = y < 0 ? 0.0f : y < a.n ? a.grad[i] : __builtin_nanf("");
+  }
+  a.factor[i] = f;
+}
+
+__global__ __launch_bounds__(1024) void loss_scale(LossFactorArgs a) {
+  __shared__ float lds[16];
+  float top = 0.0f;
+#pragma unroll 4
+  for (int64_t i = threadIdx.x; i < a.m; i += 1024) {
+    const float f = fabsf(a.factor[i]);
+    top = f < __builtin_inff() ? fmaxf(top, f) : top;
+  }
+#pragma unroll
+  for (int by = 1; by < 64; by *= 2) top = fmaxf(top, __shfl_xor(top, by));
+  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = top;
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  for (int w = 1; w < 16; ++w) top = fmaxf(top, lds[w]);
+  int e = 14;
+  if (top > 0.0f) e = 14 - ilogbf(top) - 1;  // top < 2^(ilogb + 1)
+  e = e > 120 ? 120 : e < -120 ? -120 : e;
+  a.scale[0] = ldexpf(1.0f, e);
+  a.scale[1] = ldexpf(1.0f, -e);
+}
+
+template <typename T>
+void forward_type(const LossForwardArgs& a, hipStream_t s) {
+  const uint32_t groups = (uint32_t)a.product.tiles();
+  if constexpr (sizeof(T) == 2) {
+    if (a.product.tile == 256) {
+      loss_forward<T, 256><<<groups, kThreads, 0, s>>>(a);
+      return;
+    }
+  }
+  if (a.product.tile == 128) loss_forward<T, 128><<<groups, kThreads, 0, s>>>(a);
+  else loss_forward<T, 64><<<groups, kThreads, 0, s>>>(a);
+}
+
+template <typename T>
+void gradient_type(const LossGradientArgs& a, hipStream_t s) {
+  const uint32_t groups = (uint32_t)a.product.tiles();
+  if constexpr (sizeof(T) == 2) {
+    if (a.product.tile == 256) {
+      loss_gradient<T, 256><<<groups, kThreads, 0, s>>>(a);
+      return;
+    }
+  }
+  if (a.product.tile == 128) loss_gradient<T, 128><<<groups, kThreads, 0, s>>>(a);
+  else loss_gradient<T, 64><<<groups, kThreads, 0, s>>>(a);
+}
+
+}  // namespace
+
+hipError_t launch_loss_forward(const LossForwardArgs& a, hipStream_t s) {
+  if (a.product.type == kBf16) forward_type<__bf16>(a, s);
+  else if (a.product.type == kF16) forward_type<_Float16>(a, s);
+  else forward_type<float>(a, s);
+  return hipGetLastError();
+}
+
+hipError_t launch_loss_gradient(const LossGradientArgs& a, hipStream_t s) {
+  if (a.product.type == kBf16) gradient_type<__bf16>(a, s);
+  else if (a.product.type == kF16) gradient_type<_Float16>(a, s);
+  else gradient_type<float>(a, s);
+  return hipGetLastError();
+}
+
+hipError_t launch_loss_finish(const LossFinishArgs& a, hipStream_t s) {
+  loss_finish<<<(unsigned)((a.m + 15) / 16), 256, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+hipError_t launch_teacher_weights(const TeacherArgs& a, hipStream_t s) {
+  if (a.m == 0 || a.list.per_row == 0) return hipSuccess;
+  const unsigned groups = (unsigned)((a.m + 3) / 4);
+  if (a.type == kBf16) teacher_weights<__bf16><<<groups, 256, 0, s>>>(a);
+  else if (a.type == kF16) teacher_weights<_Float16><<<groups, 256, 0, s>>>(a);
+  else teacher_weights<float><<<groups, 256, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+hipError_t launch_loss_factor(const LossFactorArgs& a, hipStream_t s) {
+  loss_factor<<<(unsigned)((a.m + 255) / 256), 256, 0, s>>>(a);
+  if (a.scale) loss_scale<<<1, 1024, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+}  // namespace xtvxy

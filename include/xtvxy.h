@@ -884,6 +884,130 @@ xtvxy_status xtvxy_embedding_backward_f16(int64_t count, int64_t k, int64_t rows
                                          const void *ids, int index_bits, float scale, int accumulate, uint16_t *dtable,
                                          int64_t lddt, void *workspace, size_t workspace_bytes, hipStream_t stream);
 
+/* ------------------------------------------------------------------------ */
+/* Losses over an output layer, with their gradients                        */
+/* ------------------------------------------------------------------------ */
+
+/* Softmax cross entropy of the layer's logits z = X W^T + bias against labels, without keeping the logits:
+ *     lse_i = log sum_j exp(z_ij),   loss_i = lse_i - z_i,label_i       (m floats each),
+ * X m x k, W n x k (one row per class), bias n floats or NULL, as for xtvxy_linear_*; labels (device) are int32_t or
+ * int64_t by index_bits (32 or 64). A negative label is a row that does not count: its loss is zero (its lse is
+ * stored all the same). A label >= n, which the host cannot see, gives loss NaN. Logits are summed and kept in fp32; the
+ * sums of exponentials of wide vocabularies are taken relative to each part's largest logit and joined in a fixed
+ * order. A bias of -infinity takes a class out; logits of +infinity give NaN, as do rows without any finite
+ * logit that count. Features and weights must be finite also in rows that do not count, where gradients are wanted.
+ * The vocabulary is processed in pieces where the workspace would grow beyond about 256 MiB.
+ *
+ * Any overlap of an output with an input or another output gives XTVXY_ERROR_ALIASING. Pointers and strides of
+ * any alignment; 16-byte aligned rows of X and W are the fast case, others are copied into the workspace (W piece by
+ * piece). aligned16 states whether X, W and their rows are 16-byte aligned with strides of at most 4 MiB. m == 0 is a
+ * no-op. k above 2^21 (fp32: 2^20), m or n above 2^31 - 1 or m above about 10^9 / 4 are XTVXY_ERROR_UNSUPPORTED.
+ * Results are bitwise reproducible for a given shape, type and alignment. */
+xtvxy_status xtvxy_linear_cross_entropy_f32_workspace_size(int64_t m, int64_t k, int64_t n, int aligned16, size_t *bytes);
+xtvxy_status xtvxy_linear_cross_entropy_f32(int64_t m, int64_t k, int64_t n, const float *X, int64_t ldx, const float *W,
+                                           int64_t ldw, const float *bias, const void *labels, int index_bits,
+                                           float *loss, float *lse, void *workspace, size_t workspace_bytes,
+                                           hipStream_t stream);
+xtvxy_status xtvxy_linear_cross_entropy_bf16_workspace_size(int64_t m, int64_t k, int64_t n, int aligned16, size_t *bytes);
+xtvxy_status xtvxy_linear_cross_entropy_bf16(int64_t m, int64_t k, int64_t n, const uint16_t *X, int64_t ldx, const uint16_t *W,
+                                           int64_t ldw, const float *bias, const void *labels, int index_bits,
+                                           float *loss, float *lse, void *workspace, size_t workspace_bytes,
+                                           hipStream_t stream);
+xtvxy_status xtvxy_linear_cross_entropy_f16_workspace_size(int64_t m, int64_t k, int64_t n, int aligned16, size_t *bytes);
+xtvxy_status xtvxy_linear_cross_entropy_f16(int64_t m, int64_t k, int64_t n, const uint16_t *X, int64_t ldx, const uint16_t *W,
+                                           int64_t ldw, const float *bias, const void *labels, int index_bits,
+                                           float *loss, float *lse, void *workspace, size_t workspace_bytes,
+                                           hipStream_t stream);
+
+/* Its gradient from grad_i = d total / d loss_i (m floats) and the forward call's lse:
+ *     d_ij = grad_i (exp(z_ij - lse_i) - [j = label_i]),   dX = d W,   dW = d^T X,   db_j = sum_i d_ij,
+ * d zero in rows with a negative label or a zero grad, NaN in rows with a label >= n. The logits are formed again,
+ * piece by piece of the vocabulary. d is formed in fp32; db sums it unrounded, and the products take it in the element
+ * type (fp16: scaled by a power of two chosen from the largest |grad|, so that small probabilities do not
+ * underflow). dX (m x k, lddx), dW (n x k, lddw) and db (n floats) may each be NULL. m == 0 gives dW = 0 and
+ * db = 0; n == 0 gives dX = 0. Otherwise as the forward call. */
+xtvxy_status xtvxy_linear_cross_entropy_backward_f32_workspace_size(int64_t m, int64_t k, int64_t n, int aligned16,
+                                                                    size_t *bytes);
+xtvxy_status xtvxy_linear_cross_entropy_backward_f32(int64_t m, int64_t k, int64_t n, const float *grad, const float *X,
+                                                    int64_t ldx, const float *W, int64_t ldw, const float *bias,
+                                                    const void *labels, int index_bits, const float *lse, float *dX,
+                                                    int64_t lddx, float *dW, int64_t lddw, float *db, void *workspace,
+                                                    size_t workspace_bytes, hipStream_t stream);
+xtvxy_status xtvxy_linear_cross_entropy_backward_bf16_workspace_size(int64_t m, int64_t k, int64_t n, int aligned16,
+                                                                    size_t *bytes);
+xtvxy_status xtvxy_linear_cross_entropy_backward_bf16(int64_t m, int64_t k, int64_t n, const float *grad, const uint16_t *X,
+                                                    int64_t ldx, const uint16_t *W, int64_t ldw, const float *bias,
+                                                    const void *labels, int index_bits, const float *lse, uint16_t *dX,
+                                                    int64_t lddx, uint16_t *dW, int64_t lddw, float *db, void *workspace,
+                                                    size_t workspace_bytes, hipStream_t stream);
+xtvxy_status xtvxy_linear_cross_entropy_backward_f16_workspace_size(int64_t m, int64_t k, int64_t n, int aligned16,
+                                                                    size_t *bytes);
+xtvxy_status xtvxy_linear_cross_entropy_backward_f16(int64_t m, int64_t k, int64_t n, const float *grad, const uint16_t *X,
+                                                    int64_t ldx, const uint16_t *W, int64_t ldw, const float *bias,
+                                                    const void *labels, int index_bits, const float *lse, uint16_t *dX,
+                                                    int64_t lddx, uint16_t *dW, int64_t lddw, float *db, void *workspace,
+                                                    size_t workspace_bytes, hipStream_t stream);
+
+/* Distillation from a teacher's top logits: row i lists s classes (classes m x s of index_bits, row stride ldc >= s)
+ * with the teacher's logits (m x s, row stride ldt >= s, of teacher_type XTVXY_TYPE_F32, _BF16 or _F16). With t =
+ * (X W^T + bias) / temperature,
+ *     P_i = softmax(teacher_i / temperature) over the listed classes,
+ *     loss_i = sum_c P_ic (log P_ic - t_i,c + lse_i),   lse_i = log sum_j exp(t_ij) over all classes:
+ * the Kullback-Leibler distance of the student's whole distribution from P. weights (m x s floats, contiguous) gets P.
+ * A negative class is an empty place; a class that a row lists twice gets both probabilities, in its first
+ * place. A row without classes, or of which all logits are -infinity, does not count: loss and weights zero. A class
+ * >= n or a NaN or +infinity logit gives NaN for the row. s up to 1024; temperature positive and finite. Otherwise as
+ * xtvxy_linear_cross_entropy_*. */
+xtvxy_status xtvxy_linear_distillation_f32_workspace_size(int64_t m, int64_t k, int64_t n, int64_t s, int aligned16,
+                                                          size_t *bytes);
+xtvxy_status xtvxy_linear_distillation_f32(int64_t m, int64_t k, int64_t n, const float *X, int64_t ldx, const float *W,
+                                          int64_t ldw, const float *bias, int64_t s, const void *classes, int64_t ldc,
+                                          int index_bits, const void *teacher, int64_t ldt, int teacher_type,
+                                          float temperature, float *loss, float *lse, float *weights, void *workspace,
+                                          size_t workspace_bytes, hipStream_t stream);
+xtvxy_status xtvxy_linear_distillation_bf16_workspace_size(int64_t m, int64_t k, int64_t n, int64_t s, int aligned16,
+                                                          size_t *bytes);
+xtvxy_status xtvxy_linear_distillation_bf16(int64_t m, int64_t k, int64_t n, const uint16_t *X, int64_t ldx, const uint16_t *W,
+                                          int64_t ldw, const float *bias, int64_t s, const void *classes, int64_t ldc,
+                                          int index_bits, const void *teacher, int64_t ldt, int teacher_type,
+                                          float temperature, float *loss, float *lse, float *weights, void *workspace,
+                                          size_t workspace_bytes, hipStream_t stream);
+xtvxy_status xtvxy_linear_distillation_f16_workspace_size(int64_t m, int64_t k, int64_t n, int64_t s, int aligned16,
+                                                          size_t *bytes);
+xtvxy_status xtvxy_linear_distillation_f16(int64_t m, int64_t k, int64_t n, const uint16_t *X, int64_t ldx, const uint16_t *W,
+                                          int64_t ldw, const float *bias, int64_t s, const void *classes, int64_t ldc,
+                                          int index_bits, const void *teacher, int64_t ldt, int teacher_type,
+                                          float temperature, float *loss, float *lse, float *weights, void *workspace,
+                                          size_t workspace_bytes, hipStream_t stream);
+
+/* Its gradient from grad and the forward call's weights and lse:
+ *     d_ij = grad_i / temperature (exp(t_ij - lse_i) - P_ij),
+ * then as xtvxy_linear_cross_entropy_backward_*. Rows whose weights are all zero take no part. */
+xtvxy_status xtvxy_linear_distillation_backward_f32_workspace_size(int64_t m, int64_t k, int64_t n, int64_t s,
+                                                                   int aligned16, size_t *bytes);
+xtvxy_status xtvxy_linear_distillation_backward_f32(int64_t m, int64_t k, int64_t n, const float *grad, const float *X,
+                                                   int64_t ldx, const float *W, int64_t ldw, const float *bias,
+                                                   int64_t s, const void *classes, int64_t ldc, int index_bits,
+                                                   const float *weights, float temperature, const float *lse, float *dX,
+                                                   int64_t lddx, float *dW, int64_t lddw, float *db, void *workspace,
+                                                   size_t workspace_bytes, hipStream_t stream);
+xtvxy_status xtvxy_linear_distillation_backward_bf16_workspace_size(int64_t m, int64_t k, int64_t n, int64_t s,
+                                                                   int aligned16, size_t *bytes);
+xtvxy_status xtvxy_linear_distillation_backward_bf16(int64_t m, int64_t k, int64_t n, const float *grad, const uint16_t *X,
+                                                   int64_t ldx, const uint16_t *W, int64_t ldw, const float *bias,
+                                                   int64_t s, const void *classes, int64_t ldc, int index_bits,
+                                                   const float *weights, float temperature, const float *lse, uint16_t *dX,
+                                                   int64_t lddx, uint16_t *dW, int64_t lddw, float *db, void *workspace,
+                                                   size_t workspace_bytes, hipStream_t stream);
+xtvxy_status xtvxy_linear_distillation_backward_f16_workspace_size(int64_t m, int64_t k, int64_t n, int64_t s,
+                                                                   int aligned16, size_t *bytes);
+xtvxy_status xtvxy_linear_distillation_backward_f16(int64_t m, int64_t k, int64_t n, const float *grad, const uint16_t *X,
+                                                   int64_t ldx, const uint16_t *W, int64_t ldw, const float *bias,
+                                                   int64_t s, const void *classes, int64_t ldc, int index_bits,
+                                                   const float *weights, float temperature, const float *lse, uint16_t *dX,
+                                                   int64_t lddx, uint16_t *dW, int64_t lddw, float *db, void *workspace,
+                                                   size_t workspace_bytes, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

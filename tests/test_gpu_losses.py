@@ -1,0 +1,397 @@
+"""GPU parity of the losses over an output layer and their gradients against the fp64 oracle, within bounds that count
+roundings: sizes from one class up, odd ones, several pieces of the vocabulary, rows that do not count, classes taken out
+by the bias, lists with empty and equal places, views, streams, graphs."""
+import pytest
+import torch
+
+import dense_linear_algebra_alpha_amd as xt
+import layer_oracle as L
+import loss_oracle as O
+from gpu_util import dev, note
+
+pytestmark = pytest.mark.gpu
+
+
+def rand(shape, seed, dtype=torch.float32, scale=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(shape, generator=g) * scale).to(dtype)
+
+
+def whole(n, shape, seed):
+    return torch.randint(0, n, shape, generator=torch.Generator().manual_seed(seed))
+
+
+def inputs(m, k, n, dt, seed, bias=True):
+    X, W = rand((m, k), seed, dt), rand((n, k), seed + 1, dt, 2.0 * max(k, 1) ** -0.5)
+    labels = whole(n, (m,), seed + 2)
+    if m > 1:
+        labels = torch.where(torch.rand(m, generator=torch.Generator().manual_seed(seed + 3)) < 0.2, -100, labels)
+    grad = rand(m, seed + 4).abs() + 0.1
+    return X, W, rand(n, seed + 5) if bias else None, labels, grad / m
+
+
+def lists(m, n, s, seed):
+    """Classes with empty and equal places and rows without any, and a teacher's logits."""
+    classes = whole(n, (m, s), seed)
+    empty = torch.rand((m, s), generator=torch.Generator().manual_seed(seed + 1)) < 0.2
+    classes = torch.where(empty, -1, classes)
+    if m > 3:
+        classes[3] = -1
+    return classes, rand((m, s), seed + 2, scale=2.0)
+
+
+def cuda(*ts):
+    return [None if t is None else t.to(dev()) for t in ts]
+
+
+def check_all(got, ref, what):
+    for t, name in zip(got, ("dX", "dW", "db")):
+        L.check(t, *ref[name], what="%s %s" % (what, name))
+
+
+SIZES = [(1, 1, 1), (3, 5, 2), (2, 8, 1), (17, 33, 65), (64, 64, 64), (65, 129, 70), (1, 256, 1000), (33, 100, 513), (300, 40, 1000),
+         (130, 264, 5000), (257, 96, 8200), (5, 1031, 300), (1000, 64, 10), (513, 520, 264), (700, 256, 2500)]
+
+
+@pytest.mark.parametrize("dtype", list(L.DTYPES))
+@pytest.mark.parametrize("size", SIZES, ids=lambda s: "%dx%dx%d" % s)
+def test_cross_entropy(size, dtype):
+    m, k, n = size
+    dt = L.DTYPES[dtype]
+    X, W, b, labels, grad = inputs(m, k, n, dt, m + k + n, (m + n) % 3 != 0)
+    labels = labels.to(torch.int32 if k % 2 else torch.int64)
+    gX, gW, gb, gl, gg = cuda(X, W, b, labels, grad)
+    note("linear_cross_entropy %s %s" % (size, dtype))
+    loss, lse = xt.linear_cross_entropy(gX, gW, gl, gb)
+    torch.cuda.synchronize()
+    target = O.of_labels(labels)
+    for got, (ref, bound), what in zip((loss, lse), O.forward(X, W, b, *target), ("loss", "lse")):
+        L.check(got, ref, bound, "%s %s %s" % (size, dtype, what))
+    note("linear_cross_entropy_backward %s %s" % (size, dtype))
+    got = xt.linear_cross_entropy_backward(gg, gX, gW, gl, lse, gb)
+    again = xt.linear_cross_entropy_backward(gg, gX, gW, gl, lse, gb)
+    torch.cuda.synchronize()
+    check_all(got, O.backward(grad, X, W, b, *target, lse=lse.cpu()), "%s %s" % (size, dtype))
+    assert all(torch.equal(a, c) for a, c in zip(got, again))
+
+
+@pytest.mark.parametrize("dtype", list(L.DTYPES))
+@pytest.mark.parametrize("size", [(1, 8, 3, 1), (17, 33, 65, 2), (65, 129, 700, 8), (300, 64, 2500, 32), (130, 264, 900, 70), (5, 16, 5000, 1024)],
+                         ids=lambda s: "%dx%dx%dx%d" % s)
+def test_distillation(size, dtype):
+    m, k, n, s = size
+    dt = L.DTYPES[dtype]
+    X, W, b, _, grad = inputs(m, k, n, dt, m + k + n, n % 2 == 0)
+    classes, teacher = lists(m, n, s, s)
+    classes = classes.to(torch.int32 if k % 2 else torch.int64)
+    teacher = teacher.to((dt, torch.float32)[s % 2])
+    T = (1.0, 2.0, 0.7)[m % 3]
+    gX, gW, gb, gc, gt, gg = cuda(X, W, b, classes, teacher, grad)
+    note("linear_distillation %s %s" % (size, dtype))
+    loss, lse, weights = xt.linear_distillation(gX, gW, gc, gt, gb, T)
+    torch.cuda.synchronize()
+    P, eP = O.targets(classes, teacher, n, T)
+    L.check(weights, P, eP + 1e-40, "%s %s weights" % (size, dtype))
+    for got, (ref, bound), what in zip((loss, lse), O.forward(X, W, b, classes, P, eP, T), ("loss", "lse")):
+        L.check(got, ref, bound, "%s %s %s" % (size, dtype, what))
+    note("linear_distillation_backward %s %s" % (size, dtype))
+    got = xt.linear_distillation_backward(gg, gX, gW, gc, weights, lse, gb, T)
+    torch.cuda.synchronize()
+    check_all(got, O.backward(grad, X, W, b, classes, weights.cpu().double(), torch.zeros_like(P), T, lse=lse.cpu()), "%s %s" % (size, dtype))
+
+
+@pytest.mark.parametrize("dtype", list(L.DTYPES))
+@pytest.mark.parametrize("k", [32, 35])
+def test_several_pieces_of_the_vocabulary(dtype, k):
+    """So many rows that d is formed in pieces; k = 35: copies of the weights' pieces too. The oracle runs on the GPU."""
+    m, n = (10000, 13001) if dtype == "f32" else (20000, 13001)
+    dt = L.DTYPES[dtype]
+    X, W, b, labels, grad = cuda(*inputs(m, k, n, dt, 7))
+    note("pieces %s %d" % (dtype, k))
+    loss, lse = xt.linear_cross_entropy(X, W, labels, b)
+    got = xt.linear_cross_entropy_backward(grad, X, W, labels, lse, b)
+    only = [xt.linear_cross_entropy_backward(grad, X, W, labels, lse, b, need_dX=i == 0, need_dW=i == 1, need_db=i == 2)[i] for i in range(3)]
+    torch.cuda.synchronize()
+    target = O.of_labels(labels)
+    for t, (ref, bound), what in zip((loss, lse), O.forward(X, W, b, *target), ("loss", "lse")):
+        L.check(t, ref, bound, what)
+    ref = O.backward(grad, X, W, b, *target, lse=lse)
+    check_all(got, ref, dtype)
+    check_all(only, ref, dtype + " alone")
+
+
+def test_many_rows_in_the_forward_pass():
+    """Statistics in pieces of the vocabulary: rows x classes beyond what is kept at once."""
+    m, k, n = 300_000, 8, 10_000
+    X, W, b, labels, _ = cuda(*inputs(m, k, n, torch.bfloat16, 9))
+    note("statistics in pieces")
+    assert xt.xtvxy_linear_cross_entropy_bf16_workspace_size(m, k, n) < m * (n // 32) * 8
+    loss, lse = xt.linear_cross_entropy(X, W, labels, b)
+    torch.cuda.synchronize()
+    rows = torch.arange(0, m, 3001, device=dev())
+    for t, (ref, bound) in zip((loss, lse), O.forward(X[rows], W, b, *O.of_labels(labels[rows]))):
+        L.check(t[rows], ref, bound, "rows")
+
+
+def test_gradient_against_differences():
+    X, W, b, labels, grad = inputs(6, 10, 17, torch.float32, 11)
+    classes, teacher = lists(6, 17, 4, 12)
+    gX, gW, gb, gl, gg, gc, gt = cuda(X, W, b, labels, grad, classes, teacher)
+    loss, lse = xt.linear_cross_entropy(gX, gW, gl, gb)
+    hard = xt.linear_cross_entropy_backward(gg, gX, gW, gl, lse, gb)
+    _, lse, weights = xt.linear_distillation(gX, gW, gc, gt, gb, 2.0)
+    soft = xt.linear_distillation_backward(gg, gX, gW, gc, weights, lse, gb, 2.0)
+    torch.cuda.synchronize()
+    P = O.targets(classes, teacher, 17, 2.0)[0]
+
+    def total(x, w, c, which):
+        z = x @ w.T + c
+        if which == "hard":
+            on = labels >= 0
+            l = torch.where(on, torch.logsumexp(z, 1) - z.gather(1, labels.clamp_min(0)[:, None])[:, 0], 0.0)
+        else:
+            logp = torch.log_softmax(z / 2.0, 1).gather(1, classes.clamp_min(0))
+            l = (P * (torch.log(P.clamp_min(1e-30)) - logp)).sum(1)
+        return (l * grad.double()).sum()
+
+    args, eps = [X.double(), W.double(), b.double()], 1e-5
+    for which, got in (("hard", hard), ("soft", soft)):
+        for i in range(3):
+            for at in (0, 5, args[i].numel() - 1):
+                def moved(by):
+                    a = [t.clone() for t in args]
+                    a[i].view(-1)[at] += by
+                    return total(*a, which)
+                slope = (moved(eps) - moved(-eps)) / (2 * eps)  # off by eps^2 f''' / 6 ~ 1e-10
+                assert abs(got[i].view(-1)[at].item() - slope.item()) <= 1e-6, (which, i, at)
+
+
+def test_rows_that_do_not_count_and_bad_ones():
+    m, k, n = 70, 40, 200
+    X, W, b, _, grad = inputs(m, k, n, torch.float32, 21)
+    labels = whole(n, (m,), 3)
+    labels[5], labels[6], labels[7] = -1, -100, -2 ** 40
+    X[6] = float("nan")  # what padding holds does not reach the loss
+    gX, gW, gb, gl, gg = cuda(X, W, b, labels, grad)
+    loss, lse = xt.linear_cross_entropy(gX, gW, gl, gb)
+    torch.cuda.synchronize()
+    assert (loss[5:8] == 0).all() and torch.isfinite(loss).all() and torch.isnan(lse[6])
+    dX, _, db = xt.linear_cross_entropy_backward(gg, gX, gW, gl, lse, gb, need_dW=False)
+    torch.cuda.synchronize()
+    assert not dX[5:8].any() and torch.isfinite(dX).all() and torch.isfinite(db).all()
+    for bad in (n, 2 ** 40):
+        gl[9] = bad
+        gX[6] = 0.0
+        loss, lse = xt.linear_cross_entropy(gX, gW, gl, gb)
+        dX, _, _ = xt.linear_cross_entropy_backward(gg, gX, gW, gl, lse, gb)
+        torch.cuda.synchronize()
+        assert torch.isnan(loss[9]) and torch.isfinite(lse).all() and loss.isnan().sum() == 1
+        assert torch.isnan(dX[9]).all() and torch.isfinite(dX[:9]).all() and torch.isfinite(dX[10:]).all()
+    # a grad of zero takes a row out, too
+    gl[9], gg[11] = 0, 0.0
+    dX, _, _ = xt.linear_cross_entropy_backward(gg, gX, gW, gl, xt.linear_cross_entropy(gX, gW, gl, gb)[1], gb)
+    torch.cuda.synchronize()
+    assert not dX[11].any() and dX[12].any()
+
+
+@pytest.mark.parametrize("dtype", list(L.DTYPES))
+def test_classes_taken_out(dtype):
+    """A bias of -infinity: whole tiles of the vocabulary, single classes, all classes; the lowest value of the type."""
+    m, k, n = 40, 64, 1500
+    dt = L.DTYPES[dtype]
+    X, W, b, labels, grad = inputs(m, k, n, dt, 31)
+    labels = labels.clamp_max(99)
+    b[100:900] = float("-inf")
+    b[1200::7] = torch.finfo(torch.float32).min
+    gX, gW, gb, gl, gg = cuda(X, W, b, labels, grad)
+    note("classes taken out %s" % dtype)
+    loss, lse = xt.linear_cross_entropy(gX, gW, gl, gb)
+    dX, dW, db = xt.linear_cross_entropy_backward(gg, gX, gW, gl, lse, gb)
+    torch.cuda.synchronize()
+    keep = torch.isfinite(b) & (b > -1e30)
+    few, where = b[keep], torch.cumsum(keep, 0) - 1
+    there = torch.where(labels >= 0, where[labels.clamp_min(0)], labels)
+    target = O.of_labels(there)
+    for t, (ref, bound) in zip((loss, lse), O.forward(X, W[keep], few, *target)):
+        L.check(t, ref, bound * 1.1, "loss")
+    ref = O.backward(grad, X, W[keep], few, *target, lse=lse.cpu())
+    check_all((dX, dW[keep.to(dev())], db[keep.to(dev())]), ref, dtype)
+    assert not dW[~keep.to(dev())].any() and not db[~keep.to(dev())].any()
+    gl[:] = 150  # taken out itself
+    loss, lse = xt.linear_cross_entropy(gX, gW, gl, gb)
+    gb[:] = float("-inf")
+    none, empty = xt.linear_cross_entropy(gX, gW, gl, gb)
+    torch.cuda.synchronize()
+    assert (loss == float("inf")).all() and torch.isnan(none).all() and (empty == float("-inf")).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_large_logits_and_small_gradients(dtype):
+    """Logits up to about 1000, and gradients that fp16 does not hold unscaled."""
+    m, k, n = 100, 128, 3000
+    dt = L.DTYPES[dtype]
+    X, W, b, labels, _ = inputs(m, k, n, dt, 41)
+    X = (X.float() * 40).to(dt)
+    grad = torch.full((m,), 1e-4)
+    gX, gW, gb, gl, gg = cuda(X, W, b, labels, grad)
+    note("large logits %s" % dtype)
+    loss, lse = xt.linear_cross_entropy(gX, gW, gl, gb)
+    got = xt.linear_cross_entropy_backward(gg, gX, gW, gl, lse, gb)
+    torch.cuda.synchronize()
+    target = O.of_labels(labels)
+    for t, (ref, bound) in zip((loss, lse), O.forward(X, W, b, *target)):
+        L.check(t, ref, bound, "loss")
+    check_all(got, O.backward(grad, X, W, b, *target, lse=lse.cpu()), dtype)
+    X = (X.float() / 40).to(dt)
+    gX = X.to(dev())
+    _, lse = xt.linear_cross_entropy(gX, gW, gl, gb)
+    for size in (1e-9, 1e-5, 300.0):
+        grad = torch.full((m,), size)
+        dX, dW, db = xt.linear_cross_entropy_backward(grad.to(dev()), gX, gW, gl, lse, gb)
+        torch.cuda.synchronize()
+        check_all((dX, dW, db), O.backward(grad, X, W, b, *target, lse=lse.cpu()), "%s %g" % (dtype, size))
+
+
+def test_teacher_rows_without_a_distribution():
+    m, k, n, s = 6, 16, 50, 4
+    X, W, b, _, grad = inputs(m, k, n, torch.float32, 51)
+    classes = whole(n, (m, s), 52)
+    for i in range(m):
+        classes[i] = torch.arange(s) + i
+    teacher = rand((m, s), 53)
+    classes[0] = -1
+    teacher[1] = float("-inf")
+    classes[2, 1] = n
+    teacher[3, 2] = float("nan")
+    teacher[4, :3] = float("-inf")
+    gX, gW, gb, gc, gt, gg = cuda(X, W, b, classes, teacher, grad)
+    loss, lse, w = xt.linear_distillation(gX, gW, gc, gt, gb)
+    dX, _, _ = xt.linear_distillation_backward(gg, gX, gW, gc, w, lse, gb)
+    torch.cuda.synchronize()
+    assert (loss[:2] == 0).all() and not w[:2].any() and not dX[:2].any()
+    assert torch.isnan(loss[2:4]).all() and torch.isnan(w[2:4]).all() and torch.isnan(dX[2:4]).all()
+    assert torch.equal(w[4].cpu(), torch.tensor([0.0, 0.0, 0.0, 1.0]))
+    # one class with all the probability is a label
+    hard, _ = xt.linear_cross_entropy(gX[4:], gW, gc[4:, 3].contiguous(), gb)
+    torch.cuda.synchronize()
+    assert hard[0] == loss[4] and torch.isfinite(loss[4:]).all()
+    none, l0, w0 = xt.linear_distillation(gX, gW, gc[:, :0].contiguous(), gt[:, :0], gb)
+    d0, _, _ = xt.linear_distillation_backward(gg, gX, gW, gc[:, :0].contiguous(), w0, l0, gb)
+    torch.cuda.synchronize()
+    assert not none.any() and torch.equal(l0, lse) and w0.shape == (m, 0) and not d0.any()
+
+
+@pytest.mark.parametrize("dtype", list(L.DTYPES))
+def test_zero_sizes(dtype):
+    d, dt = dev(), L.DTYPES[dtype]
+    e = lambda *s: torch.empty(*s, dtype=dt, device=d)  # noqa: E731
+    labels = torch.tensor([0, -1, 2], device=d)
+    b = torch.arange(3.0, device=d)
+    note("zero sizes %s" % dtype)
+    loss, lse = xt.linear_cross_entropy(e(3, 0), e(3, 0), labels, b)
+    dX, dW, db = xt.linear_cross_entropy_backward(torch.ones(3, device=d), e(3, 0), e(3, 0), labels, lse, b)
+    torch.cuda.synchronize()
+    want = torch.logsumexp(b.double(), 0)
+    assert torch.allclose(lse.double(), want.expand(3), atol=1e-6) and dX.shape == (3, 0) and dW.shape == (3, 0)
+    assert torch.allclose(loss.double(), torch.stack([want, want * 0, want - 2]), atol=1e-6)
+    p = torch.softmax(b, 0) * 2
+    assert torch.allclose(db, p - torch.tensor([1.0, 0.0, 1.0], device=d), atol=1e-6)
+    loss, lse = xt.linear_cross_entropy(e(3, 5), e(0, 5), labels)
+    dX, dW, db = xt.linear_cross_entropy_backward(torch.ones(3, device=d), e(3, 5), e(0, 5), labels, lse)
+    torch.cuda.synchronize()
+    assert torch.isnan(loss[[0, 2]]).all() and loss[1] == 0 and (lse == float("-inf")).all()
+    assert not dX.any() and dW.shape == (0, 5) and db.shape == (0,)
+    none = torch.empty(0, dtype=torch.int64, device=d)
+    loss, lse = xt.linear_cross_entropy(e(0, 5), e(4, 5), none)
+    dX, dW, db = xt.linear_cross_entropy_backward(lse, e(0, 5), e(4, 5), none, lse)
+    torch.cuda.synchronize()
+    assert loss.shape == (0,) and dX.shape == (0, 5) and not dW.any() and not db.any()
+
+
+@pytest.mark.parametrize("dtype", list(L.DTYPES))
+@pytest.mark.parametrize("size", [(70, 96, 130), (300, 100, 1000)], ids=lambda s: "%dx%dx%d" % s)
+@pytest.mark.parametrize("offset", [1, 8])
+def test_views_of_wider_buffers(size, dtype, offset):
+    m, k, n = size
+    dt = L.DTYPES[dtype]
+    X, W, b, labels, grad = inputs(m, k, n, dt, 61)
+
+    def view(t, fill=float("nan")):
+        buf = torch.full((t.shape[0], t.shape[1] + offset + 8), fill, dtype=t.dtype, device=dev())
+        v = buf[:, offset:offset + t.shape[1]]
+        v.copy_(t)
+        return buf, v
+
+    (_, vX), (_, vW), (xb, dX), (wb, dW) = view(X), view(W), view(X, 7.0), view(W, 7.0)
+    gb, gl, gg = cuda(b, labels, grad)
+    note("loss views %s %s offset %d" % (size, dtype, offset))
+    loss, lse = xt.linear_cross_entropy(vX, vW, gl, gb)
+    got = xt.linear_cross_entropy_backward(gg, vX, vW, gl, lse, gb, dX=dX, dW=dW)
+    torch.cuda.synchronize()
+    target = O.of_labels(labels)
+    for t, (ref, bound) in zip((loss, lse), O.forward(X, W, b, *target)):
+        L.check(t, ref, bound, "loss")
+    check_all(got, O.backward(grad, X, W, b, *target, lse=lse.cpu()), dtype)
+    for buf, w in ((xb, k), (wb, k)):
+        assert (buf[:, :offset] == 7.0).all() and (buf[:, offset + w:] == 7.0).all()
+
+
+def test_weights_beyond_two_to_the_31_elements():
+    m, k, n = 5, 4096, 530_000
+    W = torch.zeros(n, k, dtype=torch.float16, device=dev())
+    X, tail = rand((m, k), 71, torch.float16), rand((2, k), 72, torch.float16, 0.05)
+    W[-2:] = tail.to(dev())
+    labels = torch.tensor([n - 1, 0, n - 2, n - 1, 5])
+    gX, gl = cuda(X, labels)
+    note("weights of 2^31 elements")
+    loss, lse = xt.linear_cross_entropy(gX, W, gl)
+    dX, dW, _ = xt.linear_cross_entropy_backward(torch.ones(m, device=dev()), gX, W, gl, lse)
+    torch.cuda.synchronize()
+    z = X.double() @ tail.double().T
+    want = torch.logsumexp(torch.cat([z, torch.full((m, 1), float(n - 2), dtype=torch.float64).log()], 1), 1)
+    at = torch.tensor([1, -1, 0, 1, -1])
+    zl = torch.where(at >= 0, z.gather(1, at.clamp_min(0)[:, None])[:, 0], 0.0)
+    # 1e-4: sums of 4096 products of magnitude below 0.2, (4096 + 4) 2^-23 of their 160
+    assert (lse.cpu().double() - want).abs().max() <= 1e-4 and (loss.cpu().double() - (want - zl)).abs().max() <= 2e-4
+    d = torch.exp(z - want[:, None])
+    d[0, 1] -= 1
+    d[3, 1] -= 1
+    d[2, 0] -= 1
+    assert (dW[-2:].cpu().double() - d.T @ X.double()).abs().max() <= 2e-2 and dW[0].any() and not dW[6:-2:1000].abs().gt(1e-4).any()
+    assert (dX.cpu().double() - d @ tail.double()).abs().max() <= 1e-3
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16"])
+def test_streams_and_graph(dtype):
+    m, k, n, s = 200, 128, 3000, 8
+    dt = L.DTYPES[dtype]
+    X, W, b, labels, grad = cuda(*inputs(m, k, n, dt, 81))
+    classes, teacher = cuda(*lists(m, n, s, 82))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+
+    def step(stream=None):
+        kw = {} if stream is None else {"stream": stream}
+        loss, lse = xt.linear_cross_entropy(X, W, labels, b, **kw)
+        soft, lse2, w = xt.linear_distillation(X, W, classes, teacher, b, 2.0, **kw)
+        return (loss, lse, soft, lse2, w) + xt.linear_cross_entropy_backward(grad, X, W, labels, lse, b, **kw) \
+            + xt.linear_distillation_backward(grad, X, W, classes, w, lse2, b, 2.0, **kw)
+
+    note("losses on a stream %s" % dtype)
+    got = step(side)
+    torch.cuda.current_stream().wait_stream(side)
+    want = step()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, c) for a, c in zip(got, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for seed in range(3):
+        X.copy_(rand((m, k), 90 + seed))
+        labels.copy_(whole(n, (m,), 93 + seed))
+        note("losses replay %d" % seed)
+        graph.replay()
+        torch.cuda.synchronize()
+        want = step()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, c) for a, c in zip(out, want))
