@@ -30,6 +30,7 @@ xtvxy_status embedding_impl(int type, int64_t count, int64_t k, int64_t rows, co
 }
 
 struct GradientPlan {
+  int piece = 0;
   size_t keys[2], from[2], counts, partial, bytes = 0;
 };
 
@@ -45,8 +46,10 @@ GradientPlan plan_gradient(int type, int64_t count, int64_t k) {
     p.keys[i] = take(i == 0 || groups > 1 ? (size_t)count * 4 : 0);
     p.from[i] = take(i == 0 || groups > 1 ? (size_t)count * 4 : 0);
   }
-  p.counts = take(groups > 1 ? (size_t)groups * kDigits * 4 : 0);
-  const int64_t pieces = piece_count(count), columns = slab_columns(type);
+  p.counts = take(count > kSortUncounted ? (size_t)groups * kDigits * 4 : 0);
+  const int64_t columns = slab_columns(type);
+  p.piece = piece_tokens(count, cdiv(k, columns));
+  const int64_t pieces = piece_count(count, p.piece);
   p.partial = take(pieces > 1 ? (size_t)pieces * 2 * (cdiv(k, columns) * columns) * 4 : 0);
   return p;
 }
@@ -55,7 +58,7 @@ xtvxy_status gradient_limits(int type, int64_t count, int64_t k, int64_t rows) {
   if (count < 0 || k < 0 || rows < 0 || padded_overflow(count, k) || bytes_overflow(rows, k)) return XTVXY_ERROR_INVALID_VALUE;
   // pieces x slabs are one launch's workgroups
   const int64_t slabs = cdiv(k, slab_columns(type));
-  if (count > kMostTokens || rows > kMostRows || (slabs > 0 && piece_count(count) > (((int64_t)1 << 24) - 1) / slabs))
+  if (count > kMostTokens || rows > kMostRows || (slabs > 0 && piece_count(count, 32) > (((int64_t)1 << 24) - 1) / slabs))
     return XTVXY_ERROR_UNSUPPORTED;
   return XTVXY_SUCCESS;
 }
@@ -83,7 +86,7 @@ xtvxy_status gradient_impl(int type, int64_t count, int64_t k, int64_t rows, con
   const GradientPlan p = count > 0 ? plan_gradient(type, count, k) : GradientPlan{};
   if (count > 0 && (!ws || ws_bytes < p.bytes || reinterpret_cast<uintptr_t>(ws) % kAlign != 0)) return XTVXY_ERROR_WORKSPACE;
   char* base = static_cast<char*>(ws);
-  EmbeddingGradientArgs a{G, ldg, ids, index_bits, accumulate != 0, count, k, rows, scale, dtable, lddt, {}, {}, nullptr, nullptr};
+  EmbeddingGradientArgs a{G, ldg, ids, index_bits, accumulate != 0, count, k, rows, scale, p.piece, dtable, lddt, {}, {}, nullptr, nullptr};
   if (count > 0) {
     for (int i = 0; i < 2; ++i) {
       a.keys[i] = reinterpret_cast<uint32_t*>(base + p.keys[i]);

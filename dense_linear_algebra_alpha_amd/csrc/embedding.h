@@ -17,10 +17,11 @@ struct EmbeddingArgs {
 };
 hipError_t launch_embedding(const EmbeddingArgs& a, int type, hipStream_t s);
 
-constexpr int kSortItems = 16384;    // keys of a sorting workgroup (1024 threads x 16)
-constexpr int kDigitBits = 9;        // most bits of a sorting pass
+constexpr int kSortAlone = 1024;        // keys up to which one workgroup sorts
+constexpr int kSortUncounted = 32768;   // up to which its passes do without a launch that counts digits
+constexpr int kCountedTile = 4096;      // keys of a workgroup beyond (1024 up to there)
+constexpr int kDigitBits = 9;        // most bits of their passes
 constexpr int kDigits = 1 << kDigitBits;
-constexpr int kPieceTokens = 32;     // sorted tokens that a wavefront sums
 constexpr int kSlabBytes = 1024;     // of a row's columns, per wavefront
 
 struct EmbeddingGradientArgs {
@@ -30,6 +31,7 @@ struct EmbeddingGradientArgs {
   int32_t index_bits, accumulate;
   int64_t count, k, rows;
   float scale;
+  int32_t piece;        // tokens
   void* dtable;
   int64_t lddt;
   // workspace: tokens sorted by their row (keys; rows: no row) and where they come from, twice where
@@ -39,9 +41,12 @@ struct EmbeddingGradientArgs {
   uint32_t* counts;
   float* partial;       // [pieces][2][padded columns]
 };
-inline int64_t sort_groups(int64_t count) { return (count + kSortItems - 1) / kSortItems; }
-inline int64_t piece_count(int64_t count) { return (count + kPieceTokens - 1) / kPieceTokens; }
+inline int64_t sort_groups(int64_t count) { return count <= kSortUncounted ? (count + 1023) / 1024 : (count + kCountedTile - 1) / kCountedTile; }
 inline int64_t slab_columns(int type) { return kSlabBytes / elem_size(type); }
+// Sorted tokens that a wavefront sums: 32, or fewer where that leaves CUs without work (a wavefront loads 8 rows at a
+// time, and each time waits for memory).
+inline int piece_tokens(int64_t count, int64_t slabs) { return count * slabs >= 32 * 1024 ? 32 : count * slabs >= 16 * 1024 ? 16 : 8; }
+inline int64_t piece_count(int64_t count, int piece) { return (count + piece - 1) / piece; }
 hipError_t launch_embedding_gradient(const EmbeddingGradientArgs& a, int type, hipStream_t s);
 
 }  // namespace xtvxy

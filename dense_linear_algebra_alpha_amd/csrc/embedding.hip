@@ -5,11 +5,13 @@
 //
 // The gradient sorts the tokens by their row (a stable radix sort, 9 bits a pass or less), so that each row's sum is
 // taken in the order of the tokens, in fp32, and rounded once: it is bitwise reproducible, and needs no atomics.
-// Up to 16384 tokens one workgroup sorts in LDS; the other CUs write the table's zeros meanwhile. Beyond, each pass
-// takes a launch that counts digits and one that places the tokens, and each writes its share of the zeros.
-// Then a wavefront sums 32 sorted tokens over 1 KiB of their columns. A row whose tokens lie within the 32 is
-// written at once; of rows that cross over, which frequent words have, the sums go to the workspace and a last launch
+// Up to 1024 tokens one workgroup sorts in LDS. Beyond, each pass
+// is a launch, beyond 32768 tokens one that counts digits and one that places the tokens. Meanwhile the other CUs
+// write the table's zeros, each launch its share of them.
+// Then a wavefront sums a piece of the sorted tokens over 1 KiB of their columns. A row whose tokens lie within the
+// piece is written at once; of rows that cross over, which frequent words have, the sums go to the workspace and a last launch
 // joins them in order.
+#include <type_traits>
 #include <utility>
 
 #include "embedding.h"
@@ -29,7 +31,7 @@ __device__ __forceinline__ int64_t index_at(const void* p, int bits, int64_t i) 
 // chunks is its last 16 bytes, written twice in part. kNarrow: rows shorter than a chunk.
 template <typename T, int kLanes, bool kNarrow>
 __global__ __launch_bounds__(256) void embedding_rows(EmbeddingArgs a) {
-  constexpr int V = kChunkOf<T>, kTokens = 256 / kLanes, kBatch = 4;
+  constexpr int V = kChunkOf<T>, kTokens = 256 / kLanes, kBatch = 8;
   const int t = threadIdx.x % kLanes;
   const int64_t chunks = (a.k + V - 1) / V;
   for (int64_t i = (int64_t)blockIdx.x * kTokens + threadIdx.x / kLanes; i < a.count; i += (int64_t)gridDim.x * kTokens) {
@@ -67,7 +69,7 @@ __global__ __launch_bounds__(256) void embedding_rows(EmbeddingArgs a) {
 // the gradient: sorting
 // ---------------------------------------------------------------------------
 
-constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64, kSortRounds = kSortItems / kSortThreads;
+constexpr int kSortThreads = 1024;
 
 // The zeros of rows [first, end) of the table, by the workgroups from `groups` on.
 struct Fill {
@@ -82,11 +84,13 @@ __device__ __forceinline__ void fill_rows(const Fill& f, int64_t group, int64_t 
   if (rows <= 0) return;
   if (f.pitch == f.row_bytes && f.row_bytes * rows >= 16) {  // one stretch of memory
     char* p = f.p + f.first * f.pitch;
-    const int64_t bytes = rows * f.row_bytes, chunks = (bytes + 15) / 16;
-    for (int64_t c = group * kSortThreads + threadIdx.x; c < chunks; c += groups * kSortThreads) {
-      const int64_t at = c * 16 < bytes - 16 ? c * 16 : bytes - 16;
-      __builtin_memcpy(p + at, &zero, 16);
+    const int64_t bytes = rows * f.row_bytes, chunks = (bytes + 15) / 16, step = groups * kSortThreads;
+    int64_t c = group * kSortThreads + threadIdx.x;
+    for (; c + 7 * step < chunks - 1; c += 8 * step) {
+#pragma unroll
+      for (int u = 0; u < 8; ++u) __builtin_memcpy(p + (c + u * step) * 16, &zero, 16);
     }
+    for (; c < chunks; c += step) __builtin_memcpy(p + (c < chunks - 1 ? c * 16 : bytes - 16), &zero, 16);
     return;
   }
   for (int64_t r = f.first + group; r < f.end; r += groups) {
@@ -121,159 +125,192 @@ __device__ __forceinline__ uint32_t key_of(const SortArgs& a, int64_t i) {
   return id >= 0 && id < a.rows ? (uint32_t)id : (uint32_t)a.rows;
 }
 
+typedef __attribute__((address_space(3))) uint32_t lds_word;
+constexpr int kSortWaves = kSortThreads / 64;
+
 struct SortShared {
   uint32_t count[kSortWaves][kDigits];  // of each wavefront's keys by digit, then those of the wavefronts before
-  uint32_t base[kDigits];               // of all keys with smaller digits
+  uint32_t base[kDigits];               // where the workgroup's first key of the digit goes
+  uint32_t total[kDigits], before[kDigits];  // keys of the digit, and those before the workgroup's
   uint32_t wave_total[kSortWaves];
 };
 
-// Each key's rank among its wavefront's keys of the same digit, in order; count[wave][digit] in the end. Keys of
-// round r of wavefront w come after those of earlier rounds and wavefronts.
-__device__ __forceinline__ void rank_keys(SortShared& s, const uint32_t (&key)[kSortRounds], uint32_t (&rank)[kSortRounds],
-                                          int rounds, int shift, int bits) {
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const uint64_t below = ((uint64_t)1 << lane) - 1;
-  for (int d = threadIdx.x; d < kSortWaves * kDigits; d += kSortThreads) (&s.count[0][0])[d] = 0;
-  __syncthreads();
-  volatile uint32_t* count = s.count[wave];
+// The sum of x over the threads before this one; `totals`: a word of LDS for each wavefront.
+__device__ __forceinline__ uint32_t sum_before(uint32_t x, uint32_t* totals) {
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  uint32_t sum = x;
 #pragma unroll
-  for (int r = 0; r < kSortRounds; ++r) {
-    rank[r] = 0;
-    if (r < rounds) {
-      const uint32_t digit = (key[r] >> shift) & ((1u << bits) - 1);
-      uint64_t same = ~(uint64_t)0;
-#pragma unroll
-      for (int b = 0; b < kDigitBits; ++b) {  // bits beyond the digit's are zero in every key
-        const bool one = digit >> b & 1;
-        const uint64_t ones = __ballot(one);
-        same &= one ? ones : ~ones;
-      }
-      const uint32_t before = __popcll(same & below), first = count[digit];
-      rank[r] = first + before;
-      __builtin_amdgcn_wave_barrier();
-      if (before == 0) count[digit] = first + (uint32_t)__popcll(same);
-      __builtin_amdgcn_wave_barrier();
-    }
-  }
-  __syncthreads();
-}
-
-// count[wave][digit] becomes the sum over earlier wavefronts, base[digit] the sum over smaller digits of `total`
-// (of this workgroup's keys; with `counts`, of all workgroups') plus what earlier workgroups have of the digit.
-__device__ __forceinline__ void place_digits(SortShared& s, const uint32_t* counts, int groups) {
-  const int d = threadIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  uint32_t total = 0, earlier = 0;
-  if (d < kDigits) {
-    for (int w = 0; w < kSortWaves; ++w) {
-      const uint32_t c = s.count[w][d];
-      s.count[w][d] = total;
-      total += c;
-    }
-    if (counts) {
-      total = 0;
-#pragma unroll 8
-      for (int g = 0; g < groups; ++g) {
-        const uint32_t c = counts[g * kDigits + d];
-        if (g < (int)blockIdx.x) earlier += c;
-        total += c;
-      }
-    }
-  }
-  uint32_t sum = total;  // inclusive over the wavefront's digits
   for (int by = 1; by < 64; by *= 2) {
     const uint32_t v = __shfl_up(sum, by);
     if (lane >= by) sum += v;
   }
-  if (lane == 63) s.wave_total[wave] = sum;
+  if (lane == 63) totals[wave] = sum;
   __syncthreads();
-  uint32_t before = 0;
-  for (int w = 0; w < kDigits / 64; ++w)
-    if (w < wave) before += s.wave_total[w];
-  if (d < kDigits) s.base[d] = before + sum - total + earlier;
+  uint32_t before = sum - x;
+#pragma unroll
+  for (int w = 0; w < kSortWaves; ++w)
+    if (w < wave) before += totals[w];
+  return before;
+}
+
+// Each key's rank among its wavefront's keys of the same digit, in order; count[wave][digit] in the end. Keys of round
+// r of a wavefront come after those of earlier rounds and wavefronts. The lanes of a digit find each other bit by bit.
+template <int kRounds>
+__device__ __forceinline__ void rank_keys(SortShared& s, const uint32_t (&key)[kRounds], uint32_t (&rank)[kRounds], int shift, int bits) {
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const uint64_t below = ((uint64_t)1 << lane) - 1;
+  for (int d = threadIdx.x; d < kSortWaves * kDigits; d += kSortThreads) (&s.count[0][0])[d] = 0;
+  __syncthreads();
+  // LDS by its own instructions (a generic pointer would wait for memory as well); in order within a wavefront
+  volatile lds_word* count = (volatile lds_word*)s.count[wave];
+#pragma unroll
+  for (int r = 0; r < kRounds; ++r) {
+    const uint32_t digit = (key[r] >> shift) & ((1u << bits) - 1);
+    uint64_t same = ~(uint64_t)0;
+#pragma unroll
+    for (int b = 0; b < kDigitBits; ++b) {  // bits beyond the digit's are zero in every key
+      const bool one = digit >> b & 1;
+      const uint64_t ones = __ballot(one);
+      same &= one ? ones : ~ones;
+    }
+    const uint32_t before = __popcll(same & below), first = count[digit];
+    rank[r] = first + before;
+    __builtin_amdgcn_wave_barrier();
+    if (before == 0) count[digit] = first + (uint32_t)__popcll(same);
+    __builtin_amdgcn_wave_barrier();
+  }
   __syncthreads();
 }
 
-// All passes in one workgroup: up to kSortItems keys. Padding keys are all ones and come last.
+// base from total and before (or, where the workgroup has all keys, from its own counts), and the wavefronts' counts
+// made those of earlier wavefronts.
+__device__ __forceinline__ void place_digits(SortShared& s, bool alone) {
+  const int d = threadIdx.x;
+  uint32_t own = 0;
+  if (d < kDigits) {
+#pragma unroll
+    for (int w = 0; w < kSortWaves; ++w) {
+      const uint32_t c = s.count[w][d];
+      s.count[w][d] = own;
+      own += c;
+    }
+  }
+  const uint32_t total = d < kDigits ? (alone ? own : s.total[d]) : 0;
+  const uint32_t smaller = sum_before(total, s.wave_total);
+  if (d < kDigits) s.base[d] = smaller + (alone ? 0 : s.before[d]);
+  __syncthreads();
+}
+
+// All passes in one workgroup: up to 1024 keys. Padding keys are all ones and come last.
 __global__ __launch_bounds__(kSortThreads) void sort_all(SortArgs a) {
   __shared__ SortShared s;
-  __shared__ uint32_t keys[kSortItems];
-  __shared__ uint16_t from[kSortItems];
+  __shared__ uint32_t keys[kSortThreads], from[kSortThreads];
   if ((int)blockIdx.x >= a.groups) return fill_rows(a.fill, blockIdx.x - a.groups, gridDim.x - a.groups);
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, count = (int)a.count;
-  const int rounds = (count + kSortThreads - 1) / kSortThreads;
-  uint32_t key[kSortRounds], pos[kSortRounds], rank[kSortRounds];
-#pragma unroll
-  for (int r = 0; r < kSortRounds; ++r) {
-    const int i = (wave * rounds + r) * 64 + lane;
-    pos[r] = i;
-    key[r] = r < rounds && i < count ? key_of(a, i) : ~0u;
-  }
+  const int i = threadIdx.x, wave = threadIdx.x >> 6;
+  uint32_t key[1] = {i < a.count ? key_of(a, i) : ~0u}, pos = i, rank[1];
   for (int shift = 0; shift < a.end_bit; shift += a.bits) {
-    rank_keys(s, key, rank, rounds, shift, a.bits);
-    place_digits(s, nullptr, 1);
-#pragma unroll
-    for (int r = 0; r < kSortRounds; ++r) {
-      if (r < rounds) {
-        const uint32_t digit = (key[r] >> shift) & ((1u << a.bits) - 1);
-        const uint32_t to = s.base[digit] + s.count[wave][digit] + rank[r];
-        keys[to] = key[r];
-        from[to] = (uint16_t)pos[r];
-      }
-    }
+    rank_keys<1>(s, key, rank, shift, a.bits);
+    place_digits(s, true);
+    const uint32_t digit = (key[0] >> shift) & ((1u << a.bits) - 1);
+    const uint32_t to = s.base[digit] + s.count[wave][digit] + rank[0];
+    keys[to] = key[0];
+    from[to] = pos;
     __syncthreads();
-#pragma unroll
-    for (int r = 0; r < kSortRounds; ++r) {
-      if (r < rounds) {
-        const int i = (wave * rounds + r) * 64 + lane;
-        key[r] = keys[i];
-        pos[r] = from[i];
-      }
-    }
-    __syncthreads();
+    key[0] = keys[i];
+    pos = from[i];
   }
-#pragma unroll
-  for (int r = 0; r < kSortRounds; ++r) {
-    const int i = (wave * rounds + r) * 64 + lane;
-    if (r < rounds && i < count) {
-      a.keys_out[i] = key[r];
-      a.from_out[i] = pos[r];
-    }
+  if (i < a.count) {
+    a.keys_out[i] = key[0];
+    a.from_out[i] = pos;
   }
 }
+
+// Counters in eight copies, one for each of eight lanes: the high digits of frequent rows are alike, and additions to
+// one word of LDS wait for each other (16384 tokens, one copy: 21 us a pass).
+constexpr int kCopies = 8;
 
 __global__ __launch_bounds__(kSortThreads) void sort_count(SortArgs a) {
-  __shared__ uint32_t count[kDigits];
+  __shared__ uint32_t count[kCopies][kDigits];
   if ((int)blockIdx.x >= a.groups) return fill_rows(a.fill, blockIdx.x - a.groups, gridDim.x - a.groups);
-  if (threadIdx.x < kDigits) count[threadIdx.x] = 0;
+  for (int d = threadIdx.x; d < kCopies * kDigits; d += kSortThreads) (&count[0][0])[d] = 0;
   __syncthreads();
-  const int64_t first = (int64_t)blockIdx.x * kSortItems;
+  const int64_t first = (int64_t)blockIdx.x * kCountedTile;
 #pragma unroll
-  for (int r = 0; r < kSortRounds; ++r) {
+  for (int r = 0; r < kCountedTile / kSortThreads; ++r) {
     const int64_t i = first + r * kSortThreads + threadIdx.x;
-    if (i < a.count) atomicAdd(&count[(key_of(a, i) >> a.shift) & ((1u << a.bits) - 1)], 1u);  // whole numbers: any order
+    if (i < a.count)  // whole numbers: any order
+      atomicAdd(&count[threadIdx.x % kCopies][(key_of(a, i) >> a.shift) & ((1u << a.bits) - 1)], 1u);
   }
   __syncthreads();
-  if (threadIdx.x < kDigits) a.counts[(int64_t)blockIdx.x * kDigits + threadIdx.x] = count[threadIdx.x];
+  if (threadIdx.x >= kDigits) return;
+  uint32_t total = 0;
+  for (int c = 0; c < kCopies; ++c) total += count[c][threadIdx.x];
+  a.counts[(int64_t)blockIdx.x * kDigits + threadIdx.x] = total;
 }
 
-__global__ __launch_bounds__(kSortThreads) void sort_place(SortArgs a) {
+// One pass of a tile of 1024 kRounds keys: each goes behind all keys of smaller digits and behind those of its digit that
+// come before. kCounted: sort_count has counted the tiles' digits; else every workgroup counts all keys, which takes
+// less than a launch of its own up to kSortUncounted keys.
+template <int kRounds, bool kCounted>
+__global__ __launch_bounds__(kSortThreads) void sort_pass(SortArgs a) {
   __shared__ SortShared s;
   if ((int)blockIdx.x >= a.groups) return fill_rows(a.fill, blockIdx.x - a.groups, gridDim.x - a.groups);
-  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
-  const int64_t first = (int64_t)blockIdx.x * kSortItems;
-  uint32_t key[kSortRounds], rank[kSortRounds];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, d = threadIdx.x;
+  const int64_t first = (int64_t)blockIdx.x * (kRounds * kSortThreads);
+  const uint32_t mask = (1u << a.bits) - 1;
+  uint32_t key[kRounds], rank[kRounds];
 #pragma unroll
-  for (int r = 0; r < kSortRounds; ++r) {
-    const int64_t i = first + (wave * kSortRounds + r) * 64 + lane;
+  for (int r = 0; r < kRounds; ++r) {
+    const int64_t i = first + (wave * kRounds + r) * 64 + lane;
     key[r] = i < a.count ? key_of(a, i) : ~0u;
   }
-  rank_keys(s, key, rank, kSortRounds, a.shift, a.bits);
-  place_digits(s, a.counts, a.groups);
+  if (!kCounted) {  // of the keys before the tile, and of the others, in the wavefronts' counters
+    static_assert(kSortWaves == 2 * kCopies, "two sets of copies");
+    for (int c = d; c < kSortWaves * kDigits; c += kSortThreads) (&s.count[0][0])[c] = 0;
+    __syncthreads();
+    for (int64_t i0 = 0; i0 < a.count; i0 += 8 * kSortThreads) {
+      uint32_t digit[8];
 #pragma unroll
-  for (int r = 0; r < kSortRounds; ++r) {
-    const int64_t i = first + (wave * kSortRounds + r) * 64 + lane;
+      for (int u = 0; u < 8; ++u) {
+        const int64_t i = i0 + u * kSortThreads + threadIdx.x;
+        digit[u] = i < a.count ? (key_of(a, i) >> a.shift) & mask : ~0u;
+      }
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {  // whole numbers: any order
+        const int set = i0 + u * kSortThreads + threadIdx.x < first ? 0 : kCopies;
+        if (digit[u] != ~0u) atomicAdd(&s.count[set + d % kCopies][digit[u]], 1u);
+      }
+    }
+    __syncthreads();
+  }
+  if (d < kDigits) {
+    uint32_t total = 0, before = 0;
+    if (kCounted) {
+#pragma unroll 8
+      for (int g = 0; g < a.groups; ++g) {
+        const uint32_t c = a.counts[(int64_t)g * kDigits + d];
+        if (g < (int)blockIdx.x) before += c;
+        total += c;
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < kCopies; ++c) {
+        before += s.count[c][d];
+        total += s.count[kCopies + c][d];
+      }
+      total += before;
+    }
+    s.total[d] = total;
+    s.before[d] = before;
+  }
+  __syncthreads();
+  rank_keys<kRounds>(s, key, rank, a.shift, a.bits);
+  place_digits(s, false);
+#pragma unroll
+  for (int r = 0; r < kRounds; ++r) {
+    const int64_t i = first + (wave * kRounds + r) * 64 + lane;
     if (i >= a.count) continue;
-    const uint32_t digit = (key[r] >> a.shift) & ((1u << a.bits) - 1);
+    const uint32_t digit = (key[r] >> a.shift) & mask;
     const uint32_t to = s.base[digit] + s.count[wave][digit] + rank[r];
     a.keys_out[to] = key[r];
     a.from_out[to] = a.from ? a.from[i] : (uint32_t)i;
@@ -284,23 +321,31 @@ __global__ __launch_bounds__(kSortThreads) void sort_place(SortArgs a) {
 // the gradient: sums
 // ---------------------------------------------------------------------------
 
-// A lane's V columns of the row `key`: the sum rounded, on top of what is there where the caller accumulates.
-// The first `skip` belong to the neighbour before (V: all of them).
-template <typename T, int V>
-__device__ __forceinline__ void write_row(const EmbeddingGradientArgs& a, uint32_t key, int64_t at, int skip, const float (&sum)[V]) {
+// A lane's V columns of a row, from p on: the sum rounded, on top of `old` where the caller accumulates. The first
+// `skip` belong to the neighbour before (V: all of them).
+template <bool kAccumulate, typename T, int V>
+__device__ __forceinline__ void write_row(T* p, int skip, float scale, const float (&sum)[V], const T (&old)[V]) {
   if (skip == V) return;
-  T* p = static_cast<T*>(a.dtable) + (int64_t)key * a.lddt + at;
   T o[V];
-  if (skip == 0) {
-    if (a.accumulate) __builtin_memcpy(o, p, 16);
 #pragma unroll
-    for (int e = 0; e < V; ++e) o[e] = (T)(a.accumulate ? fmaf(sum[e], a.scale, (float)o[e]) : sum[e] * a.scale);
+  for (int e = 0; e < V; ++e) o[e] = (T)(kAccumulate ? fmaf(sum[e], scale, (float)old[e]) : sum[e] * scale);
+  if (skip == 0) {
     __builtin_memcpy(p, o, 16);
   } else {
 #pragma unroll
     for (int e = 0; e < V; ++e)
-      if (e >= skip) p[e] = (T)(a.accumulate ? fmaf(sum[e], a.scale, (float)p[e]) : sum[e] * a.scale);
+      if (e >= skip) p[e] = o[e];
   }
+}
+
+// The same of a row shorter than a chunk, by lane 0.
+template <typename T, int V>
+__device__ __forceinline__ void write_narrow(const EmbeddingGradientArgs& a, uint32_t row, const float (&sum)[V]) {
+  T* p = static_cast<T*>(a.dtable) + (int64_t)row * a.lddt;
+  if ((threadIdx.x & 63) != 0) return;
+#pragma unroll
+  for (int e = 0; e < V; ++e)
+    if (e < (int)a.k) p[e] = (T)(a.accumulate ? fmaf(sum[e], a.scale, (float)p[e]) : sum[e] * a.scale);
 }
 
 // Where a lane's V columns of slab `slab` begin and how many of them it shares; false where there are none.
@@ -324,20 +369,21 @@ __device__ __forceinline__ void load_row(const T* p, int64_t k, T (&x)[V]) {
 
 constexpr int kSumBatch = 8;  // rows under way
 
-// kNarrow: rows shorter than a chunk, which lane 0 has alone.
-template <typename T, bool kNarrow>
+// kNarrow: rows shorter than a chunk, which lane 0 has alone. kAccumulate: what the table holds is loaded along with
+// the tokens; loaded where a row ends, each of a piece's rows would wait for it (1777 tokens x 1111: 51 us).
+template <typename T, bool kNarrow, bool kAccumulate>
 __global__ __launch_bounds__(256) void embedding_sums(EmbeddingGradientArgs a, int64_t pieces, int64_t slabs) {
   constexpr int V = kChunkOf<T>;
   const int64_t task = (int64_t)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (task >= pieces * slabs) return;
-  const int64_t piece = task / slabs, slab = task % slabs, s0 = piece * kPieceTokens;
+  const int64_t piece = task / slabs, slab = task % slabs, s0 = piece * a.piece;
   const int lane = threadIdx.x & 63;
   const uint32_t none = (uint32_t)a.rows;
-  // lanes 0 .. 31: the piece; lane 32: the token after; lane 63: the one before
-  const int64_t i = lane == 63 ? s0 - 1 : s0 + (lane <= kPieceTokens ? lane : kPieceTokens);
+  // the first lanes: the piece; the next one: the token after; lane 63: the one before
+  const int64_t i = lane == 63 ? s0 - 1 : s0 + (lane <= a.piece ? lane : a.piece);
   const uint32_t key = i >= 0 && i < a.count ? a.keys[0][i] : none;
   const uint32_t from = i >= 0 && i < a.count ? a.from[0][i] : 0;
-  const int tokens = __popcll(__ballot(lane < kPieceTokens && key < none));  // those without a row come last
+  const int tokens = __popcll(__ballot(lane < a.piece && key < none));  // those without a row come last
   if (tokens == 0) return;
   int64_t at;
   int skip;
@@ -346,12 +392,14 @@ __global__ __launch_bounds__(256) void embedding_sums(EmbeddingGradientArgs a, i
   const T* G = static_cast<const T*>(a.g) + at;
   float sum[V] = {};
   bool crosses = __builtin_amdgcn_readlane(key, 63) == __builtin_amdgcn_readlane(key, 0);  // the first row began earlier
-  const bool on = tokens == kPieceTokens;
+  const bool on = tokens == a.piece;
   for (int j0 = 0; j0 < tokens; j0 += kSumBatch) {
-    T x[kSumBatch][V];
+    T x[kSumBatch][V], old[kSumBatch][V];
 #pragma unroll
     for (int b = 0; b < kSumBatch; ++b) {
       const int j = j0 + b < tokens ? j0 + b : tokens - 1;
+      if (kAccumulate && !kNarrow)
+        __builtin_memcpy(old[b], static_cast<const T*>(a.dtable) + (int64_t)(uint32_t)__builtin_amdgcn_readlane(key, j) * a.lddt + at, 16);
       load_row<T, V, kNarrow>(G + (int64_t)(uint32_t)__builtin_amdgcn_readlane(from, j) * a.ldg, a.k, x[b]);
     }
 #pragma unroll
@@ -369,11 +417,9 @@ __global__ __launch_bounds__(256) void embedding_sums(EmbeddingGradientArgs a, i
 #pragma unroll
         for (int e = 0; e < V; e += 4) *reinterpret_cast<f32x4*>(p + e) = {sum[e], sum[e + 1], sum[e + 2], sum[e + 3]};
       } else if (kNarrow) {
-        T* p = static_cast<T*>(a.dtable) + (int64_t)row * a.lddt;
-        if (lane == 0)
-          for (int e = 0; e < (int)a.k; ++e) p[e] = (T)(a.accumulate ? fmaf(sum[e], a.scale, (float)p[e]) : sum[e] * a.scale);
+        write_narrow<T, V>(a, row, sum);
       } else {
-        write_row<T, V>(a, row, at, skip, sum);
+        write_row<kAccumulate, T, V>(static_cast<T*>(a.dtable) + (int64_t)row * a.lddt + at, skip, a.scale, sum, old[b]);
       }
       crosses = false;
 #pragma unroll
@@ -388,14 +434,14 @@ template <typename T, bool kNarrow>
 __global__ __launch_bounds__(256) void embedding_join(EmbeddingGradientArgs a, int64_t pieces, int64_t slabs) {
   constexpr int V = kChunkOf<T>;
   __shared__ float join[4][64][V + 1];
-  const int64_t piece = blockIdx.x / slabs, slab = blockIdx.x % slabs, end = (piece + 1) * kPieceTokens;
+  const int64_t piece = blockIdx.x / slabs, slab = blockIdx.x % slabs, end = (piece + 1) * a.piece;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t none = (uint32_t)a.rows;
   const uint32_t* keys = a.keys[0];
   if (end >= a.count) return;
   const uint32_t key = keys[end - 1];
   if (key >= none || keys[end] != key) return;  // no row goes on
-  const int64_t start = piece * kPieceTokens;
+  const int64_t start = piece * a.piece;
   if (start > 0 && keys[start] == key && keys[start - 1] == key) return;  // it began earlier
   const float* partial = a.partial + slab * (64 * V) + lane * V;
   const int64_t slot = slabs * (64 * V);
@@ -410,7 +456,7 @@ __global__ __launch_bounds__(256) void embedding_join(EmbeddingGradientArgs a, i
   };
   if (wave == 0) add(piece * 2 + 1);
   for (int64_t q0 = piece + 1;; q0 += 64) {  // 64 pieces at a time: lane l looks whether the row goes on behind piece q0 + l
-    const int64_t next = (q0 + lane + 1) * kPieceTokens;
+    const int64_t next = (q0 + lane + 1) * a.piece;
     const uint64_t stops = __ballot(next >= a.count || keys[next < a.count ? next : 0] != key);
     const int more = stops ? __builtin_ctzll(stops) + 1 : 64;
 #pragma unroll 8
@@ -425,16 +471,18 @@ __global__ __launch_bounds__(256) void embedding_join(EmbeddingGradientArgs a, i
   for (int w = 1; w < 4; ++w)
 #pragma unroll
     for (int e = 0; e < V; ++e) sum[e] += join[w][lane][e];
-  if (kNarrow) {
-    T* p = static_cast<T*>(a.dtable) + (int64_t)key * a.lddt;
-    if (lane == 0)
-      for (int e = 0; e < (int)a.k; ++e) p[e] = (T)(a.accumulate ? fmaf(sum[e], a.scale, (float)p[e]) : sum[e] * a.scale);
-    return;
-  }
+  if (kNarrow) return write_narrow<T, V>(a, key, sum);
   int64_t at;
   int skip;
   lane_columns<V, kNarrow>(a.k, slab, &at, &skip);
-  write_row<T, V>(a, key, at, skip, sum);
+  T* p = static_cast<T*>(a.dtable) + (int64_t)key * a.lddt + at;
+  T old[V] = {};
+  if (a.accumulate) {
+    __builtin_memcpy(old, p, 16);
+    write_row<true, T, V>(p, skip, a.scale, sum, old);
+  } else {
+    write_row<false, T, V>(p, skip, a.scale, sum, old);
+  }
 }
 
 template <typename T>
@@ -447,22 +495,23 @@ void embedding_for(const EmbeddingArgs& a, hipStream_t s) {
   };
   if (a.k < V) embedding_rows<T, 4, true><<<grid(4), 256, 0, s>>>(a);
   else if (chunks <= 16) embedding_rows<T, 16, false><<<grid(16), 256, 0, s>>>(a);
-  else if (chunks <= 256) embedding_rows<T, 64, false><<<grid(64), 256, 0, s>>>(a);
+  else if (chunks <= 64 || a.count >= 1024) embedding_rows<T, 64, false><<<grid(64), 256, 0, s>>>(a);
   else embedding_rows<T, 256, false><<<grid(256), 256, 0, s>>>(a);
 }
 
 template <typename T>
 void sums_for(const EmbeddingGradientArgs& a, hipStream_t s) {
   constexpr int V = kChunkOf<T>;
-  const int64_t pieces = piece_count(a.count), slabs = (a.k + 64 * V - 1) / (64 * V);
+  const int64_t pieces = piece_count(a.count, a.piece), slabs = (a.k + 64 * V - 1) / (64 * V);
   const unsigned groups = (unsigned)((pieces * slabs + 3) / 4);
-  if (a.k < V) {
-    embedding_sums<T, true><<<groups, 256, 0, s>>>(a, pieces, slabs);
-    if (pieces > 1) embedding_join<T, true><<<(unsigned)(pieces * slabs), 256, 0, s>>>(a, pieces, slabs);
-  } else {
-    embedding_sums<T, false><<<groups, 256, 0, s>>>(a, pieces, slabs);
-    if (pieces > 1) embedding_join<T, false><<<(unsigned)(pieces * slabs), 256, 0, s>>>(a, pieces, slabs);
-  }
+  const auto run = [&](auto narrow) {
+    constexpr bool kNarrow = decltype(narrow)::value;
+    if (a.accumulate) embedding_sums<T, kNarrow, true><<<groups, 256, 0, s>>>(a, pieces, slabs);
+    else embedding_sums<T, kNarrow, false><<<groups, 256, 0, s>>>(a, pieces, slabs);
+    if (pieces > 1) embedding_join<T, kNarrow><<<(unsigned)(pieces * slabs), 256, 0, s>>>(a, pieces, slabs);
+  };
+  if (a.k < V) run(std::true_type());
+  else run(std::false_type());
 }
 
 }  // namespace
@@ -488,24 +537,26 @@ hipError_t launch_embedding_gradient(const EmbeddingGradientArgs& args, int type
   while (bits < 32 && (uint64_t)a.rows >> bits) ++bits;
   const int passes = (bits + kDigitBits - 1) / kDigitBits;
   q.bits = (bits + passes - 1) / passes;
-  const int steps = q.groups <= 1 ? 1 : 2 * passes;
+  q.end_bit = bits;
+  const bool alone = q.groups <= 1, counted = a.count > kSortUncounted;
+  const int launches = alone ? 1 : counted ? 2 * passes : passes;
   const int fillers = a.accumulate ? 0 : 512;
-  for (int step = 0; step < steps; ++step) {
-    q.fill.first = a.accumulate ? 0 : a.rows * step / steps;
-    q.fill.end = a.accumulate ? 0 : a.rows * (step + 1) / steps;
+  for (int l = 0; l < launches; ++l) {
+    q.fill.first = a.accumulate ? 0 : a.rows * l / launches;
+    q.fill.end = a.accumulate ? 0 : a.rows * (l + 1) / launches;
     const unsigned grid = (unsigned)(q.groups + fillers);
     if (grid == 0) return hipSuccess;
-    const int pass = step / 2, to = pass & 1;
+    const int pass = counted ? l / 2 : l, to = pass & 1;
     q.ids = pass == 0 ? a.ids : nullptr;
     q.keys = pass == 0 ? nullptr : a.keys[to ^ 1];
     q.from = pass == 0 ? nullptr : a.from[to ^ 1];
     q.keys_out = a.keys[to];
     q.from_out = a.from[to];
     q.shift = pass * q.bits;
-    q.end_bit = bits;
-    if (q.groups <= 1) sort_all<<<grid, kSortThreads, 0, s>>>(q);
-    else if (step % 2 == 0) sort_count<<<grid, kSortThreads, 0, s>>>(q);
-    else sort_place<<<grid, kSortThreads, 0, s>>>(q);
+    if (alone) sort_all<<<grid, kSortThreads, 0, s>>>(q);
+    else if (!counted) sort_pass<1, false><<<grid, kSortThreads, 0, s>>>(q);
+    else if (l % 2 == 0) sort_count<<<grid, kSortThreads, 0, s>>>(q);
+    else sort_pass<kCountedTile / kSortThreads, true><<<grid, kSortThreads, 0, s>>>(q);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }

@@ -23,15 +23,26 @@ __device__ __forceinline__ int64_t class_at(const ClassList& l, int64_t i, int e
 }
 
 // For every class that a strip's rows list within its columns: fn(row of the strip, its place in the list, place of its
-// value in the staging area). Lanes take the lists' entries in turn.
+// value in the staging area). Lanes take the lists' entries in turn, eight at a time: one at a time, every entry would
+// wait for memory (32 a row over 256 x 256 tiles: 30 us a tile).
 template <int WN, typename Fn>
 __device__ __forceinline__ void for_listed(const ClassList& list, int64_t i0, int rows, int64_t first_class, int columns, Fn fn) {
-  const int lane = threadIdx.x & 63;
-  const uint32_t total = (uint32_t)rows * (uint32_t)list.per_row;
-  for (uint32_t at = lane; at < total; at += 64) {
-    const uint32_t row = list.per_row == 1 ? at : at / (uint32_t)list.per_row, e = at - row * (uint32_t)list.per_row;
-    const int64_t c = class_at(list, i0 + row, (int)e) - first_class;
-    if (c >= 0 && c < columns) fn((int)row, (int)e, staged_at<WN>((int)row, (int)c >> 2) + ((int)c & 3));
+  constexpr int kBatch = 8;
+  const uint32_t per_row = (uint32_t)list.per_row, total = (uint32_t)rows * per_row;
+  for (uint32_t at0 = threadIdx.x & 63; at0 < total; at0 += 64 * kBatch) {
+    int64_t c[kBatch];
+    uint32_t row[kBatch], e[kBatch];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const uint32_t at = at0 + b * 64 < total ? at0 + b * 64 : at0;
+      row[b] = per_row == 1 ? at : at / per_row;
+      e[b] = at - row[b] * per_row;
+      c[b] = class_at(list, i0 + row[b], (int)e[b]) - first_class;
+    }
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b)
+      if (at0 + b * 64 < total && c[b] >= 0 && c[b] < columns)
+        fn((int)row[b], (int)e[b], staged_at<WN>((int)row[b], (int)c[b] >> 2) + ((int)c[b] & 3));
   }
 }
 

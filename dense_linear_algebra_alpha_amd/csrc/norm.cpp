@@ -37,7 +37,9 @@ xtvxy_status norm_impl(int type, int64_t m, int64_t n, const void* X, int64_t ld
 xtvxy_status gradient_workspace(int64_t m, int64_t n, size_t* bytes) {
   if (!bytes) return XTVXY_ERROR_NULL_POINTER;
   if (m < 0 || n < 0 || bytes_overflow(m, n) || n > INT64_MAX / 4096) return XTVXY_ERROR_INVALID_VALUE;
-  *bytes = m == 0 || n == 0 ? 0 : align_up((size_t)norm_gradient_groups(m, n) * 2 * n * 4);
+  // of either element size
+  const int64_t groups = m == 0 || n == 0 ? 0 : std::max(norm_gradient_groups(m, n, kF32), norm_gradient_groups(m, n, kBf16));
+  *bytes = align_up((size_t)groups * 2 * n * 4);
   return XTVXY_SUCCESS;
 }
 
@@ -63,7 +65,7 @@ xtvxy_status gradient_impl(int type, int64_t m, int64_t n, const void* G, int64_
     if (dweight && launch_zero(dweight, (size_t)n * 4, stream) != hipSuccess) return XTVXY_ERROR_LAUNCH;
     return status_of(dbias ? launch_zero(dbias, (size_t)n * 4, stream) : hipSuccess);
   }
-  const int64_t groups = norm_gradient_groups(m, n);
+  const int64_t groups = norm_gradient_groups(m, n, type);
   const size_t need = sums ? align_up((size_t)groups * 2 * n * 4) : 0;
   if (need > 0 && (!ws || ws_bytes < need || reinterpret_cast<uintptr_t>(ws) % kAlign != 0)) return XTVXY_ERROR_WORKSPACE;
   return status_of(launch_norm_gradient({G, X, mean, rstd, weight, dX, ldg, ldx, lddx, m, n,

@@ -34,7 +34,7 @@ struct NormGradientArgs {
   float* dbias;
 };
 // Workgroups of the gradient, each of which has column sums of its own.
-int64_t norm_gradient_groups(int64_t m, int64_t n);
+int64_t norm_gradient_groups(int64_t m, int64_t n, int type);
 constexpr int64_t kNormGradientMost = 16384;  // columns up to which a row stays in registers
 hipError_t launch_norm_gradient(const NormGradientArgs& a, int type, hipStream_t s);
 

@@ -77,7 +77,7 @@ __device__ __forceinline__ float row_sum(const float* lds, int first) {
 //     mean = sum n_w mean_w / n,  sum = sum_w (sum_w + n_w (mean_w - mean)^2).
 template <typename T, int L, int C>
 __global__ __launch_bounds__(L < 256 ? 256 : L) void norm_rows(NormArgs a) {
-  constexpr int V = kChunkOf<T>, kBlock = L < 256 ? 256 : L, kRows = kBlock / L, kWaves = L / 64;
+  constexpr int V = kChunkOf<T>, kBlock = L < 256 ? 256 : L, kRows = kBlock / L, kWaves = L / 64, kGroup = L < 64 ? L : 64;
   __shared__ float part[2][2][kBlock / 64];
   const int t = threadIdx.x % L, sub = threadIdx.x / L, lane = threadIdx.x & 63;
   const Columns<T, L, C> k(a.n, t);
@@ -88,8 +88,8 @@ __global__ __launch_bounds__(L < 256 ? 256 : L) void norm_rows(NormArgs a) {
   int own = 0;  // elements of the row that this thread counts
 #pragma unroll
   for (int c = 0; c < C; ++c) own += V - k.skip[c];
-  const float mine = group_sum((float)own, 64);
-  float counts[kWaves];  // of each wavefront of the row
+  const float mine = group_sum((float)own, kGroup);
+  float counts[kWaves > 0 ? kWaves : 1];  // of each wavefront of the row
   if constexpr (kWaves > 1) {
     if (lane == 0) part[0][0][threadIdx.x / 64] = mine;
     __syncthreads();
@@ -116,7 +116,7 @@ __global__ __launch_bounds__(L < 256 ? 256 : L) void norm_rows(NormArgs a) {
 #pragma unroll
       for (int e = 0; e < V; ++e) s += e >= k.skip[c] ? x[c][e] : 0.0f;
     // divided: the mean of a constant row is that constant
-    float mean = mine > 0.0f ? group_sum(s, 64) / mine : 0.0f, q = 0.0f;
+    float mean = mine > 0.0f ? group_sum(s, kGroup) / mine : 0.0f, q = 0.0f;
 #pragma unroll
     for (int c = 0; c < C; ++c)
 #pragma unroll
@@ -124,7 +124,7 @@ __global__ __launch_bounds__(L < 256 ? 256 : L) void norm_rows(NormArgs a) {
         const float d = x[c][e] - mean;
         q += e >= k.skip[c] ? d * d : 0.0f;
       }
-    q = group_sum(q, 64);
+    q = group_sum(q, kGroup);
     if constexpr (kWaves > 1) {
       if (lane == 0) {
         part[turn][0][threadIdx.x / 64] = mean;
@@ -206,13 +206,12 @@ constexpr int kGradientThreads = 1024;
 // A workgroup takes 1024 / L rows at a time. Its rows' column sums join in LDS at the end.
 template <typename T, int L, int C>
 __global__ __launch_bounds__(kGradientThreads) void norm_gradient_rows(NormGradientArgs a) {
-  constexpr int V = kChunkOf<T>, kRows = kGradientThreads / L, kWaves = L / 64;
+  constexpr int V = kChunkOf<T>, kRows = kGradientThreads / L, kWaves = L / 64, kGroup = L < 64 ? L : 64;
   __shared__ float part[2][2][kGradientThreads / 64];
   __shared__ __align__(16) float join[kRows][L * V];
   const int t = threadIdx.x % L, sub = threadIdx.x / L, lane = threadIdx.x & 63;
   const Columns<T, L, C> k(a.n, t);
-  float w[C][V], dw[C][V] = {}, db[C][V] = {};
-  load_vector<V>(a.weight, k, 1.0f, w);
+  float dw[C][V] = {}, db[C][V] = {};
   const float inv_n = 1.0f / (float)a.n;
   const T* X = static_cast<const T*>(a.x);
   const T* G = static_cast<const T*>(a.g);
@@ -233,6 +232,8 @@ __global__ __launch_bounds__(kGradientThreads) void norm_gradient_rows(NormGradi
     float xhat[C][V], h[C][V], s = 0.0f, q = 0.0f;
     const float r = rstd;
     const bool there = i < a.m;
+    float w[C][V];  // from L1 or L2 for each row: kept, they would not leave registers for the next row's loads
+    load_vector<V>(a.weight, k, 1.0f, w);
 #pragma unroll
     for (int c = 0; c < C; ++c)
 #pragma unroll
@@ -242,14 +243,14 @@ __global__ __launch_bounds__(kGradientThreads) void norm_gradient_rows(NormGradi
         h[c][e] = ge * w[c][e];
         s += e >= k.skip[c] ? h[c][e] : 0.0f;
         q += e >= k.skip[c] ? h[c][e] * xhat[c][e] : 0.0f;
-        if (there) {  // the same for a wavefront
+        if (there) {
           dw[c][e] = fmaf(ge, xhat[c][e], dw[c][e]);
           db[c][e] += ge;
         }
       }
     if (i0 + step < a.m) load(i + step);
-    s = group_sum(s, 64);
-    q = group_sum(q, 64);
+    s = group_sum(s, kGroup);
+    q = group_sum(q, kGroup);
     if constexpr (kWaves > 1) {
       if (lane == 0) {
         part[turn][0][threadIdx.x / 64] = s;
@@ -364,7 +365,7 @@ template <typename T, int L>
 void norm_for(const NormArgs& a, hipStream_t s) {
   constexpr int kBlock = L < 256 ? 256 : L, kRows = kBlock / L;
   const int64_t chunks = (a.n + kChunkOf<T> - 1) / kChunkOf<T>;
-  const int64_t most = 8192 * 64 / kBlock / (kBlock / 64);
+  const int64_t most = 256 * (kBlock == 256 ? 8 : 2);  // workgroups that the CUs hold
   const int64_t rows = (a.m + kRows - 1) / kRows;
   const unsigned grid = (unsigned)(rows < most ? rows : most);
   if (chunks <= L) norm_rows<T, L, 1><<<grid, kBlock, 0, s>>>(a);
@@ -379,6 +380,8 @@ void norm_type(const NormArgs& a, hipStream_t s) {
     const unsigned grid = (unsigned)(a.m < 4096 ? a.m : 4096);
     if (a.n < V) norm_any<T, 64><<<grid, 64, 0, s>>>(a);
     else norm_any<T, 1024><<<grid, 1024, 0, s>>>(a);
+  } else if (a.n <= 16 * 4 * V) {
+    norm_for<T, 16>(a, s);
   } else if (a.n <= 64 * 4 * V) {
     norm_for<T, 64>(a, s);
   } else if (a.n <= 256 * 4 * V) {
@@ -394,9 +397,12 @@ void norm_gradient_for(const NormGradientArgs& a, hipStream_t s) {
   const int64_t chunks = (a.n + V - 1) / V;
   const unsigned grid = (unsigned)a.groups;
   if (chunks <= L) norm_gradient_rows<T, L, 1><<<grid, kGradientThreads, 0, s>>>(a);
-  else if (V == 8 || chunks <= 2 * L) norm_gradient_rows<T, L, 2><<<grid, kGradientThreads, 0, s>>>(a);
-  else if constexpr (V == 4) norm_gradient_rows<T, L, 4><<<grid, kGradientThreads, 0, s>>>(a);
+  else if (L < 1024 || chunks <= 2 * L) norm_gradient_rows<T, L, 2><<<grid, kGradientThreads, 0, s>>>(a);
+  else if constexpr (L == 1024 && V == 4) norm_gradient_rows<T, L, 4><<<grid, kGradientThreads, 0, s>>>(a);
 }
+
+// Threads of a row, with up to two chunks each (fp32 rows of more than 8192: four).
+int norm_gradient_lanes(int64_t n, int chunk) { return n <= 32 * chunk ? 16 : n <= 128 * chunk ? 64 : n <= 512 * chunk ? 256 : 1024; }
 
 template <typename T>
 void norm_gradient_type(const NormGradientArgs& a, hipStream_t s) {
@@ -406,21 +412,23 @@ void norm_gradient_type(const NormGradientArgs& a, hipStream_t s) {
     if (a.dx && a.n < V) norm_gradient_any<T, 64><<<grid, 64, 0, s>>>(a);
     else if (a.dx) norm_gradient_any<T, 1024><<<grid, 1024, 0, s>>>(a);
     if (a.sums) norm_columns_any<T><<<dim3((unsigned)((a.n + 255) / 256), (unsigned)a.groups), 256, 0, s>>>(a);
-  } else if (a.n <= 64 * 16) {
-    norm_gradient_for<T, 64>(a, s);
-  } else if (a.n <= 256 * 16) {
-    norm_gradient_for<T, 256>(a, s);
   } else {
-    norm_gradient_for<T, 1024>(a, s);
+    switch (norm_gradient_lanes(a.n, V)) {
+      case 16: norm_gradient_for<T, 16>(a, s); break;
+      case 64: norm_gradient_for<T, 64>(a, s); break;
+      case 256: norm_gradient_for<T, 256>(a, s); break;
+      default: norm_gradient_for<T, 1024>(a, s); break;
+    }
   }
   if (a.sums) norm_gradient_finish<<<(unsigned)((2 * a.n + 15) / 16), 256, 0, s>>>(a);
 }
 
 }  // namespace
 
-int64_t norm_gradient_groups(int64_t m, int64_t n) {
+int64_t norm_gradient_groups(int64_t m, int64_t n, int type) {
   // rows that a workgroup takes at once; the kernels for any length take one
-  const int64_t rows = n > kNormGradientMost || n < 8 ? 1 : n <= 64 * 16 ? 16 : n <= 256 * 16 ? 4 : 1;
+  const int chunk = 16 / elem_size(type);
+  const int64_t rows = n > kNormGradientMost || n < chunk ? 1 : kGradientThreads / norm_gradient_lanes(n, chunk);
   const int64_t groups = (m + rows - 1) / rows;
   return groups < kMostGroups ? groups : kMostGroups;
 }
