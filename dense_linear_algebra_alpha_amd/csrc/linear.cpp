@@ -127,13 +127,13 @@ double product_jobs(const ProductPlan& p, int type, int tile, int64_t m, int64_t
 
 }  // namespace
 
-ProductPlan xtvxy::plan_product(int type, int64_t m, int64_t n, int64_t k, bool ring, bool split) {
+ProductPlan xtvxy::plan_product(int type, int64_t m, int64_t n, int64_t k, bool ring, bool split, int only_tile) {
   ProductPlan best;
   best.k_per_split = kTileDepth;
   if (m == 0 || n == 0) return best;
   double least = 0;
   for (int tile : {64, 128, 256}) {
-    if (!ring ? tile != 64 : (tile == 256 && type == kF32)) continue;
+    if (only_tile ? tile != only_tile : !ring ? tile != 64 : (tile == 256 && type == kF32)) continue;
     const int64_t tiles = cdiv(m, tile) * cdiv(n, tile), slots = kComputeUnits * residents(tile);
     // what a last, incomplete round of the CUs would hold may be split instead of everything
     const int64_t whole[] = {0, tiles / kComputeUnits * kComputeUnits, tiles / slots * slots};

@@ -65,10 +65,11 @@ inline bool whole_chunks(const Matrix& x) {
 
 inline size_t packed_bytes(int64_t rows, int64_t cols, int es) { return align_up((size_t)rows * padded(cols, es) * es); }
 
-// The layer's tile, split tiles and parts with the least estimated time; without `split` no tile is split.
-ProductPlan plan_product(int type, int64_t m, int64_t n, int64_t k, bool ring, bool split = true);
+// The layer's tile, split tiles and parts with the least estimated time; without `split` no tile is split. only_tile:
+// that tile, if not 0.
+ProductPlan plan_product(int type, int64_t m, int64_t n, int64_t k, bool ring, bool split = true, int only_tile = 0);
 // The same for the gradient's products dX (m x k, contraction n) and dW (n x k, contraction m), which share a tile
-// and a launch. only_tile: that tile, if not 0; dx_in_parts: dX's tiles are split alike (whole 0).
+// and a launch. dx_in_parts: dX's tiles are split alike (whole 0).
 void plan_gradient(int type, int64_t m, int64_t k, int64_t n, bool want_dx, bool want_dw, bool ring, ProductPlan* dx,
                    ProductPlan* dw, int only_tile = 0, bool dx_in_parts = false);
 

@@ -40,12 +40,40 @@ bool shape_fits(int64_t m, int64_t k, int64_t n, int es) {
          backward_fits(m, k, std::min(n, most));
 }
 
+// Workspace of the lists' order for tiles of this edge; nothing where the lists are searched.
+struct OrderPlan {
+  ListOrder order{};
+  size_t starts = 0, bytes = 0;
+};
+OrderPlan plan_order(int64_t m, int64_t n, int64_t per_row, int tile) {
+  OrderPlan p;
+  p.order.half = tile / 2;
+  p.order.columns = cdiv(n, p.order.half);
+  p.order.strip_rows = strip_rows_of(tile);
+  if (per_row < kOrderedFrom || p.order.columns > kMostHalves) return p;
+  const int64_t strips = cdiv(m, p.order.strip_rows);
+  p.starts = align_up((size_t)strips * (p.order.columns + 1) * 4);
+  p.bytes = p.starts + align_up((size_t)strips * p.order.strip_rows * per_row * 4);
+  return p;
+}
+
+// The order made, or none.
+hipError_t order_lists(const OrderPlan& p, const ClassList& list, const float* weights, int64_t m, int64_t n, char* ws,
+                       ListOrder* order, hipStream_t s) {
+  *order = p.order;
+  if (p.bytes == 0) return hipSuccess;
+  order->starts = reinterpret_cast<uint32_t*>(ws);
+  order->entries = reinterpret_cast<uint32_t*>(ws + p.starts);
+  return launch_list_order({list, *order, weights, m, n}, s);
+}
+
 struct ForwardPlan {
   bool pack_x, pack_w;
   int64_t piece;
   ProductPlan whole, last;  // of a piece, of the last one
   int64_t parts, most_parts;  // halves of tiles' columns of a piece
-  size_t x_off, w_off, stats_off, run_off, listed_off, bytes = 0;
+  OrderPlan order;
+  size_t x_off, w_off, stats_off, run_off, listed_off, order_off, bytes = 0;
 };
 
 ForwardPlan make_forward_plan(int type, int64_t m, int64_t k, int64_t n, int64_t per_row, bool x_whole, bool w_whole) {
@@ -58,7 +86,7 @@ ForwardPlan make_forward_plan(int type, int64_t m, int64_t k, int64_t n, int64_t
   p.piece = piece_of(n, per_class, most_classes(m, k, es));
   p.whole = plan_product(type, m, p.piece, k, true, false);
   const int64_t last = n - (cdiv(n, std::max<int64_t>(p.piece, 1)) - 1) * p.piece;
-  p.last = p.piece == n ? p.whole : plan_product(type, m, last, k, true, false);
+  p.last = p.piece == n ? p.whole : plan_product(type, m, last, k, true, false, p.whole.tile);
   p.parts = std::max(2 * cdiv(p.piece, p.whole.tile), 2 * cdiv(last, p.last.tile));
   const auto take = [&](bool want, size_t bytes) {
     const size_t at = p.bytes;
@@ -70,6 +98,8 @@ ForwardPlan make_forward_plan(int type, int64_t m, int64_t k, int64_t n, int64_t
   p.stats_off = take(true, (size_t)p.parts * m * 8);
   p.run_off = take(p.piece < n, (size_t)m * 8);
   p.listed_off = take(true, (size_t)m * per_row * 4);
+  p.order = plan_order(m, n, per_row, p.whole.tile);
+  p.order_off = take(true, p.order.bytes);
   return p;
 }
 
@@ -83,10 +113,11 @@ struct BackwardPlan {
   bool pack_x, pack_w, parts;
   int64_t piece, pieces, ldd;
   ProductPlan logits, last_logits, dx, dw, last_dx, last_dw;
-  size_t x_off, w_off, d_off, factor_off, scale_off, sums_off, dx_off, dw_off, bytes = 0;
+  OrderPlan order;
+  size_t x_off, w_off, d_off, factor_off, scale_off, sums_off, dx_off, dw_off, order_off, bytes = 0;
 };
 
-BackwardPlan make_backward_plan(int type, int64_t m, int64_t k, int64_t n, bool x_whole, bool w_whole, bool want_dx, bool want_dw) {
+BackwardPlan make_backward_plan(int type, int64_t m, int64_t k, int64_t n, int64_t per_row, bool x_whole, bool w_whole, bool want_dx, bool want_dw) {
   BackwardPlan p;
   const int es = elem_size(type);
   want_dx = want_dx && k > 0;
@@ -99,7 +130,7 @@ BackwardPlan make_backward_plan(int type, int64_t m, int64_t k, int64_t n, bool 
   p.ldd = cdiv(p.piece, 8) * 8;
   const int64_t last = n - (p.pieces - 1) * p.piece;
   p.logits = plan_product(type, m, p.piece, k, true, false);
-  p.last_logits = p.parts ? plan_product(type, m, last, k, true, false) : p.logits;
+  p.last_logits = p.parts ? plan_product(type, m, last, k, true, false, p.logits.tile) : p.logits;
   plan_gradient(type, m, k, p.piece, want_dx, want_dw, true, &p.dx, &p.dw, 0, p.parts);
   p.last_dx = p.dx;
   p.last_dw = p.dw;
@@ -124,13 +155,15 @@ BackwardPlan make_backward_plan(int type, int64_t m, int64_t k, int64_t n, bool 
   p.sums_off = take(true, (size_t)rows * p.piece * 4);
   p.dx_off = take(want_dx, dx_bytes);
   p.dw_off = take(want_dw, std::max(p.dw.bytes, p.last_dw.bytes));
+  p.order = plan_order(m, n, per_row, p.logits.tile);
+  p.order_off = take(true, p.order.bytes);
   return p;
 }
 
-const BackwardPlan& plan_backward(int type, int64_t m, int64_t k, int64_t n, bool x_whole, bool w_whole, bool want_dx, bool want_dw) {
+const BackwardPlan& plan_backward(int type, int64_t m, int64_t k, int64_t n, int64_t per_row, bool x_whole, bool w_whole, bool want_dx, bool want_dw) {
   thread_local PlanCache<BackwardPlan> cache;
-  return cache.get(m, k, n, (((type * 2 + x_whole) * 2 + w_whole) * 2 + want_dx) * 2 + want_dw,
-                   [&] { return make_backward_plan(type, m, k, n, x_whole, w_whole, want_dx, want_dw); });
+  return cache.get(m, k, n, ((((per_row * 4 + type) * 2 + x_whole) * 2 + w_whole) * 2 + want_dx) * 2 + want_dw,
+                   [&] { return make_backward_plan(type, m, k, n, per_row, x_whole, w_whole, want_dx, want_dw); });
 }
 
 xtvxy_status check_shape(int64_t m, int64_t k, int64_t n, int64_t per_row, int es) {
@@ -169,7 +202,7 @@ xtvxy_status backward_workspace(int type, int64_t m, int64_t k, int64_t n, int64
   *bytes = m == 0 || n == 0 ? 0 : most_bytes(k, elem_size(type), aligned16, [&](bool x, bool w) {
     size_t most = 0;  // a product alone may be split further than the two together
     for (int want = 0; want < 4; ++want)
-      most = std::max(most, plan_backward(type, m, k, n, x, w, want & 1, want & 2).bytes);
+      most = std::max(most, plan_backward(type, m, k, n, per_row, x, w, want & 1, want & 2).bytes);
     return most;
   });
   return XTVXY_SUCCESS;
@@ -278,6 +311,8 @@ xtvxy_status forward_impl(const Layer& l, const ClassList& list, const Teacher* 
                    reinterpret_cast<float*>(base + p.listed_off), weights, loss, lse};
   if (teacher && list.per_row == 0) f.weights = loss;  // no terms: never read
   if (n == 0) return status_of(launch_loss_finish(f, stream));
+  ListOrder order;
+  if (order_lists(p.order, list, weights, m, n, base + p.order_off, &order, stream) != hipSuccess) return XTVXY_ERROR_LAUNCH;
   for (int64_t j = 0; j < n; j += p.piece) {
     const int64_t classes = std::min(p.piece, n - j);
     LossForwardArgs a{};
@@ -290,6 +325,7 @@ xtvxy_status forward_impl(const Layer& l, const ClassList& list, const Teacher* 
     a.inv_temperature = inv_temperature;
     a.first_class = j;
     a.list = list;
+    a.order = order;
     a.listed = reinterpret_cast<float*>(base + p.listed_off);
     a.stats = stats;
     if (launch_loss_forward(a, stream) != hipSuccess) return XTVXY_ERROR_LAUNCH;
@@ -338,7 +374,7 @@ xtvxy_status backward_impl(const Layer& l, const float* grad, const ClassList& l
     take_plan(&g.dw, none, nullptr);
     return status_of(launch_gradient_tile(g, l.type, stream));
   }
-  const BackwardPlan& p = plan_backward(l.type, m, k, n, whole_chunks(l.mx()), whole_chunks(l.mw()), g.dx.m > 0, g.dw.m > 0);
+  const BackwardPlan& p = plan_backward(l.type, m, k, n, list.per_row, whole_chunks(l.mx()), whole_chunks(l.mw()), g.dx.m > 0, g.dw.m > 0);
   if (bad_workspace(p.bytes, ws, ws_bytes)) return XTVXY_ERROR_WORKSPACE;
   char* base = static_cast<char*>(ws);
   float* factor = reinterpret_cast<float*>(base + p.factor_off);
@@ -346,6 +382,8 @@ xtvxy_status backward_impl(const Layer& l, const float* grad, const ClassList& l
   const float inv_temperature = 1.0f / temperature;
   const float* target = labels ? nullptr : list.per_row > 0 ? weights : factor;  // none listed: never read
   if (launch_loss_factor({grad, list, target, inv_temperature, m, n, factor, scale}, stream) != hipSuccess) return XTVXY_ERROR_LAUNCH;
+  ListOrder order;
+  if (order_lists(p.order, list, target, m, n, base + p.order_off, &order, stream) != hipSuccess) return XTVXY_ERROR_LAUNCH;
   const bool products = g.dx.m > 0 || g.dw.m > 0;
   int64_t slices = 0;  // of dX's sums so far
   for (int64_t j = 0; j < n; j += p.piece) {
@@ -359,6 +397,7 @@ xtvxy_status backward_impl(const Layer& l, const float* grad, const ClassList& l
     a.inv_temperature = inv_temperature;
     a.first_class = j;
     a.list = list;
+    a.order = order;
     a.weights = target;
     a.factor = factor;
     a.lse = lse;

@@ -13,6 +13,27 @@ struct ClassList {
   int32_t bits, per_row;
 };
 
+// The lists' entries in the order in which the tiles look for them: of each strip of rows (those that a wavefront
+// stages at a time) and each half tile of columns of the whole vocabulary, entries[starts[..]] up to the next start.
+// An entry: row of the strip, column of the half tile, place in the list.
+struct ListOrder {
+  uint32_t* starts;      // [strips][columns + 1], null: the lists are searched
+  uint32_t* entries;     // [strips][strip_rows * per_row]
+  int64_t columns;       // half tiles
+  int32_t strip_rows, half;  // half: classes of a half tile
+};
+// Half tiles up to which a workgroup counts them in LDS, and places a row from which on the order pays.
+constexpr int64_t kMostHalves = 8192;
+constexpr int64_t kOrderedFrom = 9;
+inline int strip_rows_of(int tile) { return tile / 2 < 64 ? tile / 2 : 64; }
+struct OrderArgs {
+  ClassList list;
+  ListOrder order;
+  const float* weights;  // entries of weight zero are left out, null: none are
+  int64_t m, n;
+};
+hipError_t launch_list_order(const OrderArgs& a, hipStream_t s);
+
 // A piece of the logits t = (X W^T + bias) / T of which only statistics are kept: product.A is X, product.B the
 // piece's rows of W, product.n its classes from `first_class` on.
 struct LossForwardArgs {
@@ -21,6 +42,7 @@ struct LossForwardArgs {
   float inv_temperature;
   int64_t first_class;
   ClassList list;
+  ListOrder order;
   float* listed;         // [m][per_row]: t of the listed classes of this piece
   float* stats;          // [2 tiles of columns][m][2]: largest t and sum of exp(t - largest) over half a tile
 };
@@ -74,6 +96,7 @@ struct LossGradientArgs {
   float inv_temperature;
   int64_t first_class;
   ClassList list;
+  ListOrder order;
   const float* weights;
   const float* factor;
   const float* lse;

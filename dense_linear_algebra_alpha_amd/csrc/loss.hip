@@ -23,13 +23,28 @@ __device__ __forceinline__ int64_t class_at(const ClassList& l, int64_t i, int e
 }
 
 // For every class that a strip's rows list within its columns: fn(row of the strip, its place in the list, place of its
-// value in the staging area). Lanes take the lists' entries in turn, eight at a time: one at a time, every entry would
-// wait for memory (32 a row over 256 x 256 tiles: 30 us a tile).
+// value in the staging area). Short lists are searched, lanes taking their entries in turn; of long ones the tile has the
+// entries by strip and half tile: searching 32 a row took 30 us a 256 x 256 tile, as long as its product at k = 1000.
 template <int WN, typename Fn>
-__device__ __forceinline__ void for_listed(const ClassList& list, int64_t i0, int rows, int64_t first_class, int columns, Fn fn) {
-  constexpr int kBatch = 8;
-  const uint32_t per_row = (uint32_t)list.per_row, total = (uint32_t)rows * per_row;
-  for (uint32_t at0 = threadIdx.x & 63; at0 < total; at0 += 64 * kBatch) {
+__device__ __forceinline__ void for_listed(const ClassList& list, const ListOrder& order, int64_t i0, int rows,
+                                           int64_t first_class, int columns, Fn fn) {
+  const uint32_t per_row = (uint32_t)list.per_row, lane = threadIdx.x & 63;
+  if (columns <= 0) return;
+  if (order.starts) {
+    const int64_t strip = i0 / order.strip_rows;
+    const uint32_t* starts = order.starts + strip * (order.columns + 1) + first_class / WN;
+    const uint32_t* entries = order.entries + strip * order.strip_rows * per_row;
+    const uint32_t end = starts[1];
+    for (uint32_t at = starts[0] + lane; at < end; at += 64) {
+      const uint32_t e = entries[at];
+      const int row = (int)(e & 63), c = (int)(e >> 6 & 127);
+      fn(row, (int)(e >> 13), staged_at<WN>(row, c >> 2) + (c & 3));
+    }
+    return;
+  }
+  constexpr int kBatch = 4;
+  const uint32_t total = (uint32_t)rows * per_row;
+  for (uint32_t at0 = lane; at0 < total; at0 += 64 * kBatch) {
     int64_t c[kBatch];
     uint32_t row[kBatch], e[kBatch];
 #pragma unroll
@@ -46,26 +61,120 @@ __device__ __forceinline__ void for_listed(const ClassList& list, int64_t i0, in
   }
 }
 
-// The bias of a lane's columns: four neighbours of each of the FB groups of 16.
+// Whether there may be any: labels and ordered lists are looked at, other lists are short.
+template <int WN>
+__device__ __forceinline__ bool any_listed(const ClassList& list, const ListOrder& order, int64_t i0, int rows, int64_t first_class,
+                                           int columns) {
+  if (columns <= 0) return false;
+  if (order.starts) {
+    const uint32_t* starts = order.starts + i0 / order.strip_rows * (order.columns + 1) + first_class / WN;
+    return starts[0] != starts[1];
+  }
+  if (list.per_row > 1) return true;
+  const int lane = threadIdx.x & 63;
+  const int64_t c = lane < rows ? class_at(list, i0 + lane, 0) - first_class : -1;
+  return __any(c >= 0 && c < columns);
+}
+
+// A workgroup puts a strip's entries in order: counted by half tile, the counts summed, and placed. Entries of one half tile
+// come in any order: each has a value of its own.
+constexpr int kOrderThreads = 1024;
+__global__ __launch_bounds__(kOrderThreads) void list_order(OrderArgs a) {
+  __shared__ uint32_t count[kMostHalves];
+  __shared__ uint32_t totals[kOrderThreads / 64];
+  const int64_t strip = blockIdx.x, i0 = strip * a.order.strip_rows;
+  const int columns = (int)a.order.columns, per_row = a.list.per_row;
+  const int rows = a.m - i0 < a.order.strip_rows ? (int)(a.m - i0) : a.order.strip_rows;
+  uint32_t* starts = a.order.starts + strip * (columns + 1);
+  uint32_t* entries = a.order.entries + strip * a.order.strip_rows * per_row;
+  for (int h = threadIdx.x; h < columns; h += kOrderThreads) count[h] = 0;
+  __syncthreads();
+  const int half_bits = 31 - __builtin_clz(a.order.half);
+  const auto each = [&](auto fn) {
+    constexpr int kBatch = 4;
+    for (int at0 = threadIdx.x; at0 < rows * per_row; at0 += kBatch * kOrderThreads) {
+      int64_t c[kBatch];
+      int row[kBatch], e[kBatch];
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b) {
+        const int at = at0 + b * kOrderThreads < rows * per_row ? at0 + b * kOrderThreads : at0;
+        row[b] = at / per_row;
+        e[b] = at - row[b] * per_row;
+        c[b] = class_at(a.list, i0 + row[b], e[b]);
+        if (a.weights && a.weights[(i0 + row[b]) * per_row + e[b]] == 0.0f) c[b] = -1;
+      }
+#pragma unroll
+      for (int b = 0; b < kBatch; ++b)
+        if (at0 + b * kOrderThreads < rows * per_row && c[b] >= 0 && c[b] < a.n)
+          fn(row[b], e[b], (int)(c[b] >> half_bits), (int)c[b] & (a.order.half - 1));
+    }
+  };
+  each([&](int, int, int half, int) { atomicAdd(&count[half], 1u); });
+  __syncthreads();
+  // each thread sums neighbours, the threads' sums join over the wavefronts
+  const int share = (columns + kOrderThreads - 1) / kOrderThreads, h0 = threadIdx.x * share, lane = threadIdx.x & 63;
+  uint32_t own = 0;
+  for (int h = h0; h < h0 + share && h < columns; ++h) own += count[h];
+  uint32_t sum = own;
+#pragma unroll
+  for (int by = 1; by < 64; by *= 2) {
+    const uint32_t v = __shfl_up(sum, by);
+    if (lane >= by) sum += v;
+  }
+  if (lane == 63) totals[threadIdx.x >> 6] = sum;
+  __syncthreads();
+  uint32_t before = sum - own;
+  for (int w = 0; w < kOrderThreads / 64; ++w)
+    if (w < (int)(threadIdx.x >> 6)) before += totals[w];
+  for (int h = h0; h < h0 + share && h < columns; ++h) {
+    const uint32_t c = count[h];
+    starts[h] = count[h] = before;
+    before += c;
+  }
+  if (threadIdx.x == kOrderThreads - 1) starts[columns] = before;
+  __syncthreads();
+  each([&](int row, int e, int half, int column) {
+    entries[atomicAdd(&count[half], 1u)] = (uint32_t)row | (uint32_t)column << 6 | (uint32_t)e << 13;
+  });
+}
+
+// The bias over T of a lane's columns, four neighbours of each of the FB groups of 16; -infinity where there is no
+// column, whose product is zero.
 template <int FB>
-__device__ __forceinline__ void lane_bias(const float* bias, int64_t j, int64_t n, f32x4 (&b)[FB]) {
+__device__ __forceinline__ void lane_bias(const float* bias, float inv_temperature, int64_t j, int64_t n, f32x4 (&b)[FB]) {
 #pragma unroll
   for (int y = 0; y < FB; ++y) {
     const int64_t at = j + y * 16;
-    b[y] = bias && at < n ? load4<float>(bias + at, n - at >= 4 ? 4 : (int)(n - at)) : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    b[y] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    if (bias && at < n) b[y] = load4<float>(bias + at, n - at >= 4 ? 4 : (int)(n - at)) * inv_temperature;
+    if (at + 4 > n) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) b[y][e] = at + e < n ? b[y][e] : -__builtin_inff();
+    }
   }
 }
 
-// t of one row's columns of a lane: -infinity where there is no column.
+// t = z / T + bias / T of one row's columns of a lane.
 template <int FB>
-__device__ __forceinline__ void lane_logits(f32x4 (&z)[FB], const f32x4 (&bias)[FB], float inv_temperature, int64_t j, int64_t n) {
+__device__ __forceinline__ void lane_logits(const f32x4 (&z)[FB], const f32x4 (&bias)[FB], float inv_temperature, f32x4 (&t)[FB]) {
 #pragma unroll
   for (int y = 0; y < FB; ++y)
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float t = (z[y][e] + bias[y][e]) * inv_temperature;
-      z[y][e] = j + y * 16 + e < n ? t : -__builtin_inff();
-    }
+    for (int e = 0; e < 4; ++e) t[y][e] = fmaf(z[y][e], inv_temperature, bias[y][e]);
+}
+
+// exp(z c - ref) in the place of exp(z / T - ref / log2 e), c = log2 e / T, takes one operation less than the exact
+// difference with the bias and its product with log2 e: without a bias, in whole tiles, and while ref stays finite. c and
+// ref are each off by half a step: as much as the rounding of the logits themselves.
+constexpr float kLog2e = 1.44269504f, kLn2 = 0.693147181f, kFarLogit = 1e38f;
+
+__device__ __forceinline__ float max_xor16(float x) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float max_xor32(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
 
 struct StatsEnd {
@@ -77,28 +186,50 @@ struct StatsEnd {
     constexpr int WN = Strip::kWidth, kRows = Strip::kRows;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int wi = (wave >> 1) * (BM / 2), wj = (wave & 1) * (BN / 2), r = lane & 15, g = lane >> 4;
-    end_of_products(sums);
-    const int64_t j = p.j0 + wj + g * 4;
     f32x4 bias[FB];
-    lane_bias<FB>(l.bias, j, a.n, bias);
+    lane_bias<FB>(l.bias, l.inv_temperature, p.j0 + wj + g * 4, a.n, bias);
+    end_of_products(sums);
     float* stats = l.stats + (p.j0 / BN * 2 + (wave & 1)) * a.m * 2;
+    const bool plain = !l.bias && p.j0 + BN <= a.n;
+    const float c = l.inv_temperature * kLog2e;
 #pragma unroll
     for (int x = 0; x < FA; ++x) {
-      lane_logits<FB>(sums.acc[x], bias, l.inv_temperature, j, a.n);
-      float top = sums.acc[x][0][0];
+      const f32x4(&z)[FB] = sums.acc[x];
+      float top = 0.0f, s = 0.0f;
+      bool done = false;
+      if (plain) {
+        top = z[0][0];
 #pragma unroll
-      for (int y = 0; y < FB; ++y)
+        for (int y = 0; y < FB; ++y)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) top = fmaxf(top, sums.acc[x][y][e]);
-      top = fmaxf(top, __shfl_xor(top, 16));
-      top = fmaxf(top, __shfl_xor(top, 32));
-      // a row without a finite logit here has no distances from its largest one
-      const float from = top == -__builtin_inff() ? 0.0f : top;
-      float s = 0.0f;
+          for (int e = 0; e < 4; ++e) top = fmaxf(top, z[y][e]);
+        top = max_xor32(max_xor16(top)) * c;
+        done = __all(fabsf(top) < kFarLogit);
+        if (done) {
 #pragma unroll
-      for (int y = 0; y < FB; ++y)
+          for (int y = 0; y < FB; ++y)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s += fast_exp(sums.acc[x][y][e] - from);
+            for (int e = 0; e < 4; ++e) s += __builtin_amdgcn_exp2f(fmaf(z[y][e], c, -top));
+          top *= kLn2;
+        }
+      }
+      if (!done) {
+        f32x4 t[FB];
+        lane_logits<FB>(z, bias, l.inv_temperature, t);
+        top = t[0][0];
+#pragma unroll
+        for (int y = 0; y < FB; ++y)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) top = fmaxf(top, t[y][e]);
+        top = max_xor32(max_xor16(top));
+        // a row without a finite logit here has no distances from its largest one
+        const float from = top == -__builtin_inff() ? 0.0f : top;
+        s = 0.0f;
+#pragma unroll
+        for (int y = 0; y < FB; ++y)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s += fast_exp(t[y][e] - from);
+      }
       s = add_xor32(add_xor16(s));
       const int64_t i = p.i0 + wi + x * 16 + r;
       if (g == 0 && i < a.m) *reinterpret_cast<f32x2*>(stats + i * 2) = f32x2{top, s};
@@ -110,10 +241,18 @@ struct StatsEnd {
     for (int part = 0; part < BM / 2 / kRows; ++part) {
       const int64_t i0 = p.i0 + wi + part * kRows;
       if (i0 >= a.m) break;
-      sums.template stage<WN>(area, part, kRows);
+      const int rows = a.m - i0 < kRows ? (int)(a.m - i0) : kRows, columns = width < WN ? (int)width : WN;
+      // most strips of a wide vocabulary hold none of their rows' classes
+      if (!any_listed<WN>(l.list, l.order, i0, rows, l.first_class + p.j0 + wj, columns)) continue;
+#pragma unroll
+      for (int x = part * kRows / 16; x < (part + 1) * kRows / 16; ++x) {
+        f32x4 t[FB];
+        lane_logits<FB>(sums.acc[x], bias, l.inv_temperature, t);
+#pragma unroll
+        for (int y = 0; y < FB; ++y) *reinterpret_cast<f32x4*>(area + staged_at<WN>(x * 16 % kRows + r, y * 4 + g)) = t[y];
+      }
       __builtin_amdgcn_wave_barrier();
-      for_listed<WN>(l.list, i0, a.m - i0 < kRows ? (int)(a.m - i0) : kRows, l.first_class + p.j0 + wj,
-                     width < WN ? (int)width : WN,
+      for_listed<WN>(l.list, l.order, i0, rows, l.first_class + p.j0 + wj, columns,
                      [&](int row, int e, int at) { l.listed[(i0 + row) * l.list.per_row + e] = area[at]; });
       __builtin_amdgcn_wave_barrier();
     }
@@ -129,37 +268,59 @@ struct GradientEnd {
     constexpr int WN = Strip::kWidth, kRows = Strip::kRows, kLanes = WN / 8, kStep = 64 / kLanes;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int wi = (wave >> 1) * (BM / 2), wj = (wave & 1) * (BN / 2), r = lane & 15, g = lane >> 4;
-    end_of_products(sums);
-    const int64_t j = p.j0 + wj + g * 4;
     f32x4 bias[FB];
-    lane_bias<FB>(l.bias, j, a.n, bias);
+    lane_bias<FB>(l.bias, l.inv_temperature, p.j0 + wj + g * 4, a.n, bias);
+    float factors[FA], norms[FA];
+    bool near = true;
 #pragma unroll
     for (int x = 0; x < FA; ++x) {
       const int64_t i = p.i0 + wi + x * 16 + r;
-      const float factor = i < a.m ? l.factor[i] : 0.0f, lse = i < a.m ? l.lse[i] : 0.0f;
-      lane_logits<FB>(sums.acc[x], bias, l.inv_temperature, j, a.n);
-#pragma unroll
-      for (int y = 0; y < FB; ++y)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {  // a row that does not count is zero whatever its logits are
-          const float d = factor * fast_exp(sums.acc[x][y][e] - lse);
-          sums.acc[x][y][e] = factor == 0.0f ? 0.0f : d;
-        }
+      factors[x] = i < a.m ? l.factor[i] : 0.0f;
+      norms[x] = i < a.m ? l.lse[i] : 0.0f;
+      near &= fabsf(norms[x]) < kFarLogit;
     }
+    end_of_products(sums);
+    const bool plain = !l.bias && p.j0 + BN <= a.n && __all(near);
+    const float c = l.inv_temperature * kLog2e;
     float* area = reinterpret_cast<float*>(ring + wave * Strip::kArea);
     const int64_t width = a.n - p.j0 - wj;
     const int c8 = lane % kLanes;
     const int64_t column = p.j0 + wj + c8 * 8;  // of this lane's eight
-    const float scale = l.scale ? *l.scale : 1.0f;
+    constexpr bool kScaled = __is_same(T, _Float16);
+    const float scale = kScaled ? *l.scale : 1.0f;
     float column_sums[8] = {};
 #pragma unroll
     for (int part = 0; part < BM / 2 / kRows; ++part) {
       const int64_t i0 = p.i0 + wi + part * kRows;
       if (i0 >= a.m) break;
       const int rows = a.m - i0 < kRows ? (int)(a.m - i0) : kRows;
-      sums.template stage<WN>(area, part, kRows);
+#pragma unroll
+      for (int x = part * kRows / 16; x < (part + 1) * kRows / 16; ++x) {
+        const float factor = factors[x];
+        f32x4 d[FB];
+        if (plain) {
+          const float ref = norms[x] * kLog2e;
+#pragma unroll
+          for (int y = 0; y < FB; ++y)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) d[y][e] = factor * __builtin_amdgcn_exp2f(fmaf(sums.acc[x][y][e], c, -ref));
+        } else {
+          lane_logits<FB>(sums.acc[x], bias, l.inv_temperature, d);
+#pragma unroll
+          for (int y = 0; y < FB; ++y)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) d[y][e] = factor * fast_exp(d[y][e] - norms[x]);
+        }
+#pragma unroll
+        for (int y = 0; y < FB; ++y) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)  // a row that does not count is zero whatever its logits are
+            d[y][e] = factor == 0.0f ? 0.0f : d[y][e];
+          *reinterpret_cast<f32x4*>(area + staged_at<WN>(x * 16 % kRows + r, y * 4 + g)) = d[y];
+        }
+      }
       __builtin_amdgcn_wave_barrier();
-      for_listed<WN>(l.list, i0, rows, l.first_class + p.j0 + wj, width < WN ? (int)width : WN, [&](int row, int e, int at) {
+      for_listed<WN>(l.list, l.order, i0, rows, l.first_class + p.j0 + wj, width < WN ? (int)width : WN, [&](int row, int e, int at) {
         const float factor = l.factor[i0 + row], w = l.weights ? l.weights[(i0 + row) * l.list.per_row + e] : 1.0f;
         // a class that is listed twice comes here twice, maybe at once
         if (factor != 0.0f && w != 0.0f) __hip_atomic_fetch_add(area + at, -factor * w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
@@ -172,9 +333,9 @@ struct GradientEnd {
           const f32x8 v = staged8<WN>(area, row, c8);
           typename Vec<T>::x8 o;
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            column_sums[c] += v[c];
-            o[c] = (T)(v[c] * scale);
+          for (int e = 0; e < 8; ++e) {
+            column_sums[e] += v[e];
+            o[e] = (T)(kScaled ? v[e] * scale : v[e]);
           }
           if (l.d) *reinterpret_cast<typename Vec<T>::x8*>(d + row * l.ldd) = o;
         }
@@ -184,9 +345,9 @@ struct GradientEnd {
     if (!l.sums) return;
     float* out = l.sums + (p.i0 / BM * 2 + (wave >> 1)) * a.n;
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
+    for (int e = 0; e < 8; ++e) {
 #pragma unroll
-      for (int by = kLanes; by < 64; by *= 2) column_sums[c] += __shfl_xor(column_sums[c], by);
+      for (int by = kLanes; by < 64; by *= 2) column_sums[e] += __shfl_xor(column_sums[e], by);
     }
     const int count = a.n - column >= 8 ? 8 : (a.n > column ? (int)(a.n - column) : 0);
     if (lane < kLanes && count > 0) store_elems<float, 8>(out + column, count, column_sums);
@@ -218,26 +379,45 @@ __device__ __forceinline__ void join_stats(float* top, float* sum, float top2, f
   *top = t;
 }
 
-// 16 rows a workgroup: of each row a thread joins every 16th part's statistics, the 16 join in order; the terms of a
-// teacher's classes likewise.
-__global__ __launch_bounds__(256) void loss_finish(LossFinishArgs a) {
-  __shared__ float tops[16][17], sums[16][17], terms[16][17], norms[16];
+// 16 rows a workgroup: of each row a thread joins every 64th part's statistics, the 64 join in order; the terms of a
+// teacher's classes likewise. (With 16 threads a row 1000 parts of 13 rows took 9.6 us.)
+constexpr int kSlots = 64;
+__global__ __launch_bounds__(16 * kSlots) void loss_finish(LossFinishArgs a) {
+  __shared__ float tops[kSlots][17], sums[kSlots][17], terms[kSlots][17], norms[16];
   const int c = threadIdx.x & 15, slot = threadIdx.x >> 4;
   const int64_t i = (int64_t)blockIdx.x * 16 + c;
   const bool there = i < a.m;
   float top = -__builtin_inff(), sum = 0.0f;
   if (there) {
-#pragma unroll 4
-    for (int64_t p = slot; p < a.parts; p += 16) {
-      const f32x2 v = *reinterpret_cast<const f32x2*>(a.stats + (p * a.m + i) * 2);
-      join_stats(&top, &sum, v[0], v[1]);
+    for (int64_t p = slot; p < a.parts; p += 4 * kSlots) {
+      f32x2 v[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const bool part = p + u * kSlots < a.parts;
+        v[u] = *reinterpret_cast<const f32x2*>(a.stats + ((part ? p + u * kSlots : p) * a.m + i) * 2);
+        if (!part) v[u] = f32x2{-__builtin_inff(), 0.0f};
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) join_stats(&top, &sum, v[u][0], v[u][1]);
     }
   }
   tops[slot][c] = top;
   sums[slot][c] = sum;
   __syncthreads();
+  // the slots' in two steps: eight by eight, then those
+  if (slot < 8 && there) {
+    top = tops[slot * 8][c];
+    sum = sums[slot * 8][c];
+    for (int s = 1; s < 8; ++s) join_stats(&top, &sum, tops[slot * 8 + s][c], sums[slot * 8 + s][c]);
+  }
+  __syncthreads();
+  if (slot < 8) {
+    tops[slot][c] = top;
+    sums[slot][c] = sum;
+  }
+  __syncthreads();
   if (slot == 0 && there) {
-    for (int s = 1; s < 16; ++s) join_stats(&top, &sum, tops[s][c], sums[s][c]);
+    for (int s = 1; s < 8; ++s) join_stats(&top, &sum, tops[s][c], sums[s][c]);
     if (a.run && !a.first) join_stats(&top, &sum, a.run[i * 2], a.run[i * 2 + 1]);
     if (a.run && !a.last) {
       a.run[i * 2] = top;
@@ -251,7 +431,7 @@ __global__ __launch_bounds__(256) void loss_finish(LossFinishArgs a) {
   if (a.weights) {
     float s = 0.0f;
     if (there) {
-      for (int e = slot; e < a.list.per_row; e += 16) {
+      for (int e = slot; e < a.list.per_row; e += kSlots) {
         const float w = a.weights[i * a.list.per_row + e];
         if (w != 0.0f) s += w * (logf(w) - a.listed[i * a.list.per_row + e] + lse);
       }
@@ -259,7 +439,7 @@ __global__ __launch_bounds__(256) void loss_finish(LossFinishArgs a) {
     terms[slot][c] = s;
     __syncthreads();
     if (slot != 0 || !there) return;
-    for (int q = 1; q < 16; ++q) s += terms[q][c];
+    for (int q = 1; q < kSlots; ++q) s += terms[q][c];
     a.loss[i] = s;
   } else {
     if (slot != 0 || !there) return;
@@ -317,27 +497,33 @@ __global__ __launch_bounds__(256) void teacher_weights(TeacherArgs a) {
   }
 }
 
-__global__ __launch_bounds__(256) void loss_factor(LossFactorArgs a) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i >= a.m) return;
-  float f;
+__device__ __forceinline__ float factor_of(const LossFactorArgs& a, int64_t i) {
   if (a.weights) {
     float s = 0.0f;
+#pragma unroll 8
     for (int e = 0; e < a.list.per_row; ++e) s += a.weights[i * a.list.per_row + e];
-    f = s == 0.0f ? 0.0f : s == s ? a.grad[i] * a.inv_temperature : s;
-  } else {
-    const int64_t y = class_at(a.list, i, 0);
-    f = y < 0 ? 0.0f : y < a.n ? a.grad[i] : __builtin_nanf("");
+    return s == 0.0f ? 0.0f : s == s ? a.grad[i] * a.inv_temperature : s;
   }
-  a.factor[i] = f;
+  const int64_t y = class_at(a.list, i, 0);
+  return y < 0 ? 0.0f : y < a.n ? a.grad[i] : __builtin_nanf("");
 }
 
+__global__ __launch_bounds__(256) void loss_factor(LossFactorArgs a) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i < a.m) a.factor[i] = factor_of(a, i);
+}
+
+// The scale, in one workgroup; kFactor: after forming the factors itself.
+template <bool kFactor>
 __global__ __launch_bounds__(1024) void loss_scale(LossFactorArgs a) {
   __shared__ float lds[16];
   float top = 0.0f;
 #pragma unroll 4
   for (int64_t i = threadIdx.x; i < a.m; i += 1024) {
-    const float f = fabsf(a.factor[i]);
+    float f;
+    if (kFactor) a.factor[i] = f = factor_of(a, i);
+    else f = a.factor[i];
+    f = fabsf(f);
     top = f < __builtin_inff() ? fmaxf(top, f) : top;
   }
 #pragma unroll
@@ -395,8 +581,13 @@ hipError_t launch_loss_gradient(const LossGradientArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
+hipError_t launch_list_order(const OrderArgs& a, hipStream_t s) {
+  list_order<<<(unsigned)((a.m + a.order.strip_rows - 1) / a.order.strip_rows), kOrderThreads, 0, s>>>(a);
+  return hipGetLastError();
+}
+
 hipError_t launch_loss_finish(const LossFinishArgs& a, hipStream_t s) {
-  loss_finish<<<(unsigned)((a.m + 15) / 16), 256, 0, s>>>(a);
+  loss_finish<<<(unsigned)((a.m + 15) / 16), 16 * kSlots, 0, s>>>(a);
   return hipGetLastError();
 }
 
@@ -410,8 +601,12 @@ hipError_t launch_teacher_weights(const TeacherArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_loss_factor(const LossFactorArgs& a, hipStream_t s) {
-  loss_factor<<<(unsigned)((a.m + 255) / 256), 256, 0, s>>>(a);
-  if (a.scale) loss_scale<<<1, 1024, 0, s>>>(a);
+  if (a.scale && a.m * a.list.per_row <= 8192) {  // two launches: 11 us of 200 rows, one: 2.4; at 2047 x 32 one takes 12.7
+    loss_scale<true><<<1, 1024, 0, s>>>(a);
+  } else {
+    loss_factor<<<(unsigned)((a.m + 255) / 256), 256, 0, s>>>(a);
+    if (a.scale) loss_scale<false><<<1, 1024, 0, s>>>(a);
+  }
   return hipGetLastError();
 }
 
