@@ -5,7 +5,7 @@ from __future__ import annotations
 import functools
 
 from . import _abi
-from .layers import _check, _entry, _new, _pitch, _scratch, _size, _stream_of, _suffix, _torch
+from .layers import _check, _entry, _fast, _new, _pitch, _scratch, _size, _stream_of, _suffix, _torch
 
 
 # ---------------------------------------------------------------------------
@@ -88,6 +88,10 @@ def embedding(ids, table, scale=1.0, *, out=None, stream=None):
     column stride, of one type: float32, bfloat16 or float16. Negative ids are padding and give zeros; ids beyond
     the table give NaN (a check would wait for the GPU). Autograd records nothing; the gradient is
     embedding_backward's."""
+    if stream is None:  # the usual call in compiled code, as in linear
+        got = _fast("embedding", "xtvxy_embedding", table, ids, table, scale, out)
+        if got is not None:
+            return got
     dev = _on_current_gpu("table", table)
     dtype = table.dtype
     suffix = _suffix(dtype)
@@ -115,6 +119,10 @@ def embedding_backward(G, ids, rows, scale=1.0, *, dtable=None, accumulate=False
     With ``accumulate`` it is added to ``dtable``, of which only the rows that occur are touched (a table that is also
     an output layer's weight: dtable is that layer's dW); else every element is written. Negative ids and ids
     beyond the table take no part."""
+    if stream is None:
+        got = _fast("embedding_backward", "xtvxy_embedding_backward", G, G, ids, rows, scale, dtable, accumulate, workspace)
+        if got is not None:
+            return got
     dev = _on_current_gpu("G", G)
     dtype = G.dtype
     suffix = _suffix(dtype)

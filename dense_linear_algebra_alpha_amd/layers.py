@@ -142,10 +142,30 @@ def _extension():
         warnings.warn("_tensors.so is not built or does not match this torch (%s): calls take more host time; run "
                       "`python -m dense_linear_algebra_alpha_amd.build`" % e, RuntimeWarning)
         return None
-    names = ("xtvxy_linear_%s_workspace_size", "xtvxy_linear_%s", "xtvxy_linear_backward_%s_workspace_size",
-             "xtvxy_linear_backward_%s")
-    _tensors.bind(*[ctypes.cast(_entry(f % s), ctypes.c_void_p).value for s in ("f32", "bf16", "f16") for f in names])
+    names = ["xtvxy_linear_%s_workspace_size", "xtvxy_linear_%s", "xtvxy_linear_backward_%s_workspace_size",
+             "xtvxy_linear_backward_%s", "xtvxy_layer_norm_%s", "xtvxy_layer_norm_backward_workspace_size",
+             "xtvxy_layer_norm_backward_%s", "xtvxy_embedding_%s", "xtvxy_embedding_backward_%s_workspace_size",
+             "xtvxy_embedding_backward_%s"]
+    for loss in ("cross_entropy", "cross_entropy_backward", "distillation", "distillation_backward"):
+        names += ["xtvxy_linear_%s_%%s_workspace_size" % loss, "xtvxy_linear_%s_%%s" % loss]
+    _tensors.bind(*[ctypes.cast(_entry(f.replace("%s", s)), ctypes.c_void_p).value for s in ("f32", "bf16", "f16")
+                    for f in names])
     return _tensors
+
+
+def _fast(function, name, like, *args):
+    """One call of the current stream in compiled code: its result, or None where it needs the caller's checks."""
+    if not like.is_cuda:
+        return None
+    e = _extension()
+    if e is None:
+        return None
+    c = _torch()._C
+    dev = c._cuda_getDevice()
+    got = getattr(e, function)(*args, dev, c._cuda_getCurrentRawStream(dev))
+    if type(got) is int:
+        _raise(got, name, like)
+    return got
 
 
 def _raise(status, name, X):

@@ -7,7 +7,7 @@ import functools
 
 from . import _abi
 from .embeddings import _index_bits
-from .layers import _MAX_PITCH, _check, _check_bias, _entry, _features, _new, _pitch, _scratch, _size, _stream_of, _torch
+from .layers import _MAX_PITCH, _check, _check_bias, _entry, _fast, _features, _new, _pitch, _scratch, _size, _stream_of, _torch
 from .norm import _vector
 from .optimiser import _type_code
 
@@ -201,6 +201,10 @@ def linear_cross_entropy(X, W, labels, bias=None, *, loss=None, lse=None, worksp
     int64 vector (m). Rows with a negative label do not count: their loss is zero. A label beyond the classes gives
     NaN (a check would wait for the GPU). loss and lse are float32 (m); linear_cross_entropy_backward takes lse.
     Autograd records nothing, as in linear."""
+    if stream is None:  # the usual call in compiled code, as in linear
+        got = _fast("cross_entropy", "xtvxy_linear_cross_entropy", X, X, W, labels, bias, loss, lse, workspace)
+        if got is not None:
+            return got
     dev, _, suffix, m, k, n, ldx, ldw = _features(X, W)
     bp = _vector("bias", bias, n, dev)
     bits = _index_bits("labels", labels, (m,), dev)
@@ -219,6 +223,11 @@ def linear_cross_entropy_backward(grad, X, W, labels, lse, bias=None, *, need_dX
     column sums of d (float32). A mean over the rows that count has grad = 1 / their number.
 
     Outputs that are not needed are not computed and come back as None."""
+    if stream is None:
+        got = _fast("cross_entropy_backward", "xtvxy_linear_cross_entropy_backward", X, grad, X, W, labels, lse, bias, need_dX,
+                    need_dW, need_db, dX, dW, db, workspace)
+        if got is not None:
+            return got
     dev, dtype, suffix, m, k, n, ldx, ldw = _features(X, W)
     bp = _vector("bias", bias, n, dev)
     bits = _index_bits("labels", labels, (m,), dev)
@@ -244,6 +253,11 @@ def linear_distillation(X, W, classes, teacher, bias=None, temperature=1.0, *, l
     column stride; weights (m x s, float32) gets P. Negative classes are empty places; a class that a row lists
     twice gets both probabilities in its first place; rows without classes do not count. X, W and bias are as in
     linear_cross_entropy. linear_distillation_backward takes lse and weights."""
+    if stream is None:
+        got = _fast("distillation", "xtvxy_linear_distillation", X, X, W, classes, teacher, bias, temperature, loss, lse,
+                    weights, workspace)
+        if got is not None:
+            return got
     dev, _, suffix, m, k, n, ldx, ldw = _features(X, W)
     bp = _vector("bias", bias, n, dev)
     if classes.dim() != 2:
@@ -274,6 +288,11 @@ def linear_distillation_backward(grad, X, W, classes, weights, lse, bias=None, t
     """The gradient of linear_distillation: (dX, dW, db) for grad[i] = d total / d loss[i] (float32, m) from the forward
     call's weights and lse, with d[i, j] = grad[i] / temperature (softmax(t)[i, j] - P[i, j]); otherwise as
     linear_cross_entropy_backward. The gradient of a hard loss on the same layer is added to it by the caller."""
+    if stream is None:
+        got = _fast("distillation_backward", "xtvxy_linear_distillation_backward", X, grad, X, W, classes, weights, lse, bias,
+                    temperature, need_dX, need_dW, need_db, dX, dW, db, workspace)
+        if got is not None:
+            return got
     dev, dtype, suffix, m, k, n, ldx, ldw = _features(X, W)
     bp = _vector("bias", bias, n, dev)
     if classes.dim() != 2:

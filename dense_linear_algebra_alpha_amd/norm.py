@@ -5,7 +5,7 @@ from __future__ import annotations
 import functools
 
 from . import _abi
-from .layers import _check, _check_bias, _entry, _new, _pitch, _scratch, _size, _stream_of, _suffix, _torch
+from .layers import _check, _check_bias, _entry, _fast, _new, _pitch, _scratch, _size, _stream_of, _suffix, _torch
 
 
 # ---------------------------------------------------------------------------
@@ -85,6 +85,10 @@ def layer_norm(X, weight=None, bias=None, eps=1e-5, *, save_stats=False, out=Non
     each row's mean and 1 / sqrt(variance + eps) in float32 (m), which layer_norm_backward takes, and
     returns (out, mean, rstd); so it does with ``mean`` and ``rstd`` given. Autograd records nothing, as in
     linear."""
+    if stream is None:  # the usual call in compiled code, as in linear
+        got = _fast("layer_norm", "xtvxy_layer_norm", X, X, weight, bias, eps, save_stats, out, mean, rstd)
+        if got is not None:
+            return got
     dev, dtype, suffix, m, n, ldx = _rows(X)
     wp, bp = _vector("weight", weight, n, dev), _vector("bias", bias, n, dev)
     if out is None:
@@ -109,6 +113,11 @@ def layer_norm_backward(G, X, mean, rstd, weight=None, *, need_dX=True, need_dwe
     """The gradient of layer_norm: (dX, dweight, dbias) for G = d loss / d out, from the forward call's mean and
     rstd. dX has the tensors' type, dweight and dbias are float32 (n). Outputs that are not needed are not
     computed and come back as None."""
+    if stream is None:
+        got = _fast("layer_norm_backward", "xtvxy_layer_norm_backward", X, G, X, mean, rstd, weight, need_dX, need_dweight,
+                    need_dbias, dX, dweight, dbias, workspace)
+        if got is not None:
+            return got
     dev, dtype, suffix, m, n, ldx = _rows(X)
     ldg = _pitch("G", G, m, n, dtype, dev)
     for name, t in (("mean", mean), ("rstd", rstd)):
