@@ -365,7 +365,9 @@ template <typename T, int L>
 void norm_for(const NormArgs& a, hipStream_t s) {
   constexpr int kBlock = L < 256 ? 256 : L, kRows = kBlock / L;
   const int64_t chunks = (a.n + kChunkOf<T> - 1) / kChunkOf<T>;
-  const int64_t most = 256 * (kBlock == 256 ? 8 : 2);  // workgroups that the CUs hold
+  // workgroups: enough rows under way, few enough that they keep weight and bias: 16384 x 4096 of bf16 with 2, 4 and 8 of
+  // 256 threads a CU 53, 45, 46 us, 4000 x 16384 with 1 and 2 of 1024 threads 47, 48; with one a row 55, 73
+  const int64_t most = kBlock == 256 ? 1024 : 256;
   const int64_t rows = (a.m + kRows - 1) / kRows;
   const unsigned grid = (unsigned)(rows < most ? rows : most);
   if (chunks <= L) norm_rows<T, L, 1><<<grid, kBlock, 0, s>>>(a);
