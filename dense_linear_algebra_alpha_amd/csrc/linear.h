@@ -40,7 +40,7 @@ struct ProductArgs {
   int64_t whole;
   int64_t k_per_split;      // a multiple of the tile's depth; splits * k_per_split >= k
   float* partial;           // used when splits > 1 or in_parts
-  int32_t in_parts;         // nonzero: sums in one part go to `partial` too (ring kernel, whole 0)
+  int32_t in_parts;         // nonzero: sums in one part go to `partial` too (ring kernel with whole 0, few rows)
   const float* scale;       // on the device: of the sums of a gradient's product, null for 1
   __host__ __device__ int64_t tiles() const { return ((m + tile - 1) / tile) * ((n + tile - 1) / tile); }
   LinearEpilogue e;

@@ -128,7 +128,7 @@ __global__ __launch_bounds__(KW * 64) void product_few(ProductArgs a) {
     for (int s = 1; s < KW; ++s) z += sums[s][c][lane];
     const int64_t i = c / NT * 16 + r, j = j0 + c % NT * 16 + g * 4;
     if (i >= a.m || j >= a.n) continue;
-    if (a.splits > 1)
+    if (a.splits > 1 || a.in_parts)
       store4<float>(a.partial + ((int64_t)blockIdx.y * a.m + i) * a.n + j, z, a.n - j >= 4 ? 4 : (int)(a.n - j));
     else
       epilogue4<T>(a.e, i, j, a.n, z);

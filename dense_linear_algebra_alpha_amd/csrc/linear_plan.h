@@ -65,6 +65,12 @@ inline bool whole_chunks(const Matrix& x) {
 
 inline size_t packed_bytes(int64_t rows, int64_t cols, int es) { return align_up((size_t)rows * padded(cols, es) * es); }
 
+// The kernel for few rows: its wavefronts (0: not for this shape), outputs of a workgroup, and parts.
+struct FewPlan {
+  int waves = 0, outputs = 0;
+  ProductPlan product;
+};
+FewPlan plan_few(int type, int64_t m, int64_t k, int64_t n);
 // The layer's tile, split tiles and parts with the least estimated time; without `split` no tile is split. only_tile:
 // that tile, if not 0.
 ProductPlan plan_product(int type, int64_t m, int64_t n, int64_t k, bool ring, bool split = true, int only_tile = 0);

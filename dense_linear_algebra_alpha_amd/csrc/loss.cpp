@@ -67,32 +67,51 @@ hipError_t order_lists(const OrderPlan& p, const ClassList& list, const float* w
   return launch_list_order({list, *order, weights, m, n}, s);
 }
 
+// Up to 64 rows of 16 bits over so many classes that reading W is what counts: tiles of 128 have more of it under way
+// than those of 64. us: 64 x 1024 x 131072 67, 84; 33 x 3500 x 20000 89, 91; fp32, bound by the matrix unit, 129, 82.
+int loss_tile(int type, int64_t m, int64_t n) { return type != kF32 && m <= 64 && n >= 128 * kComputeUnits / 2 ? 128 : 0; }
+
 struct ForwardPlan {
   bool pack_x, pack_w;
   int64_t piece;
   ProductPlan whole, last;  // of a piece, of the last one
-  int64_t parts, most_parts;  // halves of tiles' columns of a piece
+  int64_t parts;            // halves of tiles' columns of a piece
   OrderPlan order;
-  size_t x_off, w_off, stats_off, run_off, listed_off, order_off, bytes = 0;
+  FewPlan few;              // of few rows: their products go through the workspace, whatever the operands' alignment
+  size_t x_off, w_off, stats_off, run_off, listed_off, order_off, logits_off, bytes = 0;
 };
 
 ForwardPlan make_forward_plan(int type, int64_t m, int64_t k, int64_t n, int64_t per_row, bool x_whole, bool w_whole) {
   ForwardPlan p;
   const int es = elem_size(type);
-  p.pack_x = !x_whole;
-  p.pack_w = !w_whole;
-  // statistics: 8 bytes a row and half tile of at least 32 classes
-  const int64_t per_class = std::max<int64_t>(m / 4, p.pack_w ? padded(k, es) * es : 0);
-  p.piece = piece_of(n, per_class, most_classes(m, k, es));
-  p.whole = plan_product(type, m, p.piece, k, true, false);
-  const int64_t last = n - (cdiv(n, std::max<int64_t>(p.piece, 1)) - 1) * p.piece;
-  p.last = p.piece == n ? p.whole : plan_product(type, m, last, k, true, false, p.whole.tile);
-  p.parts = std::max(2 * cdiv(p.piece, p.whole.tile), 2 * cdiv(last, p.last.tile));
   const auto take = [&](bool want, size_t bytes) {
     const size_t at = p.bytes;
     if (want) p.bytes += align_up(bytes);
     return at;
   };
+  // Few rows: one pass over W that keeps more of it under way than tiles do, then a pass over their logits. us, against
+  // tiles: bf16 1 x 4096 x 32000 53, 62; 1 x 2048 x 131072 94, 115; 7 x 512 x 100000 28, 34; fp32 16 x 4096 x 16000 63, 83;
+  // but of 17 rows and more of 16 bits 32 x 512 x 50000 23, 19, 32 x 1024 x 131072 78, 73, unless rows need copies.
+  if (m <= 16 || type == kF32 || !x_whole || !w_whole) p.few = plan_few(type, m, k, n);
+  p.pack_x = p.pack_w = false;
+  if (p.few.waves > 0) {
+    const int64_t splits = p.few.product.splits;
+    p.piece = piece_of(n, m * splits * 4, most_classes(m, k, es));
+    p.stats_off = take(true, (size_t)cdiv(p.piece, kFewChunk) * m * 8);
+    p.run_off = take(p.piece < n, (size_t)m * 8);
+    p.listed_off = take(true, (size_t)m * per_row * 4);
+    p.logits_off = take(true, (size_t)splits * m * p.piece * 4);
+    return p;
+  }
+  p.pack_x = !x_whole;
+  p.pack_w = !w_whole;
+  // statistics: 8 bytes a row and half tile of at least 32 classes
+  const int64_t per_class = std::max<int64_t>(m / 4, p.pack_w ? padded(k, es) * es : 0);
+  p.piece = piece_of(n, per_class, most_classes(m, k, es));
+  p.whole = plan_product(type, m, p.piece, k, true, false, loss_tile(type, m, p.piece));
+  const int64_t last = n - (cdiv(n, std::max<int64_t>(p.piece, 1)) - 1) * p.piece;
+  p.last = p.piece == n ? p.whole : plan_product(type, m, last, k, true, false, p.whole.tile);
+  p.parts = 2 * cdiv(p.piece, p.whole.tile);
   p.x_off = take(p.pack_x, packed_bytes(m, k, es));
   p.w_off = take(p.pack_w, packed_bytes(p.piece, k, es));
   p.stats_off = take(true, (size_t)p.parts * m * 8);
@@ -129,7 +148,7 @@ BackwardPlan make_backward_plan(int type, int64_t m, int64_t k, int64_t n, int64
   p.parts = p.pieces > 1;
   p.ldd = cdiv(p.piece, 8) * 8;
   const int64_t last = n - (p.pieces - 1) * p.piece;
-  p.logits = plan_product(type, m, p.piece, k, true, false);
+  p.logits = plan_product(type, m, p.piece, k, true, false, loss_tile(type, m, p.piece));
   p.last_logits = p.parts ? plan_product(type, m, last, k, true, false, p.logits.tile) : p.logits;
   plan_gradient(type, m, k, p.piece, want_dx, want_dw, true, &p.dx, &p.dw, 0, p.parts);
   p.last_dx = p.dx;
@@ -321,6 +340,11 @@ xtvxy_status forward_impl(const Layer& l, const ClassList& list, const Teacher* 
     f.first = j == 0;
     f.last = j + classes == n;
     take_plan(&a.product, f.last ? p.last : p.whole, nullptr);
+    if (p.few.waves > 0) {
+      take_plan(&a.product, p.few.product, base + p.logits_off);
+      a.product.in_parts = 1;
+      if (launch_product_few(a.product, p.few.waves, p.few.outputs, stream) != hipSuccess) return XTVXY_ERROR_LAUNCH;
+    }
     a.bias = l.bias ? l.bias + j : nullptr;
     a.inv_temperature = inv_temperature;
     a.first_class = j;
@@ -328,8 +352,9 @@ xtvxy_status forward_impl(const Layer& l, const ClassList& list, const Teacher* 
     a.order = order;
     a.listed = reinterpret_cast<float*>(base + p.listed_off);
     a.stats = stats;
-    if (launch_loss_forward(a, stream) != hipSuccess) return XTVXY_ERROR_LAUNCH;
-    f.parts = 2 * cdiv(classes, a.product.tile);
+    if (p.few.waves > 0 && f.first && f.last && n <= kFewClasses) return status_of(launch_loss_few_rows(a, f, stream));
+    if ((p.few.waves > 0 ? launch_loss_few(a, stream) : launch_loss_forward(a, stream)) != hipSuccess) return XTVXY_ERROR_LAUNCH;
+    f.parts = p.few.waves > 0 ? cdiv(classes, kFewChunk) : 2 * cdiv(classes, a.product.tile);
     if (launch_loss_finish(f, stream) != hipSuccess) return XTVXY_ERROR_LAUNCH;
   }
   return XTVXY_SUCCESS;

@@ -48,6 +48,11 @@ struct LossForwardArgs {
 };
 hipError_t launch_loss_forward(const LossForwardArgs& a, hipStream_t s);
 
+// The same from a piece's products, of few rows, in memory: logits [splits][m][n], the parts to be added. Statistics of
+// each kFewChunk classes, [chunks][m][2].
+constexpr int64_t kFewChunk = 4096;
+hipError_t launch_loss_few(const LossForwardArgs& a, hipStream_t s);
+
 // Joins a piece's statistics into each row's running ones and, after the last piece, forms lse and loss.
 struct LossFinishArgs {
   const float* stats;
@@ -61,6 +66,10 @@ struct LossFinishArgs {
   float* lse;
 };
 hipError_t launch_loss_finish(const LossFinishArgs& a, hipStream_t s);
+
+// Few rows' lse and loss from their logits in one launch: a workgroup a row, up to kFewClasses classes.
+constexpr int64_t kFewClasses = 32768;
+hipError_t launch_loss_few_rows(const LossForwardArgs& a, const LossFinishArgs& f, hipStream_t s);
 
 // Target weights from a teacher's logits: softmax(teacher / T) over a row's classes, equal classes' in the first.
 constexpr int64_t kMostListed = 1024;

@@ -366,6 +366,64 @@ __global__ __launch_bounds__(kThreads, TILE > 128 ? 1 : 2) void loss_forward(Los
   loss_tile<T, TILE>(a.product, ring, StatsEnd{a});
 }
 
+// t of up to four neighbouring classes of a row of logits in memory (the parts of a split product, which it adds).
+__device__ __forceinline__ f32x4 few_logits(const LossForwardArgs& a, int64_t i, int64_t j, int count) {
+  const ProductArgs& p = a.product;
+  const float none = -__builtin_inff();
+  if (count <= 0) return f32x4{none, none, none, none};
+  const float* z = p.partial + i * p.n + j;
+  f32x4 t = load4<float>(z, count);
+  for (int q = 1; q < p.splits; ++q) t += load4<float>(z + q * p.m * p.n, count);
+  const f32x4 b = a.bias ? load4<float>(a.bias + j, count) * a.inv_temperature : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int e = 0; e < 4; ++e) t[e] = e < count ? fmaf(t[e], a.inv_temperature, b[e]) : none;
+  return t;
+}
+
+__device__ __forceinline__ float wave_max(float x) {
+#pragma unroll
+  for (int by = 1; by < 16; by *= 2) x = fmaxf(x, __shfl_xor(x, by));
+  return max_xor32(max_xor16(x));
+}
+
+// A workgroup takes 4096 classes of a row; its largest t and sum through LDS.
+__global__ __launch_bounds__(256) void loss_few(LossForwardArgs a) {
+  __shared__ float tops[4], sums[4];
+  constexpr int kQuads = kFewChunk / 4 / 256;
+  const ProductArgs& p = a.product;
+  const int64_t i = blockIdx.y, j0 = (int64_t)blockIdx.x * kFewChunk;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  f32x4 t[kQuads];
+  float top = -__builtin_inff(), sum = 0.0f;
+#pragma unroll
+  for (int q = 0; q < kQuads; ++q) {
+    const int64_t j = j0 + (q * 256 + threadIdx.x) * 4;
+    t[q] = few_logits(a, i, j, p.n - j >= 4 ? 4 : (int)(p.n > j ? p.n - j : 0));
+  }
+#pragma unroll
+  for (int q = 0; q < kQuads; ++q)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) top = fmaxf(top, t[q][e]);
+  top = wave_max(top);
+  if (lane == 0) tops[wave] = top;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 4; ++w) top = fmaxf(top, tops[w]);
+  const float from = top == -__builtin_inff() ? 0.0f : top;
+#pragma unroll
+  for (int q = 0; q < kQuads; ++q)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) sum += fast_exp(t[q][e] - from);
+  sum = group_sum(sum, 64);
+  if (lane == 0) sums[wave] = sum;
+  __syncthreads();
+  if (threadIdx.x == 0) *reinterpret_cast<f32x2*>(a.stats + ((int64_t)blockIdx.x * p.m + i) * 2) = f32x2{top, sums[0] + sums[1] + sums[2] + sums[3]};
+  for (int e = threadIdx.x; e < a.list.per_row; e += 256) {
+    const int64_t c = class_at(a.list, i, e) - a.first_class;
+    if (c >= j0 && c < j0 + kFewChunk && c < p.n) a.listed[i * a.list.per_row + e] = few_logits(a, i, c, 1)[0];
+  }
+}
+
 template <typename T, int TILE>
 __global__ __launch_bounds__(kThreads, TILE > 128 ? 1 : 2) void loss_gradient(LossGradientArgs a) {
   __shared__ __align__(1024) uint8_t ring[ring_bytes(TILE)];
@@ -447,6 +505,66 @@ __global__ __launch_bounds__(16 * kSlots) void loss_finish(LossFinishArgs a) {
     a.loss[i] = y < 0 ? 0.0f : y < a.n ? lse - a.listed[i] : __builtin_nanf("");
   }
   a.lse[i] = lse;
+}
+
+// A workgroup of 1024 a row: each thread keeps the largest t and the sum of its classes, those join through LDS. (Statistics
+// and loss in launches of their own took 3 us more of 13 rows.)
+__global__ __launch_bounds__(1024) void loss_few_rows(LossForwardArgs a, LossFinishArgs f) {
+  __shared__ float tops[16], sums[16], terms[16];
+  constexpr int kQuads = 4;
+  const int64_t i = blockIdx.x, n = a.product.n;
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  float top = -__builtin_inff(), sum = 0.0f;
+  for (int64_t j0 = threadIdx.x * 4; j0 < n; j0 += kQuads * 4096) {
+    f32x4 t[kQuads];
+#pragma unroll
+    for (int q = 0; q < kQuads; ++q) {
+      const int64_t j = j0 + q * 4096;
+      t[q] = few_logits(a, i, j, n - j >= 4 ? 4 : (int)(n > j ? n - j : 0));
+    }
+    float largest = t[0][0];
+#pragma unroll
+    for (int q = 0; q < kQuads; ++q)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) largest = fmaxf(largest, t[q][e]);
+    const float from = largest == -__builtin_inff() ? 0.0f : largest;
+    float s = 0.0f;
+#pragma unroll
+    for (int q = 0; q < kQuads; ++q)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s += fast_exp(t[q][e] - from);
+    join_stats(&top, &sum, largest, s);
+  }
+  const float wave_top = wave_max(top), from = wave_top == -__builtin_inff() ? 0.0f : wave_top;
+  sum = group_sum(sum * fast_exp(top - from), 64);
+  if (lane == 0) {
+    tops[wave] = wave_top;
+    sums[wave] = sum;
+  }
+  __syncthreads();
+  top = tops[0];
+  sum = sums[0];
+  for (int w = 1; w < 16; ++w) join_stats(&top, &sum, tops[w], sums[w]);
+  const float lse = top + logf(sum);
+  float loss = 0.0f;
+  if (f.weights) {
+    for (int e = threadIdx.x; e < f.list.per_row; e += 1024) {
+      const float w = f.weights[i * f.list.per_row + e];
+      const int64_t c = class_at(f.list, i, e);
+      if (w != 0.0f) loss += w * (logf(w) - (c >= 0 && c < n ? few_logits(a, i, c, 1)[0] : 0.0f) + lse);
+    }
+    loss = group_sum(loss, 64);
+    if (lane == 0) terms[wave] = loss;
+    __syncthreads();
+    loss = terms[0];
+    for (int w = 1; w < 16; ++w) loss += terms[w];
+  } else if (threadIdx.x == 0) {
+    const int64_t y = class_at(f.list, i, 0);
+    loss = y < 0 ? 0.0f : y < n ? lse - few_logits(a, i, y, 1)[0] : __builtin_nanf("");
+  }
+  if (threadIdx.x != 0) return;
+  f.loss[i] = loss;
+  f.lse[i] = lse;
 }
 
 // A wavefront a row.
@@ -578,6 +696,17 @@ hipError_t launch_loss_gradient(const LossGradientArgs& a, hipStream_t s) {
   if (a.product.type == kBf16) gradient_type<__bf16>(a, s);
   else if (a.product.type == kF16) gradient_type<_Float16>(a, s);
   else gradient_type<float>(a, s);
+  return hipGetLastError();
+}
+
+hipError_t launch_loss_few(const LossForwardArgs& a, hipStream_t s) {
+  const dim3 grid((unsigned)((a.product.n + kFewChunk - 1) / kFewChunk), (unsigned)a.product.m);
+  loss_few<<<grid, 256, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+hipError_t launch_loss_few_rows(const LossForwardArgs& a, const LossFinishArgs& f, hipStream_t s) {
+  loss_few_rows<<<(unsigned)a.product.m, 1024, 0, s>>>(a, f);
   return hipGetLastError();
 }
 
