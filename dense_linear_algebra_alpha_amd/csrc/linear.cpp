@@ -150,6 +150,7 @@ ProductPlan xtvxy::plan_product(int type, int64_t m, int64_t n, int64_t k, bool 
         if (least == 0 || us < least) {
           least = us;
           best = p;
+          best.us = us;
         }
       }
     }
@@ -187,6 +188,7 @@ void xtvxy::plan_gradient(int type, int64_t m, int64_t k, int64_t n, bool want_d
             least = us;
             *dx = want_dx ? px : ProductPlan{};
             *dw = want_dw ? pw : ProductPlan{};
+            dx->us = dw->us = us;
           }
         }
       }

@@ -16,6 +16,7 @@ struct ProductPlan {
   int tile = 0;  // 0: the kernel for any alignment; 64, 128, 256: the ring kernel's tile
   int64_t whole = 0, splits = 1, k_per_split = 0;
   size_t bytes = 0;  // partial sums
+  double us = 0;     // estimated time of the launch (of a gradient's two products together)
 };
 
 // Plans of the shapes of a thread's latest calls. The search takes 1.2 us for a layer (15 at most over 600 shapes)

@@ -16,8 +16,12 @@ namespace {
 
 // Most bytes of a piece's d, and of the statistics or copies of a piece's forward pass. Pieces of fewer classes
 // than kLeastPiece would leave the products of the gradient without depth.
-constexpr int64_t kPieceBytes = (int64_t)1 << 28;
+constexpr int64_t kPieceBytes = (int64_t)1 << 29;
 constexpr int64_t kLeastPiece = 4096;
+// The sum of dX's parts: a launch, and the parts read (4 slices of 67 MB and the result: 86 us).
+constexpr double kFinishUs = 8.0, kPartsBytesPerUs = 3.5e6;
+// What d costs more from memory than from the cache (8192 x 65536 of bf16: 300 us, 4096 x 100000 190).
+constexpr double kCachedBytesPerUs = 4e6;
 
 // Pieces of a vocabulary of n of at most `bytes` with `per_class` of them a class, all of one width but the last.
 int64_t piece_of(int64_t n, int64_t per_class, int64_t most) {
@@ -136,6 +140,22 @@ struct BackwardPlan {
   size_t x_off, w_off, d_off, factor_off, scale_off, sums_off, dx_off, dw_off, order_off, bytes = 0;
 };
 
+// The products of pieces of that many classes.
+void plan_pieces(BackwardPlan* p, int type, int64_t m, int64_t k, int64_t n, int64_t piece, bool want_dx, bool want_dw) {
+  p->piece = piece;
+  p->pieces = cdiv(n, piece);
+  p->parts = p->pieces > 1;
+  p->ldd = cdiv(piece, 8) * 8;
+  const int64_t last = n - (p->pieces - 1) * piece;
+  p->logits = plan_product(type, m, piece, k, true, false, loss_tile(type, m, piece));
+  p->last_logits = p->parts ? plan_product(type, m, last, k, true, false, p->logits.tile) : p->logits;
+  plan_gradient(type, m, k, piece, want_dx, want_dw, true, &p->dx, &p->dw, 0, p->parts);
+  p->last_dx = p->dx;
+  p->last_dw = p->dw;
+  const int tile = want_dx ? p->dx.tile : p->dw.tile;
+  if (p->parts && (want_dx || want_dw)) plan_gradient(type, m, k, last, want_dx, want_dw, true, &p->last_dx, &p->last_dw, tile, true);
+}
+
 BackwardPlan make_backward_plan(int type, int64_t m, int64_t k, int64_t n, int64_t per_row, bool x_whole, bool w_whole, bool want_dx, bool want_dw) {
   BackwardPlan p;
   const int es = elem_size(type);
@@ -143,18 +163,30 @@ BackwardPlan make_backward_plan(int type, int64_t m, int64_t k, int64_t n, int64
   want_dw = want_dw && k > 0;
   p.pack_x = !x_whole;
   p.pack_w = !w_whole;
-  p.piece = piece_of(n, m * es + (p.pack_w ? padded(k, es) * es : 0), most_classes(m, k, es));
-  p.pieces = cdiv(n, p.piece);
-  p.parts = p.pieces > 1;
-  p.ldd = cdiv(p.piece, 8) * 8;
-  const int64_t last = n - (p.pieces - 1) * p.piece;
-  p.logits = plan_product(type, m, p.piece, k, true, false, loss_tile(type, m, p.piece));
-  p.last_logits = p.parts ? plan_product(type, m, last, k, true, false, p.logits.tile) : p.logits;
-  plan_gradient(type, m, k, p.piece, want_dx, want_dw, true, &p.dx, &p.dw, 0, p.parts);
-  p.last_dx = p.dx;
-  p.last_dw = p.dw;
+  // Of the numbers of pieces that fit, the one with the least estimated time: small ones stay in the cache, and their tiles
+  // may leave CUs without work. (In pieces of up to 128, 256, 512 MiB and 1 GiB, ms with the forward pass: bf16 8192 x
+  // 2048 x 65536 6.65, 6.85, 6.81, 6.83; 4096 x 128 x 100000 1.08, 1.13, 1.23, 1.24; 4096 x 1023 x 30000 1.22, 1.10, 1.12,
+  // 1.13; fp32 4096 x 512 x 50000 6.73, 6.76, 6.24, 6.29.)
+  const int64_t per_class = m * es + (p.pack_w ? padded(k, es) * es : 0), most = most_classes(m, k, es);
+  const int64_t fewest = cdiv(n, piece_of(n, per_class, most));
+  double least = 0;
+  for (int64_t pieces : {fewest, fewest + 1, fewest + 2, fewest + 3, 2 * fewest, 2 * fewest + 1, 3 * fewest, 4 * fewest,
+                         5 * fewest, 8 * fewest}) {
+    const int64_t piece = pieces == 1 ? n : cdiv(cdiv(n, pieces), 256) * 256;
+    if (pieces > fewest && piece < kLeastPiece) continue;
+    BackwardPlan q = p;
+    plan_pieces(&q, type, m, k, n, piece, want_dx, want_dw);
+    const double slices = q.parts && want_dx ? (q.pieces - 1) * q.dx.splits + q.last_dx.splits : 0;
+    // d of more than 128 MiB leaves the cache between its kernel and the products
+    const double size = (double)m * piece * es, out = std::min(1.0, std::max(0.0, size / ((int64_t)1 << 27) - 1.0));
+    const double us = out * m * n * es / kCachedBytesPerUs + (q.pieces - 1) * (q.logits.us + q.dx.us) + q.last_logits.us + q.last_dx.us + 6.0 * q.pieces +
+                      (slices > 0 ? kFinishUs + slices * m * k * 4 / kPartsBytesPerUs : 0.0);
+    if (least == 0 || us < least) {
+      least = us;
+      p = q;
+    }
+  }
   const int tile = want_dx ? p.dx.tile : p.dw.tile;
-  if (p.parts && (want_dx || want_dw)) plan_gradient(type, m, k, last, want_dx, want_dw, true, &p.last_dx, &p.last_dw, tile, true);
   size_t dx_bytes = p.dx.bytes;
   if (p.parts && want_dx) {  // dX's sums over the pieces join in the end
     p.dx.whole = p.last_dx.whole = 0;
