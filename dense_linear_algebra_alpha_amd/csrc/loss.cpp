@@ -135,6 +135,7 @@ const ForwardPlan& plan_forward(int type, int64_t m, int64_t k, int64_t n, int64
 struct BackwardPlan {
   bool pack_x, pack_w, parts;
   int64_t piece, pieces, ldd;
+  int64_t slice = 0, slices = 0;  // floats of a part of dX, parts that there is room for
   ProductPlan logits, last_logits, dx, dw, last_dx, last_dw;
   OrderPlan order;
   size_t x_off, w_off, d_off, factor_off, scale_off, sums_off, dx_off, dw_off, order_off, bytes = 0;
@@ -188,9 +189,12 @@ BackwardPlan make_backward_plan(int type, int64_t m, int64_t k, int64_t n, int64
   }
   const int tile = want_dx ? p.dx.tile : p.dw.tile;
   size_t dx_bytes = p.dx.bytes;
-  if (p.parts && want_dx) {  // dX's sums over the pieces join in the end
+  if (p.parts && want_dx) {  // dX's sums over the pieces join in the end, or whenever they fill their place
     p.dx.whole = p.last_dx.whole = 0;
-    dx_bytes = (size_t)((p.pieces - 1) * p.dx.splits + p.last_dx.splits) * cdiv(m, tile) * cdiv(k, tile) * tile * tile * 4;
+    p.slice = cdiv(m, tile) * cdiv(k, tile) * tile * tile;
+    const int64_t all = (p.pieces - 1) * p.dx.splits + p.last_dx.splits, more = std::max(p.dx.splits, p.last_dx.splits);
+    p.slices = std::min(all, std::max(more + 1, kPieceBytes / (p.slice * 4)));
+    dx_bytes = (size_t)p.slices * p.slice * 4;
   }
   const auto take = [&](bool want, size_t bytes) {
     const size_t at = p.bytes;
@@ -481,9 +485,13 @@ xtvxy_status backward_impl(const Layer& l, const float* grad, const ClassList& l
     take_plan(&piece.dw, dw, base + p.dw_off);
     const int tile = g.dx.m > 0 ? dx.tile : dw.tile;
     if (p.parts && g.dx.m > 0) {
+      if (slices + dx.splits > p.slices) {
+        if (launch_sum_slices(reinterpret_cast<float*>(base + p.dx_off), slices, p.slice, stream) != hipSuccess) return XTVXY_ERROR_LAUNCH;
+        slices = 1;
+      }
       piece.dx.in_parts = 1;
       piece.dx.whole = 0;
-      piece.dx.partial += slices * piece.dx.tiles() * tile * tile;
+      piece.dx.partial += slices * p.slice;
       slices += dx.splits;
     }
     piece.dw_first = m > classes;

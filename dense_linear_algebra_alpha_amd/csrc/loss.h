@@ -116,4 +116,7 @@ struct LossGradientArgs {
 };
 hipError_t launch_loss_gradient(const LossGradientArgs& a, hipStream_t s);
 
+// slices[0] = the sum of `count` slices of `elements` floats (a multiple of 4) in their order.
+hipError_t launch_sum_slices(float* slices, int64_t count, int64_t elements, hipStream_t s);
+
 }  // namespace xtvxy

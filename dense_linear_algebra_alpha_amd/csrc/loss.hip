@@ -657,6 +657,16 @@ __global__ __launch_bounds__(1024) void loss_scale(LossFactorArgs a) {
   a.scale[1] = ldexpf(1.0f, -e);
 }
 
+__global__ __launch_bounds__(256) void sum_slices(float* slices, int64_t count, int64_t quads) {
+  for (int64_t q = (int64_t)blockIdx.x * 256 + threadIdx.x; q < quads; q += (int64_t)gridDim.x * 256) {
+    f32x4* p = reinterpret_cast<f32x4*>(slices) + q;
+    f32x4 s = p[0];
+#pragma unroll 4
+    for (int64_t c = 1; c < count; ++c) s += p[c * quads];
+    p[0] = s;
+  }
+}
+
 template <typename T>
 void forward_type(const LossForwardArgs& a, hipStream_t s) {
   const uint32_t groups = (uint32_t)a.product.tiles();
@@ -717,6 +727,12 @@ hipError_t launch_list_order(const OrderArgs& a, hipStream_t s) {
 
 hipError_t launch_loss_finish(const LossFinishArgs& a, hipStream_t s) {
   loss_finish<<<(unsigned)((a.m + 15) / 16), 16 * kSlots, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+hipError_t launch_sum_slices(float* slices, int64_t count, int64_t elements, hipStream_t s) {
+  const int64_t groups = (elements / 4 + 255) / 256;
+  sum_slices<<<(unsigned)(groups < 65536 ? groups : 65536), 256, 0, s>>>(slices, count, elements / 4);
   return hipGetLastError();
 }
 

@@ -121,6 +121,21 @@ def test_several_pieces_of_the_vocabulary(dtype, k):
     check_all(only, ref, dtype + " alone")
 
 
+def test_parts_of_dx_joined_on_the_way():
+    """More pieces of the vocabulary than there is room for their parts of dX."""
+    m, k, n = 65536, 1024, 13_000
+    X, W, b, labels, grad = cuda(*inputs(m, k, n, torch.bfloat16, 15))
+    note("parts of dX")
+    # four pieces, each a part of 268 MB at least, and d of one
+    assert xt.xtvxy_linear_cross_entropy_backward_bf16_workspace_size(m, k, n) < 4 * m * k * 4
+    _, lse = xt.linear_cross_entropy(X, W, labels, b)
+    dX, _, _ = xt.linear_cross_entropy_backward(grad, X, W, labels, lse, b)
+    torch.cuda.synchronize()
+    rows = torch.arange(0, m, 131, device=dev())
+    ref = O.backward(grad[rows], X[rows], W, b, *O.of_labels(labels[rows]), lse=lse[rows])
+    L.check(dX[rows], *ref["dX"], what="dX")
+
+
 def test_many_rows_in_the_forward_pass():
     """Statistics in pieces of the vocabulary: rows x classes beyond what is kept at once."""
     m, k, n = 300_000, 8, 10_000
