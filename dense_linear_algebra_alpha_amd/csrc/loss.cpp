@@ -18,6 +18,7 @@ namespace {
 // than kLeastPiece would leave the products of the gradient without depth.
 constexpr int64_t kPieceBytes = (int64_t)1 << 29;
 constexpr int64_t kLeastPiece = 4096;
+constexpr double kMemoryUs = 8.0;  // what logits in memory cost besides their product
 // The sum of dX's parts: a launch, and the parts read (4 slices of 67 MB and the result: 86 us).
 constexpr double kFinishUs = 8.0, kPartsBytesPerUs = 3.5e6;
 // What d costs more from memory than from the cache (8192 x 65536 of bf16: 300 us, 4096 x 100000 190).
@@ -75,12 +76,29 @@ hipError_t order_lists(const OrderPlan& p, const ClassList& list, const float* w
 // than those of 64. us: 64 x 1024 x 131072 67, 84; 33 x 3500 x 20000 89, 91; fp32, bound by the matrix unit, 129, 82.
 int loss_tile(int type, int64_t m, int64_t n) { return type != kF32 && m <= 64 && n >= 128 * kComputeUnits / 2 ? 128 : 0; }
 
+// Few tiles over a long contraction: their products are split over it, and the logits' parts joined in memory, where that
+// pays in spite of the launches more. us, with their gradient: fp32 924 x 4072 x 144 184 to 87, 93 x 1415 x 105 77 to 49;
+// bf16 500 x 4096 x 300 56 to 44.
+struct MemoryPlan {
+  ProductPlan product;
+  size_t parts_off = 0, logits_off = 0;
+  bool used = false;
+};
+MemoryPlan plan_memory(int type, int64_t m, int64_t k, int64_t n, const ProductPlan& tiles) {
+  MemoryPlan p;
+  if (n > kFewClasses || m * n * 4 > kPieceBytes / 4) return p;
+  p.product = plan_product(type, m, n, k, true);
+  p.used = p.product.splits > 1 && p.product.us + kMemoryUs < tiles.us;
+  return p;
+}
+
 struct ForwardPlan {
   bool pack_x, pack_w;
   int64_t piece;
   ProductPlan whole, last;  // of a piece, of the last one
   int64_t parts;            // halves of tiles' columns of a piece
   OrderPlan order;
+  MemoryPlan memory;
   FewPlan few;              // of few rows: their products go through the workspace, whatever the operands' alignment
   size_t x_off, w_off, stats_off, run_off, listed_off, order_off, logits_off, bytes = 0;
 };
@@ -116,13 +134,16 @@ ForwardPlan make_forward_plan(int type, int64_t m, int64_t k, int64_t n, int64_t
   const int64_t last = n - (cdiv(n, std::max<int64_t>(p.piece, 1)) - 1) * p.piece;
   p.last = p.piece == n ? p.whole : plan_product(type, m, last, k, true, false, p.whole.tile);
   p.parts = 2 * cdiv(p.piece, p.whole.tile);
+  if (p.piece == n) p.memory = plan_memory(type, m, k, n, p.whole);
   p.x_off = take(p.pack_x, packed_bytes(m, k, es));
   p.w_off = take(p.pack_w, packed_bytes(p.piece, k, es));
   p.stats_off = take(true, (size_t)p.parts * m * 8);
   p.run_off = take(p.piece < n, (size_t)m * 8);
   p.listed_off = take(true, (size_t)m * per_row * 4);
-  p.order = plan_order(m, n, per_row, p.whole.tile);
+  if (!p.memory.used) p.order = plan_order(m, n, per_row, p.whole.tile);
   p.order_off = take(true, p.order.bytes);
+  p.memory.parts_off = take(p.memory.used, p.memory.product.bytes);
+  p.memory.logits_off = take(p.memory.used, (size_t)m * n * 4);
   return p;
 }
 
@@ -138,6 +159,7 @@ struct BackwardPlan {
   int64_t slice = 0, slices = 0;  // floats of a part of dX, parts that there is room for
   ProductPlan logits, last_logits, dx, dw, last_dx, last_dw;
   OrderPlan order;
+  MemoryPlan memory;
   size_t x_off, w_off, d_off, factor_off, scale_off, sums_off, dx_off, dw_off, order_off, bytes = 0;
 };
 
@@ -206,12 +228,15 @@ BackwardPlan make_backward_plan(int type, int64_t m, int64_t k, int64_t n, int64
   p.d_off = take(want_dx || want_dw, (size_t)m * p.ldd * es);
   p.factor_off = take(true, (size_t)m * 4);
   p.scale_off = take(type == kF16, 8);
-  const int64_t rows = std::max(cdiv(m, p.logits.tile), cdiv(m, p.last_logits.tile)) * 2;
+  if (!p.parts) p.memory = plan_memory(type, m, k, n, p.logits);
+  const int64_t rows = p.memory.used ? cdiv(m, kMemoryRows) : cdiv(m, p.logits.tile) * 2;
   p.sums_off = take(true, (size_t)rows * p.piece * 4);
   p.dx_off = take(want_dx, dx_bytes);
   p.dw_off = take(want_dw, std::max(p.dw.bytes, p.last_dw.bytes));
-  p.order = plan_order(m, n, per_row, p.logits.tile);
+  if (!p.memory.used) p.order = plan_order(m, n, per_row, p.logits.tile);
   p.order_off = take(true, p.order.bytes);
+  p.memory.parts_off = take(p.memory.used, p.memory.product.bytes);
+  p.memory.logits_off = take(p.memory.used, (size_t)m * n * 4);
   return p;
 }
 
@@ -322,6 +347,21 @@ hipError_t pack_operands(const Layer& l, bool pack_x, bool pack_w, void* x_copy,
   return pack.jobs > 0 && l.k > 0 ? launch_pack(pack, l.type, s) : hipSuccess;
 }
 
+// The logits of one piece as fp32 in memory, which `a` has as its one part then.
+hipError_t logits_in_memory(ProductArgs* a, const MemoryPlan& p, char* base, hipStream_t s) {
+  take_plan(a, p.product, base + p.parts_off);
+  hipError_t e = launch_layer_ring(*a, s);
+  if (e != hipSuccess) return e;
+  float* logits = reinterpret_cast<float*>(base + p.logits_off);
+  ProductArgs sum = *a;
+  sum.type = kF32;  // of what is written; the parts are fp32 in any case
+  sum.e = {nullptr, nullptr, 0, nullptr, 0, logits, a->n, XTVXY_ACT_NONE};
+  e = launch_product_finish(sum, s);
+  a->partial = logits;
+  a->splits = 1;
+  return e;
+}
+
 // A teacher's logits; labels: teacher null.
 struct Teacher {
   const void* logits;
@@ -381,6 +421,7 @@ xtvxy_status forward_impl(const Layer& l, const ClassList& list, const Teacher* 
       a.product.in_parts = 1;
       if (launch_product_few(a.product, p.few.waves, p.few.outputs, stream) != hipSuccess) return XTVXY_ERROR_LAUNCH;
     }
+    if (p.memory.used && logits_in_memory(&a.product, p.memory, base, stream) != hipSuccess) return XTVXY_ERROR_LAUNCH;
     a.bias = l.bias ? l.bias + j : nullptr;
     a.inv_temperature = inv_temperature;
     a.first_class = j;
@@ -388,7 +429,7 @@ xtvxy_status forward_impl(const Layer& l, const ClassList& list, const Teacher* 
     a.order = order;
     a.listed = reinterpret_cast<float*>(base + p.listed_off);
     a.stats = stats;
-    if (p.few.waves > 0 && f.first && f.last && n <= kFewClasses) return status_of(launch_loss_few_rows(a, f, stream));
+    if (p.memory.used || (p.few.waves > 0 && f.first && f.last && n <= kFewClasses)) return status_of(launch_loss_few_rows(a, f, stream));
     if ((p.few.waves > 0 ? launch_loss_few(a, stream) : launch_loss_forward(a, stream)) != hipSuccess) return XTVXY_ERROR_LAUNCH;
     f.parts = p.few.waves > 0 ? cdiv(classes, kFewChunk) : 2 * cdiv(classes, a.product.tile);
     if (launch_loss_finish(f, stream) != hipSuccess) return XTVXY_ERROR_LAUNCH;
@@ -466,7 +507,14 @@ xtvxy_status backward_impl(const Layer& l, const float* grad, const ClassList& l
     a.d = products ? base + p.d_off : nullptr;
     a.ldd = cdiv(classes, 8) * 8;
     a.sums = o.db ? reinterpret_cast<float*>(base + p.sums_off) : nullptr;
-    if (launch_loss_gradient(a, stream) != hipSuccess) return XTVXY_ERROR_LAUNCH;
+    int64_t sum_rows = 2 * cdiv(m, a.product.tile);
+    if (p.memory.used) {
+      if (logits_in_memory(&a.product, p.memory, base, stream) != hipSuccess) return XTVXY_ERROR_LAUNCH;
+      if (launch_loss_gradient_memory(a, stream) != hipSuccess) return XTVXY_ERROR_LAUNCH;
+      sum_rows = cdiv(m, kMemoryRows);
+    } else if (launch_loss_gradient(a, stream) != hipSuccess) {
+      return XTVXY_ERROR_LAUNCH;
+    }
 
     GradientArgs piece = g;
     const ProductPlan &dx = last ? p.last_dx : p.dx, &dw = last ? p.last_dw : p.dw;
@@ -498,7 +546,7 @@ xtvxy_status backward_impl(const Layer& l, const float* grad, const ClassList& l
     piece.n = classes;
     piece.db = o.db ? o.db + j : nullptr;
     piece.sums = a.sums;
-    piece.sum_rows = 2 * cdiv(m, a.product.tile);
+    piece.sum_rows = sum_rows;
     if (launch_gradient_ring(piece, l.type, tile, stream) != hipSuccess) return XTVXY_ERROR_LAUNCH;
     piece.db = nullptr;
     if (p.parts && g.dx.m > 0) {  // all pieces' parts at once, after the last

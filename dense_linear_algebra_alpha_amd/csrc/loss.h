@@ -71,6 +71,12 @@ hipError_t launch_loss_finish(const LossFinishArgs& a, hipStream_t s);
 constexpr int64_t kFewClasses = 32768;
 hipError_t launch_loss_few_rows(const LossForwardArgs& a, const LossFinishArgs& f, hipStream_t s);
 
+// d from a product's logits in memory (product.partial: [m][n], one part), as launch_loss_gradient's; column sums of every
+// kMemoryRows rows.
+constexpr int64_t kMemoryRows = 8;
+struct LossGradientArgs;
+hipError_t launch_loss_gradient_memory(const LossGradientArgs& a, hipStream_t s);
+
 // Target weights from a teacher's logits: softmax(teacher / T) over a row's classes, equal classes' in the first.
 constexpr int64_t kMostListed = 1024;
 struct TeacherArgs {

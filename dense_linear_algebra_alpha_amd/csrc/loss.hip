@@ -507,19 +507,21 @@ __global__ __launch_bounds__(16 * kSlots) void loss_finish(LossFinishArgs a) {
   a.lse[i] = lse;
 }
 
-// A workgroup of 1024 a row: each thread keeps the largest t and the sum of its classes, those join through LDS. (Statistics
+// A workgroup of kRowThreads a row: each thread keeps the largest t and the sum of its classes, those join through LDS. (Statistics
 // and loss in launches of their own took 3 us more of 13 rows.)
-__global__ __launch_bounds__(1024) void loss_few_rows(LossForwardArgs a, LossFinishArgs f) {
-  __shared__ float tops[16], sums[16], terms[16];
+template <int kRowThreads>
+__global__ __launch_bounds__(kRowThreads) void loss_few_rows(LossForwardArgs a, LossFinishArgs f) {
+  constexpr int kRowWaves = kRowThreads / 64;
+  __shared__ float tops[kRowWaves], sums[kRowWaves], terms[kRowWaves];
   constexpr int kQuads = 4;
   const int64_t i = blockIdx.x, n = a.product.n;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   float top = -__builtin_inff(), sum = 0.0f;
-  for (int64_t j0 = threadIdx.x * 4; j0 < n; j0 += kQuads * 4096) {
+  for (int64_t j0 = threadIdx.x * 4; j0 < n; j0 += kQuads * 4 * kRowThreads) {
     f32x4 t[kQuads];
 #pragma unroll
     for (int q = 0; q < kQuads; ++q) {
-      const int64_t j = j0 + q * 4096;
+      const int64_t j = j0 + q * 4 * kRowThreads;
       t[q] = few_logits(a, i, j, n - j >= 4 ? 4 : (int)(n > j ? n - j : 0));
     }
     float largest = t[0][0];
@@ -544,11 +546,11 @@ __global__ __launch_bounds__(1024) void loss_few_rows(LossForwardArgs a, LossFin
   __syncthreads();
   top = tops[0];
   sum = sums[0];
-  for (int w = 1; w < 16; ++w) join_stats(&top, &sum, tops[w], sums[w]);
+  for (int w = 1; w < kRowWaves; ++w) join_stats(&top, &sum, tops[w], sums[w]);
   const float lse = top + logf(sum);
   float loss = 0.0f;
   if (f.weights) {
-    for (int e = threadIdx.x; e < f.list.per_row; e += 1024) {
+    for (int e = threadIdx.x; e < f.list.per_row; e += kRowThreads) {
       const float w = f.weights[i * f.list.per_row + e];
       const int64_t c = class_at(f.list, i, e);
       if (w != 0.0f) loss += w * (logf(w) - (c >= 0 && c < n ? few_logits(a, i, c, 1)[0] : 0.0f) + lse);
@@ -557,7 +559,7 @@ __global__ __launch_bounds__(1024) void loss_few_rows(LossForwardArgs a, LossFin
     if (lane == 0) terms[wave] = loss;
     __syncthreads();
     loss = terms[0];
-    for (int w = 1; w < 16; ++w) loss += terms[w];
+    for (int w = 1; w < kRowWaves; ++w) loss += terms[w];
   } else if (threadIdx.x == 0) {
     const int64_t y = class_at(f.list, i, 0);
     loss = y < 0 ? 0.0f : y < n ? lse - few_logits(a, i, y, 1)[0] : __builtin_nanf("");
@@ -565,6 +567,46 @@ __global__ __launch_bounds__(1024) void loss_few_rows(LossForwardArgs a, LossFin
   if (threadIdx.x != 0) return;
   f.loss[i] = loss;
   f.lse[i] = lse;
+}
+
+// Four columns a thread over eight rows; a row's listed classes are looked through for each.
+template <typename T>
+__global__ __launch_bounds__(256) void loss_gradient_memory(LossGradientArgs a) {
+  const ProductArgs& p = a.product;
+  const int64_t j = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4, i0 = (int64_t)blockIdx.y * kMemoryRows;
+  if (j >= a.ldd) return;
+  const int64_t i1 = i0 + kMemoryRows < p.m ? i0 + kMemoryRows : p.m;
+  const int count = p.n - j >= 4 ? 4 : p.n > j ? (int)(p.n - j) : 0;
+  constexpr bool kScaled = __is_same(T, _Float16);
+  const float scale = kScaled ? *a.scale : 1.0f;
+  f32x4 bias = {0.0f, 0.0f, 0.0f, 0.0f}, sum = bias;
+  if (a.bias && count > 0) bias = load4<float>(a.bias + j, count) * a.inv_temperature;
+#pragma unroll 2
+  for (int64_t i = i0; i < i1; ++i) {
+    const float factor = a.factor[i], lse = a.lse[i];
+    f32x4 d = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (factor != 0.0f && count > 0) {
+      const f32x4 z = load4<float>(p.partial + i * p.n + j, count);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) d[e] = e < count ? factor * fast_exp(fmaf(z[e], a.inv_temperature, bias[e]) - lse) : 0.0f;
+      for (int l = 0; l < a.list.per_row; ++l) {
+        const int64_t c = class_at(a.list, i, l) - j;
+        if (c < 0 || c >= count) continue;
+        const float w = a.weights ? a.weights[i * a.list.per_row + l] : 1.0f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (e == c && w != 0.0f) d[e] -= factor * w;
+      }
+    }
+    sum += d;
+    if (a.d) {
+      typename Vec<T>::x4 o;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[e] = (T)(kScaled ? d[e] * scale : d[e]);
+      *reinterpret_cast<typename Vec<T>::x4*>(static_cast<T*>(a.d) + i * a.ldd + j) = o;
+    }
+  }
+  if (a.sums && count > 0) store4<float>(a.sums + (int64_t)blockIdx.y * p.n + j, sum, count);
 }
 
 // A wavefront a row.
@@ -716,7 +758,17 @@ hipError_t launch_loss_few(const LossForwardArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_loss_few_rows(const LossForwardArgs& a, const LossFinishArgs& f, hipStream_t s) {
-  loss_few_rows<<<(unsigned)a.product.m, 1024, 0, s>>>(a, f);
+  if (a.product.n > 4096) loss_few_rows<1024><<<(unsigned)a.product.m, 1024, 0, s>>>(a, f);
+  else if (a.product.n > 256) loss_few_rows<256><<<(unsigned)a.product.m, 256, 0, s>>>(a, f);
+  else loss_few_rows<64><<<(unsigned)a.product.m, 64, 0, s>>>(a, f);
+  return hipGetLastError();
+}
+
+hipError_t launch_loss_gradient_memory(const LossGradientArgs& a, hipStream_t s) {
+  const dim3 grid((unsigned)((a.ldd / 4 + 255) / 256), (unsigned)((a.product.m + kMemoryRows - 1) / kMemoryRows));
+  if (a.product.type == kBf16) loss_gradient_memory<__bf16><<<grid, 256, 0, s>>>(a);
+  else if (a.product.type == kF16) loss_gradient_memory<_Float16><<<grid, 256, 0, s>>>(a);
+  else loss_gradient_memory<float><<<grid, 256, 0, s>>>(a);
   return hipGetLastError();
 }
 

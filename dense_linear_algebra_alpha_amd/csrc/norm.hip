@@ -23,6 +23,18 @@ namespace {
 template <typename T>
 constexpr int kChunkOf = 16 / sizeof(T);  // elements of a chunk
 
+typedef u32x4 unaligned_chunk __attribute__((aligned(2)));
+constexpr int64_t kL2Bytes = 32 << 20;  // of the eight XCDs
+
+// kStreamed: past the L2s, for outputs that do not fit there.
+template <bool kStreamed, typename T, int V>
+__device__ __forceinline__ void store_chunk(T* p, const T (&o)[V]) {
+  u32x4 v;
+  __builtin_memcpy(&v, o, 16);
+  if (kStreamed) __builtin_nontemporal_store(v, reinterpret_cast<unaligned_chunk*>(p));
+  else __builtin_memcpy(p, &v, 16);
+}
+
 // The chunks of a row that a thread owns: chunk c begins at column at[c]; the first skip[c] of its elements
 // belong to another chunk (all of them where the chunk is beyond the row).
 template <typename T, int L, int C>
@@ -75,7 +87,7 @@ __device__ __forceinline__ float row_sum(const float* lds, int first) {
 // A row's mean and sum of squared distances from it. Each wavefront forms its own mean first and takes
 // distances from that (no cancellation); the wavefronts' (mean, distances) join as
 //     mean = sum n_w mean_w / n,  sum = sum_w (sum_w + n_w (mean_w - mean)^2).
-template <typename T, int L, int C>
+template <typename T, int L, int C, bool kStreamed>
 __global__ __launch_bounds__(L < 256 ? 256 : L) void norm_rows(NormArgs a) {
   constexpr int V = kChunkOf<T>, kBlock = L < 256 ? 256 : L, kRows = kBlock / L, kWaves = L / 64, kGroup = L < 64 ? L : 64;
   __shared__ float part[2][2][kBlock / 64];
@@ -157,7 +169,7 @@ __global__ __launch_bounds__(L < 256 ? 256 : L) void norm_rows(NormArgs a) {
       T o[V];
 #pragma unroll
       for (int e = 0; e < V; ++e) o[e] = (T)fmaf((x[c][e] - mean) * rstd, w[c][e], b[c][e]);
-      __builtin_memcpy(out + k.at[c], o, 16);
+      store_chunk<kStreamed>(out + k.at[c], o);
     }
   }
 }
@@ -361,18 +373,25 @@ __global__ __launch_bounds__(256) void norm_gradient_finish(NormGradientArgs a) 
 
 constexpr int64_t kMostGroups = 256;  // one workgroup per CU
 
+template <typename T, int L, bool kStreamed>
+void norm_launch(const NormArgs& a, unsigned grid, hipStream_t s) {
+  constexpr int kBlock = L < 256 ? 256 : L;
+  const int64_t chunks = (a.n + kChunkOf<T> - 1) / kChunkOf<T>;
+  if (chunks <= L) norm_rows<T, L, 1, kStreamed><<<grid, kBlock, 0, s>>>(a);
+  else if (chunks <= 2 * L) norm_rows<T, L, 2, kStreamed><<<grid, kBlock, 0, s>>>(a);
+  else norm_rows<T, L, 4, kStreamed><<<grid, kBlock, 0, s>>>(a);
+}
+
+// Workgroups: enough rows under way, few enough that they keep weight and bias. us, with 2, 4 and 8 (of 1024 threads 1, 2, 4)
+// a CU: 16384 x 4096 of bf16 50, 53, 54, streamed 49, 51, 52; 4000 x 16384 51, 53, 58, streamed 49 with 2; one
+// workgroup a row 56, 71. Rows of a wavefront or less: 9.5, 9.2, 9.1 at 40000 x 256.
 template <typename T, int L>
 void norm_for(const NormArgs& a, hipStream_t s) {
-  constexpr int kBlock = L < 256 ? 256 : L, kRows = kBlock / L;
-  const int64_t chunks = (a.n + kChunkOf<T> - 1) / kChunkOf<T>;
-  // workgroups: enough rows under way, few enough that they keep weight and bias: 16384 x 4096 of bf16 with 2, 4 and 8 of
-  // 256 threads a CU 53, 45, 46 us, 4000 x 16384 with 1 and 2 of 1024 threads 47, 48; with one a row 55, 73
-  const int64_t most = kBlock == 256 ? 1024 : 256;
-  const int64_t rows = (a.m + kRows - 1) / kRows;
-  const unsigned grid = (unsigned)(rows < most ? rows : most);
-  if (chunks <= L) norm_rows<T, L, 1><<<grid, kBlock, 0, s>>>(a);
-  else if (chunks <= 2 * L) norm_rows<T, L, 2><<<grid, kBlock, 0, s>>>(a);
-  else norm_rows<T, L, 4><<<grid, kBlock, 0, s>>>(a);
+  constexpr int kRows = L < 256 ? 256 / L : 1;
+  const int64_t most = L < 256 ? 1024 : 512, groups = (a.m + kRows - 1) / kRows;
+  const unsigned grid = (unsigned)(groups < most ? groups : most);
+  if (a.m * a.n * (int64_t)sizeof(T) > kL2Bytes) norm_launch<T, L, true>(a, grid, s);
+  else norm_launch<T, L, false>(a, grid, s);
 }
 
 template <typename T>

@@ -51,7 +51,8 @@ def check_all(got, ref, what):
 
 SIZES = [(1, 1, 1), (3, 5, 2), (2, 8, 1), (17, 33, 65), (64, 64, 64), (65, 129, 70), (1, 256, 1000), (33, 100, 513), (300, 40, 1000),
          (130, 264, 5000), (257, 96, 8200), (5, 1031, 300), (1000, 64, 10), (513, 520, 264), (700, 256, 2500),
-         (1, 4096, 300), (32, 77, 9000), (16, 8200, 200), (33, 96, 17000), (20, 9, 4097)]
+         (1, 4096, 300), (32, 77, 9000), (16, 8200, 200), (33, 96, 17000), (20, 9, 4097),
+         (93, 1415, 105), (200, 4072, 144), (48, 3776, 110), (40, 9000, 600)]
 
 
 @pytest.mark.parametrize("dtype", list(L.DTYPES))
@@ -77,7 +78,7 @@ def test_cross_entropy(size, dtype):
 
 
 @pytest.mark.parametrize("dtype", list(L.DTYPES))
-@pytest.mark.parametrize("size", [(1, 8, 3, 1), (17, 33, 65, 2), (65, 129, 700, 8), (300, 64, 2500, 32), (130, 264, 900, 70), (5, 16, 5000, 1024), (40, 16, 600, 200), (31, 8192, 100, 20)],
+@pytest.mark.parametrize("size", [(1, 8, 3, 1), (17, 33, 65, 2), (65, 129, 700, 8), (300, 64, 2500, 32), (130, 264, 900, 70), (5, 16, 5000, 1024), (40, 16, 600, 200), (31, 8192, 100, 20), (100, 4072, 144, 30), (50, 6000, 5, 4)],
                          ids=lambda s: "%dx%dx%dx%d" % s)
 def test_distillation(size, dtype):
     m, k, n, s = size
