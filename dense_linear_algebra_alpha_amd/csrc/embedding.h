@@ -17,7 +17,7 @@ struct EmbeddingArgs {
 };
 hipError_t launch_embedding(const EmbeddingArgs& a, int type, hipStream_t s);
 
-constexpr int kSortAlone = 1024;        // keys up to which one workgroup sorts
+constexpr int kSortAlone = 4096;        // keys up to which one workgroup sorts
 constexpr int kSortUncounted = 32768;   // up to which its passes do without a launch that counts digits
 constexpr int kCountedTile = 4096;      // keys of a workgroup beyond (1024 up to there)
 constexpr int kDigitBits = 9;        // most bits of their passes
@@ -41,7 +41,7 @@ struct EmbeddingGradientArgs {
   uint32_t* counts;
   float* partial;       // [pieces][2][padded columns]
 };
-inline int64_t sort_groups(int64_t count) { return count <= kSortUncounted ? (count + 1023) / 1024 : (count + kCountedTile - 1) / kCountedTile; }
+inline int64_t sort_groups(int64_t count) { return count <= kSortAlone ? (count > 0) : count <= kSortUncounted ? (count + 1023) / 1024 : (count + kCountedTile - 1) / kCountedTile; }
 inline int64_t slab_columns(int type) { return kSlabBytes / elem_size(type); }
 // Sorted tokens that a wavefront sums: 32, or fewer where that leaves CUs without work (a wavefront loads 8 rows at a
 // time, and each time waits for memory).

@@ -5,7 +5,7 @@
 //
 // The gradient sorts the tokens by their row (a stable radix sort, 9 bits a pass or less), so that each row's sum is
 // taken in the order of the tokens, in fp32, and rounded once: it is bitwise reproducible, and needs no atomics.
-// Up to 1024 tokens one workgroup sorts in LDS. Beyond, each pass
+// Up to 4096 tokens one workgroup sorts in LDS. Beyond, each pass
 // is a launch, beyond 32768 tokens one that counts digits and one that places the tokens. Meanwhile the other CUs
 // write the table's zeros, each launch its share of them.
 // Then a wavefront sums a piece of the sorted tokens over 1 KiB of their columns. A row whose tokens lie within the
@@ -213,27 +213,43 @@ __device__ __forceinline__ void place_digits(SortShared& s, bool alone) {
   __syncthreads();
 }
 
-// All passes in one workgroup: up to 1024 keys. Padding keys are all ones and come last.
+// All passes in one workgroup: up to 1024 kRounds keys. Padding keys are all ones and come last.
+template <int kRounds>
 __global__ __launch_bounds__(kSortThreads) void sort_all(SortArgs a) {
   __shared__ SortShared s;
-  __shared__ uint32_t keys[kSortThreads], from[kSortThreads];
+  __shared__ uint32_t keys[kRounds * kSortThreads], from[kRounds * kSortThreads];
   if ((int)blockIdx.x >= a.groups) return fill_rows(a.fill, blockIdx.x - a.groups, gridDim.x - a.groups);
-  const int i = threadIdx.x, wave = threadIdx.x >> 6;
-  uint32_t key[1] = {i < a.count ? key_of(a, i) : ~0u}, pos = i, rank[1];
-  for (int shift = 0; shift < a.end_bit; shift += a.bits) {
-    rank_keys<1>(s, key, rank, shift, a.bits);
-    place_digits(s, true);
-    const uint32_t digit = (key[0] >> shift) & ((1u << a.bits) - 1);
-    const uint32_t to = s.base[digit] + s.count[wave][digit] + rank[0];
-    keys[to] = key[0];
-    from[to] = pos;
-    __syncthreads();
-    key[0] = keys[i];
-    pos = from[i];
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  const auto item = [&](int r) { return (wave * kRounds + r) * 64 + lane; };
+  uint32_t key[kRounds], pos[kRounds], rank[kRounds];
+#pragma unroll
+  for (int r = 0; r < kRounds; ++r) {
+    pos[r] = item(r);
+    key[r] = item(r) < a.count ? key_of(a, item(r)) : ~0u;
   }
-  if (i < a.count) {
-    a.keys_out[i] = key[0];
-    a.from_out[i] = pos;
+  for (int shift = 0; shift < a.end_bit; shift += a.bits) {
+    rank_keys<kRounds>(s, key, rank, shift, a.bits);
+    place_digits(s, true);
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r) {
+      const uint32_t digit = (key[r] >> shift) & ((1u << a.bits) - 1);
+      const uint32_t to = s.base[digit] + s.count[wave][digit] + rank[r];
+      keys[to] = key[r];
+      from[to] = pos[r];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < kRounds; ++r) {
+      key[r] = keys[item(r)];
+      pos[r] = from[item(r)];
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < kRounds; ++r) {
+    if (item(r) < a.count) {
+      a.keys_out[item(r)] = key[r];
+      a.from_out[item(r)] = pos[r];
+    }
   }
 }
 
@@ -573,7 +589,8 @@ hipError_t launch_embedding_gradient(const EmbeddingGradientArgs& args, int type
     q.keys_out = a.keys[to];
     q.from_out = a.from[to];
     q.shift = pass * q.bits;
-    if (alone) sort_all<<<grid, kSortThreads, 0, s>>>(q);
+    if (alone && a.count <= kSortThreads) sort_all<1><<<grid, kSortThreads, 0, s>>>(q);
+    else if (alone) sort_all<kSortAlone / kSortThreads><<<grid, kSortThreads, 0, s>>>(q);
     else if (!counted) sort_pass<1, false><<<grid, kSortThreads, 0, s>>>(q);
     else if (l % 2 == 0) sort_count<<<grid, kSortThreads, 0, s>>>(q);
     else sort_pass<kCountedTile / kSortThreads, true><<<grid, kSortThreads, 0, s>>>(q);

@@ -38,7 +38,7 @@ def backward(G, ids, rows, scale, before=None):
 
 
 SIZES = [(1, 1, 1), (5, 3, 7), (31, 64, 10), (32, 8, 1), (33, 8, 1), (64, 128, 2), (65, 17, 3), (1000, 100, 37), (100, 1111, 5000),
-         (4096, 260, 50001), (300, 2500, 511), (300, 24, 512), (16384, 64, 3), (16385, 64, 1000), (1024, 64, 1000), (1025, 64, 1000), (65537, 16, 3000), (40000, 72, 70001), (70000, 8, 300_000),
+         (4096, 260, 50001), (300, 2500, 511), (300, 24, 512), (16384, 64, 3), (16385, 64, 1000), (1024, 64, 1000), (1025, 64, 1000), (4096, 8, 100), (4097, 16, 70_000), (65537, 16, 3000), (40000, 72, 70001), (70000, 8, 300_000),
          (20000, 40, 300_000), (50000, 4, 1)]
 
 
