@@ -12,7 +12,7 @@ using namespace xtvxy;
 
 namespace {
 
-constexpr int64_t kMostTokens = (int64_t)1 << 30;
+constexpr int64_t kMostTokens = (int64_t)1 << 26;  // a sorting workgroup reads the counts of all others
 constexpr int64_t kMostRows = INT32_MAX - 1;
 
 Matrix indices(const void* p, int64_t n, int bits) { return {p, 1, n, n > 0 ? n : 1, bits / 8}; }

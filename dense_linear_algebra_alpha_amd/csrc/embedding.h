@@ -44,8 +44,9 @@ struct EmbeddingGradientArgs {
 inline int64_t sort_groups(int64_t count) { return count <= kSortAlone ? (count > 0) : count <= kSortUncounted ? (count + 1023) / 1024 : (count + kCountedTile - 1) / kCountedTile; }
 inline int64_t slab_columns(int type) { return kSlabBytes / elem_size(type); }
 // Sorted tokens that a wavefront sums: 32, or fewer where that leaves CUs without work (a wavefront loads 8 rows at a
-// time, and each time waits for memory).
-inline int piece_tokens(int64_t count, int64_t slabs) { return count * slabs >= 32 * 1024 ? 32 : count * slabs >= 16 * 1024 ? 16 : 8; }
+// time, and each time waits for memory). us with 8, 16 and 32: 4000 tokens of two slabs 24, 26, 32; 8000 of two 32, 33, 39;
+// 40000 of one 56, 52, 55; 16384 of four 80, 75, 76; 65536 of two 106, 98, 92.
+inline int piece_tokens(int64_t count, int64_t slabs) { return count * slabs >= 96 * 1024 ? 32 : count * slabs >= 24 * 1024 ? 16 : 8; }
 inline int64_t piece_count(int64_t count, int piece) { return (count + piece - 1) / piece; }
 hipError_t launch_embedding_gradient(const EmbeddingGradientArgs& a, int type, hipStream_t s);
 

@@ -19,6 +19,7 @@ namespace {
 constexpr int64_t kPieceBytes = (int64_t)1 << 29;
 constexpr int64_t kLeastPiece = 4096;
 constexpr double kMemoryUs = 8.0;  // what logits in memory cost besides their product
+constexpr int64_t kMostMemoryRows = 65535 * kMemoryRows;  // their second grid dimension
 // The sum of dX's parts: a launch, and the parts read (4 slices of 67 MB and the result: 86 us).
 constexpr double kFinishUs = 8.0, kPartsBytesPerUs = 3.5e6;
 // What d costs more from memory than from the cache (8192 x 65536 of bf16: 300 us, 4096 x 100000 190).
@@ -86,7 +87,7 @@ struct MemoryPlan {
 };
 MemoryPlan plan_memory(int type, int64_t m, int64_t k, int64_t n, const ProductPlan& tiles) {
   MemoryPlan p;
-  if (n > kFewClasses || m * n * 4 > kPieceBytes / 4) return p;
+  if (n > kFewClasses || m > kMostMemoryRows || m * n * 4 > kPieceBytes / 4) return p;
   p.product = plan_product(type, m, n, k, true);
   p.used = p.product.splits > 1 && p.product.us + kMemoryUs < tiles.us;
   return p;

@@ -12,8 +12,8 @@ using namespace xtvxy;
 
 namespace {
 
-// A launch's grid counts 16 or 256 columns a workgroup.
-bool too_wide(int64_t n) { return n > INT32_MAX; }
+// The last launch of the gradient takes 16 of 2 n columns a workgroup of 256: its threads stay below 2^32.
+bool too_wide(int64_t n) { return n >= (int64_t)1 << 27; }
 
 xtvxy_status norm_impl(int type, int64_t m, int64_t n, const void* X, int64_t ldx, const float* weight, const float* bias,
                        float eps, void* out, int64_t ldo, float* mean, float* rstd, hipStream_t stream) {

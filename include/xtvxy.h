@@ -818,8 +818,8 @@ xtvxy_status xtvxy_adamw_state_values(xtvxy_adamw optimiser, void *const *m_out,
  * X and out share one element type (fp32, or bf16 / fp16 bit patterns); weight, bias (n floats, NULL: ones,
  * zeros) and the statistics mean and rstd (m floats, NULL: not stored) are fp32. Everything is computed in
  * fp32, the squares as distances from the mean, and rounded once as it is stored. NaN and infinities spread
- * over their row as the formulas say. eps finite and >= 0. m == 0 or n == 0 is a no-op. An output that
- * overlaps an input or another output gives XTVXY_ERROR_ALIASING. Pointers and strides of any alignment;
+ * over their row as the formulas say. eps finite and >= 0; n below 2^27. m == 0 or n == 0 is a no-op. An output
+ * that overlaps an input or another output gives XTVXY_ERROR_ALIASING. Pointers and strides of any alignment;
  * results are bitwise reproducible. */
 xtvxy_status xtvxy_layer_norm_f32(int64_t m, int64_t n, const float *X, int64_t ldx, const float *weight,
                                  const float *bias, float eps, float *out, int64_t ldo, float *mean, float *rstd,
@@ -865,11 +865,11 @@ xtvxy_status xtvxy_embedding_f16(int64_t count, int64_t k, int64_t rows, const v
 
 /* Its gradient from G = d loss / d out (count x k):
  *     dtable_r = scale sum over ids[i] = r of G_i   (+ dtable_r, where accumulate is nonzero),
- * each row summed in fp32 in the order of the tokens (up to 32 at a time, then those sums) and rounded once, so
+ * each row summed in fp32 in the order of the tokens (8 to 32 at a time, then those sums) and rounded once, so
  * that results are bitwise reproducible. Without accumulate every element of dtable (rows x k) is written, zero
  * where no id points; with it only the rows that occur are read and written: so the gradient of a table that is
  * also an output layer's weight is added to that layer's. Negative ids and ids >= rows take no part.
- * dtable may overlap neither G nor ids. count up to 2^30, rows below 2^31 - 1, and count / 32 times the KiB of
+ * dtable may overlap neither G nor ids. count up to 2^26, rows below 2^31 - 1, and count / 32 times the KiB of
  * a row below 2^24 (XTVXY_ERROR_UNSUPPORTED beyond). */
 xtvxy_status xtvxy_embedding_backward_f32_workspace_size(int64_t count, int64_t k, int64_t rows, size_t *bytes);
 xtvxy_status xtvxy_embedding_backward_f32(int64_t count, int64_t k, int64_t rows, const float *G, int64_t ldg,
@@ -896,12 +896,14 @@ xtvxy_status xtvxy_embedding_backward_f16(int64_t count, int64_t k, int64_t rows
  * sums of exponentials of wide vocabularies are taken relative to each part's largest logit and joined in a fixed
  * order. A bias of -infinity takes a class out; logits of +infinity give NaN, as do rows without any finite
  * logit that count. Features and weights must be finite also in rows that do not count, where gradients are wanted.
- * The vocabulary is processed in pieces where the workspace would grow beyond about 256 MiB.
+ * The vocabulary is processed in pieces where they would take more than 512 MiB of workspace. (Logits of up to 32
+ * rows, or of few tiles over a long contraction, 128 MiB at most, pass through the workspace.)
  *
  * Any overlap of an output with an input or another output gives XTVXY_ERROR_ALIASING. Pointers and strides of
  * any alignment; 16-byte aligned rows of X and W are the fast case, others are copied into the workspace (W piece by
  * piece). aligned16 states whether X, W and their rows are 16-byte aligned with strides of at most 4 MiB. m == 0 is a
- * no-op. k above 2^21 (fp32: 2^20), m or n above 2^31 - 1 or m above about 10^9 / 4 are XTVXY_ERROR_UNSUPPORTED.
+ * no-op. k above 2^21 (fp32: 2^20), n above 2^31 - 1, m above 2^24 - 64, and ceil(m / 64) ceil(k / 64) above about 2^24
+ * are XTVXY_ERROR_UNSUPPORTED.
  * Results are bitwise reproducible for a given shape, type and alignment. */
 xtvxy_status xtvxy_linear_cross_entropy_f32_workspace_size(int64_t m, int64_t k, int64_t n, int aligned16, size_t *bytes);
 xtvxy_status xtvxy_linear_cross_entropy_f32(int64_t m, int64_t k, int64_t n, const float *X, int64_t ldx, const float *W,
@@ -922,7 +924,8 @@ xtvxy_status xtvxy_linear_cross_entropy_f16(int64_t m, int64_t k, int64_t n, con
 /* Its gradient from grad_i = d total / d loss_i (m floats) and the forward call's lse:
  *     d_ij = grad_i (exp(z_ij - lse_i) - [j = label_i]),   dX = d W,   dW = d^T X,   db_j = sum_i d_ij,
  * d zero in rows with a negative label or a zero grad, NaN in rows with a label >= n. The logits are formed again,
- * piece by piece of the vocabulary. d is formed in fp32; db sums it unrounded, and the products take it in the element
+ * piece by piece of the vocabulary: the workspace holds one piece of d and, besides, parts of dX and what the products
+ * of linear_backward take. d is formed in fp32; db sums it unrounded, and the products take it in the element
  * type (fp16: scaled by a power of two chosen from the largest |grad|, so that small probabilities do not
  * underflow). dX (m x k, lddx), dW (n x k, lddw) and db (n floats) may each be NULL. m == 0 gives dW = 0 and
  * db = 0; n == 0 gives dX = 0. Otherwise as the forward call. */
@@ -982,7 +985,8 @@ xtvxy_status xtvxy_linear_distillation_f16(int64_t m, int64_t k, int64_t n, cons
 
 /* Its gradient from grad and the forward call's weights and lse:
  *     d_ij = grad_i / temperature (exp(t_ij - lse_i) - P_ij),
- * then as xtvxy_linear_cross_entropy_backward_*. Rows whose weights are all zero take no part. */
+ * then as xtvxy_linear_cross_entropy_backward_*. Rows whose weights are all zero take no part. weights as the forward
+ * call stores them: with weights in two places of one class results are right, but not reproducible to the bit. */
 xtvxy_status xtvxy_linear_distillation_backward_f32_workspace_size(int64_t m, int64_t k, int64_t n, int64_t s,
                                                                    int aligned16, size_t *bytes);
 xtvxy_status xtvxy_linear_distillation_backward_f32(int64_t m, int64_t k, int64_t n, const float *grad, const float *X,
