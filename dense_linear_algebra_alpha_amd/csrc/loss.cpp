@@ -89,7 +89,8 @@ MemoryPlan plan_memory(int type, int64_t m, int64_t k, int64_t n, const ProductP
   MemoryPlan p;
   if (n > kFewClasses || m > kMostMemoryRows || m * n * 4 > kPieceBytes / 4) return p;
   p.product = plan_product(type, m, n, k, true);
-  p.used = p.product.splits > 1 && p.product.us + kMemoryUs < tiles.us;
+  // every tile split: whole ones would be stored by the product's own epilogue, in its element type
+  p.used = p.product.splits > 1 && p.product.whole == 0 && p.product.us + kMemoryUs < tiles.us;
   return p;
 }
 

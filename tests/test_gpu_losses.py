@@ -122,6 +122,23 @@ def test_several_pieces_of_the_vocabulary(dtype, k):
     check_all(only, ref, dtype + " alone")
 
 
+@pytest.mark.parametrize("size", [(1118, 912, 12800), (924, 4072, 144), (600, 2000, 1000), (1500, 700, 9000)], ids=lambda s: "%dx%dx%d" % s)
+def test_tiles_that_no_round_is_full_of(size):
+    """fp32 products whose last round of tiles would be split: all tiles are, with the logits in memory, or none. The
+    oracle runs on the GPU."""
+    m, k, n = size
+    X, W, b, _, grad = cuda(*inputs(m, k, n, torch.float32, 19))
+    classes, teacher = cuda(*lists(m, n, 13, 20))
+    note("last rounds %s" % (size,))
+    loss, lse, weights = xt.linear_distillation(X, W, classes, teacher, b)
+    got = xt.linear_distillation_backward(grad, X, W, classes, weights, lse, b)
+    torch.cuda.synchronize()
+    P, eP = O.targets(classes, teacher, n, 1.0)
+    for t, (ref, bound) in zip((loss, lse), O.forward(X, W, b, classes, P, eP)):
+        L.check(t, ref, bound, "loss")
+    check_all(got, O.backward(grad, X, W, b, classes, weights.double(), torch.zeros_like(P), lse=lse), "%s" % (size,))
+
+
 def test_parts_of_dx_joined_on_the_way():
     """More pieces of the vocabulary than there is room for their parts of dX."""
     m, k, n = 65536, 1024, 13_000
