@@ -56,7 +56,7 @@ OrderPlan plan_order(int64_t m, int64_t n, int64_t per_row, int tile) {
   p.order.half = tile / 2;
   p.order.columns = cdiv(n, p.order.half);
   p.order.strip_rows = strip_rows_of(tile);
-  if (per_row < kOrderedFrom || p.order.columns > kMostHalves) return p;
+  if (!order_pays(m, n, per_row) || p.order.columns > kMostHalves) return p;
   const int64_t strips = cdiv(m, p.order.strip_rows);
   p.starts = align_up((size_t)strips * (p.order.columns + 1) * 4);
   p.bytes = p.starts + align_up((size_t)strips * p.order.strip_rows * per_row * 4);
@@ -398,18 +398,23 @@ xtvxy_status forward_impl(const Layer& l, const ClassList& list, const Teacher* 
   if (bad_workspace(p.bytes, ws, ws_bytes)) return XTVXY_ERROR_WORKSPACE;
   char* base = static_cast<char*>(ws);
   float* weights = teacher ? teacher->weights : nullptr;
+  TeacherArgs t{};
   if (teacher && list.per_row > 0) {
     const int type = teacher->type == XTVXY_TYPE_F32 ? kF32 : teacher->type == XTVXY_TYPE_BF16 ? kBf16 : kF16;
-    if (launch_teacher_weights({list, teacher->logits, teacher->ld, type, inv_temperature, m, n, weights}, stream) != hipSuccess)
-      return XTVXY_ERROR_LAUNCH;
+    t = {list, teacher->logits, teacher->ld, type, inv_temperature, m, n, weights};
+    if (list.per_row > kLaneListed) {
+      if (launch_teacher_weights(t, stream) != hipSuccess) return XTVXY_ERROR_LAUNCH;
+      t.teacher = nullptr;
+    }
   }
   float* stats = reinterpret_cast<float*>(base + p.stats_off);
   LossFinishArgs f{stats, 0, m, n, p.piece < n ? reinterpret_cast<float*>(base + p.run_off) : nullptr, 1, n == 0, list,
-                   reinterpret_cast<float*>(base + p.listed_off), weights, loss, lse};
+                   reinterpret_cast<float*>(base + p.listed_off), weights, loss, lse, t};
   if (teacher && list.per_row == 0) f.weights = loss;  // no terms: never read
   if (n == 0) return status_of(launch_loss_finish(f, stream));
   ListOrder order;
-  if (order_lists(p.order, list, weights, m, n, base + p.order_off, &order, stream) != hipSuccess) return XTVXY_ERROR_LAUNCH;
+  if (order_lists(p.order, list, t.teacher ? nullptr : weights, m, n, base + p.order_off, &order, stream) != hipSuccess)
+    return XTVXY_ERROR_LAUNCH;
   for (int64_t j = 0; j < n; j += p.piece) {
     const int64_t classes = std::min(p.piece, n - j);
     LossForwardArgs a{};

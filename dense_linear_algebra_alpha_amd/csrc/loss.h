@@ -22,9 +22,14 @@ struct ListOrder {
   int64_t columns;       // half tiles
   int32_t strip_rows, half;  // half: classes of a half tile
 };
-// Half tiles up to which a workgroup counts them in LDS, and places a row from which on the order pays.
+// Half tiles up to which a workgroup counts them in LDS.
 constexpr int64_t kMostHalves = 8192;
-constexpr int64_t kOrderedFrom = 9;
+// The order is a launch of 3 to 6 us; searched lists cost every tile its rows' places. us, ordered and searched, with the
+// gradient, bf16: 64 x 512 x 192 with 48 a row 45, 42; 512 x 512 x 4000 with 24 56, 48, with 48 60, 57; 1024 x 512 x 8000
+// with 24 89, 87, with 48 93, 101; 4096 x 512 x 2000 with 24 91, 91, with 48 96, 104; 4096 x 512 x 16000 with 12 334, 351.
+inline bool order_pays(int64_t m, int64_t n, int64_t per_row) {
+  return per_row >= 9 && (double)per_row * (1.0 + (double)m * n / (1 << 23)) >= 52.0;
+}
 inline int strip_rows_of(int tile) { return tile / 2 < 64 ? tile / 2 : 64; }
 struct OrderArgs {
   ClassList list;
@@ -53,6 +58,19 @@ hipError_t launch_loss_forward(const LossForwardArgs& a, hipStream_t s);
 constexpr int64_t kFewChunk = 4096;
 hipError_t launch_loss_few(const LossForwardArgs& a, hipStream_t s);
 
+// Target weights from a teacher's logits: softmax(teacher / T) over a row's classes, equal classes' in the first.
+constexpr int64_t kMostListed = 1024;
+// Up to so many a row the launch that forms the loss forms the weights as well, a lane a class (a launch of 4 to 6 us less).
+constexpr int64_t kLaneListed = 64;
+struct TeacherArgs {
+  ClassList list;
+  const void* teacher;
+  int64_t ldt;
+  int32_t type;
+  float inv_temperature;
+  int64_t m, n;
+  float* weights;
+};
 // Joins a piece's statistics into each row's running ones and, after the last piece, forms lse and loss.
 struct LossFinishArgs {
   const float* stats;
@@ -64,6 +82,7 @@ struct LossFinishArgs {
   const float* weights;  // [m][per_row], null: labels
   float* loss;
   float* lse;
+  TeacherArgs teacher;   // teacher.teacher: the weights are formed first, null: they are there
 };
 hipError_t launch_loss_finish(const LossFinishArgs& a, hipStream_t s);
 
@@ -77,17 +96,7 @@ constexpr int64_t kMemoryRows = 8;
 struct LossGradientArgs;
 hipError_t launch_loss_gradient_memory(const LossGradientArgs& a, hipStream_t s);
 
-// Target weights from a teacher's logits: softmax(teacher / T) over a row's classes, equal classes' in the first.
-constexpr int64_t kMostListed = 1024;
-struct TeacherArgs {
-  ClassList list;
-  const void* teacher;
-  int64_t ldt;
-  int32_t type;
-  float inv_temperature;
-  int64_t m, n;
-  float* weights;
-};
+// The weights in a launch of their own.
 hipError_t launch_teacher_weights(const TeacherArgs& a, hipStream_t s);
 
 // factor_i of d_ij = factor_i (softmax_ij - target_ij): grad_i / T, 0 for rows that do not count, NaN for bad ones; and,

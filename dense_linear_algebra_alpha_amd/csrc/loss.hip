@@ -437,6 +437,39 @@ __device__ __forceinline__ void join_stats(float* top, float* sum, float top2, f
   *top = t;
 }
 
+__device__ __forceinline__ float teacher_at(const TeacherArgs& a, int64_t at) {
+  if (a.type == kBf16) return (float)static_cast<const __bf16*>(a.teacher)[at];
+  if (a.type == kF16) return (float)static_cast<const _Float16*>(a.teacher)[at];
+  return static_cast<const float*>(a.teacher)[at];
+}
+
+// A row's weight as stored: a class beyond the vocabulary or an infinite or missing logit makes the whole row no distribution.
+__device__ __forceinline__ float stored_weight(bool bad, float sum, float w) {
+  return bad || !(sum < __builtin_inff()) ? __builtin_nanf("") : w;
+}
+
+// The weights of a row of up to kLaneListed classes, by a wavefront.
+__device__ __forceinline__ void teacher_row(const TeacherArgs& a, int64_t i) {
+  const int lane = threadIdx.x & 63, count = a.list.per_row;
+  const int64_t at = lane < count ? class_at(a.list, i, lane) : -1;
+  const bool valid = at >= 0 && at < a.n;
+  const int32_t c = valid ? (int32_t)at : -1;
+  const float t = valid ? teacher_at(a, i * a.ldt + lane) * a.inv_temperature : -__builtin_inff();
+  const bool bad = __any(at >= a.n || t != t);
+  float top = t;
+#pragma unroll
+  for (int by = 1; by < 64; by *= 2) top = fmaxf(top, __shfl_xor(top, by));
+  const float own = expf(t - (top == -__builtin_inff() ? 0.0f : top)), sum = group_sum(own, 64);
+  float w = 0.0f;
+  bool first = true;
+  for (int f = 0; f < count; ++f) {
+    const bool same = __builtin_amdgcn_readlane(c, f) == c;
+    if (same && f < lane) first = false;
+    if (same && f >= lane) w += __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, own), f));
+  }
+  if (lane < count) a.weights[i * count + lane] = stored_weight(bad, sum, first && valid && sum > 0.0f ? w / sum : 0.0f);
+}
+
 // 16 rows a workgroup: of each row a thread joins every 64th part's statistics, the 64 join in order; the terms of a
 // teacher's classes likewise. (With 16 threads a row 1000 parts of 13 rows took 9.6 us.)
 constexpr int kSlots = 64;
@@ -445,6 +478,10 @@ __global__ __launch_bounds__(16 * kSlots) void loss_finish(LossFinishArgs a) {
   const int c = threadIdx.x & 15, slot = threadIdx.x >> 4;
   const int64_t i = (int64_t)blockIdx.x * 16 + c;
   const bool there = i < a.m;
+  if (a.last && a.teacher.teacher) {  // a wavefront a row
+    const int64_t row = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 6);
+    if (row < a.m) teacher_row(a.teacher, row);
+  }
   float top = -__builtin_inff(), sum = 0.0f;
   if (there) {
     for (int64_t p = slot; p < a.parts; p += 4 * kSlots) {
@@ -516,6 +553,7 @@ __global__ __launch_bounds__(kRowThreads) void loss_few_rows(LossForwardArgs a, 
   constexpr int kQuads = 4;
   const int64_t i = blockIdx.x, n = a.product.n;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  if (f.teacher.teacher && wave == 0) teacher_row(f.teacher, i);
   float top = -__builtin_inff(), sum = 0.0f;
   for (int64_t j0 = threadIdx.x * 4; j0 < n; j0 += kQuads * 4 * kRowThreads) {
     f32x4 t[kQuads];
@@ -609,7 +647,7 @@ __global__ __launch_bounds__(256) void loss_gradient_memory(LossGradientArgs a) 
   if (a.sums && count > 0) store4<float>(a.sums + (int64_t)blockIdx.y * p.n + j, sum, count);
 }
 
-// A wavefront a row.
+// Weights of rows of more classes, a wavefront a row.
 template <typename T>
 __global__ __launch_bounds__(256) void teacher_weights(TeacherArgs a) {
   __shared__ int32_t classes[4][kMostListed];
@@ -652,8 +690,7 @@ __global__ __launch_bounds__(256) void teacher_weights(TeacherArgs a) {
       if (same && f >= e) w += weights[wave][f];
     }
     w = first && c >= 0 && sum > 0.0f ? w / sum : 0.0f;
-    // a class beyond the vocabulary or an infinite or missing logit: the whole row is no distribution
-    a.weights[i * count + e] = bad || !(sum < __builtin_inff()) ? __builtin_nanf("") : w;
+    a.weights[i * count + e] = stored_weight(bad, sum, w);
   }
 }
 
