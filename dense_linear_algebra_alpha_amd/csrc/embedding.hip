@@ -5,12 +5,15 @@
 //
 // The gradient sorts the tokens by their row (a stable radix sort, 9 bits a pass or less), so that each row's sum is
 // taken in the order of the tokens, in fp32, and rounded once: it is bitwise reproducible, and needs no atomics.
-// Up to 4096 tokens one workgroup sorts in LDS. Beyond, each pass
-// is a launch, beyond 32768 tokens one that counts digits and one that places the tokens. Meanwhile the other CUs
-// write the table's zeros, each launch its share of them.
+// Up to 4096 tokens one workgroup sorts in LDS. Beyond, each pass is a launch, beyond 32768 tokens one that counts
+// digits and one that places the tokens. Meanwhile the other CUs write the table's zeros, each launch its share of them.
 // Then a wavefront sums a piece of the sorted tokens over 1 KiB of their columns. A row whose tokens lie within the
 // piece is written at once; of rows that cross over, which frequent words have, the sums go to the workspace and a last launch
 // joins them in order.
+//
+// us of the kernels: lookup of 16384 tokens in 65536 x 4096 of bf16 32 (8.5 TB/s of rows read and written, 6.8 at memory); its
+// gradient with 16384 tokens, 50001 x 2048: two sorting passes with the zeros of 205 MB 37 (5.6 TB/s), sums 24, join 6; 1777
+// fp16 tokens of 1111 added to 10007 rows: sort 10, sums 7.5, join 4.5, each of them a launch and its chain of loads.
 #include <type_traits>
 #include <utility>
 

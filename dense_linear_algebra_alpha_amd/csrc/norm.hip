@@ -11,6 +11,9 @@
 // workgroup and the gradient's column sums stay in registers; the next row is loaded before the sums of the
 // current one are joined.
 //
+// us of the kernels: forward with statistics, bf16 16384 x 4096, 52 (5.1 TB/s, what a copy reaches), 1 x 4096 2.5;
+// gradient of the same 78 (5.3 TB/s) and 5 for the columns' sums of 256 workgroups, fp32 5001 x 1111 15.5 and 4.
+//
 // A row's last chunk of 16 bytes, where n is no multiple of one, is the last 16 bytes of the row: memory
 // takes any alignment, a branch around its loads would make every row wait for them. What it shares with
 // the chunk before counts once in the sums and is stored twice with the same value.

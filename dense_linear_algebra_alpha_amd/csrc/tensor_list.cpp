@@ -4,8 +4,8 @@
 // 8 us for 200, this 1.2). linear() and linear_backward(): the checks, outputs and
 // workspace of one call of the layer and the call itself (7.6 and 14.7 us from Python, 3.7 and
 // 8.0 here; a small layer takes the GPU 4 us); the functions after them the same of layer norm, embedding and the
-// losses. Host code only; built against torch's headers, resolved
-// against the torch that the process has imported; the C entry points come in by bind().
+// losses (one row's layer norm 8.6 us a call from Python, 5.0 here, a token's embedding 8.0 and 4.9). Host code only; built
+// against torch's headers, resolved against the torch that the process has imported; the C entry points come in by bind().
 #include <ATen/ops/empty.h>
 #include <torch/csrc/autograd/python_variable.h>
 

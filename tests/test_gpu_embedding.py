@@ -1,5 +1,5 @@
-"""GPU parity of the embedding lookup and its gradient: token counts around the pieces of 32 and the sorting workgroup
-of 16384, tables that take one to three sorting passes, frequent rows, padding, views, streams, graphs."""
+"""GPU parity of the embedding lookup and its gradient: token counts around the pieces of 8 to 32 and the sorting
+workgroups, tables that take one to three sorting passes, frequent rows, padding, views, streams, graphs."""
 import pytest
 import torch
 
