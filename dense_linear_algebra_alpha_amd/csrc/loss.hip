@@ -613,34 +613,53 @@ __global__ __launch_bounds__(kRowThreads) void loss_few_rows(LossForwardArgs a, 
   f.lse[i] = lse;
 }
 
-// Four columns a thread over eight rows; a row's listed classes are looked through for each.
+// A workgroup takes 1024 columns of kMemoryRows rows, four a thread. What their lists take off d is summed in LDS first: one
+// entry a thread at a time. (Each thread looking through the lists of its rows took 1.4 us a place of 300 rows.)
 template <typename T>
 __global__ __launch_bounds__(256) void loss_gradient_memory(LossGradientArgs a) {
+  __shared__ f32x4 targets[kMemoryRows][256];
   const ProductArgs& p = a.product;
-  const int64_t j = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4, i0 = (int64_t)blockIdx.y * kMemoryRows;
-  if (j >= a.ldd) return;
-  const int64_t i1 = i0 + kMemoryRows < p.m ? i0 + kMemoryRows : p.m;
+  const int64_t j0 = (int64_t)blockIdx.x * 1024, j = j0 + threadIdx.x * 4, i0 = (int64_t)blockIdx.y * kMemoryRows;
+  const int rows = p.m - i0 < kMemoryRows ? (int)(p.m - i0) : (int)kMemoryRows;
   const int count = p.n - j >= 4 ? 4 : p.n > j ? (int)(p.n - j) : 0;
+#pragma unroll
+  for (int r = 0; r < kMemoryRows; ++r) targets[r][threadIdx.x] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  __syncthreads();
+  constexpr int kBatch = 4;
+  const int per_row = a.list.per_row, total = rows * per_row;
+  for (int at0 = threadIdx.x; at0 < total; at0 += kBatch * 256) {
+    int64_t c[kBatch];
+    int row[kBatch], e[kBatch];
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      const int at = at0 + b * 256 < total ? at0 + b * 256 : at0;
+      row[b] = at / per_row;
+      e[b] = at - row[b] * per_row;
+      c[b] = class_at(a.list, i0 + row[b], e[b]) - j0;
+    }
+#pragma unroll
+    for (int b = 0; b < kBatch; ++b) {
+      if (at0 + b * 256 >= total || c[b] < 0 || c[b] >= 1024 || c[b] >= p.n - j0) continue;
+      const float factor = a.factor[i0 + row[b]], w = a.weights ? a.weights[(i0 + row[b]) * per_row + e[b]] : 1.0f;
+      if (factor != 0.0f && w != 0.0f)
+        __hip_atomic_fetch_add(reinterpret_cast<float*>(&targets[row[b]][0]) + c[b], factor * w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+    }
+  }
+  __syncthreads();
+  if (j >= a.ldd) return;
   constexpr bool kScaled = __is_same(T, _Float16);
   const float scale = kScaled ? *a.scale : 1.0f;
   f32x4 bias = {0.0f, 0.0f, 0.0f, 0.0f}, sum = bias;
   if (a.bias && count > 0) bias = load4<float>(a.bias + j, count) * a.inv_temperature;
 #pragma unroll 2
-  for (int64_t i = i0; i < i1; ++i) {
+  for (int r = 0; r < rows; ++r) {
+    const int64_t i = i0 + r;
     const float factor = a.factor[i], lse = a.lse[i];
     f32x4 d = {0.0f, 0.0f, 0.0f, 0.0f};
     if (factor != 0.0f && count > 0) {
-      const f32x4 z = load4<float>(p.partial + i * p.n + j, count);
+      const f32x4 z = load4<float>(p.partial + i * p.n + j, count), target = targets[r][threadIdx.x];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) d[e] = e < count ? factor * fast_exp(fmaf(z[e], a.inv_temperature, bias[e]) - lse) : 0.0f;
-      for (int l = 0; l < a.list.per_row; ++l) {
-        const int64_t c = class_at(a.list, i, l) - j;
-        if (c < 0 || c >= count) continue;
-        const float w = a.weights ? a.weights[i * a.list.per_row + l] : 1.0f;
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (e == c && w != 0.0f) d[e] -= factor * w;
-      }
+      for (int e = 0; e < 4; ++e) d[e] = e < count ? factor * fast_exp(fmaf(z[e], a.inv_temperature, bias[e]) - lse) - target[e] : 0.0f;
     }
     sum += d;
     if (a.d) {
@@ -653,67 +672,116 @@ __global__ __launch_bounds__(256) void loss_gradient_memory(LossGradientArgs a) 
   if (a.sums && count > 0) store4<float>(a.sums + (int64_t)blockIdx.y * p.n + j, sum, count);
 }
 
-// Weights of rows of more classes, a wavefront a row.
-template <typename T>
+// Weights of rows of more classes, a workgroup a row. A class finds the places that list it through a table in LDS, at most
+// half full: its least place and their number; where there are several, the first adds them in their order. (Comparing every
+// two places took 1032 us of 300 rows of 1000, 72 of 256 a row.)
+constexpr int kPlaces = 2 * kMostListed;
+
 __global__ __launch_bounds__(256) void teacher_weights(TeacherArgs a) {
-  __shared__ int32_t classes[4][kMostListed];
-  __shared__ float weights[4][kMostListed];
+  __shared__ int32_t keys[kPlaces];
+  __shared__ uint32_t least[kPlaces], many[kPlaces];
+  __shared__ float weights[kMostListed];
+  __shared__ uint16_t places[kMostListed];
+  __shared__ float tops[4], sums[4];
+  __shared__ int bads[4];
+  constexpr int kEach = kMostListed / 256;
+  const int64_t i = blockIdx.x;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, count = a.list.per_row;
-  const int64_t i = (int64_t)blockIdx.x * 4 + wave;
-  if (i >= a.m) return;
-  const T* teacher = static_cast<const T*>(a.teacher) + i * a.ldt;
-  bool bad = false;
-  float top = -__builtin_inff();
-  for (int e = lane; e < count; e += 64) {
-    const int64_t c = class_at(a.list, i, e);
-    bad |= c >= a.n;
-    const bool valid = c >= 0 && c < a.n;
-    const float t = valid ? (float)teacher[e] * a.inv_temperature : -__builtin_inff();
-    classes[wave][e] = valid ? (int32_t)c : -1;
-    weights[wave][e] = t;
-    bad |= t != t;
-    top = fmaxf(top, t);
+  for (int h = threadIdx.x; h < kPlaces; h += 256) {
+    keys[h] = -1;
+    least[h] = ~0u;
+    many[h] = 0;
   }
+  __syncthreads();
+  float t[kEach], top = -__builtin_inff(), sum = 0.0f;
+  bool bad = false, valid[kEach];
 #pragma unroll
-  for (int by = 1; by < 64; by *= 2) top = fmaxf(top, __shfl_xor(top, by));
+  for (int q = 0; q < kEach; ++q) {
+    const int e = q * 256 + threadIdx.x;
+    const int64_t c = e < count ? class_at(a.list, i, e) : -1;
+    valid[q] = c >= 0 && c < a.n;
+    t[q] = valid[q] ? teacher_at(a, i * a.ldt + e) * a.inv_temperature : -__builtin_inff();
+    bad |= c >= a.n || t[q] != t[q];
+    top = fmaxf(top, t[q]);
+    if (e >= count) continue;
+    uint32_t h = kPlaces;  // no place
+    if (valid[q]) {
+      h = (uint32_t)c * 2654435761u >> 21;
+      static_assert(kPlaces == 1 << 11, "bits of a place");
+      for (int old; (old = atomicCAS(&keys[h], -1, (int32_t)c)) != -1 && old != (int32_t)c;) h = (h + 1) % kPlaces;
+      atomicMin(&least[h], (uint32_t)e);
+      atomicAdd(&many[h], 1u);
+    }
+    places[e] = (uint16_t)h;
+  }
+  top = wave_max(top);
   bad = __any(bad);
+  if (lane == 0) {
+    tops[wave] = top;
+    bads[wave] = bad;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    top = fmaxf(top, tops[w]);
+    bad |= bads[w] != 0;
+  }
   const float from = top == -__builtin_inff() ? 0.0f : top;
-  float sum = 0.0f;
-  for (int e = lane; e < count; e += 64) {
-    const float w = expf(weights[wave][e] - from);
-    weights[wave][e] = w;
-    sum += w;
+  float own[kEach];
+#pragma unroll
+  for (int q = 0; q < kEach; ++q) {
+    const int e = q * 256 + threadIdx.x;
+    own[q] = expf(t[q] - from);
+    if (e < count) weights[e] = own[q];
+    sum += own[q];
   }
   sum = group_sum(sum, 64);
-  __builtin_amdgcn_wave_barrier();
-  for (int e = lane; e < count; e += 64) {
-    const int32_t c = classes[wave][e];
+  if (lane == 0) sums[wave] = sum;
+  __syncthreads();
+  sum = sums[0] + sums[1] + sums[2] + sums[3];
+#pragma unroll
+  for (int q = 0; q < kEach; ++q) {
+    const int e = q * 256 + threadIdx.x;
+    if (e >= count) continue;
     float w = 0.0f;
-    bool first = true;
-    for (int f = 0; f < count; ++f) {
-      const bool same = classes[wave][f] == c;
-      if (same && f < e) first = false;
-      if (same && f >= e) w += weights[wave][f];
+    if (valid[q] && least[places[e]] == (uint32_t)e) {
+      w = own[q];
+      if (many[places[e]] > 1)
+        for (int f = e + 1; f < count; ++f)
+          if (places[f] == places[e]) w += weights[f];
     }
-    w = first && c >= 0 && sum > 0.0f ? w / sum : 0.0f;
-    a.weights[i * count + e] = stored_weight(bad, sum, w);
+    a.weights[i * count + e] = stored_weight(bad, sum, sum > 0.0f ? w / sum : 0.0f);
   }
 }
 
+// Of a row's weights only whether there are any, and whether they are a distribution. kLanes lanes a row.
+template <int kLanes>
 __device__ __forceinline__ float factor_of(const LossFactorArgs& a, int64_t i) {
   if (a.weights) {
-    float s = 0.0f;
+    bool any = false, bad = false;
 #pragma unroll 8
-    for (int e = 0; e < a.list.per_row; ++e) s += a.weights[i * a.list.per_row + e];
-    return s == 0.0f ? 0.0f : s == s ? a.grad[i] * a.inv_temperature : s;
+    for (int e = threadIdx.x % kLanes; e < a.list.per_row; e += kLanes) {
+      const float w = a.weights[i * a.list.per_row + e];
+      any |= w != 0.0f;
+      bad |= w != w;
+    }
+    if constexpr (kLanes > 1) {
+      const int shift = (threadIdx.x & 63) / kLanes * kLanes;
+      const uint64_t lanes = ~(uint64_t)0 >> (64 - kLanes);
+      any = (__ballot(any) >> shift & lanes) != 0;
+      bad = (__ballot(bad) >> shift & lanes) != 0;
+    }
+    return bad ? __builtin_nanf("") : any ? a.grad[i] * a.inv_temperature : 0.0f;
   }
   const int64_t y = class_at(a.list, i, 0);
   return y < 0 ? 0.0f : y < a.n ? a.grad[i] : __builtin_nanf("");
 }
 
+template <int kLanes>
 __global__ __launch_bounds__(256) void loss_factor(LossFactorArgs a) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i < a.m) a.factor[i] = factor_of(a, i);
+  const int64_t i = ((int64_t)blockIdx.x * 256 + threadIdx.x) / kLanes;
+  const float f = factor_of<kLanes>(a, i < a.m ? i : a.m - 1);
+  if (i < a.m && threadIdx.x % kLanes == 0) a.factor[i] = f;
 }
 
 // The scale, in one workgroup; kFactor: after forming the factors itself.
@@ -724,7 +792,7 @@ __global__ __launch_bounds__(1024) void loss_scale(LossFactorArgs a) {
 #pragma unroll 4
   for (int64_t i = threadIdx.x; i < a.m; i += 1024) {
     float f;
-    if (kFactor) a.factor[i] = f = factor_of(a, i);
+    if (kFactor) a.factor[i] = f = factor_of<1>(a, i);
     else f = a.factor[i];
     f = fabsf(f);
     top = f < __builtin_inff() ? fmaxf(top, f) : top;
@@ -833,20 +901,22 @@ hipError_t launch_sum_slices(float* slices, int64_t count, int64_t elements, hip
 
 hipError_t launch_teacher_weights(const TeacherArgs& a, hipStream_t s) {
   if (a.m == 0 || a.list.per_row == 0) return hipSuccess;
-  const unsigned groups = (unsigned)((a.m + 3) / 4);
-  if (a.type == kBf16) teacher_weights<__bf16><<<groups, 256, 0, s>>>(a);
-  else if (a.type == kF16) teacher_weights<_Float16><<<groups, 256, 0, s>>>(a);
-  else teacher_weights<float><<<groups, 256, 0, s>>>(a);
+  teacher_weights<<<(unsigned)a.m, 256, 0, s>>>(a);
   return hipGetLastError();
 }
 
 hipError_t launch_loss_factor(const LossFactorArgs& a, hipStream_t s) {
-  if (a.scale && a.m * a.list.per_row <= 8192) {  // two launches: 11 us of 200 rows, one: 2.4; at 2047 x 32 one takes 12.7
+  // two launches: 11 us of 200 rows, one: 2.4; at 2047 x 32 one takes 12.7
+  if (a.scale && a.list.per_row <= 32 && a.m * a.list.per_row <= 8192) {
     loss_scale<true><<<1, 1024, 0, s>>>(a);
-  } else {
-    loss_factor<<<(unsigned)((a.m + 255) / 256), 256, 0, s>>>(a);
-    if (a.scale) loss_scale<false><<<1, 1024, 0, s>>>(a);
+    return hipGetLastError();
   }
+  const auto groups = [&](int lanes) { return (unsigned)((a.m * lanes + 255) / 256); };
+  // us, with 1, 16 and 64 lanes a row (500 x 512 x 2000 with its gradient): 8 weights 37.9, 38.2, 37.8; 32 47.3, 46.8, 46.8;
+  // 300 87, 72, 73; 1000 184, 138, 137
+  if (!a.weights || a.list.per_row <= 8) loss_factor<1><<<groups(1), 256, 0, s>>>(a);
+  else loss_factor<16><<<groups(16), 256, 0, s>>>(a);
+  if (a.scale) loss_scale<false><<<1, 1024, 0, s>>>(a);
   return hipGetLastError();
 }
 

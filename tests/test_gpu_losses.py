@@ -103,6 +103,29 @@ def test_distillation(size, dtype):
 
 
 @pytest.mark.parametrize("dtype", list(L.DTYPES))
+@pytest.mark.parametrize("size", [(64, 32, 1, 900), (7, 512, 65, 65), (300, 64, 50, 300), (40, 4000, 300, 250), (33, 16, 1000, 1024),
+                                  (500, 2048, 1100, 129), (20, 8, 40000, 513)], ids=lambda s: "%dx%dx%dx%d" % s)
+def test_long_lists(size, dtype):
+    """More places than lanes, most classes listed several times; logits in tiles and in memory."""
+    m, k, n, s = size
+    X, W, b, _, grad = inputs(m, k, n, L.DTYPES[dtype], m + s)
+    classes, teacher = lists(m, n, s, s + 1)
+    classes[-1] = classes[-1, 0]
+    gX, gW, gb, gc, gt, gg = cuda(X, W, b, classes, teacher, grad)
+    note("long lists %s %s" % (size, dtype))
+    loss, lse, weights = xt.linear_distillation(gX, gW, gc, gt, gb, 1.5)
+    got = xt.linear_distillation_backward(gg, gX, gW, gc, weights, lse, gb, 1.5)
+    again = xt.linear_distillation_backward(gg, gX, gW, gc, weights, lse, gb, 1.5)
+    torch.cuda.synchronize()
+    P, eP = O.targets(classes, teacher, n, 1.5)
+    L.check(weights, P, eP + 1e-40, "%s %s weights" % (size, dtype))
+    for t, (ref, bound), what in zip((loss, lse), O.forward(X, W, b, classes, P, eP, 1.5), ("loss", "lse")):
+        L.check(t, ref, bound, "%s %s %s" % (size, dtype, what))
+    check_all(got, O.backward(grad, X, W, b, classes, weights.cpu().double(), torch.zeros_like(P), 1.5, lse=lse.cpu()), "%s %s" % (size, dtype))
+    assert all(torch.equal(x, y) for x, y in zip(got, again))
+
+
+@pytest.mark.parametrize("dtype", list(L.DTYPES))
 @pytest.mark.parametrize("k", [32, 35])
 def test_several_pieces_of_the_vocabulary(dtype, k):
     """So many rows that d is formed in pieces; k = 35: copies of the weights' pieces too. The oracle runs on the GPU."""
