@@ -229,7 +229,7 @@ BackwardPlan make_backward_plan(int type, int64_t m, int64_t k, int64_t n, int64
   p.w_off = take(p.pack_w, packed_bytes(p.piece, k, es));
   p.d_off = take(want_dx || want_dw, (size_t)m * p.ldd * es);
   p.factor_off = take(true, (size_t)m * 4);
-  p.scale_off = take(type == kF16, 8);
+  p.scale_off = take(type != kF32, 8);
   if (!p.parts) p.memory = plan_memory(type, m, k, n, p.logits);
   const int64_t rows = p.memory.used ? cdiv(m, kMemoryRows) : cdiv(m, p.logits.tile) * 2;
   p.sums_off = take(true, (size_t)rows * p.piece * 4);
@@ -487,7 +487,7 @@ xtvxy_status backward_impl(const Layer& l, const float* grad, const ClassList& l
   if (bad_workspace(p.bytes, ws, ws_bytes)) return XTVXY_ERROR_WORKSPACE;
   char* base = static_cast<char*>(ws);
   float* factor = reinterpret_cast<float*>(base + p.factor_off);
-  float* scale = l.type == kF16 ? reinterpret_cast<float*>(base + p.scale_off) : nullptr;
+  float* scale = l.type == kF16 || (l.type == kBf16 && labels) ? reinterpret_cast<float*>(base + p.scale_off) : nullptr;
   const float inv_temperature = 1.0f / temperature;
   const float* target = labels ? nullptr : list.per_row > 0 ? weights : factor;  // none listed: never read
   if (launch_loss_factor({grad, list, target, inv_temperature, m, n, factor, scale}, stream) != hipSuccess) return XTVXY_ERROR_LAUNCH;

@@ -99,8 +99,11 @@ hipError_t launch_loss_gradient_memory(const LossGradientArgs& a, hipStream_t s)
 // The weights in a launch of their own.
 hipError_t launch_teacher_weights(const TeacherArgs& a, hipStream_t s);
 
-// factor_i of d_ij = factor_i (softmax_ij - target_ij): grad_i / T, 0 for rows that do not count, NaN for bad ones; and,
-// for fp16, powers of two scale[0] and scale[1] = 1 / scale[0] with which the largest |factor| is in [2^13, 2^14).
+// factor_i of d_ij = factor_i (softmax_ij - target_ij): grad_i / T, 0 for rows that do not count, NaN for bad ones; and
+// scale[0] and scale[1] = 1 / scale[0] with which the largest |factor| becomes 2^13. For fp16 that keeps d in its range. For
+// 16 bits and labels it takes a rounding away: most of d is its label's place, factor_i (softmax - 1), and under a mean all
+// rows have one factor, whose rounding would be in all of them (bf16 566 x 384 x 7650, in the 2-norm: dX off
+// by 2.46e-3, scaled 1.68e-3, of which its own rounding 1.65e-3); scaled that place is a power of two but for its softmax.
 struct LossFactorArgs {
   const float* grad;
   ClassList list;

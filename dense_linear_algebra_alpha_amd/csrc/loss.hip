@@ -292,8 +292,8 @@ struct GradientEnd {
     const int64_t width = a.n - p.j0 - wj;
     const int c8 = lane % kLanes;
     const int64_t column = p.j0 + wj + c8 * 8;  // of this lane's eight
-    constexpr bool kScaled = __is_same(T, _Float16);
-    const float scale = kScaled ? *l.scale : 1.0f;
+    constexpr bool kScaled = sizeof(T) == 2;
+    const float scale = kScaled && l.scale ? *l.scale : 1.0f;
     float column_sums[8] = {};
 #pragma unroll
     for (int part = 0; part < BM / 2 / kRows; ++part) {
@@ -647,8 +647,8 @@ __global__ __launch_bounds__(256) void loss_gradient_memory(LossGradientArgs a) 
   }
   __syncthreads();
   if (j >= a.ldd) return;
-  constexpr bool kScaled = __is_same(T, _Float16);
-  const float scale = kScaled ? *a.scale : 1.0f;
+  constexpr bool kScaled = sizeof(T) == 2;
+  const float scale = kScaled && a.scale ? *a.scale : 1.0f;
   f32x4 bias = {0.0f, 0.0f, 0.0f, 0.0f}, sum = bias;
   if (a.bias && count > 0) bias = load4<float>(a.bias + j, count) * a.inv_temperature;
 #pragma unroll 2
@@ -803,11 +803,11 @@ __global__ __launch_bounds__(1024) void loss_scale(LossFactorArgs a) {
   __syncthreads();
   if (threadIdx.x != 0) return;
   for (int w = 1; w < 16; ++w) top = fmaxf(top, lds[w]);
-  int e = 14;
-  if (top > 0.0f) e = 14 - ilogbf(top) - 1;  // top < 2^(ilogb + 1)
-  e = e > 120 ? 120 : e < -120 ? -120 : e;
-  a.scale[0] = ldexpf(1.0f, e);
-  a.scale[1] = ldexpf(1.0f, -e);
+  if (top == 0.0f) top = 1.0f;
+  const int e = ilogbf(top), up = 13 - e > 120 ? 120 : 13 - e < -120 ? -120 : 13 - e;
+  const float digits = ldexpf(top, -e);
+  a.scale[0] = ldexpf(1.0f / digits, up);
+  a.scale[1] = ldexpf(digits, -up);
 }
 
 __global__ __launch_bounds__(256) void sum_slices(float* slices, int64_t count, int64_t quads) {

@@ -926,8 +926,8 @@ xtvxy_status xtvxy_linear_cross_entropy_f16(int64_t m, int64_t k, int64_t n, con
  * d zero in rows with a negative label or a zero grad, NaN in rows with a label >= n. The logits are formed again,
  * piece by piece of the vocabulary: the workspace holds one piece of d and, besides, parts of dX and what the products
  * of linear_backward take. d is formed in fp32; db sums it unrounded, and the products take it in the element
- * type (fp16: scaled by a power of two chosen from the largest |grad|, so that small probabilities do not
- * underflow). dX (m x k, lddx), dW (n x k, lddw) and db (n floats) may each be NULL. m == 0 gives dW = 0 and
+ * type (16 bits: scaled so that the largest |grad| becomes a power of two, in fp16 2^13, and the products divided by as
+ * much: small probabilities do not underflow, and under a mean the places of the labels are hardly rounded). dX (m x k, lddx), dW (n x k, lddw) and db (n floats) may each be NULL. m == 0 gives dW = 0 and
  * db = 0; n == 0 gives dX = 0. Otherwise as the forward call. */
 xtvxy_status xtvxy_linear_cross_entropy_backward_f32_workspace_size(int64_t m, int64_t k, int64_t n, int aligned16,
                                                                     size_t *bytes);
@@ -985,7 +985,7 @@ xtvxy_status xtvxy_linear_distillation_f16(int64_t m, int64_t k, int64_t n, cons
 
 /* Its gradient from grad and the forward call's weights and lse:
  *     d_ij = grad_i / temperature (exp(t_ij - lse_i) - P_ij),
- * then as xtvxy_linear_cross_entropy_backward_*. Rows whose weights are all zero take no part. weights as the forward
+ * then as xtvxy_linear_cross_entropy_backward_* (bf16 without the scale). Rows whose weights are all zero take no part. weights as the forward
  * call stores them: with weights in two places of one class results are right, but not reproducible to the bit. */
 xtvxy_status xtvxy_linear_distillation_backward_f32_workspace_size(int64_t m, int64_t k, int64_t n, int64_t s,
                                                                    int aligned16, size_t *bytes);

@@ -125,6 +125,35 @@ def test_long_lists(size, dtype):
     assert all(torch.equal(x, y) for x, y in zip(got, again))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("m", [566, 1150, 9000])
+def test_rounding_of_a_mean(m, dtype):
+    """1 / m in 16 bits is off by up to half a step, alike in all rows. d is scaled so that it is a power of two, and what is
+    left is the rounding of its softmax, as that of d / grad here, and the outputs' own: independent, so that their squares
+    add; a tenth more for what is left of their product. The oracle runs on the GPU."""
+    k, n = 96, 3000
+    dt = L.DTYPES[dtype]
+    X, W, _, labels, _ = cuda(*inputs(m, k, n, dt, m, bias=False))
+    grad = torch.full((m,), 1.0 / m, device=dev())
+    note("rounding of a mean %s %d" % (dtype, m))
+    _, lse = xt.linear_cross_entropy(X, W, labels)
+    dX, dW, _ = xt.linear_cross_entropy_backward(grad, X, W, labels, lse)
+    torch.cuda.synchronize()
+    x, w, on = X.double(), W.double(), labels >= 0
+    d = torch.softmax(x @ w.T, 1)
+    d[on, labels[on]] -= 1.0
+    d *= on[:, None]
+    rounded = (d * 2.0 ** 13).to(dt).double() * 2.0 ** -13
+    for got, ref, near, what in ((dX, d @ w, rounded @ w, "dX"), (dW, d.T @ x, rounded.T @ x, "dW")):
+        ref, near = ref / m, near / m
+        off = float((got.double() - ref).norm() / ref.norm())
+        inside = float((near - ref).norm() / ref.norm())
+        # the output's own, scaled so that no fp16 output is below the smallest numbers
+        own = float(((ref * 2.0 ** 12).to(dt).double() * 2.0 ** -12 - ref).norm() / ref.norm())
+        least = L.smallest(dt) / 2 * ref.numel() ** 0.5 / float(ref.norm())
+        assert off < 1.1 * (inside ** 2 + own ** 2 + least ** 2) ** 0.5, (what, off, inside, own, least)
+
+
 @pytest.mark.parametrize("dtype", list(L.DTYPES))
 @pytest.mark.parametrize("k", [32, 35])
 def test_several_pieces_of_the_vocabulary(dtype, k):
