@@ -241,9 +241,11 @@ __global__ __launch_bounds__(kGradientThreads) void norm_gradient_rows(NormGradi
     mean = a.mean[row];
     rstd = a.rstd[row];
   };
-  load(i);
+  constexpr bool kAhead = C * V < 16 || sizeof(T) == 2;
+  if (kAhead) load(i);
   int turn = 0;
   for (int64_t i0 = (int64_t)blockIdx.x * kRows; i0 < a.m; i0 += step, i += step, turn ^= 1) {
+    if (!kAhead) load(i);
     float xhat[C][V], h[C][V], s = 0.0f, q = 0.0f;
     const float r = rstd;
     const bool there = i < a.m;
@@ -263,7 +265,7 @@ __global__ __launch_bounds__(kGradientThreads) void norm_gradient_rows(NormGradi
           db[c][e] += ge;
         }
       }
-    if (i0 + step < a.m) load(i + step);
+    if (kAhead && i0 + step < a.m) load(i + step);
     s = group_sum(s, kGroup);
     q = group_sum(q, kGroup);
     if constexpr (kWaves > 1) {
