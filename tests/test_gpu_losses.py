@@ -481,3 +481,40 @@ def test_streams_and_graph(dtype):
         want = step()
         torch.cuda.synchronize()
         assert all(torch.equal(a, c) for a, c in zip(out, want))
+
+
+def test_calls_at_once():
+    """Four host threads, each with its sizes and its stream, against the same calls one after the other."""
+    import threading
+
+    sizes = [(300, 64, 1000, "bf16"), (7, 512, 5000, "f16"), (93, 1415, 105, "f32"), (1000, 96, 3000, "bf16")]
+    given = [cuda(*inputs(m, k, n, L.DTYPES[t], m)) for m, k, n, t in sizes]
+
+    def calls(X, W, b, labels, grad):
+        out = []
+        for _ in range(5):
+            loss, lse = xt.linear_cross_entropy(X, W, labels, b)
+            out.append((loss, lse) + xt.linear_cross_entropy_backward(grad, X, W, labels, lse, b))
+        return out
+
+    note("calls at once")
+    expected = [calls(*g) for g in given]
+    torch.cuda.synchronize()
+    results, errors = [None] * len(given), []
+
+    def run(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                results[i] = calls(*given[i])
+        except Exception as e:  # shown by the test
+            errors.append(e)
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(len(given))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors
+    for got, ref in zip(results, expected):
+        assert all(torch.equal(a, b) for x, y in zip(got, ref) for a, b in zip(x, y))
