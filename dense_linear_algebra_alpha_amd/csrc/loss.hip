@@ -12,8 +12,8 @@
 // fourth product; keeping them costs as much memory as the vocabulary is wide), turned into d, and the piece's d,
 // in the element type, goes through the layer's gradient kernel.
 //
-// Tiles are the product's: of 256 x 256 the product over 1000 features takes 26 us, the epilogue 15 to 20, in which the
-// matrix unit waits. us: bf16 8192 x 2048 x 65536 forward 1634 (1.35 PFLOP/s, matrix unit 68% busy), with the gradient 6600; fp16
+// Tiles are the product's: of 256 x 256 the product over 1000 features takes 26 us, first loads and epilogue 15 to 20, in
+// which the matrix unit waits. us: bf16 8192 x 2048 x 65536 forward 1634 (1.35 PFLOP/s, matrix unit 68% busy), with the gradient 6600; fp16
 // 2047 x 1000 x 30001 with 32 classes a row 615 with the gradient (187 forward, 185 d, 238 its products); fp32 512 x 768 x
 // 16384 100 (fp32 matrix unit 89% busy). Few rows are bound by W: fp16 13 x 4096 x 32000 60, of which its one pass 51 (5.2
 // TB/s).
