@@ -593,6 +593,7 @@ hipError_t launch_embedding_gradient(const EmbeddingGradientArgs& args, int type
     q.from_out = a.from[to];
     q.shift = pass * q.bits;
     if (alone && a.count <= kSortThreads) sort_all<1><<<grid, kSortThreads, 0, s>>>(q);
+    else if (alone && a.count <= 2 * kSortThreads) sort_all<2><<<grid, kSortThreads, 0, s>>>(q);
     else if (alone) sort_all<kSortAlone / kSortThreads><<<grid, kSortThreads, 0, s>>>(q);
     else if (!counted) sort_pass<1, false><<<grid, kSortThreads, 0, s>>>(q);
     else if (l % 2 == 0) sort_count<<<grid, kSortThreads, 0, s>>>(q);
