@@ -422,13 +422,15 @@ void norm_gradient_for(const NormGradientArgs& a, hipStream_t s) {
   constexpr int V = kChunkOf<T>;
   const int64_t chunks = (a.n + V - 1) / V;
   const unsigned grid = (unsigned)a.groups;
-  if (chunks <= L) norm_gradient_rows<T, L, 1><<<grid, kGradientThreads, 0, s>>>(a);
-  else if (L < 1024 || chunks <= 2 * L) norm_gradient_rows<T, L, 2><<<grid, kGradientThreads, 0, s>>>(a);
+  if constexpr (L < 512) {
+    if (chunks <= L) return norm_gradient_rows<T, L, 1><<<grid, kGradientThreads, 0, s>>>(a);
+  }
+  if (L < 1024 || chunks <= 2 * L) norm_gradient_rows<T, L, 2><<<grid, kGradientThreads, 0, s>>>(a);
   else if constexpr (L == 1024 && V == 4) norm_gradient_rows<T, L, 4><<<grid, kGradientThreads, 0, s>>>(a);
 }
 
 // Threads of a row, with up to two chunks each (fp32 rows of more than 8192: four).
-int norm_gradient_lanes(int64_t n, int chunk) { return n <= 32 * chunk ? 16 : n <= 128 * chunk ? 64 : n <= 512 * chunk ? 256 : 1024; }
+int norm_gradient_lanes(int64_t n, int chunk) { return n <= 32 * chunk ? 16 : n <= 128 * chunk ? 64 : n <= 512 * chunk ? 256 : n <= 1024 * chunk ? 512 : 1024; }
 
 template <typename T>
 void norm_gradient_type(const NormGradientArgs& a, hipStream_t s) {
@@ -443,6 +445,7 @@ void norm_gradient_type(const NormGradientArgs& a, hipStream_t s) {
       case 16: norm_gradient_for<T, 16>(a, s); break;
       case 64: norm_gradient_for<T, 64>(a, s); break;
       case 256: norm_gradient_for<T, 256>(a, s); break;
+      case 512: norm_gradient_for<T, 512>(a, s); break;
       default: norm_gradient_for<T, 1024>(a, s); break;
     }
   }
