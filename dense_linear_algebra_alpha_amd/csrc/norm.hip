@@ -422,15 +422,23 @@ void norm_gradient_for(const NormGradientArgs& a, hipStream_t s) {
   constexpr int V = kChunkOf<T>;
   const int64_t chunks = (a.n + V - 1) / V;
   const unsigned grid = (unsigned)a.groups;
-  if constexpr (L < 512) {
+  if constexpr (L == 16) {
     if (chunks <= L) return norm_gradient_rows<T, L, 1><<<grid, kGradientThreads, 0, s>>>(a);
   }
-  if (L < 1024 || chunks <= 2 * L) norm_gradient_rows<T, L, 2><<<grid, kGradientThreads, 0, s>>>(a);
-  else if constexpr (L == 1024 && V == 4) norm_gradient_rows<T, L, 4><<<grid, kGradientThreads, 0, s>>>(a);
+  if constexpr (L == 1024 && V == 4) {
+    if (chunks > 2 * L) return norm_gradient_rows<T, L, 4><<<grid, kGradientThreads, 0, s>>>(a);
+  }
+  norm_gradient_rows<T, L, 2><<<grid, kGradientThreads, 0, s>>>(a);
 }
 
-// Threads of a row, with up to two chunks each (fp32 rows of more than 8192: four).
-int norm_gradient_lanes(int64_t n, int chunk) { return n <= 32 * chunk ? 16 : n <= 128 * chunk ? 64 : n <= 512 * chunk ? 256 : n <= 1024 * chunk ? 512 : 1024; }
+// Threads of a row, the fewest with up to two chunks each (fp32 rows of more than 8192: four): a second chunk keeps more loads
+// under way. us with twice the threads and one chunk: bf16 16384 x 2048 50, two 46; 16384 x 5120 144, 116; fp32 20000 x 768
+// 44, 40; 8000 x 2560 68, 51.
+int norm_gradient_lanes(int64_t n, int chunk) {
+  int lanes = 16;
+  while (lanes < 1024 && n > 2 * lanes * chunk) lanes *= 2;
+  return lanes;
+}
 
 template <typename T>
 void norm_gradient_type(const NormGradientArgs& a, hipStream_t s) {
@@ -443,7 +451,9 @@ void norm_gradient_type(const NormGradientArgs& a, hipStream_t s) {
   } else {
     switch (norm_gradient_lanes(a.n, V)) {
       case 16: norm_gradient_for<T, 16>(a, s); break;
+      case 32: norm_gradient_for<T, 32>(a, s); break;
       case 64: norm_gradient_for<T, 64>(a, s); break;
+      case 128: norm_gradient_for<T, 128>(a, s); break;
       case 256: norm_gradient_for<T, 256>(a, s); break;
       case 512: norm_gradient_for<T, 512>(a, s); break;
       default: norm_gradient_for<T, 1024>(a, s); break;
