@@ -518,3 +518,76 @@ def test_calls_at_once():
     assert not errors
     for got, ref in zip(results, expected):
         assert all(torch.equal(a, b) for x, y in zip(got, ref) for a, b in zip(x, y))
+
+
+def fresh(m, k, n, dt, seed, s, edges):
+    """Inputs made on the GPU; lists that hold classes on both sides of each edge, empty and equal places and rows without any."""
+    g = torch.Generator(dev()).manual_seed(seed)
+    X, W = (torch.randn(r, k, generator=g, device=dev()).to(dt) for r in (m, n))
+    W *= 2.0 * k ** -0.5
+    b, grad = torch.randn(n, generator=g, device=dev()), torch.rand(m, generator=g, device=dev()) + 0.1
+    classes = torch.randint(0, n, (m, s), generator=g, device=dev())
+    near = torch.tensor([0, n - 1] + [e + by for e in edges for by in (-1, 0)], device=dev())
+    at = torch.rand(m, s, generator=g, device=dev()) < 0.5
+    classes = torch.where(at, near[torch.randint(0, len(near), (m, s), generator=g, device=dev())], classes)
+    classes[torch.rand(m, s, generator=g, device=dev()) < 0.2] = -1
+    classes[3] = -1
+    return X, W, b, grad / m, classes, torch.randn(m, s, generator=g, device=dev()) * 2.0
+
+
+def inside(got, ref, bound, what):
+    over = ((got.double() - ref).abs() / bound).max().item()
+    assert over <= 1.0, "%s: error %.3g times its bound" % (what, over)
+
+
+# 300 x 66001: copies of W, whose pieces hold 4096 classes of 12001 in both directions. 20000 x 35: pieces of the gradient's d, of
+# a multiple of 256 classes (10000 rows of fp32). Lists of 8 are searched, of 48 and 100 put in order; the weights of 100 are
+# formed in a launch of their own, of the others with the last piece.
+@pytest.mark.parametrize("dtype", list(L.DTYPES))
+@pytest.mark.parametrize("s", [8, 48, 100])
+@pytest.mark.parametrize("many", [False, True])
+def test_lists_over_several_pieces(many, s, dtype):
+    """Distillation over a vocabulary that is processed in pieces. The oracle runs on the GPU."""
+    dt = L.DTYPES[dtype]
+    es = torch.finfo(dt).bits // 8
+    m, k, n = (40000 // es, 35, 13001) if many else (300, 132000 // es + 1, 12001)
+    X, W, b, grad, classes, teacher = fresh(m, k, n, dt, s, s, range(256, n, 256) if many else (4096, 8192))
+    T = 1.5
+    size = getattr(xt, "xtvxy_linear_distillation_backward_%s_workspace_size" % dtype)
+    assert size(m, k, n, s, 0) < (m * n * es if many else n * k * es)  # neither all of d nor a copy of all of W
+    note("lists over pieces %d %d %s" % (many, s, dtype))
+    loss, lse, weights = xt.linear_distillation(X, W, classes, teacher, b, T)
+    got = xt.linear_distillation_backward(grad, X, W, classes, weights, lse, b, T)
+    again = xt.linear_distillation_backward(grad, X, W, classes, weights, lse, b, T)
+    torch.cuda.synchronize()
+    P, eP = O.targets(classes, teacher, n, T)
+    inside(weights, P, eP + 1e-40, "weights")
+    assert loss[3] == 0 and not weights[3].any()
+    for t, (ref, bound), what in zip((loss, lse), O.forward(X, W, b, classes, P, eP, T), ("loss", "lse")):
+        inside(t, ref, bound, what)
+    ref = O.backward(grad, X, W, b, classes, weights.double(), torch.zeros_like(P), T, lse=lse)
+    for t, u, name in zip(got, again, ("dX", "dW", "db")):
+        inside(t, *ref[name], what=name)
+        assert torch.equal(t, u)
+
+
+@pytest.mark.parametrize("dtype", list(L.DTYPES))
+@pytest.mark.parametrize("s", [5, 40, 70])
+def test_few_rows_over_several_pieces(s, dtype):
+    """So many classes that few rows' logits, which pass through the workspace, are taken in two pieces. The oracle runs on
+    the GPU."""
+    m, k, n, edge = (32, 8, 1_500_001, 750_080) if dtype == "f32" else (16, 8, 3_000_001, 1_500_160)
+    T = 2.0
+    X, W, b, grad, classes, teacher = fresh(m, k, n, L.DTYPES[dtype], s, s, [edge])
+    assert getattr(xt, "xtvxy_linear_distillation_%s_workspace_size" % dtype)(m, k, n, s) < m * n * 4
+    note("few rows over pieces %d %s" % (s, dtype))
+    loss, lse, weights = xt.linear_distillation(X, W, classes, teacher, b, T)
+    dX, dW, db = xt.linear_distillation_backward(grad, X, W, classes, weights, lse, b, T)
+    torch.cuda.synchronize()
+    P, eP = O.targets(classes, teacher, n, T)
+    inside(weights, P, eP + 1e-40, "weights")
+    for t, (ref, bound), what in zip((loss, lse), O.forward(X, W, b, classes, P, eP, T), ("loss", "lse")):
+        inside(t, ref, bound, what)
+    ref = O.backward(grad, X, W, b, classes, weights.double(), torch.zeros_like(P), T, lse=lse)
+    for t, name in zip((dX, dW, db), ("dX", "dW", "db")):
+        inside(t, *ref[name], what=name)
