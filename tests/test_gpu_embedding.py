@@ -186,3 +186,48 @@ def test_streams_and_graph(count):
         eo, eg = xt.embedding(ids, table), xt.embedding_backward(G, ids, rows)
         torch.cuda.synchronize()
         assert torch.equal(o.nan_to_num(1.0), eo.nan_to_num(1.0)) and torch.equal(g, eg)
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+@pytest.mark.parametrize("dtype", list(L.DTYPES))
+@pytest.mark.parametrize("size", [(40000, 1111, 37), (40001, 1111, 5000), (98400, 260, 300), (12000, 5003, 2)], ids=lambda s: "%dx%dx%d" % s)
+def test_pieces_of_32_tokens(size, dtype, accumulate):
+    """Rows of many slabs whose tokens go through many pieces of 32 (16 where the slabs are fewer). Whole numbers, whose sums in
+    fp32 are exact: no token is lost or added twice. The oracle runs on the GPU."""
+    count, k, rows = size
+    dt = L.DTYPES[dtype]
+    ids = words(count, rows, count).to(dev())
+    g = torch.Generator(dev()).manual_seed(k)
+    G = torch.randint(-4, 5, (count, k), generator=g, device=dev()).to(dt)
+    before = torch.randint(-4, 5, (rows, k), generator=g, device=dev()).to(dt)
+    note("embedding pieces of 32 %s %s" % (size, dtype))
+    got = xt.embedding_backward(G, ids, rows, 0.5, dtable=before.clone(), accumulate=accumulate)
+    torch.cuda.synchronize()
+    there = (ids >= 0) & (ids < rows)
+    want = torch.zeros(rows, k, dtype=torch.float64, device=dev()).index_add_(0, ids[there], G[there].double()) * 0.5
+    if accumulate:
+        want += before.double()
+    assert want.abs().max() < 2.0 ** 15  # within fp16, and whole sums within fp32
+    assert torch.equal(got, want.float().to(dt))
+
+
+@pytest.mark.parametrize("dtype", list(L.DTYPES))
+@pytest.mark.parametrize("lanes, chunks", [(16, 31.5), (64, 98.5), (256, 139)])
+def test_lookups_beyond_the_caches(lanes, chunks, dtype):
+    """Outputs of more than 32 MiB, which are stored past the L2s, by 16, 64 and 256 threads a row; widths that are no whole
+    number of 16 bytes."""
+    dt = L.DTYPES[dtype]
+    es = torch.finfo(dt).bits // 8
+    k = int(chunks * 16 / es) + 1
+    count, rows = (36 << 20) // (k * es), 3001
+    ids = words(count, rows, k).to(dev())
+    table = rand((rows, k), 1, dt).to(dev())
+    note("embedding beyond the caches %d %s" % (k, dtype))
+    out = xt.embedding(ids, table, 2.5)
+    torch.cuda.synchronize()
+    assert out.numel() * es > 32 << 20
+    want = (table.float()[ids.clamp(0, rows - 1)] * 2.5).to(dt)
+    want[ids < 0] = 0.0
+    want[ids >= rows] = float("nan")
+    assert torch.equal(torch.isnan(out), torch.isnan(want))
+    assert torch.equal(out.nan_to_num(1.0), want.nan_to_num(1.0))
