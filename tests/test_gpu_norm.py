@@ -187,3 +187,35 @@ def test_streams_and_graph():
         torch.cuda.synchronize()
         assert torch.equal(o, eo) and all(torch.equal(a, c) for a, c in zip(gr, eg))
     assert d.type == "cuda"
+
+
+# Rows in turns: so many that every workgroup takes three turns, the last one of a part of them. Gradient: 256 workgroups,
+# each of 1024 / lanes rows a turn with the fewest lanes (16 to 1024) that have two 16-byte chunks of a row each, one (the
+# first) or four (fp32 9152). Forward: 16 lanes up to 64 chunks, 64 up to 256, 256 up to 1024, 1024 up to 4096, 1024
+# workgroups of 256 / lanes rows a turn or 512 of one. The last in 16 bits: the forward's registers, the gradient's kernels
+# for any length.
+IN_TURNS_16 = [(33000, 100), (33001, 250), (33000, 500), (8300, 1001), (4201, 1999), (2200, 4096), (1100, 5117), (700, 12000), (1100, 20001)]
+IN_TURNS_32 = [(33000, 61), (33001, 125), (33000, 250), (8300, 501), (4201, 1000), (2200, 2047), (1100, 4090), (1050, 6001), (700, 9152), (1050, 16384)]
+
+
+@pytest.mark.parametrize("dtype, size", [(t, s) for t in L.DTYPES for s in (IN_TURNS_32 if t == "f32" else IN_TURNS_16)],
+                         ids=lambda v: v if isinstance(v, str) else "%dx%d" % v)
+def test_rows_in_turns(dtype, size):
+    """Every row of many turns against the oracle, on the GPU. G is whole numbers: their sums in fp32 are exact, so that dbias
+    tells a row that is lost or counted twice."""
+    m, n = size
+    dt = L.DTYPES[dtype]
+    g = torch.Generator(dev()).manual_seed(m + n)
+    X = (torch.randn(m, n, generator=g, device=dev()) * 2.0 + 0.7).to(dt)
+    G = torch.randint(-3, 4, (m, n), generator=g, device=dev()).to(dt)
+    w, b = (torch.randn(n, generator=g, device=dev()) + 1.0 for _ in range(2))
+    note("layer_norm in turns %s %s" % (size, dtype))
+    out, mean, rstd = xt.layer_norm(X, w, b, save_stats=True)
+    got = xt.layer_norm_backward(G, X, mean, rstd, w)
+    torch.cuda.synchronize()
+    for t, (ref, bound), what in zip((out, mean, rstd), N.forward(X, w, b, 1e-5), ("out", "mean", "rstd")):
+        L.check(t, ref, bound, "%s %s %s" % (size, dtype, what))
+    ref = N.backward(G, X, mean, rstd, w)
+    for t, name in zip(got, ("dX", "dweight", "dbias")):
+        L.check(t, *ref[name], what="%s %s %s" % (size, dtype, name))
+    assert torch.equal(got[2].double(), G.double().sum(0))
