@@ -17,6 +17,8 @@
 // A row's last chunk of 16 bytes, where n is no multiple of one, is the last 16 bytes of the row: memory
 // takes any alignment, a branch around its loads would make every row wait for them. What it shares with
 // the chunk before counts once in the sums and is stored twice with the same value.
+#include <type_traits>
+
 #include "linear_util.h"
 #include "norm.h"
 
@@ -177,32 +179,46 @@ __global__ __launch_bounds__(L < 256 ? 256 : L) void norm_rows(NormArgs a) {
   }
 }
 
-// The sum over a workgroup of kThreads, the same in every thread; `lds` has kThreads / 64 floats.
-template <int kThreads>
-__device__ __forceinline__ float block_sum(float x, float* lds) {
-  x = group_sum(x, 64);
+// The sum over a workgroup of kThreads, the same in every thread; `lds` has kThreads / 64 numbers.
+template <int kThreads, typename Sum>
+__device__ __forceinline__ Sum block_sum(Sum x, Sum* lds) {
+  if constexpr (sizeof(Sum) == 4) {
+    x = group_sum(x, 64);
+  } else {
+#pragma unroll
+    for (int by = 1; by < 64; by *= 2) x += __shfl_xor(x, by);
+  }
   __syncthreads();
   if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = x;
   __syncthreads();
-  return row_sum<kThreads / 64>(lds, 0);
+  x = lds[0];
+#pragma unroll
+  for (int w = 1; w < kThreads / 64; ++w) x += lds[w];
+  return x;
 }
 
-// Rows shorter than a chunk or longer than the registers of 1024 threads: a workgroup walks the row once for
+// Sums of rows longer than registers are fp64: a thread's may have 2^17 terms. In fp32 the mean of 4 10^7 times 1.1 drifts to
+// 1.1002, which 1 / sqrt(eps) makes 0.06. (us, fp32: 2000 x 20001 111, summed in fp32 104; 1000 x 100003 385, 375.)
+template <int kThreads>
+using RowSum = std::conditional_t<kThreads == 64, float, double>;
+
+// Rows shorter than a chunk (64 threads) or longer than the registers of 1024 threads: a workgroup walks the row once for
 // the mean, once for the distances and once for the output (the second and third time out of L2).
 template <typename T, int kThreads>
 __global__ __launch_bounds__(kThreads) void norm_any(NormArgs a) {
-  __shared__ float lds[kThreads / 64];
+  typedef RowSum<kThreads> Sum;
+  __shared__ Sum lds[kThreads / 64];
   for (int64_t i = blockIdx.x; i < a.m; i += gridDim.x) {
     const T* x = static_cast<const T*>(a.x) + i * a.ldx;
     T* out = static_cast<T*>(a.out) + i * a.ldo;
-    float s = 0.0f, q = 0.0f;
-    for (int64_t j = threadIdx.x; j < a.n; j += kThreads) s += (float)x[j];
-    const float mean = block_sum<kThreads>(s, lds) / (float)a.n;
+    Sum s = 0, q = 0;
+    for (int64_t j = threadIdx.x; j < a.n; j += kThreads) s += (Sum)(float)x[j];
+    const float mean = (float)(block_sum<kThreads>(s, lds) / (Sum)a.n);
     for (int64_t j = threadIdx.x; j < a.n; j += kThreads) {
-      const float d = (float)x[j] - mean;
+      const Sum d = (Sum)((float)x[j] - mean);
       q += d * d;
     }
-    const float rstd = 1.0f / sqrtf(block_sum<kThreads>(q, lds) / (float)a.n + a.eps);
+    const float rstd = (float)(1 / sqrt(block_sum<kThreads>(q, lds) / (Sum)a.n + (Sum)a.eps));
     if (threadIdx.x == 0) {
       if (a.mean) a.mean[i] = mean;
       if (a.rstd) a.rstd[i] = rstd;
@@ -315,23 +331,33 @@ __global__ __launch_bounds__(kGradientThreads) void norm_gradient_rows(NormGradi
     }
 }
 
-// Rows of any length: the sums and dX of a row by one workgroup, which walks it twice.
+// Rows of any length: the sums and dX of a row by one workgroup, which walks it twice. The sums are as norm_any's, four terms
+// at a time in fp32. (us, 2000 x 32768 of bf16: 265, each term in fp64 345, all in fp32 251.)
 template <typename T, int kThreads>
 __global__ __launch_bounds__(kThreads) void norm_gradient_any(NormGradientArgs a) {
-  __shared__ float lds[kThreads / 64];
+  typedef RowSum<kThreads> Sum;
+  __shared__ Sum lds[kThreads / 64];
   for (int64_t i = blockIdx.x; i < a.m; i += gridDim.x) {
     const T* x = static_cast<const T*>(a.x) + i * a.ldx;
     const T* g = static_cast<const T*>(a.g) + i * a.ldg;
     T* dx = static_cast<T*>(a.dx) + i * a.lddx;
     const float mean = a.mean[i], rstd = a.rstd[i];
-    float s = 0.0f, q = 0.0f;
-    for (int64_t j = threadIdx.x; j < a.n; j += kThreads) {
-      const float h = (float)g[j] * (a.weight ? a.weight[j] : 1.0f);
-      s += h;
-      q += h * (((float)x[j] - mean) * rstd);
+    Sum all_h = 0, all_hx = 0;
+    constexpr int kBatch = kThreads == 64 ? 1 : 4;
+    for (int64_t j0 = threadIdx.x; j0 < a.n; j0 += kBatch * kThreads) {
+      float some_h = 0.0f, some_hx = 0.0f;
+#pragma unroll
+      for (int u = 0; u < kBatch; ++u) {
+        const bool there = j0 + u * kThreads < a.n;
+        const int64_t j = there ? j0 + u * kThreads : j0;
+        const float h = (float)g[j] * (a.weight ? a.weight[j] : 1.0f), hx = h * (((float)x[j] - mean) * rstd);
+        some_h += there ? h : 0.0f;
+        some_hx += there ? hx : 0.0f;
+      }
+      all_h += (Sum)some_h;
+      all_hx += (Sum)some_hx;
     }
-    s = block_sum<kThreads>(s, lds) / (float)a.n;
-    q = block_sum<kThreads>(q, lds) / (float)a.n;
+    const float s = (float)(block_sum<kThreads>(all_h, lds) / (Sum)a.n), q = (float)(block_sum<kThreads>(all_hx, lds) / (Sum)a.n);
     for (int64_t j = threadIdx.x; j < a.n; j += kThreads) {
       const float h = (float)g[j] * (a.weight ? a.weight[j] : 1.0f);
       dx[j] = (T)(rstd * (h - s - ((float)x[j] - mean) * rstd * q));

@@ -219,3 +219,18 @@ def test_rows_in_turns(dtype, size):
     for t, name in zip(got, ("dX", "dweight", "dbias")):
         L.check(t, *ref[name], what="%s %s %s" % (size, dtype, name))
     assert torch.equal(got[2].double(), G.double().sum(0))
+
+
+@pytest.mark.parametrize("dtype", list(L.DTYPES))
+@pytest.mark.parametrize("n", [33_000, 100_003, 40_000_003])
+def test_long_constant_rows(n, dtype):
+    """The mean of a constant row is that constant at any length: sums that drift would leave distances, which 1 / sqrt(eps)
+    blows up."""
+    dt = L.DTYPES[dtype]
+    X = torch.full((2, n), 1.1, dtype=dt, device=dev())
+    X[1] = -300.7
+    note("layer_norm constant %d %s" % (n, dtype))
+    out, mean, rstd = xt.layer_norm(X, save_stats=True)
+    torch.cuda.synchronize()
+    assert torch.equal(mean, X[:, 0].float()) and not out.any()
+    assert torch.allclose(rstd, torch.full_like(rstd, 1e-5 ** -0.5))
