@@ -12,7 +12,7 @@ using namespace xtvxy;
 
 namespace {
 
-// The last launch of the gradient takes 16 of 2 n columns a workgroup of 256: its threads stay below 2^32.
+// What the sums of a row are made for: up to 2^17 terms of each of 1024 threads.
 bool too_wide(int64_t n) { return n >= (int64_t)1 << 27; }
 
 xtvxy_status norm_impl(int type, int64_t m, int64_t n, const void* X, int64_t ldx, const float* weight, const float* bias,

@@ -384,22 +384,26 @@ __global__ __launch_bounds__(256) void norm_columns_any(NormGradientArgs a) {
 }
 
 // dweight and dbias from the workgroups' sums [groups][2][n], in fp64 and in a fixed order: 16 columns of the
-// 2 n a workgroup, as in column_sum.
+// 2 n a workgroup at a time, as in column_sum.
 __global__ __launch_bounds__(256) void norm_gradient_finish(NormGradientArgs a) {
   __shared__ double lds[256];
   const int c = threadIdx.x & 15, slot = threadIdx.x >> 4;
-  const int64_t j = (int64_t)blockIdx.x * 16 + c;
-  double s = 0.0;
-  if (j < 2 * a.n) {
+  for (int64_t j0 = (int64_t)blockIdx.x * 16; j0 < 2 * a.n; j0 += (int64_t)gridDim.x * 16) {
+    const int64_t j = j0 + c;
+    double s = 0.0;
+    if (j < 2 * a.n) {
 #pragma unroll 4
-    for (int64_t g = slot; g < a.groups; g += 16) s += (double)a.sums[g * 2 * a.n + j];
+      for (int64_t g = slot; g < a.groups; g += 16) s += (double)a.sums[g * 2 * a.n + j];
+    }
+    lds[threadIdx.x] = s;
+    __syncthreads();
+    if (slot == 0 && j < 2 * a.n) {
+      for (int p = 1; p < 16; ++p) s += lds[p * 16 + c];
+      float* out = j < a.n ? a.dweight : a.dbias;
+      if (out) out[j < a.n ? j : j - a.n] = (float)s;
+    }
+    __syncthreads();
   }
-  lds[threadIdx.x] = s;
-  __syncthreads();
-  if (slot != 0 || j >= 2 * a.n) return;
-  for (int p = 1; p < 16; ++p) s += lds[p * 16 + c];
-  float* out = j < a.n ? a.dweight : a.dbias;
-  if (out) out[j < a.n ? j : j - a.n] = (float)s;
 }
 
 constexpr int64_t kMostGroups = 256;  // one workgroup per CU
@@ -485,7 +489,8 @@ void norm_gradient_type(const NormGradientArgs& a, hipStream_t s) {
       default: norm_gradient_for<T, 1024>(a, s); break;
     }
   }
-  if (a.sums) norm_gradient_finish<<<(unsigned)((2 * a.n + 15) / 16), 256, 0, s>>>(a);
+  const int64_t finish = (2 * a.n + 15) / 16, most = 1 << 20;  // threads of a launch stay below 2^32
+  if (a.sums) norm_gradient_finish<<<(unsigned)(finish < most ? finish : most), 256, 0, s>>>(a);
 }
 
 }  // namespace

@@ -234,3 +234,30 @@ def test_long_constant_rows(n, dtype):
     torch.cuda.synchronize()
     assert torch.equal(mean, X[:, 0].float()) and not out.any()
     assert torch.allclose(rstd, torch.full_like(rstd, 1e-5 ** -0.5))
+
+
+def test_longest_rows():
+    """A row of 2^27 - 1 columns, the most. The row's sums are fp64 of four terms at a time in fp32; what is left are the roundings
+    of xhat (2), h (1), the means of h (3 additions, stored) and h xhat (the same, and 4 of its terms) and of the formula
+    (5), each 2^-24 of what it rounds."""
+    n, U = 2 ** 27 - 1, N.U
+    g = torch.Generator(dev()).manual_seed(1)
+    X = torch.randn(1, n, generator=g, device=dev()) + 100.0
+    G, w = torch.full((1, n), 0.1, device=dev()), torch.rand(n, generator=g, device=dev()) * 0.01 + 1.0
+    note("layer_norm of 2^27 - 1 columns")
+    out, mean, rstd = xt.layer_norm(X, w, save_stats=True)
+    got = xt.layer_norm_backward(G, X, mean, rstd, w)
+    torch.cuda.synchronize()
+    x = X.double()
+    ref = x.mean()
+    var = ((x - ref) ** 2).mean()
+    assert abs(mean.double() - ref) <= 2 * U * ref and abs(rstd.double() * torch.sqrt(var + 1e-5) - 1) <= 8 * U
+    d = x - ref
+    # mean off by 2 U of itself, the distance from it, rstd and two products
+    assert ((out.double() - d * rstd.double() * w).abs() <= rstd * w * (2 * U * ref + 4 * U * d.abs()) * 1.01).all()
+    xhat, h = (x - mean.double()) * rstd.double(), G.double() * w
+    s, q, qa = h.mean(), (h * xhat).mean(), (h * xhat).abs().mean()
+    want = rstd.double() * (h - s - xhat * q)
+    bound = rstd * U * (h + 4 * s + 8 * qa * xhat.abs() + 2 * xhat.abs() * q.abs() + 5 * (h + s.abs() + (xhat * q).abs())) * 1.01
+    assert ((got[0].double() - want).abs() <= bound).all()
+    assert ((got[1].double() - (G * xhat)[0]).abs() <= 4 * U * (G * xhat)[0].abs()).all() and torch.equal(got[2], G[0])

@@ -139,3 +139,12 @@ def test_helpers_refuse_what_the_kernels_cannot_take():
                  lambda: xt.embedding(ids, X, out=X), lambda: xt.embedding_backward(X, ids, 4, dtable=X)):
         with pytest.raises(xt.XtvxyError):
             call()
+
+
+@pytest.mark.parametrize("s", SUFFIXES)
+def test_widest_layer_norm(s):
+    """Rows of up to 2^27 - 1 columns are taken, wider ones refused; both before anything is launched."""
+    far = {"G": A, "X": 2 * A, "dX": 3 * A, "weight": 4 * A, "dweight": 5 * A, "dbias": 6 * A, "mean": 7 * A, "rstd": 8 * A}
+    for n, want in ((2 ** 27 - 1, WORKSPACE), (2 ** 27 - 8, WORKSPACE), (2 ** 27, UNSUPPORTED)):
+        assert norm_backward_status(s, m=1, n=n, ldg=n, ldx=n, lddx=n, **far) == want
+    assert norm_status(s, m=1, n=2 ** 27, ldx=2 ** 27, ldo=2 ** 27, X=A, out=2 * A, weight=3 * A, bias=4 * A) == UNSUPPORTED
