@@ -89,6 +89,49 @@ __device__ __forceinline__ float row_sum(const float* lds, int first) {
   return s;
 }
 
+// A row's squares may have left fp32 where its variance (with eps) is infinite or NaN (distances beyond 1.8e19), or below 2^-100
+// (next to an eps as small, below 1e-19).
+constexpr float kLeastVariance = 0x1p-100f, kMostRstd = 0x1p50f;
+__device__ __forceinline__ bool out_of_range(float variance) { return !(variance >= kLeastVariance && variance < __builtin_inff()); }
+
+// The sum over a workgroup of kThreads, or over a wavefront (64), the same in every thread; `lds` has kThreads / 64 doubles.
+template <int kThreads>
+__device__ __forceinline__ double wide_sum(double x, double* lds) {
+#pragma unroll
+  for (int by = 1; by < 64; by *= 2) x += __shfl_xor(x, by);
+  if constexpr (kThreads > 64) {
+    __syncthreads();
+    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = x;
+    __syncthreads();
+    x = lds[0];
+    for (int w = 1; w < kThreads / 64; ++w) x += lds[w];
+  }
+  return x;
+}
+
+// Row i, by thread t of kThreads, with its sums in fp64; where not `always`, only if its variance is below kLeastVariance.
+template <typename T, int kThreads>
+__device__ __forceinline__ void wide_row(const NormArgs& a, int64_t i, int t, double* lds, bool always) {
+  const T* x = static_cast<const T*>(a.x) + i * a.ldx;
+  T* out = static_cast<T*>(a.out) + i * a.ldo;
+  double s = 0.0, q = 0.0;
+  for (int64_t j = t; j < a.n; j += kThreads) s += (double)(float)x[j];
+  const float mean = (float)(wide_sum<kThreads>(s, lds) / (double)a.n);
+  for (int64_t j = t; j < a.n; j += kThreads) {
+    const double d = (double)((float)x[j] - mean);
+    q += d * d;
+  }
+  const double variance = wide_sum<kThreads>(q, lds) / (double)a.n + (double)a.eps;
+  if (!always && variance >= kLeastVariance) return;
+  const float rstd = (float)(1.0 / sqrt(variance));
+  if (t == 0) {
+    if (a.mean) a.mean[i] = mean;
+    if (a.rstd) a.rstd[i] = rstd;
+  }
+  for (int64_t j = t; j < a.n; j += kThreads)
+    out[j] = (T)fmaf(((float)x[j] - mean) * rstd, a.weight ? a.weight[j] : 1.0f, a.bias ? a.bias[j] : 0.0f);
+}
+
 // A row's mean and sum of squared distances from it. Each wavefront forms its own mean first and takes
 // distances from that (no cancellation); the wavefronts' (mean, distances) join as
 //     mean = sum n_w mean_w / n,  sum = sum_w (sum_w + n_w (mean_w - mean)^2).
@@ -96,6 +139,7 @@ template <typename T, int L, int C, bool kStreamed>
 __global__ __launch_bounds__(L < 256 ? 256 : L) void norm_rows(NormArgs a) {
   constexpr int V = kChunkOf<T>, kBlock = L < 256 ? 256 : L, kRows = kBlock / L, kWaves = L / 64, kGroup = L < 64 ? L : 64;
   __shared__ float part[2][2][kBlock / 64];
+  __shared__ double wide[kBlock / 64];
   const int t = threadIdx.x % L, sub = threadIdx.x / L, lane = threadIdx.x & 63;
   const Columns<T, L, C> k(a.n, t);
   float w[C][V], b[C][V];
@@ -120,6 +164,7 @@ __global__ __launch_bounds__(L < 256 ? 256 : L) void norm_rows(NormArgs a) {
   Chunks<T, C> next;
   next.load(X + (i < a.m ? i : a.m - 1) * a.ldx, k);
   int turn = 0;
+  uint32_t largest = 0;  // rstd, as bits: NaN is beyond all
   for (int64_t i0 = (int64_t)blockIdx.x * kRows; i0 < a.m; i0 += step, i += step, turn ^= 1) {
     float x[C][V];
 #pragma unroll
@@ -161,8 +206,11 @@ __global__ __launch_bounds__(L < 256 ? 256 : L) void norm_rows(NormArgs a) {
         q += squares[v] + counts[v] * d * d;
       }
     }
-    const float rstd = 1.0f / sqrtf(q / n + a.eps);
     if (i >= a.m) continue;
+    const float variance = q / n + a.eps;
+    const float rstd = fmaf(variance, 0.0f, 1.0f / sqrtf(variance));  // NaN of an infinite variance
+    const uint32_t bits = __float_as_uint(rstd);
+    largest = largest > bits ? largest : bits;
     if (t == 0) {
       if (a.mean) a.mean[i] = mean;
       if (a.rstd) a.rstd[i] = rstd;
@@ -177,54 +225,48 @@ __global__ __launch_bounds__(L < 256 ? 256 : L) void norm_rows(NormArgs a) {
       store_chunk<kStreamed>(out + k.at[c], o);
     }
   }
-}
-
-// The sum over a workgroup of kThreads, the same in every thread; `lds` has kThreads / 64 numbers.
-template <int kThreads, typename Sum>
-__device__ __forceinline__ Sum block_sum(Sum x, Sum* lds) {
-  if constexpr (sizeof(Sum) == 4) {
-    x = group_sum(x, 64);
-  } else {
-#pragma unroll
-    for (int by = 1; by < 64; by *= 2) x += __shfl_xor(x, by);
-  }
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = x;
-  __syncthreads();
-  x = lds[0];
-#pragma unroll
-  for (int w = 1; w < kThreads / 64; ++w) x += lds[w];
-  return x;
-}
-
-// Sums of rows longer than registers are fp64: a thread's may have 2^17 terms. In fp32 the mean of 4 10^7 times 1.1 drifts to
-// 1.1002, which 1 / sqrt(eps) makes 0.06. (us, fp32: 2000 x 20001 111, summed in fp32 104; 1000 x 100003 385, 375.)
-template <int kThreads>
-using RowSum = std::conditional_t<kThreads == 64, float, double>;
-
-// Rows shorter than a chunk (64 threads) or longer than the registers of 1024 threads: a workgroup walks the row once for
-// the mean, once for the distances and once for the output (the second and third time out of L2).
-template <typename T, int kThreads>
-__global__ __launch_bounds__(kThreads) void norm_any(NormArgs a) {
-  typedef RowSum<kThreads> Sum;
-  __shared__ Sum lds[kThreads / 64];
-  for (int64_t i = blockIdx.x; i < a.m; i += gridDim.x) {
-    const T* x = static_cast<const T*>(a.x) + i * a.ldx;
-    T* out = static_cast<T*>(a.out) + i * a.ldo;
-    Sum s = 0, q = 0;
-    for (int64_t j = threadIdx.x; j < a.n; j += kThreads) s += (Sum)(float)x[j];
-    const float mean = (float)(block_sum<kThreads>(s, lds) / (Sum)a.n);
-    for (int64_t j = threadIdx.x; j < a.n; j += kThreads) {
-      const Sum d = (Sum)((float)x[j] - mean);
-      q += d * d;
+  // Rows out of range (of an infinite variance all outputs are NaN so far) once more, by the workgroup or, where a wavefront
+  // has rows of its own, by it. (us, 10392 x 1269 of bf16 13.50, without the two operations a row that look for them 13.49,
+  // handled where they occur 13.9; 5001 x 1111 of fp32 12.9, 12.7; 2000 x 32768 of bf16 121, 117.)
+  constexpr int kTeam = L > 64 ? kBlock : 64, kTeamRows = kTeam / L;
+  if (!__any(largest > __float_as_uint(kMostRstd))) return;  // alike in a whole team
+  __threadfence();
+  if (L > 64) __syncthreads();
+  for (int64_t i0 = (int64_t)blockIdx.x * kRows + threadIdx.x / kTeam * kTeamRows; i0 < a.m; i0 += step)
+    for (int64_t row = i0; row < i0 + kTeamRows && row < a.m; ++row) {
+      const float first = (float)static_cast<const T*>(a.out)[row * a.ldo];
+      wide_row<T, kTeam>(a, row, threadIdx.x % kTeam, wide, first != first);
     }
-    const float rstd = (float)(1 / sqrt(block_sum<kThreads>(q, lds) / (Sum)a.n + (Sum)a.eps));
-    if (threadIdx.x == 0) {
+}
+
+// Rows longer than the registers of 1024 threads: a workgroup walks the row once for the mean, once for the distances and
+// once for the output (the second and third time out of L2). The sums are fp64: a thread's may have 2^17 terms. In fp32 the
+// mean of 4 10^7 times 1.1 drifts to 1.1002, which 1 / sqrt(eps) makes 0.06. (us, fp32: 2000 x 20001 111, summed in fp32 104;
+// 1000 x 100003 385, 375.)
+template <typename T>
+__global__ __launch_bounds__(1024) void norm_long(NormArgs a) {
+  __shared__ double lds[1024 / 64];
+  for (int64_t i = blockIdx.x; i < a.m; i += gridDim.x) wide_row<T, 1024>(a, i, threadIdx.x, lds, true);
+}
+
+// Rows shorter than a chunk, a wavefront each.
+template <typename T>
+__global__ __launch_bounds__(64) void norm_short(NormArgs a) {
+  const int j = threadIdx.x;
+  const bool on = j < a.n;
+  for (int64_t i = blockIdx.x; i < a.m; i += gridDim.x) {
+    const float x = on ? (float)static_cast<const T*>(a.x)[i * a.ldx + j] : 0.0f;
+    const float mean = group_sum(x, 64) / (float)a.n, d = on ? x - mean : 0.0f;
+    const float variance = group_sum(d * d, 64) / (float)a.n + a.eps, rstd = 1.0f / sqrtf(variance);
+    if (out_of_range(variance)) {
+      wide_row<T, 64>(a, i, threadIdx.x, nullptr, true);
+      continue;
+    }
+    if (j == 0) {
       if (a.mean) a.mean[i] = mean;
       if (a.rstd) a.rstd[i] = rstd;
     }
-    for (int64_t j = threadIdx.x; j < a.n; j += kThreads)
-      out[j] = (T)fmaf(((float)x[j] - mean) * rstd, a.weight ? a.weight[j] : 1.0f, a.bias ? a.bias[j] : 0.0f);
+    if (on) static_cast<T*>(a.out)[i * a.ldo + j] = (T)fmaf(d * rstd, a.weight ? a.weight[j] : 1.0f, a.bias ? a.bias[j] : 0.0f);
   }
 }
 
@@ -331,7 +373,16 @@ __global__ __launch_bounds__(kGradientThreads) void norm_gradient_rows(NormGradi
     }
 }
 
-// Rows of any length: the sums and dX of a row by one workgroup, which walks it twice. The sums are as norm_any's, four terms
+// The sum of either type over a workgroup.
+template <int kThreads>
+using RowSum = std::conditional_t<kThreads == 64, float, double>;
+template <int kThreads>
+__device__ __forceinline__ RowSum<kThreads> block_sum(RowSum<kThreads> x, RowSum<kThreads>* lds) {
+  if constexpr (kThreads == 64) return group_sum(x, 64);
+  else return wide_sum<kThreads>(x, lds);
+}
+
+// Rows of any length: the sums and dX of a row by one workgroup, which walks it twice. The sums of long ones are fp64, four terms
 // at a time in fp32. (us, 2000 x 32768 of bf16: 265, each term in fp64 345, all in fp32 251.)
 template <typename T, int kThreads>
 __global__ __launch_bounds__(kThreads) void norm_gradient_any(NormGradientArgs a) {
@@ -434,8 +485,8 @@ void norm_type(const NormArgs& a, hipStream_t s) {
   constexpr int V = kChunkOf<T>;
   if (a.n < V || a.n > 1024 * 4 * V) {
     const unsigned grid = (unsigned)(a.m < 4096 ? a.m : 4096);
-    if (a.n < V) norm_any<T, 64><<<grid, 64, 0, s>>>(a);
-    else norm_any<T, 1024><<<grid, 1024, 0, s>>>(a);
+    if (a.n < V) norm_short<T><<<grid, 64, 0, s>>>(a);
+    else norm_long<T><<<grid, 1024, 0, s>>>(a);
   } else if (a.n <= 16 * 4 * V) {
     norm_for<T, 16>(a, s);
   } else if (a.n <= 64 * 4 * V) {

@@ -817,8 +817,8 @@ xtvxy_status xtvxy_adamw_state_values(xtvxy_adamw optimiser, void *const *m_out,
  *     out_ij = (x_ij - mean_i) rstd_i weight_j + bias_j.
  * X and out share one element type (fp32, or bf16 / fp16 bit patterns); weight, bias (n floats, NULL: ones,
  * zeros) and the statistics mean and rstd (m floats, NULL: not stored) are fp32. Everything is computed in
- * fp32 (the sums over rows that are too long for registers in fp64), the squares as distances from the mean, and
- * rounded once as it is stored. NaN and infinities spread
+ * fp32 (the sums over rows that are too long for registers, or whose squares or sums leave fp32, in fp64), the squares as
+ * distances from the mean, and rounded once as it is stored. NaN and infinities spread
  * over their row as the formulas say. eps finite and >= 0; n below 2^27. m == 0 or n == 0 is a no-op. An output
  * that overlaps an input or another output gives XTVXY_ERROR_ALIASING. Pointers and strides of any alignment;
  * results are bitwise reproducible. */

@@ -261,3 +261,45 @@ def test_longest_rows():
     bound = rstd * U * (h + 4 * s + 8 * qa * xhat.abs() + 2 * xhat.abs() * q.abs() + 5 * (h + s.abs() + (xhat * q).abs())) * 1.01
     assert ((got[0].double() - want).abs() <= bound).all()
     assert ((got[1].double() - (G * xhat)[0]).abs() <= 4 * U * (G * xhat)[0].abs()).all() and torch.equal(got[2], G[0])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("n", [3, 8, 100, 1000, 1030, 4096, 5003, 12000, 20001, 40000])
+def test_rows_whose_squares_leave_fp32(n, dtype):
+    """Distances whose squares are beyond fp32's largest or below its smallest numbers, next to ordinary rows."""
+    dt = L.DTYPES[dtype]
+    X = rand((23, n), n)
+    X *= torch.tensor([1.0, 1e20, 1e-25, 3e37, 1e-30, 1e10, 1e-15, 1e19])[torch.arange(23) % 8][:, None]
+    X[8] = 0.0
+    X[9] += 1e25  # the mean is far, the distances as those of row 1
+    X = X.to(dt)
+    w, b = rand(n, 1, offset=1.0), rand(n, 2)
+    for eps in (0.0, 1e-38, 1e-5, 1e30):
+        note("layer_norm scaled rows %d %s %g" % (n, dtype, eps))
+        out, mean, rstd = xt.layer_norm(*cuda(X, w, b), eps, save_stats=True)
+        torch.cuda.synchronize()
+        # a row without distances has no 1 / 0
+        rows = [i for i in range(23) if eps > 0 or (X[i] != X[i, 0]).any()]
+        for t, (ref, bound), what in zip((out, mean, rstd), N.forward(X, w, b, eps), ("out", "mean", "rstd")):
+            L.check(t[rows], ref[rows], bound[rows], "%s eps %g" % (what, eps))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("size", [(33000, 100), (8300, 1001), (2200, 4096), (1100, 12000)], ids=lambda s: "%dx%d" % s)
+def test_rows_next_to_those_that_leave_fp32(size, dtype):
+    """Rows of any turn of a workgroup, and what they leave of the others: every bit."""
+    m, n = size
+    dt = L.DTYPES[dtype]
+    X, w, b = cuda(rand((m, n), 1, dt), rand(n, 2, offset=1.0), rand(n, 3))
+    plain = xt.layer_norm(X, w, b, 0.0, save_stats=True)
+    rows = torch.tensor([0, 5, m // 3, m // 2 + 1, m - 2, m - 1], device=dev())
+    scales = torch.tensor([1e25, 1e-24, 1e30, 1e-30, 1e-23, 1e20], device=dev())
+    X[rows] = (X[rows].float() * scales[:, None]).to(dt)
+    note("layer_norm next to far rows %s %s" % (size, dtype))
+    got = xt.layer_norm(X, w, b, 0.0, save_stats=True)
+    torch.cuda.synchronize()
+    for t, (ref, bound), what in zip(got, N.forward(X[rows], w, b, 0.0), ("out", "mean", "rstd")):
+        L.check(t[rows], ref, bound, what)
+    others = torch.ones(m, dtype=torch.bool, device=dev())
+    others[rows] = False
+    assert all(torch.equal(t[others], u[others]) for t, u in zip(got, plain))
