@@ -463,8 +463,10 @@ template <typename T, int L, bool kStreamed>
 void norm_launch(const NormArgs& a, unsigned grid, hipStream_t s) {
   constexpr int kBlock = L < 256 ? 256 : L;
   const int64_t chunks = (a.n + kChunkOf<T> - 1) / kChunkOf<T>;
-  if (chunks <= L) norm_rows<T, L, 1, kStreamed><<<grid, kBlock, 0, s>>>(a);
-  else if (chunks <= 2 * L) norm_rows<T, L, 2, kStreamed><<<grid, kBlock, 0, s>>>(a);
+  if constexpr (L == 16) {  // more threads come with more chunks than threads
+    if (chunks <= L) return norm_rows<T, L, 1, kStreamed><<<grid, kBlock, 0, s>>>(a);
+  }
+  if (chunks <= 2 * L) norm_rows<T, L, 2, kStreamed><<<grid, kBlock, 0, s>>>(a);
   else norm_rows<T, L, 4, kStreamed><<<grid, kBlock, 0, s>>>(a);
 }
 
