@@ -591,3 +591,30 @@ def test_few_rows_over_several_pieces(s, dtype):
     ref = O.backward(grad, X, W, b, classes, weights.double(), torch.zeros_like(P), T, lse=lse)
     for t, name in zip((dX, dW, db), ("dX", "dW", "db")):
         inside(t, *ref[name], what=name)
+
+
+@pytest.mark.parametrize("offset", [0, 400, -3000])
+@pytest.mark.parametrize("size", [(64, 5120), (200, 20480), (130, 5000)], ids=lambda s: "%dx%d" % s)
+def test_far_logits_keep_their_distances(size, offset):
+    """fp32 logits that are whole numbers, exact: an exponential is off by its distance's roundings, however far from zero
+    all of them are. Features that are one for one row and weigh nothing make dW hold d itself."""
+    m, n = size
+    g = torch.Generator(dev()).manual_seed(n)
+    X = torch.cat([torch.ones(m, 1, device=dev()), torch.randint(-2, 3, (m, 15), generator=g, device=dev()).float(), torch.eye(m, device=dev())], 1)
+    W = torch.zeros(n, 16 + m, device=dev())
+    W[:, 0], W[:, 1:16] = offset, torch.randint(-1, 2, (n, 15), generator=g, device=dev()).float()
+    labels = torch.randint(0, n, (m,), generator=g, device=dev())
+    grad = torch.rand(m, generator=g, device=dev()) + 0.5
+    note("far logits %s %d" % (size, offset))
+    loss, lse = xt.linear_cross_entropy(X, W, labels)
+    _, dW, _ = xt.linear_cross_entropy_backward(grad, X, W, labels, lse)
+    torch.cuda.synchronize()
+    t = X.double() @ W.double().T
+    ref, e, p = O._lse(t, torch.zeros_like(t))
+    inside(lse, ref[:, 0], e[:, 0], "lse")
+    inside(loss, ref[:, 0] - t.gather(1, labels[:, None])[:, 0], e[:, 0] + 2 * O.U * ref[:, 0].abs(), "loss")
+    far = t - lse.double()[:, None]  # rounded once, then as every exponential
+    p, on = torch.exp(far), torch.zeros_like(t).scatter_(1, labels[:, None], 1.0)
+    d = grad.double()[:, None] * (p - on)
+    bound = grad.double()[:, None] * (p * (O._exp_error(far) + O.U * far.abs() + 4 * O.U) + 2 * O.U * on) + 2 * O.U * d.abs()
+    inside(dW[:, 16:].T, d, bound + 1e-40, "d")
