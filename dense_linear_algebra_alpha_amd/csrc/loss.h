@@ -27,6 +27,7 @@ constexpr int64_t kMostHalves = 8192;
 // The order is a launch of 3 to 6 us; searched lists cost every tile its rows' places. us, ordered and searched, with the
 // gradient, bf16: 64 x 512 x 192 with 48 a row 45, 42; 512 x 512 x 4000 with 24 56, 48, with 48 60, 57; 1024 x 512 x 8000
 // with 24 89, 87, with 48 93, 101; 4096 x 512 x 2000 with 24 91, 91, with 48 96, 104; 4096 x 512 x 16000 with 12 334, 351.
+// Of these the rule misses one: it orders 512 x 512 x 4000 with 48.
 inline bool order_pays(int64_t m, int64_t n, int64_t per_row) {
   return per_row >= 9 && (double)per_row * (1.0 + (double)m * n / (1 << 23)) >= 52.0;
 }

@@ -13,10 +13,10 @@
 // in the element type, goes through the layer's gradient kernel.
 //
 // Tiles are the product's: of 256 x 256 the product over 1000 features takes 26 us, first loads and epilogue 15 to 20, in
-// which the matrix unit waits. us: bf16 8192 x 2048 x 65536 forward 1634 (1.35 PFLOP/s, matrix unit 68% busy), with the gradient 6600; fp16
-// 2047 x 1000 x 30001 with 32 classes a row 615 with the gradient (187 forward, 185 d, 238 its products); fp32 512 x 768 x
-// 16384 100 (fp32 matrix unit 89% busy). Few rows are bound by W: fp16 13 x 4096 x 32000 60, of which its one pass 51 (5.2
-// TB/s).
+// which the matrix unit waits. us: bf16 8192 x 2048 x 65536 forward 1590 to 1660 from card to card (1.39 to 1.33 PFLOP/s, matrix
+// unit 68% busy), with the gradient 6600; fp16 2047 x 1000 x 30001 with 32 classes a row 610 with the gradient (186 forward,
+// 182 d, 232 its products); fp32 512 x 768 x 16384 100 (fp32 matrix unit 89% busy). Few rows are bound by W: fp16 13 x 4096 x
+// 32000 60, of which its one pass 51 (5.2 TB/s).
 #include "linear_ring.h"
 #include "loss.h"
 
@@ -172,9 +172,10 @@ __device__ __forceinline__ void lane_logits(const f32x4 (&z)[FB], const f32x4 (&
 // exp(z c - ref) in the place of exp(z / T - ref / log2 e), c = log2 e / T, takes one operation less than the exact
 // difference with the bias and its product with log2 e: for 16-bit features without a bias, in whole tiles, and while ref stays
 // finite. c and ref are each off by half a step, together 2^-23 |z| of the exponential: about the rounding of the logits
-// themselves, and for logits up to 4000 below half a step of an fp16 d. In fp32 that would be seen (1024 x 512 x 32768 with logits up to 30: dX off by
-// 2.09e-6 instead of 2.05e-6; 64 x 256 x 16384, up to 120: 4.65e-6 instead of 3.68e-6; logits that are exact and 3000 below
-// zero: 290 roundings of d), and costs 0.1 to 0.5% (773.7 us with the gradient against 772.9).
+// themselves, and for logits up to 4000 below half a step of an fp16 d. In fp32 that would be seen (1024 x 512 x 32768 with
+// logits up to 30: dX off by 2.09e-6 instead of 2.05e-6; 64 x 256 x 16384, up to 120: 4.65e-6 instead of 3.68e-6; logits that
+// are exact and 3000 below zero: 290 roundings of d). The exact difference costs 0.1 to 0.5% there (773.7 us with the
+// gradient against 772.9).
 constexpr float kLog2e = 1.44269504f, kLn2 = 0.693147181f, kFarLogit = 1e38f;
 
 __device__ __forceinline__ float max_xor16(float x) {
@@ -268,6 +269,10 @@ struct StatsEnd {
   }
 };
 
+// d is stored in the type of the features: the matrix instructions of its two products take both operands in one type, and the
+// layer's gradient rounds its own d alike. What that costs 16-bit dX and dW, in the 2-norm: bf16 1.64e-3 (their own
+// rounding) to 2.22e-3, fp16 2.1e-4 to 2.9e-4, where rows have unlike factors (alike: see LossFactorArgs). A d of two
+// 16-bit parts would double the work of the products, which are half of the time. Column sums take it in fp32.
 struct GradientEnd {
   const LossGradientArgs& l;
   template <typename T, int BM, int BN, typename S>

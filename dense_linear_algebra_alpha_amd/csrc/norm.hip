@@ -6,13 +6,15 @@
 //     dweight = sum_i g_ij xhat_ij,  dbias = sum_i g_ij.
 //
 // Both are bound by memory: the forward pass reads and writes each element once, the gradient reads two and
-// writes one. A row stays in the registers of the threads that share it (a wavefront, 4 or 16) between its
-// sums and its output. Threads keep their columns from row to row, so weight and bias are loaded once per
-// workgroup and the gradient's column sums stay in registers; the next row is loaded before the sums of the
-// current one are joined.
+// writes one. Forward: a row is shared by 16, 64, 256 or 1024 threads, in whose registers it stays between its sums and its
+// output; threads keep their columns from row to row, so weight and bias are loaded once per workgroup, and the next row is
+// loaded before the sums of the current one are joined. (In 16 bits, rows of more than 16384 columns are more than the
+// registers hold: 75 of a thread's go to scratch memory.) Gradient: a row is shared by 16 to 1024 threads, every power of
+// two; its column sums stay in registers, the weight is reloaded for every row, and the next row is loaded ahead but for fp32
+// rows of more than 8192 columns. Rows shorter than 16 bytes, or longer than the registers, have kernels of their own.
 //
-// us of the kernels: forward with statistics, bf16 16384 x 4096, 52 (5.1 TB/s, what a copy reaches), 1 x 4096 2.5;
-// gradient of the same 78 (5.3 TB/s) and 5 for the columns' sums of 256 workgroups, fp32 5001 x 1111 15.5 and 4.
+// us of the kernels: forward with statistics, bf16 16384 x 4096, alone 53 (5.1 TB/s, what a copy reaches), one of many 47;
+// 1 x 4096 2.3; gradient of the same 78 (5.3 TB/s) and 5 for the columns' sums of 256 workgroups, fp32 5001 x 1111 16 and 4.
 //
 // A row's last chunk of 16 bytes, where n is no multiple of one, is the last 16 bytes of the row: memory
 // takes any alignment, a branch around its loads would make every row wait for them. What it shares with
@@ -482,6 +484,12 @@ void norm_for(const NormArgs& a, hipStream_t s) {
   else norm_launch<T, L, false>(a, grid, s);
 }
 
+// Threads of a row: the fewest of 16, 64, 256 and 1024 with up to four chunks each. us with these, and with twice or half as
+// many: bf16 40000 x 256 9.4, 10.5; 30000 x 500 12.6, 11.1; 20000 x 768 12.9, 13.5 with half, 17.8; 10392 x 1269 13.6, 14.5;
+// 16384 x 2048 24.2, 22.5; 16384 x 4096 47.6, 53.1 with half, 58.1; 8192 x 5120 34.1, 33.5; 4000 x 12000 42.9, 37.5 with half;
+// 4000 x 16384 49.0, 49.2 with half; fp32 40000 x 250 17.1, 14.6; 8192 x 768 9.9, 10.3; 5001 x 1111 12.8, 10.0 with half; 4000 x
+// 4000 20.9, 21.0; 4000 x 6000 38.6, 33.2 with half. So every power of two would serve some widths better; with these four
+// a call takes up to 29% longer than with the best.
 template <typename T>
 void norm_type(const NormArgs& a, hipStream_t s) {
   constexpr int V = kChunkOf<T>;

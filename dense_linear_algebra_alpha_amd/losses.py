@@ -220,7 +220,8 @@ def linear_cross_entropy_backward(grad, X, W, labels, lse, bias=None, *, need_dX
                                   dW=None, db=None, workspace=None, stream=None):
     """The gradient of linear_cross_entropy: (dX, dW, db) for grad[i] = d total / d loss[i] (float32, m) from the
     forward call's lse. With d[i, j] = grad[i] (softmax(z)[i, j] - [j == labels[i]]): dX = d W, dW = d^T X, and db the
-    column sums of d (float32). A mean over the rows that count has grad = 1 / their number.
+    column sums of d (float32). A mean over the rows that count has grad = 1 / their number. The products take d in the
+    features' type: 16-bit dX and dW are off by up to 1.41 times their own rounding.
 
     Outputs that are not needed are not computed and come back as None."""
     if stream is None:
