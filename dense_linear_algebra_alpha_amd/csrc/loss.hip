@@ -169,14 +169,22 @@ __device__ __forceinline__ void lane_logits(const f32x4 (&z)[FB], const f32x4 (&
     for (int e = 0; e < 4; ++e) t[y][e] = fmaf(z[y][e], inv_temperature, bias[y][e]);
 }
 
-// exp(z c - ref) in the place of exp(z / T - ref / log2 e), c = log2 e / T, takes one operation less than the exact
-// difference with the bias and its product with log2 e: for 16-bit features without a bias, in whole tiles, and while ref stays
-// finite. c and ref are each off by half a step, together 2^-23 |z| of the exponential: about the rounding of the logits
-// themselves, and for logits up to 4000 below half a step of an fp16 d. In fp32 that would be seen (1024 x 512 x 32768 with
-// logits up to 30: dX off by 2.09e-6 instead of 2.05e-6; 64 x 256 x 16384, up to 120: 4.65e-6 instead of 3.68e-6; logits that
-// are exact and 3000 below zero: 290 roundings of d). The exact difference costs 0.1 to 0.5% there (773.7 us with the
-// gradient against 772.9).
-constexpr float kLog2e = 1.44269504f, kLn2 = 0.693147181f, kFarLogit = 1e38f;
+// Of 16-bit features without a bias, in whole tiles, exp(t - u) is exp2(z c - ref), c = log2 e / T and ref = u log2 e: one
+// operation less than the difference with the bias and its product with log2 e. What the roundings of c and ref leave, 2^-23
+// |u|, is nearly alike in all of a row's logits that count, those next to u: one factor a row takes it out. Beyond
+// kFarLogit ref's rounding would leave no distance (at 1e11 it was thousands). The factors cost nothing that shows (us with
+// and without, with the gradient: bf16 8192 x 2048 x 65536 6656, 6661; 2048 x 256 x 32768 242.9, 242.0). fp32 takes the exact
+// difference, at 0.1 to 0.5% (1024 x 512 x 32768 with the gradient 773.7, 772.9).
+constexpr float kLog2e = 1.44269504f, kLn2 = 0.693147181f, kFarLogit = 1e6f;
+struct Log2Scale {
+  float c, rest;  // rest: what c's rounding takes off the product with T u, per u
+  __device__ __forceinline__ explicit Log2Scale(float inv_temperature)
+      : c(inv_temperature * kLog2e), rest(fmaf(inv_temperature, kLog2e, -c) / inv_temperature) {}
+  // of exp2(z c - ref), z next to T u: the constant log2 e's own rounding is in both and cancels
+  __device__ __forceinline__ float correction(float u, float ref) const {
+    return __builtin_amdgcn_exp2f(fmaf(u, rest, -fmaf(u, kLog2e, -ref)));
+  }
+};
 
 __device__ __forceinline__ float max_xor16(float x) {
   const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
@@ -201,7 +209,7 @@ struct StatsEnd {
     end_of_products(sums);
     float* stats = l.stats + (p.j0 / BN * 2 + (wave & 1)) * a.m * 2;
     const bool plain = sizeof(T) == 2 && !l.bias && p.j0 + BN <= a.n;
-    const float c = l.inv_temperature * kLog2e;
+    const Log2Scale log2(l.inv_temperature);
 #pragma unroll
     for (int x = 0; x < FA; ++x) {
       const f32x4(&z)[FB] = sums.acc[x];
@@ -213,14 +221,15 @@ struct StatsEnd {
         for (int y = 0; y < FB; ++y)
 #pragma unroll
           for (int e = 0; e < 4; ++e) top = fmaxf(top, z[y][e]);
-        top = max_xor32(max_xor16(top)) * c;
-        done = __all(fabsf(top) < kFarLogit);
+        const float ref = max_xor32(max_xor16(top)) * log2.c;
+        done = __all(fabsf(ref) < kFarLogit);
         if (done) {
 #pragma unroll
           for (int y = 0; y < FB; ++y)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) s += __builtin_amdgcn_exp2f(fmaf(z[y][e], c, -top));
-          top *= kLn2;
+            for (int e = 0; e < 4; ++e) s += __builtin_amdgcn_exp2f(fmaf(z[y][e], log2.c, -ref));
+          top = ref * kLn2;
+          s *= log2.correction(top, ref);
         }
       }
       if (!done) {
@@ -295,7 +304,7 @@ struct GradientEnd {
     }
     end_of_products(sums);
     const bool plain = sizeof(T) == 2 && !l.bias && p.j0 + BN <= a.n && __all(near);
-    const float c = l.inv_temperature * kLog2e;
+    const Log2Scale log2(l.inv_temperature);
     float* area = reinterpret_cast<float*>(ring + wave * Strip::kArea);
     const int64_t width = a.n - p.j0 - wj;
     const int c8 = lane % kLanes;
@@ -314,10 +323,11 @@ struct GradientEnd {
         f32x4 d[FB];
         if (plain) {
           const float ref = norms[x] * kLog2e;
+          const float near_factor = factor * log2.correction(norms[x], ref);
 #pragma unroll
           for (int y = 0; y < FB; ++y)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) d[y][e] = factor * __builtin_amdgcn_exp2f(fmaf(sums.acc[x][y][e], c, -ref));
+            for (int e = 0; e < 4; ++e) d[y][e] = near_factor * __builtin_amdgcn_exp2f(fmaf(sums.acc[x][y][e], log2.c, -ref));
         } else {
           lane_logits<FB>(sums.acc[x], bias, l.inv_temperature, d);
 #pragma unroll

@@ -618,3 +618,68 @@ def test_far_logits_keep_their_distances(size, offset):
     d = grad.double()[:, None] * (p - on)
     bound = grad.double()[:, None] * (p * (O._exp_error(far) + O.U * far.abs() + 4 * O.U) + 2 * O.U * on) + 2 * O.U * d.abs()
     inside(dW[:, 16:].T, d, bound + 1e-40, "d")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("temperature", [1.0, 2.0, 0.7])
+@pytest.mark.parametrize("offset", [0, 400, -3008])
+@pytest.mark.parametrize("size", [(64, 8192), (300, 20480), (130, 5000)], ids=lambda s: "%dx%d" % s)
+def test_far_logits_of_16_bits(size, offset, temperature, dtype):
+    """The same of 16-bit features: their losses and db are fp32, and only dX and dW see d rounded."""
+    m, n = size
+    dt = L.DTYPES[dtype]
+    g = torch.Generator(dev()).manual_seed(n)
+    X = torch.cat([torch.ones(m, 1, device=dev()), torch.randint(-2, 3, (m, 15), generator=g, device=dev()).float()], 1).to(dt)
+    W = torch.zeros(n, 16, device=dev())
+    W[:, 0], W[:, 1:] = offset, torch.randint(-1, 2, (n, 15), generator=g, device=dev()).float()
+    W = W.to(dt)
+    classes = torch.randint(0, n, (m, 3), generator=g, device=dev())
+    teacher = torch.randn(m, 3, generator=g, device=dev())
+    grad = torch.rand(m, generator=g, device=dev()) + 0.5
+    note("far logits of 16 bits %s %d %g %s" % (size, offset, temperature, dtype))
+    loss, lse, weights = xt.linear_distillation(X, W, classes, teacher, None, temperature)
+    _, _, db = xt.linear_distillation_backward(grad, X, W, classes, weights, lse, None, temperature)
+    torch.cuda.synchronize()
+    inv = float(torch.tensor(1.0) / torch.tensor(temperature))  # in fp32, as the call has it
+    t = (X.double() @ W.double().T) * inv
+    et = t.abs() * (0.0 if temperature in (1.0, 2.0) else O.U)  # each t is rounded once, or exact
+    ref, e, _ = O._lse(t, et)
+    inside(lse, ref[:, 0], e[:, 0], "lse")
+    P = weights.double()
+    ts = t.gather(1, classes)
+    inner = torch.where(P > 0, torch.log(P.clamp_min(1e-300)) - ts + ref, 0.0)
+    size_of = torch.where(P > 0, torch.log(P.clamp_min(1e-300)).abs() + ts.abs() + ref.abs(), 0.0)
+    inside(loss, (P * inner).sum(1), e[:, 0] + 6 * O.U * (P * size_of).sum(1) + 1e-30, "loss")
+    far = t - lse.double()[:, None]
+    p = torch.exp(far)
+    T = torch.zeros_like(t).scatter_add_(1, classes, P)
+    d = grad.double()[:, None] * inv * (p - T)
+    bound = grad.double()[:, None] * inv * (p * (O._exp_error(far) + et + O.U * far.abs() + 6 * O.U) + 4 * O.U * T) + 2 * O.U * d.abs()
+    inside(db, d.sum(0), bound.sum(0) + (m + 4) * 2 * O.U * d.abs().sum(0) + 1e-40, "db")
+
+
+@pytest.mark.parametrize("dtype", list(L.DTYPES))
+def test_logits_beyond_what_their_exponents_resolve(dtype):
+    """Logits of 2^36 and more (2^30 in fp16): finite, a few equal largest ones, everything else infinitely far below."""
+    m, k, n = 70, 8, 4096
+    dt = L.DTYPES[dtype]
+    big = 2.0 ** 15 if dtype == "f16" else 2.0 ** 18
+    X, W = torch.zeros(m, k, device=dev()), torch.zeros(n, k, device=dev())
+    X[:, 0], W[:, 0] = big, big
+    X[:, 0] *= torch.tensor([1.0, 1.25, 1.5, 1.375], device=dev())[torch.arange(m, device=dev()) % 4]
+    W[[5, 1000, 4000], 0] = big * 1.75
+    labels = torch.tensor([5, 1000, 4000], device=dev())[torch.arange(m, device=dev()) % 3]
+    X, W = X.to(dt), W.to(dt)
+    grad = torch.ones(m, device=dev())
+    note("huge logits %s" % dtype)
+    loss, lse = xt.linear_cross_entropy(X, W, labels)
+    dX, dW, db = xt.linear_cross_entropy_backward(grad, X, W, labels, lse)
+    torch.cuda.synchronize()
+    top = X[:, 0].double() * big * 1.75  # log 3 is below half of its step
+    assert torch.equal(lse.double(), top) and not loss.any()
+    d = torch.zeros(m, n, dtype=torch.float64, device=dev())  # exp(0) of each, less the label
+    d[:, [5, 1000, 4000]] = 1.0
+    d[torch.arange(m), labels] = 0.0
+    assert torch.equal(db.double(), d.sum(0))
+    # sums of a few multiples of 2^12 and 2^16, exact; beyond fp16's largest they round to infinity
+    assert torch.equal(dX, (d @ W.double()).to(dt)) and torch.equal(dW, (d.T @ X.double()).to(dt))

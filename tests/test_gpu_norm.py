@@ -22,6 +22,8 @@ def cuda(*ts):
 
 # one element; rows shorter than 16 bytes; one wavefront, four and sixteen a row, each with every number of chunks a
 # thread; rows beyond the registers; odd widths at each
+# (threads a row since then: forward 16, 64, 256 or 1024, gradient every power of two from 16 to 1024; IN_TURNS_16 and
+# IN_TURNS_32 below reach each of them with rows enough for several turns)
 SIZES = [(1, 1), (3, 2), (7, 5), (1, 8), (5, 9), (4, 64), (9, 100), (1, 511), (70, 512), (13, 777), (33, 1024), (6, 1111),
          (1100, 1030), (5, 2048), (3, 2049), (1, 4096), (300, 4096), (4, 5001), (2, 8192), (3, 10007), (2, 16384), (3, 16385),
          (2, 20001), (2, 33000), (5000, 96), (4099, 260)]
