@@ -303,8 +303,8 @@ struct GradientEnd {
       near &= fabsf(norms[x]) < kFarLogit;
     }
     end_of_products(sums);
-    const bool plain = sizeof(T) == 2 && !l.bias && p.j0 + BN <= a.n && __all(near);
     const Log2Scale log2(l.inv_temperature);
+    const bool plain = sizeof(T) == 2 && !l.bias && p.j0 + BN <= a.n && log2.c < __builtin_inff() && __all(near);
     float* area = reinterpret_cast<float*>(ring + wave * Strip::kArea);
     const int64_t width = a.n - p.j0 - wj;
     const int c8 = lane % kLanes;

@@ -1,6 +1,8 @@
 """GPU parity of the losses over an output layer and their gradients against the fp64 oracle, within bounds that count
 roundings: sizes from one class up, odd ones, several pieces of the vocabulary, rows that do not count, classes taken out
 by the bias, lists with empty and equal places, views, streams, graphs."""
+import math
+
 import pytest
 import torch
 
@@ -683,3 +685,26 @@ def test_logits_beyond_what_their_exponents_resolve(dtype):
     assert torch.equal(db.double(), d.sum(0))
     # sums of a few multiples of 2^12 and 2^16, exact; beyond fp16's largest they round to infinity
     assert torch.equal(dX, (d @ W.double()).to(dt)) and torch.equal(dW, (d.T @ X.double()).to(dt))
+
+
+@pytest.mark.parametrize("dtype", list(L.DTYPES))
+def test_smallest_temperature(dtype):
+    """1 / temperature is finite, its product with log2 e is not: logits of zero stay zero."""
+    m, k, n, T = 70, 16, 8192, 3e-39
+    dt = L.DTYPES[dtype]
+    X, W = torch.zeros(m, k, dtype=dt, device=dev()), rand((n, k), 1, dt).to(dev())
+    classes, teacher = torch.full((m, 2), 7, device=dev()), torch.zeros(m, 2, device=dev())
+    classes[:, 1] = n - 1
+    grad = torch.full((m,), 2.0 ** -130, device=dev())
+    note("smallest temperature %s" % dtype)
+    loss, lse, weights = xt.linear_distillation(X, W, classes, teacher, None, T)
+    _, _, db = xt.linear_distillation_backward(grad, X, W, classes, weights, lse, None, T)
+    torch.cuda.synchronize()
+    assert (weights == 0.5).all()
+    assert ((lse.double() - math.log(n)).abs() <= 4 * O.U * math.log(n)).all()
+    assert ((loss.double() - math.log(n / 2)).abs() <= 8 * O.U * math.log(n)).all()
+    d = torch.full((n,), 1.0 / n, dtype=torch.float64, device=dev())
+    d[[7, n - 1]] -= 0.5
+    want = m * 2.0 ** -130 * float(torch.tensor(1.0) / torch.tensor(T)) * d
+    # lse off by 4 steps of log n, the factor and sums of m equal terms
+    assert ((db.double() - want).abs() <= want.abs() * (4 * math.log(n) + m + 8) * O.U).all()
